@@ -329,6 +329,75 @@ KDA_API kda_status kda_chunk_fwd_static_scratch(const kda_shape* shape, const vo
                                                 float* final_state, void* stream,
                                                 void** status_word);
 
+/* ------------------------------------------------------------------------------
+ * The gated delta rule with one scalar gate per token and value head.
+ *
+ * Operation (per sequence and value head hv, q and k of key head hv / (HV / H)):
+ *     S_t = e^{g_t} S_{t-1} + beta_t k_t (v_t - e^{g_t} S_{t-1}^T k_t)^T
+ *     o_t = scale * S_t^T q_t
+ * This is the recurrence above with every entry of g_t equal; stated with a scalar
+ * the gate costs 1 / K of the bytes, and the decay between two tokens factors out
+ * of the products over key dims, so any decay is exact (no KDA_ERR_DECAY_RANGE).
+ * The conventions at the top of this file hold; g and beta are [B, T, HV] fp32 and
+ * need 4-byte alignment only.
+ */
+
+/*
+ * Forward.  q, k [B, T, H, K], v, out [B, T, HV, V] io_dtype; initial_state and
+ * final_state [NS, HV, K, V] fp32 or NULL; cu_seqlens as in kda_chunk_fwd;
+ * final_state may be initial_state.  fp32 I/O runs the token recurrence.
+ * workspace: kda_gdr_fwd_workspace_size(shape) bytes, nothing in it needs
+ * initialising; its first word is the status kda_read_device_status reads
+ * (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens, whose sequences are then
+ * taken as empty, or KDA_ERR_DEVICE_TIMEOUT).
+ */
+KDA_API size_t kda_gdr_fwd_workspace_size(const kda_shape* shape);
+KDA_API kda_status kda_gdr_fwd(const kda_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                               const float* beta, float scale, const float* initial_state,
+                               const int32_t* cu_seqlens, void* out, float* final_state, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Recurrent step for serving: T (typically 1) new tokens of each of B sequences,
+ * states updated in place.  Any io_dtype, num_seqs = 0.
+ *   state  [B, HV, K, V] fp32; with slots, a pool [num_slots, HV, K, V]
+ *   slots  [B] int32 or NULL: sequence b's state is state[slots[b]]; a negative slot
+ *          marks an empty row (its out is 0, no state is read or written).  The
+ *          non-negative slots must differ from one another.  A slot >= num_slots is
+ *          treated as empty and sets bit 1 of *status_word.
+ *   num_slots  entries of the pool (0 without slots)
+ *   status_word  device word or NULL; bits are only ever added, the caller clears it
+ *          (kda_read_device_status reads it: KDA_ERR_DEVICE_BOUNDS)
+ */
+KDA_API kda_status kda_gdr_step(const kda_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                                const float* beta, float scale, float* state, const int32_t* slots, int num_slots,
+                                void* out, uint32_t* status_word, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Layer norm over the last dimension (the norm in front of a layer's projections).
+ *     y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps), var biased
+ * x [rows, D] io_dtype with x_stride >= D elements from row to row; y [rows, D]
+ * contiguous, io_dtype; weight and bias [D] fp32 or NULL (ones, zeros); mean and rstd
+ * [rows] fp32 or NULL (not written).  Any D >= 1; pointers need their element's
+ * alignment only (16-byte aligned rows run the vector kernels).  Outputs must not
+ * overlap inputs or each other.  No workspace, nothing is checked on the device.
+ */
+KDA_API kda_status kda_layer_norm_fwd(int64_t rows, int D, kda_dtype io_dtype, const void* x, int64_t x_stride,
+                                      const float* weight, const float* bias, float eps, void* y, float* mean,
+                                      float* rstd, void* stream);
+
+/*
+ * Its gradients, from the forward's x, mean and rstd: dx [rows, D] io_dtype,
+ * dweight and dbias [D] fp32 (each may be NULL, not all three).  The rows' sum for
+ * dweight and dbias is taken in a fixed order (the same bits on every call);
+ * workspace: kda_layer_norm_bwd_workspace_size(rows, D) bytes, uninitialised.
+ */
+KDA_API size_t kda_layer_norm_bwd_workspace_size(int64_t rows, int D);
+KDA_API kda_status kda_layer_norm_bwd(int64_t rows, int D, kda_dtype io_dtype, const void* x, int64_t x_stride,
+                                      const void* dy, int64_t dy_stride, const float* weight, const float* mean,
+                                      const float* rstd, void* dx, float* dweight, float* dbias, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,4 +26,12 @@ from ._lib import (  # noqa: F401
     load_library,
     make_shape,
 )
+from ._gdr import (  # noqa: F401
+    kda_gdr_fwd,
+    kda_gdr_fwd_workspace_size,
+    kda_gdr_step,
+    kda_layer_norm_bwd,
+    kda_layer_norm_bwd_workspace_size,
+    kda_layer_norm_fwd,
+)
 from .builder import build  # noqa: F401
