@@ -345,7 +345,9 @@ KDA_API kda_status kda_chunk_fwd_static_scratch(const kda_shape* shape, const vo
 /*
  * Forward.  q, k [B, T, H, K], v, out [B, T, HV, V] io_dtype; initial_state and
  * final_state [NS, HV, K, V] fp32 or NULL; cu_seqlens as in kda_chunk_fwd;
- * final_state may be initial_state.  fp32 I/O runs the token recurrence.
+ * final_state may be initial_state.  bf16 I/O runs in chunks of 64 tokens on the
+ * tensor cores, every fp32 operand in two bf16 parts (states to about 4e-6); fp32
+ * I/O runs the token recurrence.
  * workspace: kda_gdr_fwd_workspace_size(shape) bytes, nothing in it needs
  * initialising; its first word is the status kda_read_device_status reads
  * (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens, whose sequences are then

@@ -12,6 +12,9 @@ namespace gdr {
 cudaError_t launch_step(const Params& p, float* state, const int32_t* slots, int num_slots, int K, int V, bool bf16,
                         cudaStream_t stream);
 cudaError_t launch_recurrent(const Params& p, int K, int V, bool bf16, cudaStream_t stream);
+size_t chunk_slots(size_t tokens, size_t ns, bool packed, int T);
+size_t chunk_fwd_bytes(size_t slots, int HV);
+cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long wait_ns, int K, int V, cudaStream_t st);
 }  // namespace gdr
 namespace ln {
 size_t bwd_workspace_bytes(long rows, int D);
@@ -63,6 +66,21 @@ kda_status check_shape(const kda_shape* s, bool packed, Sizes& z) {
   return KDA_OK;
 }
 
+// Limit of the kernels' bounded waits: 2 s, or KDA_WAIT_LIMIT_NS (read at each call).
+unsigned long long wait_limit_ns() {
+  const char* e = std::getenv("KDA_WAIT_LIMIT_NS");
+  if (e) {
+    char* end = nullptr;
+    const unsigned long long v = std::strtoull(e, &end, 10);
+    if (end != e && v > 0) return v;
+  }
+  return 2000000000ull;
+}
+
+// bf16 I/O runs the chunk kernels; fp32 I/O the token recurrence (its q, k and v are not
+// exact tensor-core operands).
+bool chunked(const kda_shape* s, const Sizes& z) { return s->io_dtype == KDA_BF16 && z.tokens > 0; }
+
 bool good_scale(float scale) { return scale > 0.f && std::isfinite(scale); }
 
 }  // namespace
@@ -72,7 +90,9 @@ extern "C" {
 size_t kda_gdr_fwd_workspace_size(const kda_shape* s) {
   Sizes z;
   if (check_shape(s, s && s->num_seqs > 0, z) != KDA_OK) return 0;
-  return kda::kWorkspaceBytes;
+  if (!chunked(s, z)) return kda::kWorkspaceBytes;
+  return kda::kWorkspaceBytes +
+         kda::gdr::chunk_fwd_bytes(kda::gdr::chunk_slots(z.tokens, z.ns, s->num_seqs > 0, s->T), s->HV);
 }
 
 kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const void* v, const float* g,
@@ -101,7 +121,11 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
   if (cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
   const kda::gdr::Params p{q, k, v, g, beta, initial_state, cu_seqlens, out, final_state, status, scale, s->T,
                            s->H, s->HV, static_cast<int>(z.ns)};
-  return kda::gdr::launch_recurrent(p, s->K, s->V, s->io_dtype == KDA_BF16, cs) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  const cudaError_t e =
+      chunked(s, z) ? kda::gdr::launch_chunk_fwd(p, static_cast<uint8_t*>(workspace) + kda::kWorkspaceBytes,
+                                                 wait_limit_ns(), s->K, s->V, cs)
+                    : kda::gdr::launch_recurrent(p, s->K, s->V, s->io_dtype == KDA_BF16, cs);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_gdr_step(const kda_shape* s, const void* q, const void* k, const void* v, const float* g,

@@ -1,0 +1,129 @@
+// gdr_chunk.cuh -- the chunk form of the gated delta rule with a scalar gate: layouts and
+// helpers shared by its kernels (gdr_chunk.cu: forward; gdr_grad.cu: backward).
+//
+// Mathematics, per chunk of C = 64 tokens of one (sequence, value head).  With gc the
+// running sum of g inside the chunk, D_ij = e^{gc_i - gc_j} (i >= j), G = e^{gc} and
+// E = e^{gc_last - gc} per row, gamma = e^{gc_last}, S the state entering the chunk:
+//     M  = strict_tril(beta_i (k_i . k_j) D_ij),   P = scale tril((q_i . k_j) D_ij)
+//     T  = (I + M)^{-1},   R = P T
+//     Y  = beta (v - G (k S)),   vn = T Y
+//     o  = scale G (q S) + R Y,   S' = gamma S + k^T (E vn)
+// (o's inner part is P vn = P T Y.)  The gate is a scalar per token, so it stays out of the
+// products: k and q enter the tensor cores exactly as they lie in memory, in bf16, and
+// every decay is a factor <= 1 on a row of an fp32 result; there is no range of g that the
+// form cannot take.
+//
+// Precision: q, k, v and d_out are exact bf16 operands.  Every fp32 operand (S, Y, vn, T,
+// R) is taken as two bf16 parts, high + low (2^-18 of the value is lost), and the parts'
+// products are summed in fp32; states and gates stay in fp32 registers.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gdr_common.cuh"
+#include "sm103.cuh"
+
+namespace kda {
+namespace gdr {
+
+constexpr int C = 64;                                  // tokens of a chunk
+constexpr unsigned long long kDrainNs = 2000000000ull; // limit for work already issued
+
+// Record of one (chunk, value head), written by the preparation and read by the chains:
+// [T; R] as two K-major, 128-byte-swizzled bf16 tiles of 128 rows x 64 (high, then low
+// parts), then per-row factors (fp32): G, E, beta, gamma.
+constexpr uint32_t kTileBytes = 128 * 128;
+constexpr uint32_t kRecFactors = 2 * kTileBytes;
+constexpr uint32_t kRecBytes = kRecFactors + 1024;
+
+struct ChunkParams {
+  Params p;
+  uint8_t* rec;       // [slots, HV] records
+  // backward: what the chains leave for the gradient kernel, as operand images, per (slot, hv)
+  uint8_t* states;    // S entering the chunk: [2 parts][V / 64][K rows][64] bf16
+  uint8_t* dstates;   // dS' leaving it, same layout
+  uint8_t* vn;        // vn: [2 parts][V / 64][64 rows][64]
+  uint8_t* z;         // z, same layout
+  const void* dout;   // [tokens, HV, V] bf16
+  const float* dfin;  // [NS, HV, K, V] or null
+  void* dv;           // [tokens, HV, V] bf16
+  float* ds0;         // [NS, HV, K, V] or null
+  unsigned long long wait_ns;
+  int chunks;         // chunks of a sequence (fixed length) or slots in all (packed)
+  int slots;
+};
+
+struct ChainMaps {
+  CUtensorMap q, k;   // boxes of 64 dims x 64 tokens
+  CUtensorMap v;      // forward: v, reverse: d_out; boxes of N columns x 64 tokens
+};
+
+// First slot of a sequence's chunks.  Packed sequences: floor(tok0 / 64) + seq leaves room
+// for every sequence's partial chunk without reading the other lengths.
+__device__ __forceinline__ int first_slot(const ChunkParams& a, int seq, long tok0) {
+  return a.p.cu ? static_cast<int>(tok0 >> 6) + seq : seq * a.chunks;
+}
+__device__ __forceinline__ int num_chunks(int len) { return (len + C - 1) >> 6; }
+
+// The sequence and chunk of a slot; false where the slot holds no chunk.
+__device__ __forceinline__ bool find_chunk(const ChunkParams& a, int slot, int& seq, long& tok, int& rows) {
+  long tok0;
+  int len, m;
+  if (a.p.cu == nullptr) {
+    seq = slot / a.chunks;
+    m = slot - seq * a.chunks;
+    tok0 = static_cast<long>(seq) * a.p.T;
+    len = a.p.T;
+  } else {
+    int lo = 0, hi = a.p.num_seqs - 1;  // the last sequence whose first slot is <= slot
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((a.p.cu[mid] >> 6) + mid <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo;
+    if (!seq_tokens(a.p.cu, a.p.T, a.p.num_seqs, a.p.status, seq, tok0, len)) return false;
+    m = slot - first_slot(a, seq, tok0);
+  }
+  if (m < 0 || m >= num_chunks(len)) return false;
+  tok = tok0 + 64l * m;
+  rows = min(C, len - C * m);
+  return true;
+}
+
+// Two fp32 values as packed bf16 high parts and low parts.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - __low2float(h), x1 - __high2float(h));
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
+  split2(x[0], x[1], hi.x, lo.x);
+  split2(x[2], x[3], hi.y, lo.y);
+  split2(x[4], x[5], hi.z, lo.z);
+  split2(x[6], x[7], hi.w, lo.w);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte offset of 16-byte chunk `c` (0..7) of row r in a tile of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t c) {
+  return (r >> 3) * 1024u + (r & 7) * 128u + ((c ^ (r & 7)) << 4);
+}
+// The same for 64-byte rows (4 chunks), 64-byte swizzle.
+__device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t c) {
+  return (r >> 3) * 512u + (r & 7) * 64u + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace gdr
+}  // namespace kda
