@@ -360,6 +360,28 @@ KDA_API kda_status kda_gdr_fwd(const kda_shape* shape, const void* q, const void
                                size_t workspace_bytes, void* stream);
 
 /*
+ * Backward: the gradients of sum_t <d_out_t, o_t> + <d_final_state, S_final> with
+ * respect to every input of kda_gdr_fwd, in chunk form: the states entering the
+ * chunks and the state gradients leaving them are carried by two chains side by side,
+ * then every chunk's gradients follow in parallel.  bf16 I/O (KDA_ERR_UNSUPPORTED
+ * for fp32), K, V in {64, 128}.
+ *   d_out           [B, T, HV, V]  bf16;  d_final_state [NS, HV, K, V] fp32 or NULL (zeros)
+ *   dq, dk          [B, T, H, K]   bf16, summed over the value heads of a key head in
+ *                   fp32 in a fixed order (the same bits on every call)
+ *   dv              [B, T, HV, V]  bf16;  dg, dbeta [B, T, HV] fp32
+ *   d_initial_state [NS, HV, K, V] fp32 or NULL (not written)
+ *   workspace       kda_gdr_bwd_workspace_size(shape) bytes (at K = V = 128, 225 KiB a
+ *                   chunk and value head), uninitialised; status as kda_gdr_fwd's
+ * The outputs must not overlap each other or any input.
+ */
+KDA_API size_t kda_gdr_bwd_workspace_size(const kda_shape* shape);
+KDA_API kda_status kda_gdr_bwd(const kda_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                               const float* beta, float scale, const float* initial_state,
+                               const int32_t* cu_seqlens, const void* d_out, const float* d_final_state, void* dq,
+                               void* dk, void* dv, float* dg, float* dbeta, float* d_initial_state,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Recurrent step for serving: T (typically 1) new tokens of each of B sequences,
  * states updated in place.  Any io_dtype, num_seqs = 0.
  *   state  [B, HV, K, V] fp32; with slots, a pool [num_slots, HV, K, V]

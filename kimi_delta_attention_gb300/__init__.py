@@ -27,6 +27,8 @@ from ._lib import (  # noqa: F401
     make_shape,
 )
 from ._gdr import (  # noqa: F401
+    kda_gdr_bwd,
+    kda_gdr_bwd_workspace_size,
     kda_gdr_fwd,
     kda_gdr_fwd_workspace_size,
     kda_gdr_step,

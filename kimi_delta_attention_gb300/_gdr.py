@@ -121,6 +121,40 @@ def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=Non
     return out, final_state
 
 
+def kda_gdr_bwd_workspace_size(shape: KdaShape) -> int:
+    return int(load_library().kda_gdr_bwd_workspace_size(ctypes.byref(shape)))
+
+
+def kda_gdr_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seqlens=None, d_final_state=None,
+                output_d_initial_state=True, workspace=None, stream=None):
+    """Gradients of sum <d_out, o> + <d_final_state, S_final> for kda_gdr_fwd with the same
+    arguments (bf16).  Returns (dq, dk, dv, dg, dbeta, d_initial_state): dq, dk, dv bf16,
+    the others fp32, in the inputs' shapes."""
+    lib = _lib._lib or load_library()
+    shape, addr, ns, device, scale = _rule_args(q, k, v, g, beta, scale, cu_seqlens)
+    states = (ns, shape.HV, shape.K, shape.V)
+    s0 = _need("initial_state", initial_state, _f32, states, device)
+    do = _need("d_out", d_out, v.dtype, v.shape, device)
+    dfin = _need("d_final_state", d_final_state, _f32, states, device)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dg, dbeta = torch.empty_like(g), torch.empty_like(beta)
+    ds0 = torch.empty(states, dtype=_f32, device=device) if output_d_initial_state else None
+    made = [dq, dk, dv, dg, dbeta, ds0]
+    ref = ctypes.byref(shape)
+    if workspace is None:
+        workspace = torch.empty(lib.kda_gdr_bwd_workspace_size(ref) or 256, dtype=torch.uint8, device=device)
+        made.append(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise KdaError(1, f"workspace must be contiguous on {device}")
+    stream, current = _stream(device, stream)
+    with _on(device):
+        _check(lib.kda_gdr_bwd(ref, *addr, scale, s0, _ptr_or_none(cu_seqlens), do, dfin, dq.data_ptr(), dk.data_ptr(),
+                               dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr_or_none(ds0), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), stream))
+    _keep(made, stream, current, device)
+    return dq, dk, dv, dg, dbeta, ds0
+
+
 def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, status=None, stream=None):
     """Recurrent step for serving: q, k [B,T,H,K]; v [B,T,HV,V]; g, beta [B,T,HV] fp32;
     state [B,HV,K,V] fp32, updated in place, or with slots [B] int32 a pool

@@ -34,7 +34,7 @@ EXPORTS = ("kda_chunk_fwd", "kda_recurrent_fwd", "kda_chunk_fwd_workspace_size",
            "kda_chunk_fwd_kernel_name", "kda_chunk_fwd_kernel_launches", "kda_chunk_fwd_static_scratch", "kda_decode", "kda_chunk_fwd_gated",
            "kda_chunk_states_size", "kda_chunk_states", "kda_chunk_output", "kda_backward_workspace_size",
            "kda_backward",
-           "kda_gdr_fwd_workspace_size", "kda_gdr_fwd", "kda_gdr_step", "kda_layer_norm_fwd",
+           "kda_gdr_fwd_workspace_size", "kda_gdr_fwd", "kda_gdr_bwd_workspace_size", "kda_gdr_bwd", "kda_gdr_step", "kda_layer_norm_fwd",
            "kda_layer_norm_bwd_workspace_size", "kda_layer_norm_bwd")
 GATE_KINDS = {"bounded": 0, "softplus": 1}
 
@@ -112,6 +112,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.kda_gdr_fwd_workspace_size.restype = S
         lib.kda_gdr_fwd.argtypes = fwd_args
         lib.kda_gdr_fwd.restype = I
+        lib.kda_gdr_bwd_workspace_size.argtypes = [SH]
+        lib.kda_gdr_bwd_workspace_size.restype = S
+        lib.kda_gdr_bwd.argtypes = [SH, P, P, P, P, P, F, P, P, P, P, P, P, P, P, P, P, P, S, P]
+        lib.kda_gdr_bwd.restype = I
         lib.kda_gdr_step.argtypes = [SH, P, P, P, P, P, F, P, P, I, P, P, P]
         lib.kda_gdr_step.restype = I
         lib.kda_layer_norm_fwd.argtypes = [L, I, I, P, L, P, P, F, P, P, P, P]

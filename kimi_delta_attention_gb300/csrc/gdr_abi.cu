@@ -15,6 +15,10 @@ cudaError_t launch_recurrent(const Params& p, int K, int V, bool bf16, cudaStrea
 size_t chunk_slots(size_t tokens, size_t ns, bool packed, int T);
 size_t chunk_fwd_bytes(size_t slots, int HV);
 cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long wait_ns, int K, int V, cudaStream_t st);
+size_t chunk_bwd_bytes(size_t slots, int HV, int K, int V);
+cudaError_t launch_chunk_bwd(const Params& p, const void* dout, const float* dfin, void* dq, void* dk, void* dv,
+                             float* dg, float* dbeta, float* ds0, uint8_t* ws, float* shares,
+                             unsigned long long wait_ns, int K, int V, cudaStream_t st);
 }  // namespace gdr
 namespace ln {
 size_t bwd_workspace_bytes(long rows, int D);
@@ -109,8 +113,8 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
     if (p && !aligned(p, 16)) return KDA_ERR_ALIGNMENT;
   if (!aligned(g, 4) || !aligned(beta, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_ALIGNMENT;
   const Span o{out, z.v}, f{final_state, z.state}, w{workspace, workspace_bytes};
-  const Span ins[] = {{q, z.qk}, {k, z.qk}, {v, z.v}, {g, z.gate}, {beta, z.gate}, {initial_state, z.state}};
-  for (int i = 0; i < 6; ++i) {
+  const Span ins[] = {{q, z.qk}, {k, z.qk}, {v, z.v}, {g, z.gate}, {beta, z.gate}, {initial_state, z.state}, {cu_seqlens, cu_seqlens ? (z.ns + 1) * 4 : 0}};
+  for (int i = 0; i < 7; ++i) {
     if (overlaps(o, ins[i]) || overlaps(w, ins[i])) return KDA_ERR_INVALID_ARG;
     if (overlaps(f, ins[i]) && !(i == 5 && final_state == initial_state)) return KDA_ERR_INVALID_ARG;
   }
@@ -126,6 +130,72 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
                                                  wait_limit_ns(), s->K, s->V, cs)
                     : kda::gdr::launch_recurrent(p, s->K, s->V, s->io_dtype == KDA_BF16, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+namespace {
+// Workspace of the backward: the status word, the chunks' intermediates, and with grouped
+// value heads their fp32 shares of dq and dk.
+size_t bwd_shares_at(const kda_shape* s, const Sizes& z) {
+  return kda::kWorkspaceBytes + kda::gdr::chunk_bwd_bytes(kda::gdr::chunk_slots(z.tokens, z.ns, s->num_seqs > 0, s->T),
+                                                          s->HV, s->K, s->V);
+}
+size_t bwd_bytes(const kda_shape* s, const Sizes& z) {
+  if (z.tokens == 0) return kda::kWorkspaceBytes;
+  return bwd_shares_at(s, z) + (s->HV != s->H ? 2 * z.tokens * s->HV * s->K * sizeof(float) : 0);
+}
+}  // namespace
+
+size_t kda_gdr_bwd_workspace_size(const kda_shape* s) {
+  Sizes z;
+  if (check_shape(s, s && s->num_seqs > 0, z) != KDA_OK || s->io_dtype != KDA_BF16) return 0;
+  return bwd_bytes(s, z);
+}
+
+kda_status kda_gdr_bwd(const kda_shape* s, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, float scale, const float* initial_state, const int32_t* cu_seqlens,
+                       const void* d_out, const float* d_final_state, void* dq, void* dk, void* dv, float* dg,
+                       float* dbeta, float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
+  Sizes z;
+  const kda_status st = check_shape(s, cu_seqlens != nullptr, z);
+  if (st != KDA_OK) return st;
+  if (!good_scale(scale)) return KDA_ERR_INVALID_ARG;
+  if (s->io_dtype != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < bwd_bytes(s, z)) return KDA_ERR_WORKSPACE;
+  if (z.tokens > 0 && (!q || !k || !v || !g || !beta || !d_out || !dq || !dk || !dv || !dg || !dbeta))
+    return KDA_ERR_INVALID_ARG;
+  const void* ptrs16[] = {q, k, v, initial_state, d_out, d_final_state, dq, dk, dv, d_initial_state, workspace};
+  for (const void* p : ptrs16)
+    if (p && !aligned(p, 16)) return KDA_ERR_ALIGNMENT;
+  if (!aligned(g, 4) || !aligned(beta, 4) || !aligned(dg, 4) || !aligned(dbeta, 4) || !aligned(cu_seqlens, 4))
+    return KDA_ERR_ALIGNMENT;
+  const Span ins[] = {{q, z.qk}, {k, z.qk}, {v, z.v}, {g, z.gate}, {beta, z.gate}, {initial_state, z.state},
+                      {d_out, z.v}, {d_final_state, z.state}, {cu_seqlens, cu_seqlens ? (z.ns + 1) * 4 : 0}};
+  const Span outs[] = {{dq, z.qk}, {dk, z.qk}, {dv, z.v}, {dg, z.gate}, {dbeta, z.gate}, {d_initial_state, z.state},
+                       {workspace, workspace_bytes}};
+  for (int i = 0; i < 7; ++i) {
+    for (const Span& j : ins)
+      if (overlaps(outs[i], j)) return KDA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 7; ++j)
+      if (overlaps(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
+  }
+  if (z.ns == 0) return KDA_OK;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  if (cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
+  if (z.tokens == 0) {  // no tokens: the state's gradient passes through
+    if (!d_initial_state) return KDA_OK;
+    const cudaError_t e = d_final_state ? cudaMemcpyAsync(d_initial_state, d_final_state, z.state, cudaMemcpyDeviceToDevice, cs)
+                                        : cudaMemsetAsync(d_initial_state, 0, z.state, cs);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  }
+  const kda::gdr::Params p{q, k, v, g, beta, initial_state, cu_seqlens, nullptr, nullptr, status, scale, s->T,
+                           s->H, s->HV, static_cast<int>(z.ns)};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return kda::gdr::launch_chunk_bwd(p, d_out, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state,
+                                    ws + kda::kWorkspaceBytes, reinterpret_cast<float*>(ws + bwd_shares_at(s, z)),
+                                    wait_limit_ns(), s->K, s->V, cs) == cudaSuccess
+             ? KDA_OK
+             : KDA_ERR_CUDA;
 }
 
 kda_status kda_gdr_step(const kda_shape* s, const void* q, const void* k, const void* v, const float* g,

@@ -90,31 +90,17 @@ __global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constan
     tmem_alloc(tslot, 64);
     tmem_relinquish();
   }
-  // gc in log2 units, kept as a float and what the float misses of the double sum: decays
-  // between neighbours stay exact after a steep drop.  g below -120 already is e^g = 0.
-  double run = 0.;
-  {
+  if (warp == 1) {
+    float h[2], l[2];
+    gate_scan(p, tok, rows, hv, lane, h, l);
+    gh[2 * lane] = h[0];
+    gh[2 * lane + 1] = h[1];
+    gl[2 * lane] = l[0];
+    gl[2 * lane + 1] = l[1];
+  } else if (warp == 2) {
     const int i0 = 2 * lane;
-    float g0 = i0 < rows ? p.g[(tok + i0) * p.HV + hv] : 0.f, g1 = i0 + 1 < rows ? p.g[(tok + i0 + 1) * p.HV + hv] : 0.f;
-    g0 = g0 < -120.f ? -120.f : g0;
-    g1 = g1 < -120.f ? -120.f : g1;
-    const double d0 = 1.4426950408889634 * g0, d1 = 1.4426950408889634 * g1;
-    run = d0 + d1;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const double up = __shfl_up_sync(0xFFFFFFFFu, run, s);
-      if (lane >= s) run += up;
-    }
-    if (warp == 1) {
-      const double r0 = run - d1;
-      gh[i0] = static_cast<float>(r0);
-      gh[i0 + 1] = static_cast<float>(run);
-      gl[i0] = static_cast<float>(r0 - static_cast<double>(gh[i0]));
-      gl[i0 + 1] = static_cast<float>(run - static_cast<double>(gh[i0 + 1]));
-    } else if (warp == 2) {
-      bs[i0] = i0 < rows ? p.beta[(tok + i0) * p.HV + hv] : 0.f;
-      bs[i0 + 1] = i0 + 1 < rows ? p.beta[(tok + i0 + 1) * p.HV + hv] : 0.f;
-    }
+    bs[i0] = i0 < rows ? p.beta[(tok + i0) * p.HV + hv] : 0.f;
+    bs[i0 + 1] = i0 + 1 < rows ? p.beta[(tok + i0 + 1) * p.HV + hv] : 0.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -221,22 +207,36 @@ __global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constan
 // products land in 2 N columns and are added when read), so that a product is one
 // instruction per 16 of K: the chain is bound by the latency of these three steps, not by
 // the tensor cores' rate.
+//
+// SAVE is the same recurrence for the backward: no output (the q and R rows are not
+// loaded; what lies in their place only meets lanes that nobody reads); the state entering
+// each chunk goes to memory in fp32, vn as an operand image in two bf16 parts.
+//
+// REVERSE carries the state's gradient from the last chunk to the first, with dS' the
+// gradient leaving the chunk:
+//   1. D1 = k dS'                               z = T^T (E k dS') + R^T do
+//   2. D2 = T^T (E D1),  D2' = R^T do           dv = beta z
+//   3. D3 = k^T (-G beta z) + q^T (scale G do)  dS = gamma dS' + D3
+// with the transposed operands read from the same tiles (MN-major), so M is 128 where only
+// 64 lanes are wanted: the other lanes' atom is some other tile and nobody reads them.
 namespace chain {
 constexpr int NT = 288;
-template <int K, int N>
+enum Mode { FORWARD, SAVE, REVERSE };
+template <int K, int N, Mode MODE>
 struct Lay {
+  static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : C;    // REVERSE: rows 64-127 hold scale G do
   // a stage: [k; q] tiles at 0, then
   static constexpr uint32_t REC = (K / 64) * kTileBytes;          // the record
-  static constexpr uint32_t VS = REC + kRecBytes;                 // v: 64 rows x N
+  static constexpr uint32_t VS = REC + kRecBytes;                 // v (or do): 64 rows x N
   static constexpr uint32_t STAGE = VS + C * N * 2;
   static constexpr uint32_t S = 2 * STAGE;                        // S parts: K-rows of 2 N columns
   static constexpr uint32_t Y = S + 128 * 2 * N * 2;              // Y, then E vn
-  static constexpr uint32_t BAR = Y + C * 2 * N * 2;
+  static constexpr uint32_t BAR = Y + YROWS * 2 * N * 2;
   static constexpr uint32_t SMEM = BAR + 128 + 1024;
-  static constexpr uint32_t LBO_S = 128 * 128, LBO_Y = C * 128;   // between 64-column atoms
-  static constexpr uint32_t TX = STAGE;
+  static constexpr uint32_t LBO_S = 128 * 128, LBO_Y = YROWS * 128;   // between 64-column atoms
+  static constexpr uint32_t TX = MODE == SAVE ? (K / 64) * 8192 + 2 * 8192 + 1024 + C * N * 2 : STAGE;
 };
-enum { FULL0 = 0, FULL1, D1, D2, D3, SREADY, YREADY, VREADY, DRAIN, NBAR };
+enum { FULL0 = 0, FULL1, D1, D2, D3, SREADY, YREADY, VREADY, QREADY, DRAIN, NBAR };
 }  // namespace chain
 
 // CPT values of a row as the two parts of a 2 N-column operand (c0: first column).
@@ -255,38 +255,74 @@ __device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, 
     }
   }
 }
+// The same as the two parts of a 64-row operand image in memory.
+template <int CPT>
+__device__ __forceinline__ void put_image(uint8_t* hi, uint8_t* lo, int row, int c0, const float (&x)[CPT]) {
+#pragma unroll
+  for (int j = 0; j < CPT / 8; ++j) {
+    uint4 h, l;
+    split8(x + 8 * j, h, l);
+    *reinterpret_cast<uint4*>(hi + sw128(row, (c0 >> 3) + j)) = h;
+    *reinterpret_cast<uint4*>(lo + sw128(row, (c0 >> 3) + j)) = l;
+  }
+}
+template <int CPT>
+__device__ __forceinline__ void put_bf16(void* out, size_t at, const float (&x)[CPT]) {
+  __nv_bfloat16* op = static_cast<__nv_bfloat16*>(out) + at;
+#pragma unroll
+  for (int j = 0; j < CPT / 8; ++j)
+    *reinterpret_cast<uint4*>(op + 8 * j) =
+        make_uint4(pack_bf16(x[8 * j], x[8 * j + 1]), pack_bf16(x[8 * j + 2], x[8 * j + 3]),
+                   pack_bf16(x[8 * j + 4], x[8 * j + 5]), pack_bf16(x[8 * j + 6], x[8 * j + 7]));
+}
+__device__ __forceinline__ void st_global_v8(float* p, const float* x) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
 template <int CPT>
 __device__ __forceinline__ void tmem_ld(uint32_t t, float (&x)[CPT]) {
   if constexpr (CPT == 16) tmem_ld16(t, x);
   else tmem_ld32(t, x);
 }
+// x = the sum of the two parts' products
+template <int N, int CPT>
+__device__ __forceinline__ void tmem_ld_parts(uint32_t t, float (&x)[CPT]) {
+  float y[CPT];
+  tmem_ld<CPT>(t, x);
+  tmem_ld<CPT>(t + N, y);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) x[j] += y[j];
+}
 
-template <int K, int N>
-__global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a,
-                                                                 int V) {
-  using L = chain::Lay<K, N>;
+template <int K, int N, chain::Mode MODE>
+__device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkParams& a, int V, int block, uint8_t* raw) {
+  using L = chain::Lay<K, N, MODE>;
   using namespace chain;
   constexpr int CPT = N / 2;
-  extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
   volatile uint32_t* failed = tslot + 1;
   const Params& p = a.p;
   const int slices = V / N;
-  const int unit = blockIdx.x / slices, v0 = (blockIdx.x % slices) * N;
+  const int unit = block / slices, v0 = (block % slices) * N;
   const int seq = unit / p.HV, hv = unit % p.HV, hk = hv / (p.HV / p.H);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long tok0;
   int len;
   seq_tokens(p.cu, p.T, p.num_seqs, p.status, seq, tok0, len);
   const int nch = num_chunks(len), slot0 = first_slot(a, seq, tok0);
+  const auto chunk = [&](int n) { return MODE == REVERSE ? nch - 1 - n : n; };  // of step n
   if (tid == 0) {
-    for (int b = 0; b < NBAR; ++b) mbar_init(&bars[b], b == SREADY ? 8 : (b == YREADY || b == VREADY) ? 4 : 1);
+    for (int b = 0; b < NBAR; ++b)
+      mbar_init(&bars[b], b == SREADY ? 8 : (b == YREADY || b == VREADY || b == QREADY) ? 4 : 1);
     *failed = 0u;
     fence_mbar_init();
   }
   constexpr uint32_t TCOLS = N == 32 ? 256 : 512;
+  constexpr uint32_t TD2 = 2 * N, TD3 = 4 * N, TD2R = 6 * N;
   if (warp == 8) {
     tmem_alloc(tslot, TCOLS);
     tmem_relinquish();
@@ -317,13 +353,20 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
       if (lane == 0) {
         uint8_t* st = sm + (n & 1) * L::STAGE;
         uint64_t* full = &bars[FULL0 + (n & 1)];
-        const int tok = static_cast<int>(tok0 + C * static_cast<long>(n));
+        const int tok = static_cast<int>(tok0 + C * static_cast<long>(chunk(n)));
+        const uint8_t* rec = a.rec + (static_cast<size_t>(slot0 + chunk(n)) * p.HV + hv) * kRecBytes;
         mbar_arrive_expect_tx_relaxed(full, L::TX);
-        bulk_load(st + L::REC, a.rec + (static_cast<size_t>(slot0 + n) * p.HV + hv) * kRecBytes, kRecBytes, full);
+        if (MODE == SAVE) {
+          bulk_load(st + L::REC, rec, 8192, full);
+          bulk_load(st + L::REC + kTileBytes, rec + kTileBytes, 8192, full);
+          bulk_load(st + L::REC + kRecFactors, rec + kRecFactors, 1024, full);
+        } else {
+          bulk_load(st + L::REC, rec, kRecBytes, full);
+        }
 #pragma unroll
         for (int b = 0; b < K / 64; ++b) {
           tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
-          tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
+          if (MODE != SAVE) tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
         }
         tma_load_3d(st + L::VS, &maps.v, full, v0, hv, tok);
       }
@@ -331,39 +374,57 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
     };
     int issued = 0, landed = 0;
     for (; issued < 2 && issued < nch; ++issued) load(issued);
-    constexpr uint32_t id1 = idesc_f16kind(128, 2 * N) | IDESC_B_MN_MAJOR;
-    constexpr uint32_t id1h = idesc_f16kind(128, N == 32 ? 2 * N : N) | IDESC_B_MN_MAJOR;
-    constexpr uint32_t id3 = id1 | IDESC_A_MN_MAJOR;
+    constexpr uint32_t id2n = idesc_f16kind(128, 2 * N) | IDESC_B_MN_MAJOR;   // both parts of B
+    constexpr uint32_t idn = idesc_f16kind(128, N == 32 ? 2 * N : N) | IDESC_B_MN_MAJOR;  // the high part (N = 32: both)
     const uint64_t ds = sdesc(sb + L::S, L::LBO_S, 1024, 2), dy = sdesc(sb + L::Y, L::LBO_Y, 1024, 2);
     for (int n = 0; n < nch; ++n) {
       const uint32_t ph = n & 1, st = sb + ph * L::STAGE;
-      const uint64_t dkq = sdesc_sw128(st), dt = sdesc_sw128(st + L::REC), dkt = sdesc(st, kTileBytes, 1024, 2);
+      const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2);
+      const uint64_t dt = MODE == REVERSE ? sdesc(st + L::REC, kTileBytes, 1024, 2) : sdesc_sw128(st + L::REC);
       if (!wait(FULL0 + (n & 1), (n >> 1) & 1)) break;
       landed = n + 1;
       if (!wait(SREADY, ph)) break;
       tc_fence_after();
 #pragma unroll
       for (int s = 0; s < K / 16; ++s)
-        umma_f16_warp(tmem, dkq + (((s >> 2) * kTileBytes + (s & 3) * 32) >> 4), ds + (s * 2048 >> 4), id1, s > 0);
+        umma_f16_warp(tmem, dkq + (((s >> 2) * kTileBytes + (s & 3) * 32) >> 4), ds + (s * 2048 >> 4), id2n, s > 0);
       umma_commit_warp(&bars[D1]);
-      // everything that read the other stage is done (SREADY): chunk n + 1 into it
+      // everything that read the other stage is done (SREADY): the next chunk into it
       if (n > 0 && issued < nch) {
         load(issued);
         ++issued;
       }
+      if (MODE == REVERSE) {
+        if (!wait(QREADY, ph)) break;
+        tc_fence_after();
+        const uint64_t dd = sdesc(st + L::VS, 8192, 1024, 2);
+        constexpr uint32_t idr = idesc_f16kind(128, N) | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)  // R^T do, the two parts of R (rows 64-127 of the record's tiles)
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            umma_f16_warp(tmem + TD2R, dt + ((h * kTileBytes + 8192 + s * 2048) >> 4), dd + (s * 2048 >> 4), idr,
+                          h + s > 0);
+#pragma unroll
+        for (int s = 4; s < 8; ++s)  // q^T (scale G do)
+          umma_f16_warp(tmem + TD3, dkt + (s * 2048 >> 4), dy + (s * 2048 >> 4), id2n | IDESC_A_MN_MAJOR, s > 4);
+      }
       if (!wait(YREADY, ph)) break;
       tc_fence_after();
+      constexpr uint32_t am = MODE == REVERSE ? IDESC_A_MN_MAJOR : 0u;
+      constexpr uint32_t as = MODE == REVERSE ? 2048 : 32;   // bytes of 16 of K in [T; R]
 #pragma unroll
-      for (int s = 0; s < 4; ++s) umma_f16_warp(tmem + 2 * N, dt + (s * 32 >> 4), dy + (s * 2048 >> 4), id1, s > 0);
+      for (int s = 0; s < 4; ++s) umma_f16_warp(tmem + TD2, dt + (s * as >> 4), dy + (s * 2048 >> 4), id2n | am, s > 0);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        umma_f16_warp(tmem + 2 * N, dt + ((kTileBytes + s * 32) >> 4), dy + (s * 2048 >> 4), id1h, 1u);
+        umma_f16_warp(tmem + TD2, dt + ((kTileBytes + s * as) >> 4), dy + (s * 2048 >> 4), idn | am, 1u);
       umma_commit_warp(&bars[D2]);
       if (!wait(VREADY, ph)) break;
       tc_fence_after();
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        umma_f16_warp(tmem + 4 * N, dkt + (s * 2048 >> 4), dy + (s * 2048 >> 4), id3, s > 0);
+        umma_f16_warp(tmem + TD3, dkt + (s * 2048 >> 4), dy + (s * 2048 >> 4), id2n | IDESC_A_MN_MAJOR,
+                      MODE == REVERSE || s > 0);
       umma_commit_warp(&bars[D3]);
     }
     // what is in flight ends before the CTA gives up its memory
@@ -371,18 +432,20 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
     umma_commit_warp(&bars[DRAIN]);
     mbar_wait(&bars[DRAIN], 0, kDrainNs);
   } else {
-    // ----------------------------------------------- state, Y, vn, output ---
+    // ------------------------------------------ state, Y, vn (z), output ---
     const int quad = warp & 3, c0 = (warp >> 2) * CPT;
     const int r = 32 * quad + lane;                  // TMEM lane: key dim of S, row of [k; q]
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + c0;
     const size_t soff = ((static_cast<size_t>(seq) * p.HV + hv) * K + r) * V + v0 + c0;
     const bool isk = quad < 2;                       // token rows of k; else rows r - 64 of q
     const int i = r & 63;
+    const float* first = MODE == REVERSE ? a.dfin : p.s0;
+    float* final = MODE == FORWARD ? p.sfin : MODE == REVERSE ? a.ds0 : nullptr;
     float s[CPT];
-    if (p.s0 && r < K) {
+    if (first && r < K) {
 #pragma unroll
       for (int j = 0; j < CPT / 4; ++j) {
-        const float4 t = *reinterpret_cast<const float4*>(p.s0 + soff + 4 * j);
+        const float4 t = *reinterpret_cast<const float4*>(first + soff + 4 * j);
         s[4 * j] = t.x; s[4 * j + 1] = t.y; s[4 * j + 2] = t.z; s[4 * j + 3] = t.w;
       }
     } else {
@@ -397,14 +460,29 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
       const uint32_t ph = n & 1;
       uint8_t* st = sm + ph * L::STAGE;
       const float* fac = reinterpret_cast<const float*>(st + L::REC + kRecFactors);
-      const long tok = tok0 + C * static_cast<long>(n) + i;
-      const bool live = C * n + i < len;
+      const int c = chunk(n);
+      const size_t tok = static_cast<size_t>(tok0 + C * static_cast<long>(c) + i);
+      const bool live = C * c + i < len;
+      if (MODE != FORWARD && r < K) {
+        float* img = (MODE == SAVE ? a.states : a.dstates) +
+                     ((static_cast<size_t>(slot0 + c) * p.HV + hv) * K + r) * V + v0 + c0;
+#pragma unroll
+        for (int j = 0; j < CPT / 8; ++j) st_global_v8(img + 8 * j, s + 8 * j);
+      }
       if (!(good = wait(FULL0 + (n & 1), (n >> 1) & 1))) break;
       const float row = fac[i], gamma = fac[192];
+      const size_t orow = (tok * p.HV + hv) * V + v0 + c0;
+      // rows past the sequence's end hold the next one's tokens, whatever they are: every
+      // operand that meets them in a sum over tokens has them zeroed first
+      auto clear_row = [&](uint8_t* tile) {
+#pragma unroll
+        for (int b = 0; b < K / 64; ++b)
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<uint4*>(tile + b * kTileBytes + sw128(i, ch)) = make_uint4(0, 0, 0, 0);
+      };
       float x[CPT], y[CPT];
-      if (isk) {
-        const float be = fac[128 + i], tail = fac[64 + i];
-        float vv[CPT];
+      auto load_v = [&](float (&o)[CPT]) {
 #pragma unroll
         for (int j = 0; j < CPT / 8; ++j) {
           const uint32_t ch = (c0 >> 3) + j;
@@ -412,85 +490,98 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            vv[8 * j + 2 * e] = __uint_as_float(w[e] << 16);
-            vv[8 * j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            o[8 * j + 2 * e] = __uint_as_float(w[e] << 16);
+            o[8 * j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
           }
         }
+      };
+      if (isk) {
+        const float be = fac[128 + i], tail = fac[64 + i];
+        if (MODE != REVERSE) load_v(y);
         if (!(good = wait(D1, ph))) break;
         tc_fence_after();
-        tmem_ld<CPT>(tl, x);
-        tmem_ld<CPT>(tl + N, y);
-        tmem_ld_wait();
-        // rows past the sequence's end hold the next one's tokens, whatever they are: their
-        // rows of Y are zero, and so are their rows of k before k^T (E vn)
+        tmem_ld_parts<N, CPT>(tl, x);
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) x[j] = live ? be * (vv[j] - row * (x[j] + y[j])) : 0.f;
-        if (!live && warp < 4) {
-#pragma unroll
-          for (int b = 0; b < K / 64; ++b)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(st + b * kTileBytes + sw128(i, c)) = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < CPT; ++j) {
+          const float t = MODE == REVERSE ? tail * x[j] : be * (y[j] - row * x[j]);
+          x[j] = live ? t : 0.f;
         }
+        if (!live && warp < 4) clear_row(st);
         put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, x);
         fence_proxy_async_smem();
         tc_fence_before();
         arrive(YREADY);
         if (!(good = wait(D2, ph))) break;
         tc_fence_after();
-        tmem_ld<CPT>(tl + 2 * N, x);
-        tmem_ld<CPT>(tl + 3 * N, y);
-        tmem_ld_wait();
+        tmem_ld_parts<N, CPT>(tl + TD2, x);
+        if (MODE == REVERSE) {
+          tmem_ld<CPT>(tl + TD2R, y);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) x[j] = live ? tail * (x[j] + y[j]) : 0.f;
-        put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, x);
+          for (int j = 0; j < CPT; ++j) x[j] += y[j];
+        }
+        const float f = MODE == REVERSE ? -row * be : tail;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+          x[j] = live ? x[j] : 0.f;
+          y[j] = f * x[j];
+        }
+        put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, y);
         fence_proxy_async_smem();
         tc_fence_before();
         arrive(VREADY);
-      } else {
+        if (MODE != FORWARD) {
+          uint8_t* img = (MODE == SAVE ? a.vn : a.z) +
+                         (static_cast<size_t>(slot0 + c) * p.HV + hv) * (4 * C * static_cast<size_t>(V)) + (v0 >> 6) * 8192;
+          put_image<CPT>(img, img + 2 * C * static_cast<size_t>(V), i, c0, x);
+        }
+        if (MODE == REVERSE && live) {
+#pragma unroll
+          for (int j = 0; j < CPT; ++j) y[j] = be * x[j];
+          put_bf16<CPT>(a.dv, orow, y);
+        }
+      } else if (MODE == FORWARD) {
         if (!(good = wait(D1, ph))) break;
         tc_fence_after();
-        tmem_ld<CPT>(tl, x);
-        tmem_ld<CPT>(tl + N, y);
-        tmem_ld_wait();
+        tmem_ld_parts<N, CPT>(tl, x);
         const float f = p.scale * row;
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) x[j] = f * (x[j] + y[j]);
+        for (int j = 0; j < CPT; ++j) x[j] *= f;
         if (!(good = wait(D2, ph))) break;
         tc_fence_after();
-        tmem_ld<CPT>(tl + 2 * N, y);
-        tmem_ld_wait();
+        tmem_ld_parts<N, CPT>(tl + TD2, y);
 #pragma unroll
         for (int j = 0; j < CPT; ++j) x[j] += y[j];
-        tmem_ld<CPT>(tl + 3 * N, y);
-        tmem_ld_wait();
-        if (live) {
-          __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + (static_cast<size_t>(tok) * p.HV + hv) * V + v0 + c0;
+        if (live) put_bf16<CPT>(p.out, orow, x);
+      } else if (MODE == REVERSE) {
+        load_v(x);
+        const float f = p.scale * row;
 #pragma unroll
-          for (int j = 0; j < CPT / 8; ++j) {
-            uint32_t w[4];
+        for (int j = 0; j < CPT; ++j) x[j] = live ? f * x[j] : 0.f;
+        if (!live) {
+          if (warp < 4) clear_row(st + 8192);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16(x[8 * j + 2 * e] + y[8 * j + 2 * e], x[8 * j + 2 * e + 1] + y[8 * j + 2 * e + 1]);
-            *reinterpret_cast<uint4*>(op + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int j = 0; j < CPT / 8; ++j)
+            *reinterpret_cast<uint4*>(st + L::VS + sw128(i, (c0 >> 3) + j)) = make_uint4(0, 0, 0, 0);
         }
+        put_parts<N, CPT>(sm + L::Y, L::LBO_Y, 64 + i, c0, x);
+        fence_proxy_async_smem();
+        arrive(QREADY);
       }
       if (!(good = wait(D3, ph))) break;
       tc_fence_after();
-      tmem_ld<CPT>(tl + 4 * N, x);
-      tmem_ld<CPT>(tl + 5 * N, y);
-      tmem_ld_wait();
+      tmem_ld_parts<N, CPT>(tl + TD3, x);
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) s[j] = fmaf(gamma, s[j], x[j] + y[j]);
+      for (int j = 0; j < CPT; ++j) s[j] = fmaf(gamma, s[j], x[j]);
       put_parts<N, CPT>(sm + L::S, L::LBO_S, r, c0, s);
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(SREADY);
     }
-    if (good && p.sfin && r < K) {
+    if (good && final && r < K) {
 #pragma unroll
       for (int j = 0; j < CPT / 4; ++j)
-        *reinterpret_cast<float4*>(p.sfin + soff + 4 * j) = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+        *reinterpret_cast<float4*>(final + soff + 4 * j) = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
     }
   }
   tc_fence_before();
@@ -499,6 +590,24 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, TCOLS);
   }
+}
+
+template <int K, int N>
+__global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a,
+                                                                 int V) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  chain_body<K, N, chain::FORWARD>(maps, a, V, blockIdx.x, raw);
+}
+
+// The backward's two chains in one launch: even blocks SAVE (maps: v), odd blocks REVERSE
+// (maps_r: d_out).  They share nothing but the records, so they run side by side.
+template <int K>
+__global__ void __launch_bounds__(chain::NT, 1) gdr_chains_kernel(const __grid_constant__ ChainMaps maps,
+                                                                  const __grid_constant__ ChainMaps maps_r,
+                                                                  const ChunkParams a, int V) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  if (blockIdx.x & 1) chain_body<K, 64, chain::REVERSE>(maps_r, a, V, blockIdx.x >> 1, raw);
+  else chain_body<K, 64, chain::SAVE>(maps, a, V, blockIdx.x >> 1, raw);
 }
 
 // ------------------------------------------------------------------- host ---
@@ -548,14 +657,28 @@ cudaError_t launch_prep(const ChainMaps& maps, const ChunkParams& a, cudaStream_
 
 template <int K, int N>
 cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cudaStream_t st) {
-  constexpr uint32_t bytes = chain::Lay<K, N>::SMEM;
+  constexpr uint32_t bytes = chain::Lay<K, N, chain::FORWARD>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(gdr_chain_kernel<K, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   gdr_chain_kernel<K, N><<<static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / N), chain::NT, bytes, st>>>(maps, a, V);
   return cudaGetLastError();
 }
 
+template <int K>
+cudaError_t launch_chains(const ChainMaps& maps, const ChainMaps& maps_r, const ChunkParams& a, int V, cudaStream_t st) {
+  constexpr uint32_t bytes = chain::Lay<K, 64, chain::REVERSE>::SMEM;   // the larger of the two
+  static_assert(bytes >= chain::Lay<K, 64, chain::SAVE>::SMEM, "shared memory of the two chains");
+  cudaError_t e = cudaFuncSetAttribute(gdr_chains_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  gdr_chains_kernel<K><<<2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / 64), chain::NT, bytes, st>>>(maps, maps_r, a, V);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+// gdr_grad.cu
+cudaError_t launch_grads(const ChainMaps& maps, const ChunkParams& a, int K, int V, cudaStream_t st);
+cudaError_t launch_group_sum(const float* shares, void* dq, void* dk, size_t tokens, int H, int G, int K, cudaStream_t st);
 
 // Slots of chunk records: every chunk (packed: floor(T / 64) and one more per sequence).
 size_t chunk_slots(size_t tokens, size_t ns, bool packed, int T) {
@@ -584,6 +707,51 @@ cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long w
   if (e != cudaSuccess) return e;
   if (K == 128) return N == 32 ? launch_chain<128, 32>(maps, a, V, st) : launch_chain<128, 64>(maps, a, V, st);
   return N == 32 ? launch_chain<64, 32>(maps, a, V, st) : launch_chain<64, 64>(maps, a, V, st);
+}
+
+// Bytes of a backward's intermediates per (slot, value head): the record, S and dS', vn and z.
+size_t chunk_bwd_bytes(size_t slots, int HV, int K, int V) {
+  return slots * HV * (kRecBytes + 8 * static_cast<size_t>(K) * V + 8 * static_cast<size_t>(C) * V);
+}
+
+cudaError_t launch_chunk_bwd(const Params& p, const void* dout, const float* dfin, void* dq, void* dk, void* dv,
+                             float* dg, float* dbeta, float* ds0, uint8_t* ws, float* shares,
+                             unsigned long long wait_ns, int K, int V, cudaStream_t st) {
+  const size_t tokens = p.cu ? static_cast<size_t>(p.T) : static_cast<size_t>(p.num_seqs) * p.T;
+  ChunkParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.p = p;
+  a.wait_ns = wait_ns;
+  a.chunks = (p.T + C - 1) / C;
+  a.slots = static_cast<int>(chunk_slots(tokens, p.num_seqs, p.cu != nullptr, p.T));
+  const size_t units = static_cast<size_t>(a.slots) * p.HV, kv = 4 * static_cast<size_t>(K) * V, cv = 4 * static_cast<size_t>(C) * V;
+  a.rec = ws;
+  a.states = reinterpret_cast<float*>(a.rec + units * kRecBytes);
+  a.dstates = a.states + units * kv / 4;
+  a.vn = a.rec + units * (kRecBytes + 2 * kv);
+  a.z = a.vn + units * cv;
+  a.dout = dout;
+  a.dfin = dfin;
+  a.dv = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.ds0 = ds0;
+  const bool grouped = p.HV != p.H;
+  a.dq = grouped ? static_cast<void*>(shares) : dq;
+  a.dk = grouped ? static_cast<void*>(shares + tokens * p.HV * K) : dk;
+  ChainMaps maps, maps_r;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!make_map(&maps.q, p.q, K, p.H, tokens, 64) || !make_map(&maps.k, p.k, K, p.H, tokens, 64) ||
+      !make_map(&maps.v, p.v, V, p.HV, tokens, 64))
+    return cudaErrorInvalidValue;
+  maps_r = maps;
+  if (!make_map(&maps_r.v, dout, V, p.HV, tokens, 64)) return cudaErrorInvalidValue;
+  cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
+  if (e != cudaSuccess) return e;
+  e = K == 128 ? launch_chains<128>(maps, maps_r, a, V, st) : launch_chains<64>(maps, maps_r, a, V, st);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_grads(maps_r, a, K, V, st)) != cudaSuccess || !grouped) return e;
+  return launch_group_sum(static_cast<const float*>(a.dq), dq, dk, tokens, p.H, p.HV / p.H, K, st);
 }
 
 }  // namespace gdr

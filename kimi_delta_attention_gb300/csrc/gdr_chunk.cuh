@@ -40,14 +40,18 @@ constexpr uint32_t kRecBytes = kRecFactors + 1024;
 struct ChunkParams {
   Params p;
   uint8_t* rec;       // [slots, HV] records
-  // backward: what the chains leave for the gradient kernel, as operand images, per (slot, hv)
-  uint8_t* states;    // S entering the chunk: [2 parts][V / 64][K rows][64] bf16
-  uint8_t* dstates;   // dS' leaving it, same layout
-  uint8_t* vn;        // vn: [2 parts][V / 64][64 rows][64]
+  // backward: what the chains leave for the gradient kernel, per (slot, hv)
+  float* states;      // S entering the chunk [K, V]
+  float* dstates;     // dS' leaving it
+  uint8_t* vn;        // vn as an operand image: [2 parts][V / 64][64 rows][64] bf16
   uint8_t* z;         // z, same layout
   const void* dout;   // [tokens, HV, V] bf16
   const float* dfin;  // [NS, HV, K, V] or null
+  void* dq;           // [tokens, H, K] bf16, or with grouped heads fp32 shares [tokens, HV, K]
+  void* dk;
   void* dv;           // [tokens, HV, V] bf16
+  float* dg;          // [tokens, HV]
+  float* dbeta;
   float* ds0;         // [NS, HV, K, V] or null
   unsigned long long wait_ns;
   int chunks;         // chunks of a sequence (fixed length) or slots in all (packed)
@@ -123,6 +127,29 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// gc of a chunk's rows 2 lane, 2 lane + 1 (one warp), in log2 units, as a float and what
+// the float misses of the double sum: decays between neighbours stay exact after a steep
+// drop.  g below -120 already is e^g = 0.  Rows past the end have g = 0.
+__device__ __forceinline__ void gate_scan(const Params& p, long tok, int rows, int hv, int lane, float (&hi)[2],
+                                          float (&lo)[2]) {
+  const int i0 = 2 * lane;
+  float g0 = i0 < rows ? p.g[(tok + i0) * p.HV + hv] : 0.f, g1 = i0 + 1 < rows ? p.g[(tok + i0 + 1) * p.HV + hv] : 0.f;
+  g0 = g0 < -120.f ? -120.f : g0;
+  g1 = g1 < -120.f ? -120.f : g1;
+  const double d0 = 1.4426950408889634 * g0, d1 = 1.4426950408889634 * g1;
+  double run = d0 + d1;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const double up = __shfl_up_sync(0xFFFFFFFFu, run, s);
+    if (lane >= s) run += up;
+  }
+  const double r0 = run - d1;
+  hi[0] = static_cast<float>(r0);
+  hi[1] = static_cast<float>(run);
+  lo[0] = static_cast<float>(r0 - static_cast<double>(hi[0]));
+  lo[1] = static_cast<float>(run - static_cast<double>(hi[1]));
 }
 
 }  // namespace gdr
