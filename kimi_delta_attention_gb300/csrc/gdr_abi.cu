@@ -81,6 +81,13 @@ unsigned long long wait_limit_ns() {
   return 2000000000ull;
 }
 
+// The chunk kernels' part of a workspace: 128-byte aligned, after the status word.
+constexpr size_t kChunkAlign = 128;
+uint8_t* chunk_part(void* workspace) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(workspace) + kda::kWorkspaceBytes;
+  return reinterpret_cast<uint8_t*>((at + kChunkAlign - 1) & ~(kChunkAlign - 1));
+}
+
 // bf16 I/O runs the chunk kernels; fp32 I/O the token recurrence (its q, k and v are not
 // exact tensor-core operands).
 bool chunked(const kda_shape* s, const Sizes& z) { return s->io_dtype == KDA_BF16 && z.tokens > 0; }
@@ -95,7 +102,7 @@ size_t kda_gdr_fwd_workspace_size(const kda_shape* s) {
   Sizes z;
   if (check_shape(s, s && s->num_seqs > 0, z) != KDA_OK) return 0;
   if (!chunked(s, z)) return kda::kWorkspaceBytes;
-  return kda::kWorkspaceBytes +
+  return kda::kWorkspaceBytes + kChunkAlign +
          kda::gdr::chunk_fwd_bytes(kda::gdr::chunk_slots(z.tokens, z.ns, s->num_seqs > 0, s->T), s->HV);
 }
 
@@ -126,8 +133,7 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
   const kda::gdr::Params p{q, k, v, g, beta, initial_state, cu_seqlens, out, final_state, status, scale, s->T,
                            s->H, s->HV, static_cast<int>(z.ns)};
   const cudaError_t e =
-      chunked(s, z) ? kda::gdr::launch_chunk_fwd(p, static_cast<uint8_t*>(workspace) + kda::kWorkspaceBytes,
-                                                 wait_limit_ns(), s->K, s->V, cs)
+      chunked(s, z) ? kda::gdr::launch_chunk_fwd(p, chunk_part(workspace), wait_limit_ns(), s->K, s->V, cs)
                     : kda::gdr::launch_recurrent(p, s->K, s->V, s->io_dtype == KDA_BF16, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -135,13 +141,13 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
 namespace {
 // Workspace of the backward: the status word, the chunks' intermediates, and with grouped
 // value heads their fp32 shares of dq and dk.
-size_t bwd_shares_at(const kda_shape* s, const Sizes& z) {
-  return kda::kWorkspaceBytes + kda::gdr::chunk_bwd_bytes(kda::gdr::chunk_slots(z.tokens, z.ns, s->num_seqs > 0, s->T),
+size_t bwd_shares_at(const kda_shape* s, const Sizes& z) {  // from chunk_part()
+  return kda::gdr::chunk_bwd_bytes(kda::gdr::chunk_slots(z.tokens, z.ns, s->num_seqs > 0, s->T),
                                                           s->HV, s->K, s->V);
 }
 size_t bwd_bytes(const kda_shape* s, const Sizes& z) {
   if (z.tokens == 0) return kda::kWorkspaceBytes;
-  return bwd_shares_at(s, z) + (s->HV != s->H ? 2 * z.tokens * s->HV * s->K * sizeof(float) : 0);
+  return kda::kWorkspaceBytes + kChunkAlign + bwd_shares_at(s, z) + (s->HV != s->H ? 2 * z.tokens * s->HV * s->K * sizeof(float) : 0);
 }
 }  // namespace
 
@@ -190,9 +196,8 @@ kda_status kda_gdr_bwd(const kda_shape* s, const void* q, const void* k, const v
   }
   const kda::gdr::Params p{q, k, v, g, beta, initial_state, cu_seqlens, nullptr, nullptr, status, scale, s->T,
                            s->H, s->HV, static_cast<int>(z.ns)};
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  return kda::gdr::launch_chunk_bwd(p, d_out, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state,
-                                    ws + kda::kWorkspaceBytes, reinterpret_cast<float*>(ws + bwd_shares_at(s, z)),
+  uint8_t* ws = chunk_part(workspace);
+  return kda::gdr::launch_chunk_bwd(p, d_out, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state, ws, reinterpret_cast<float*>(ws + bwd_shares_at(s, z)),
                                     wait_limit_ns(), s->K, s->V, cs) == cudaSuccess
              ? KDA_OK
              : KDA_ERR_CUDA;

@@ -11,61 +11,78 @@ namespace {
 
 // ------------------------------------------------------------ preparation ---
 // One CTA of 128 threads per (chunk, value head).  [k; q] k^T is one product of M = 128
-// (rows 0-63: k, 64-127: q), read back a row a thread.  Then thread i < 64 solves
-// x (I + M) = e_i, thread 64 + i solves x (I + M) = P_i: row i of T and of R = P T by the
-// same code, from the last column to the first, right-looking (once x_l is known it leaves
-// every x_j, j < l, independently), in fp32 with two columns per instruction.
+// (rows 0-63: k, 64-127: q), read back a row a thread into M and P (fp32, shared memory).
+// Then X (I + M) = [I; P] for the 128 rows X = [T; R], R = P T, in 16-column blocks from the
+// last to the first:
+//     X_J = ([I; P]_J - sum over L > J of X_L M_LJ) T_JJ
+// with T_JJ, the inverse of the diagonal block, by substitution (a row a thread), and the
+// block products on warp-level TF32 tensor instructions, each operand in two TF32 parts
+// (2^-20).  A row block of 16 needs no other: a warp walks its row blocks alone.
+// What bounds it is instruction fetch: written out straight (the solves unrolled into
+// registers), the code ran once per CTA at an instruction a cycle and SM, 47 us for 2048
+// chunks and heads by plain substitution, 87 us with these same block products unrolled.
+// So the block product is one small loop body and its operands stay in shared memory.
 namespace prep {
 constexpr int NT = 128;
-constexpr uint32_t LDM = 68;                           // floats between rows of M (conflict-free rows)
-// [k; q] tiles at 0, then the record's image over them
-constexpr uint32_t OFF_M = 33792;
-constexpr uint32_t OFF_GC = OFF_M + C * LDM * 4;       // gc high parts, low parts (log2), beta
-constexpr uint32_t OFF_BAR = OFF_GC + 3 * C * 4;
+constexpr uint32_t LDM = 68;                           // floats between rows of M, P and X: no bank conflicts
+// [k; q] tiles at 0; then X (128 rows, rows 64-127 start as P) over them; then the record's image
+constexpr uint32_t OFF_M = 128 * LDM * 4;
+constexpr uint32_t OFF_GC = OFF_M + C * LDM * 4;       // gc high parts, low parts (log2), beta, block factors
+constexpr uint32_t OFF_BAR = OFF_GC + 4 * C * 4;
 constexpr uint32_t SMEM = OFF_BAR + 64 + 1024;
+static_assert(OFF_M >= kRecBytes && OFF_M >= 2 * kTileBytes, "the record's image and the tiles fit");
+
+// Two TF32 parts by truncation (the low 13 bits cleared).
+__device__ __forceinline__ void tf32_parts(float x, uint32_t& h, uint32_t& l) {
+  h = __float_as_uint(x) & 0xFFFFE000u;
+  l = __float_as_uint(x - __uint_as_float(h)) & 0xFFFFE000u;
+}
+// acc (16 x 16, two 8-column tiles) += A B, both 16 x 16 floats in shared memory.  K is
+// taken in the order 0, 2, 4, 6, 1, 3, 5, 7 of an 8-column tile, for A's rows to be read in pairs.
+__device__ __forceinline__ void block_mma(float (&acc)[2][4], const float* x, int ldx, const float* b, int ldb, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  float cross[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // apart: shorter chains
+  uint32_t ah[2][4], al[2][4], bh[2][2][2], bl[2][2][2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const float2 u = *reinterpret_cast<const float2*>(x + g * ldx + 8 * s + 2 * t);
+    const float2 w = *reinterpret_cast<const float2*>(x + (g + 8) * ldx + 8 * s + 2 * t);
+    tf32_parts(u.x, ah[s][0], al[s][0]);
+    tf32_parts(w.x, ah[s][1], al[s][1]);
+    tf32_parts(u.y, ah[s][2], al[s][2]);
+    tf32_parts(w.y, ah[s][3], al[s][3]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) tf32_parts(b[(8 * s + 2 * t + e) * ldb + 8 * n + g], bh[s][n][e], bl[s][n][e]);
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      mma_tf32_m16n8k8(acc[n], ah[s], bh[s][n][0], bh[s][n][1]);
+      mma_tf32_m16n8k8(cross[n], ah[s], bl[s][n][0], bl[s][n][1]);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma_tf32_m16n8k8(cross[n], al[s], bh[s][n][0], bh[s][n][1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] += cross[n][e];
+}
 }  // namespace prep
 
-__device__ __forceinline__ uint64_t pack2f(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2f(uint64_t x, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
-// x_j -= x_l M_lj for l = HI .. LO and j < l; x holds columns in pairs.
-template <int HI, int LO>
-__device__ __forceinline__ void solve_columns(uint64_t (&x)[32], const float* m) {
-#pragma unroll
-  for (int l = HI; l >= LO; --l) {
-    float a, b;
-    unpack2f(x[l >> 1], a, b);
-    const float xl = (l & 1) ? b : a;
-    const uint64_t n = pack2f(-xl, -xl);
-    const ulonglong2* row = reinterpret_cast<const ulonglong2*>(m + l * prep::LDM);
-#pragma unroll
-    for (int j = 0; 4 * j < l; ++j) {  // M_lj = 0 for j >= l: the last group may run past l
-      const ulonglong2 r = row[j];
-      x[2 * j] = fma2(n, r.x, x[2 * j]);
-      if (4 * j + 2 < l) x[2 * j + 1] = fma2(n, r.y, x[2 * j + 1]);
-    }
-  }
-}
-
 template <int K>
-__global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
+__global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  float* xs = reinterpret_cast<float*>(sm);
   float* ms = reinterpret_cast<float*>(sm + prep::OFF_M);
   float* gh = reinterpret_cast<float*>(sm + prep::OFF_GC);
   float* gl = gh + C;
   float* bs = gl + C;
+  float* cf = bs + C;                             // e^{gc of the 16-block's last row - gc_j}
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + prep::OFF_BAR);  // [0]: tiles; [1]: product
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 2);
   const Params& p = a.p;
@@ -97,6 +114,9 @@ __global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constan
     gh[2 * lane + 1] = h[1];
     gl[2 * lane] = l[0];
     gl[2 * lane + 1] = l[1];
+    const float eh = __shfl_sync(0xFFFFFFFFu, h[1], lane | 7), el = __shfl_sync(0xFFFFFFFFu, l[1], lane | 7);
+    cf[2 * lane] = ex2((eh - h[0]) + (el - l[0]));
+    cf[2 * lane + 1] = ex2((eh - h[1]) + (el - l[1]));
   } else if (warp == 2) {
     const int i0 = 2 * lane;
     bs[i0] = i0 < rows ? p.beta[(tok + i0) * p.HV + hv] : 0.f;
@@ -130,53 +150,135 @@ __global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constan
     mbar_wait(&bar[1], 0, kDrainNs);
   }
   tc_fence_after();
-  uint64_t x[32];
+  // M and P.  D_ij = e^{gc_i - gc_j} directly in the row's own 16-block; before it through
+  // the block's last row, as two factors <= 1, one per row and block, one per column
   {
     const uint32_t t = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    const float f = isq ? p.scale : be;
-    const int last = isq ? i : i - 1;            // columns 0 .. last of the row are not zero
-    const bool have = i < rows;                  // rows past the sequence's end: M = P = 0
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float y[32];
-      tmem_ld32(t + 32 * h, y);
+    const float f = i < rows ? (isq ? p.scale : be) : 0.f;   // rows past the sequence's end: M = P = 0
+    const int last = isq ? i : i - 1, own = i >> 4;          // columns 0 .. last of the row are not zero
+    float* dst = (isq ? xs + C * prep::LDM : ms) + i * prep::LDM;  // P over the tiles
+    const int blocks = 2 + 2 * (warp & 1);                   // (rows 0-31 end in column 31)
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      float y[16];
+      tmem_ld16(t + 16 * b, y);
       tmem_ld_wait();
+      const float* ch = gh + 16 * b;
+      if (b >= blocks - 2) {                                 // a block of some of the warp's rows
+        const float fb = f * ex2(fminf((hi - ch[15]) + (lo - gl[16 * b + 15]), 0.f));
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int c = 32 * h + j;
-        y[j] = (have && c <= last) ? f * y[j] * ex2((hi - gh[c]) + (lo - gl[c])) : 0.f;
-      }
-      if (!isq) {
+        for (int j = 0; j < 16; ++j) {
+          const float d = b == own ? f * ex2((hi - ch[j]) + (lo - gl[16 * b + j])) : fb * cf[16 * b + j];
+          y[j] = (16 * b + j <= last && i < rows) ? y[j] * d : 0.f;
+        }
+      } else {
+        const float fb = f * ex2((hi - ch[15]) + (lo - gl[16 * b + 15]));
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(ms + i * prep::LDM + 32 * h + 4 * j) =
-              make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+        for (int j = 0; j < 16; ++j) y[j] = i < rows ? y[j] * (fb * cf[16 * b + j]) : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int c = 32 * h + 2 * j;
-        x[16 * h + j] = isq ? pack2f(y[2 * j], y[2 * j + 1]) : pack2f(c == i ? 1.f : 0.f, c + 1 == i ? 1.f : 0.f);
-      }
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(dst + 16 * b + 4 * j) = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
     }
   }
   tc_fence_before();
-  __syncthreads();  // M is in shared memory, the accumulator is read
+  __syncthreads();  // M and P are in shared memory, the accumulator is read
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 64);
   }
-  if (i >= 32) solve_columns<63, 32>(x, ms);     // (warps of rows 0-31: x_l = 0 there)
-  solve_columns<31, 1>(x, ms);
-  // the record's image over the tiles (the product that read them is complete)
+  if (warp < 2) {   // T_JJ: row i of its block of I + M inverted, in the block's place
+    const int rr = tid & 15;
+    float* mb = ms + (tid & ~15) * prep::LDM + (tid & ~15);
+    float x[16];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float y[8];
+    for (int j = 0; j < 16; ++j) x[j] = j == rr ? 1.f : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) unpack2f(x[4 * c + e], y[2 * e], y[2 * e + 1]);
-    uint4 h, l;
-    split8(y, h, l);
-    *reinterpret_cast<uint4*>(sm + sw128(tid, c)) = h;
-    *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, c)) = l;
+    for (int l = 15; l >= 1; --l)
+#pragma unroll
+      for (int j = 0; 4 * j < l; ++j) {
+        const float4 r = *reinterpret_cast<const float4*>(mb + l * prep::LDM + 4 * j);
+        x[4 * j] = fmaf(-x[l], r.x, x[4 * j]);
+        if (4 * j + 1 < l) x[4 * j + 1] = fmaf(-x[l], r.y, x[4 * j + 1]);
+        if (4 * j + 2 < l) x[4 * j + 2] = fmaf(-x[l], r.z, x[4 * j + 2]);
+        if (4 * j + 3 < l) x[4 * j + 3] = fmaf(-x[l], r.w, x[4 * j + 3]);
+      }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(mb + rr * prep::LDM + 4 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+  }
+  __syncthreads();
+  // row blocks (0-3 of T, 4-7 of R), shared out so that every warp has 8 to 10 of the 37
+  // block products
+  {
+    const int turn = (warp + blockIdx.x) & 3, g = lane >> 2, t = lane & 3;
+    uint32_t tasks = turn == 0 ? 0x7u : turn == 1 ? 0x03u : turn == 2 ? 0x56u : 0x412u;
+    const int count = turn == 0 ? 1 : turn == 3 ? 3 : 2;
+#pragma unroll 1
+    for (int q = 0; q < count; ++q, tasks >>= 4) {
+      const int rb = tasks & 7, I = rb & 3;
+      float* xr = xs + 16 * rb * prep::LDM;
+#pragma unroll 1
+      for (int J = I; J >= 0; --J) {
+        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+        for (int L = I; L > J; --L)
+          prep::block_mma(acc, xr + 16 * L, prep::LDM, ms + 16 * L * prep::LDM + 16 * J, prep::LDM, lane);
+        float* xj = xr + 16 * J + g * prep::LDM + 2 * t;
+        const float* tb = ms + 16 * J * (prep::LDM + 1);
+        if (rb < 4 && J == I) {                    // T's diagonal block
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            *reinterpret_cast<float2*>(xj + 8 * n) = *reinterpret_cast<const float2*>(tb + g * prep::LDM + 8 * n + 2 * t);
+            *reinterpret_cast<float2*>(xj + 8 * n + 8 * prep::LDM) =
+                *reinterpret_cast<const float2*>(tb + (g + 8) * prep::LDM + 8 * n + 2 * t);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float2 u = make_float2(0.f, 0.f), w = u;
+            if (rb >= 4) {
+              u = *reinterpret_cast<const float2*>(xj + 8 * n);
+              w = *reinterpret_cast<const float2*>(xj + 8 * n + 8 * prep::LDM);
+            }
+            *reinterpret_cast<float2*>(xj + 8 * n) = make_float2(u.x - acc[n][0], u.y - acc[n][1]);
+            *reinterpret_cast<float2*>(xj + 8 * n + 8 * prep::LDM) = make_float2(w.x - acc[n][2], w.y - acc[n][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+          }
+          __syncwarp();
+          prep::block_mma(acc, xr + 16 * J, prep::LDM, tb, prep::LDM, lane);
+          __syncwarp();
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            *reinterpret_cast<float2*>(xj + 8 * n) = make_float2(acc[n][0], acc[n][1]);
+            *reinterpret_cast<float2*>(xj + 8 * n + 8 * prep::LDM) = make_float2(acc[n][2], acc[n][3]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncthreads();
+  // rows of X to the record's image, over them
+  {
+    float y[C];
+    const int own = i >> 4;                        // columns past the row's own block are zero
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float4 u = (j >> 2) <= own ? *reinterpret_cast<const float4*>(xs + tid * prep::LDM + 4 * j)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      y[4 * j] = u.x; y[4 * j + 1] = u.y; y[4 * j + 2] = u.z; y[4 * j + 3] = u.w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint4 h, l;
+      split8(y + 8 * c, h, l);
+      *reinterpret_cast<uint4*>(sm + sw128(tid, c)) = h;
+      *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, c)) = l;
+    }
   }
   float* fac = reinterpret_cast<float*>(sm + kRecFactors);
   if (!isq) {
@@ -197,8 +299,8 @@ __global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constan
 // ------------------------------------------------------------------ chain ---
 // One CTA per (sequence, value head, N value columns): the columns of S never meet.  Warps
 // 0-7 hold the state in fp32 registers (warp w: key dims 32 (w % 4) + lane, half w / 4 of
-// the columns) and do everything between the products; warp 8 loads the chunks two ahead
-// (TMA tiles of k, q and v, the record by bulk copy) and issues the products.  Per chunk:
+// the columns) and do everything between the products, warp 8 issues the products, warp 9
+// loads the chunks two ahead (TMA tiles of k, q and v, the record by bulk copy).  Per chunk:
 //   1. D1 = [k; q] S      M = 128, K = key dims       lanes 0-63: k S, 64-127: q S
 //   2. D2 = [T; R] Y      M = 128, K = 64             lanes 0-63: vn,  64-127: R Y
 //   3. D3 = k^T (E vn)    M = 128 key dims, K = 64    S = gamma S + D3 in registers
@@ -220,7 +322,7 @@ __global__ void __launch_bounds__(prep::NT) gdr_prep_kernel(const __grid_constan
 // with the transposed operands read from the same tiles (MN-major), so M is 128 where only
 // 64 lanes are wanted: the other lanes' atom is some other tile and nobody reads them.
 namespace chain {
-constexpr int NT = 288;
+constexpr int NT = 320;
 enum Mode { FORWARD, SAVE, REVERSE };
 template <int K, int N, Mode MODE>
 struct Lay {
@@ -236,16 +338,16 @@ struct Lay {
   static constexpr uint32_t LBO_S = 128 * 128, LBO_Y = YROWS * 128;   // between 64-column atoms
   static constexpr uint32_t TX = MODE == SAVE ? (K / 64) * 8192 + 2 * 8192 + 1024 + C * N * 2 : STAGE;
 };
-enum { FULL0 = 0, FULL1, D1, D2, D3, SREADY, YREADY, VREADY, QREADY, DRAIN, NBAR };
+enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, D1, D2, D3, SREADY, YREADY, VREADY, QREADY, DRAIN, NBAR };
 }  // namespace chain
 
-// CPT values of a row as the two parts of a 2 N-column operand (c0: first column).
+// CPT values of a row (in pairs) as the two parts of a 2 N-column operand (c0: first column).
 template <int N, int CPT>
-__device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, int c0, const float (&x)[CPT]) {
+__device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, int c0, const uint64_t (&x)[CPT / 2]) {
 #pragma unroll
   for (int j = 0; j < CPT / 8; ++j) {
     uint4 h, l;
-    split8(x + 8 * j, h, l);
+    split8(x + 4 * j, h, l);
     if constexpr (N == 32) {
       *reinterpret_cast<uint4*>(base + sw128(row, (c0 >> 3) + j)) = h;
       *reinterpret_cast<uint4*>(base + sw128(row, 4 + (c0 >> 3) + j)) = l;
@@ -257,27 +359,35 @@ __device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, 
 }
 // The same as the two parts of a 64-row operand image in memory.
 template <int CPT>
-__device__ __forceinline__ void put_image(uint8_t* hi, uint8_t* lo, int row, int c0, const float (&x)[CPT]) {
+__device__ __forceinline__ void put_image(uint8_t* hi, uint8_t* lo, int row, int c0, const uint64_t (&x)[CPT / 2]) {
 #pragma unroll
   for (int j = 0; j < CPT / 8; ++j) {
     uint4 h, l;
-    split8(x + 8 * j, h, l);
+    split8(x + 4 * j, h, l);
     *reinterpret_cast<uint4*>(hi + sw128(row, (c0 >> 3) + j)) = h;
     *reinterpret_cast<uint4*>(lo + sw128(row, (c0 >> 3) + j)) = l;
   }
 }
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+  float a, b;
+  unpack2f(x, a, b);
+  return pack_bf16(a, b);
+}
 template <int CPT>
-__device__ __forceinline__ void put_bf16(void* out, size_t at, const float (&x)[CPT]) {
+__device__ __forceinline__ void put_bf16(void* out, size_t at, const uint64_t (&x)[CPT / 2]) {
   __nv_bfloat16* op = static_cast<__nv_bfloat16*>(out) + at;
 #pragma unroll
   for (int j = 0; j < CPT / 8; ++j)
     *reinterpret_cast<uint4*>(op + 8 * j) =
-        make_uint4(pack_bf16(x[8 * j], x[8 * j + 1]), pack_bf16(x[8 * j + 2], x[8 * j + 3]),
-                   pack_bf16(x[8 * j + 4], x[8 * j + 5]), pack_bf16(x[8 * j + 6], x[8 * j + 7]));
+        make_uint4(pack_pair(x[4 * j]), pack_pair(x[4 * j + 1]), pack_pair(x[4 * j + 2]), pack_pair(x[4 * j + 3]));
 }
-__device__ __forceinline__ void st_global_v8(float* p, const float* x) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+// (32-byte aligned: the workspace only)
+__device__ __forceinline__ void st_global_v8(float* p, const uint64_t* x) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack2f(x[j], f[2 * j], f[2 * j + 1]);
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
                : "memory");
 }
 template <int CPT>
@@ -287,20 +397,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&x)[CPT]) {
 }
 // x = the sum of the two parts' products
 template <int N, int CPT>
-__device__ __forceinline__ void tmem_ld_parts(uint32_t t, float (&x)[CPT]) {
-  float y[CPT];
-  tmem_ld<CPT>(t, x);
-  tmem_ld<CPT>(t + N, y);
+__device__ __forceinline__ void tmem_ld_parts(uint32_t t, uint64_t (&x)[CPT / 2]) {
+  float a[CPT], b[CPT];
+  tmem_ld<CPT>(t, a);
+  tmem_ld<CPT>(t + N, b);
   tmem_ld_wait();
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) x[j] += y[j];
+  for (int j = 0; j < CPT / 2; ++j) x[j] = add2(pack2f(a[2 * j], a[2 * j + 1]), pack2f(b[2 * j], b[2 * j + 1]));
 }
 
 template <int K, int N, chain::Mode MODE>
 __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkParams& a, int V, int block, uint8_t* raw) {
   using L = chain::Lay<K, N, MODE>;
   using namespace chain;
-  constexpr int CPT = N / 2;
+  constexpr int CPT = N / 2, H2 = CPT / 2;
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
@@ -333,7 +443,8 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   const uint32_t tmem = *tslot;
   // waits of a whole warp; false once the CTA has failed
   auto wait = [&](int b, uint32_t parity) {
-    bool ok = *failed == 0u && mbar_wait(&bars[b], parity, a.wait_ns);
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[b], parity))) return true;
+    const bool ok = *failed == 0u && mbar_wait(&bars[b], parity, a.wait_ns);
     if (__all_sync(0xFFFFFFFFu, ok)) return true;
     if (lane == 0 && *failed == 0u) {
       atomicOr(p.status, kStatusTimeout);
@@ -346,16 +457,23 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     if (lane == 0) mbar_arrive(&bars[b]);
   };
 
-  if (warp == 8) {
-    // ------------------------------------------------ loads and products ---
-    const uint32_t sb = smem_u32(sm);
-    auto load = [&](int n) {
+  if (warp == 9) {
+    // ---------------------------------------------------------------- loads ---
+    int n = 0;
+    for (; n < nch; ++n) {
+      // a stage's readers are done once the next chunk's products may start (EMPTY)
+      if (n >= 2 && !wait(EMPTY0 + (n & 1), ((n >> 1) - 1) & 1)) break;
       if (lane == 0) {
         uint8_t* st = sm + (n & 1) * L::STAGE;
         uint64_t* full = &bars[FULL0 + (n & 1)];
         const int tok = static_cast<int>(tok0 + C * static_cast<long>(chunk(n)));
         const uint8_t* rec = a.rec + (static_cast<size_t>(slot0 + chunk(n)) * p.HV + hv) * kRecBytes;
         mbar_arrive_expect_tx_relaxed(full, L::TX);
+#pragma unroll
+        for (int b = 0; b < K / 64; ++b) {
+          tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
+          if (MODE != SAVE) tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
+        }
         if (MODE == SAVE) {
           bulk_load(st + L::REC, rec, 8192, full);
           bulk_load(st + L::REC + kTileBytes, rec + kTileBytes, 8192, full);
@@ -363,17 +481,16 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         } else {
           bulk_load(st + L::REC, rec, kRecBytes, full);
         }
-#pragma unroll
-        for (int b = 0; b < K / 64; ++b) {
-          tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
-          if (MODE != SAVE) tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
-        }
         tma_load_3d(st + L::VS, &maps.v, full, v0, hv, tok);
       }
       __syncwarp();
-    };
-    int issued = 0, landed = 0;
-    for (; issued < 2 && issued < nch; ++issued) load(issued);
+    }
+    // what was issued lands before the CTA gives up its memory (the last two may not have
+    // been waited for by anybody if the chain failed)
+    for (int m = n < 2 ? 0 : n - 2; m < n; ++m) mbar_wait(&bars[FULL0 + (m & 1)], (m >> 1) & 1, kDrainNs);
+  } else if (warp == 8) {
+    // ------------------------------------------------------------- products ---
+    const uint32_t sb = smem_u32(sm);
     constexpr uint32_t id2n = idesc_f16kind(128, 2 * N) | IDESC_B_MN_MAJOR;   // both parts of B
     constexpr uint32_t idn = idesc_f16kind(128, N == 32 ? 2 * N : N) | IDESC_B_MN_MAJOR;  // the high part (N = 32: both)
     const uint64_t ds = sdesc(sb + L::S, L::LBO_S, 1024, 2), dy = sdesc(sb + L::Y, L::LBO_Y, 1024, 2);
@@ -382,53 +499,37 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2);
       const uint64_t dt = MODE == REVERSE ? sdesc(st + L::REC, kTileBytes, 1024, 2) : sdesc_sw128(st + L::REC);
       if (!wait(FULL0 + (n & 1), (n >> 1) & 1)) break;
-      landed = n + 1;
       if (!wait(SREADY, ph)) break;
       tc_fence_after();
 #pragma unroll
-      for (int s = 0; s < K / 16; ++s)
-        umma_f16_warp(tmem, dkq + (((s >> 2) * kTileBytes + (s & 3) * 32) >> 4), ds + (s * 2048 >> 4), id2n, s > 0);
+      for (int b = 0; b < K / 64; ++b)
+        umma4<32, 2048>(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0);
       umma_commit_warp(&bars[D1]);
-      // everything that read the other stage is done (SREADY): the next chunk into it
-      if (n > 0 && issued < nch) {
-        load(issued);
-        ++issued;
-      }
+      if (n > 0 && lane == 0) mbar_arrive(&bars[EMPTY0 + ((n - 1) & 1)]);
+      __syncwarp();
       if (MODE == REVERSE) {
         if (!wait(QREADY, ph)) break;
         tc_fence_after();
         const uint64_t dd = sdesc(st + L::VS, 8192, 1024, 2);
         constexpr uint32_t idr = idesc_f16kind(128, N) | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)  // R^T do, the two parts of R (rows 64-127 of the record's tiles)
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            umma_f16_warp(tmem + TD2R, dt + ((h * kTileBytes + 8192 + s * 2048) >> 4), dd + (s * 2048 >> 4), idr,
-                          h + s > 0);
-#pragma unroll
-        for (int s = 4; s < 8; ++s)  // q^T (scale G do)
-          umma_f16_warp(tmem + TD3, dkt + (s * 2048 >> 4), dy + (s * 2048 >> 4), id2n | IDESC_A_MN_MAJOR, s > 4);
+        // R^T do, the two parts of R (rows 64-127 of the record's tiles); q^T (scale G do)
+        umma4<2048, 2048>(tmem + TD2R, dt + (8192 >> 4), dd, idr, 0u);
+        umma4<2048, 2048>(tmem + TD2R, dt + ((kTileBytes + 8192) >> 4), dd, idr, 1u);
+        umma4<2048, 2048>(tmem + TD3, dkt + (8192 >> 4), dy + (8192 >> 4), id2n | IDESC_A_MN_MAJOR, 0u);
       }
       if (!wait(YREADY, ph)) break;
       tc_fence_after();
       constexpr uint32_t am = MODE == REVERSE ? IDESC_A_MN_MAJOR : 0u;
       constexpr uint32_t as = MODE == REVERSE ? 2048 : 32;   // bytes of 16 of K in [T; R]
-#pragma unroll
-      for (int s = 0; s < 4; ++s) umma_f16_warp(tmem + TD2, dt + (s * as >> 4), dy + (s * 2048 >> 4), id2n | am, s > 0);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        umma_f16_warp(tmem + TD2, dt + ((kTileBytes + s * as) >> 4), dy + (s * 2048 >> 4), idn | am, 1u);
+      umma4<as, 2048>(tmem + TD2, dt, dy, id2n | am, 0u);
+      umma4<as, 2048>(tmem + TD2, dt + (kTileBytes >> 4), dy, idn | am, 1u);
       umma_commit_warp(&bars[D2]);
       if (!wait(VREADY, ph)) break;
       tc_fence_after();
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        umma_f16_warp(tmem + TD3, dkt + (s * 2048 >> 4), dy + (s * 2048 >> 4), id2n | IDESC_A_MN_MAJOR,
-                      MODE == REVERSE || s > 0);
+      umma4<2048, 2048>(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, MODE == REVERSE);
       umma_commit_warp(&bars[D3]);
     }
     // what is in flight ends before the CTA gives up its memory
-    for (int n = landed; n < issued; ++n) mbar_wait(&bars[FULL0 + (n & 1)], (n >> 1) & 1, kDrainNs);
     umma_commit_warp(&bars[DRAIN]);
     mbar_wait(&bars[DRAIN], 0, kDrainNs);
   } else {
@@ -441,16 +542,12 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     const int i = r & 63;
     const float* first = MODE == REVERSE ? a.dfin : p.s0;
     float* final = MODE == FORWARD ? p.sfin : MODE == REVERSE ? a.ds0 : nullptr;
-    float s[CPT];
-    if (first && r < K) {
+    uint64_t s[H2];
 #pragma unroll
-      for (int j = 0; j < CPT / 4; ++j) {
-        const float4 t = *reinterpret_cast<const float4*>(first + soff + 4 * j);
-        s[4 * j] = t.x; s[4 * j + 1] = t.y; s[4 * j + 2] = t.z; s[4 * j + 3] = t.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < CPT; ++j) s[j] = 0.f;
+    for (int j = 0; j < H2 / 2; ++j) {
+      const float4 t = first && r < K ? *reinterpret_cast<const float4*>(first + soff + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      s[2 * j] = pack2f(t.x, t.y);
+      s[2 * j + 1] = pack2f(t.z, t.w);
     }
     put_parts<N, CPT>(sm + L::S, L::LBO_S, r, c0, s);
     fence_proxy_async_smem();
@@ -462,15 +559,16 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       const float* fac = reinterpret_cast<const float*>(st + L::REC + kRecFactors);
       const int c = chunk(n);
       const size_t tok = static_cast<size_t>(tok0 + C * static_cast<long>(c) + i);
-      const bool live = C * c + i < len;
+      const bool live = C * c + i < len, whole = C * c + C <= len;  // this row; every row of the chunk
       if (MODE != FORWARD && r < K) {
         float* img = (MODE == SAVE ? a.states : a.dstates) +
                      ((static_cast<size_t>(slot0 + c) * p.HV + hv) * K + r) * V + v0 + c0;
 #pragma unroll
-        for (int j = 0; j < CPT / 8; ++j) st_global_v8(img + 8 * j, s + 8 * j);
+        for (int j = 0; j < CPT / 8; ++j) st_global_v8(img + 8 * j, s + 4 * j);
       }
       if (!(good = wait(FULL0 + (n & 1), (n >> 1) & 1))) break;
-      const float row = fac[i], gamma = fac[192];
+      const float row = fac[i];
+      const uint64_t gamma = pack2f(fac[192], fac[192]);
       const size_t orow = (tok * p.HV + hv) * V + v0 + c0;
       // rows past the sequence's end hold the next one's tokens, whatever they are: every
       // operand that meets them in a sum over tokens has them zeroed first
@@ -481,32 +579,34 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
           for (int ch = 0; ch < 8; ++ch)
             *reinterpret_cast<uint4*>(tile + b * kTileBytes + sw128(i, ch)) = make_uint4(0, 0, 0, 0);
       };
-      float x[CPT], y[CPT];
-      auto load_v = [&](float (&o)[CPT]) {
+      uint64_t x[H2], y[H2], o[MODE == FORWARD ? H2 : 1];
+      auto load_v = [&](uint64_t (&out)[H2], float f) {  // f times this thread's values of v (do)
+        const uint64_t ff = pack2f(f, f);
 #pragma unroll
         for (int j = 0; j < CPT / 8; ++j) {
           const uint32_t ch = (c0 >> 3) + j;
           const uint4 u = *reinterpret_cast<const uint4*>(st + L::VS + (N == 32 ? sw64(i, ch) : sw128(i, ch)));
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[8 * j + 2 * e] = __uint_as_float(w[e] << 16);
-            o[8 * j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-          }
+          for (int e = 0; e < 4; ++e)
+            out[4 * j + e] = mul2(ff, pack2f(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
         }
       };
       if (isk) {
         const float be = fac[128 + i], tail = fac[64 + i];
-        if (MODE != REVERSE) load_v(y);
+        if (MODE != REVERSE) load_v(y, be);
+        const float f1 = MODE == REVERSE ? tail : -be * row, f2 = MODE == REVERSE ? -row * be : tail;
+        const uint64_t ff1 = pack2f(f1, f1), ff2 = pack2f(f2, f2);
         if (!(good = wait(D1, ph))) break;
         tc_fence_after();
         tmem_ld_parts<N, CPT>(tl, x);
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-          const float t = MODE == REVERSE ? tail * x[j] : be * (y[j] - row * x[j]);
-          x[j] = live ? t : 0.f;
+        for (int j = 0; j < H2; ++j) x[j] = MODE == REVERSE ? mul2(ff1, x[j]) : fma2(ff1, x[j], y[j]);
+        if (!whole && !live) {
+#pragma unroll
+          for (int j = 0; j < H2; ++j) x[j] = 0;
+          if (warp < 4) clear_row(st);
         }
-        if (!live && warp < 4) clear_row(st);
         put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, x);
         fence_proxy_async_smem();
         tc_fence_before();
@@ -515,16 +615,16 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         tc_fence_after();
         tmem_ld_parts<N, CPT>(tl + TD2, x);
         if (MODE == REVERSE) {
-          tmem_ld<CPT>(tl + TD2R, y);
+          float t[CPT];
+          tmem_ld<CPT>(tl + TD2R, t);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < CPT; ++j) x[j] += y[j];
+          for (int j = 0; j < H2; ++j) x[j] = add2(x[j], pack2f(t[2 * j], t[2 * j + 1]));
         }
-        const float f = MODE == REVERSE ? -row * be : tail;
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-          x[j] = live ? x[j] : 0.f;
-          y[j] = f * x[j];
+        for (int j = 0; j < H2; ++j) {
+          if (MODE == REVERSE && !live) x[j] = 0;   // (vn is zero there by itself: row i of T is e_i)
+          y[j] = mul2(ff2, x[j]);
         }
         put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, y);
         fence_proxy_async_smem();
@@ -536,29 +636,26 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
           put_image<CPT>(img, img + 2 * C * static_cast<size_t>(V), i, c0, x);
         }
         if (MODE == REVERSE && live) {
+          const uint64_t bb = pack2f(be, be);
 #pragma unroll
-          for (int j = 0; j < CPT; ++j) y[j] = be * x[j];
+          for (int j = 0; j < H2; ++j) y[j] = mul2(bb, x[j]);
           put_bf16<CPT>(a.dv, orow, y);
         }
       } else if (MODE == FORWARD) {
+        const uint64_t f = pack2f(p.scale * row, p.scale * row);
         if (!(good = wait(D1, ph))) break;
         tc_fence_after();
         tmem_ld_parts<N, CPT>(tl, x);
-        const float f = p.scale * row;
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) x[j] *= f;
         if (!(good = wait(D2, ph))) break;
         tc_fence_after();
         tmem_ld_parts<N, CPT>(tl + TD2, y);
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) x[j] += y[j];
-        if (live) put_bf16<CPT>(p.out, orow, x);
+        for (int j = 0; j < H2; ++j) o[j] = fma2(f, x[j], y[j]);
       } else if (MODE == REVERSE) {
-        load_v(x);
-        const float f = p.scale * row;
+        load_v(x, p.scale * row);
+        if (!whole && !live) {
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) x[j] = live ? f * x[j] : 0.f;
-        if (!live) {
+          for (int j = 0; j < H2; ++j) x[j] = 0;
           if (warp < 4) clear_row(st + 8192);
 #pragma unroll
           for (int j = 0; j < CPT / 8; ++j)
@@ -572,16 +669,24 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       tc_fence_after();
       tmem_ld_parts<N, CPT>(tl + TD3, x);
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) s[j] = fmaf(gamma, s[j], x[j]);
+      for (int j = 0; j < H2; ++j) s[j] = fma2(gamma, s[j], x[j]);
       put_parts<N, CPT>(sm + L::S, L::LBO_S, r, c0, s);
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(SREADY);
+      // the output only now: its stores, a row a thread, would hold up the other warps'
+      // shared-memory stores on the way to step 3 (250 of 3340 cycles a chunk)
+      if constexpr (MODE == FORWARD)
+        if (!isk && live) put_bf16<CPT>(p.out, orow, o);
     }
     if (good && final && r < K) {
 #pragma unroll
-      for (int j = 0; j < CPT / 4; ++j)
-        *reinterpret_cast<float4*>(final + soff + 4 * j) = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+      for (int j = 0; j < H2 / 2; ++j) {
+        float4 t;
+        unpack2f(s[2 * j], t.x, t.y);
+        unpack2f(s[2 * j + 1], t.z, t.w);
+        *reinterpret_cast<float4*>(final + soff + 4 * j) = t;
+      }
     }
   }
   tc_fence_before();

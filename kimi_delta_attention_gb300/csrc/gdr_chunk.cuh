@@ -96,18 +96,51 @@ __device__ __forceinline__ bool find_chunk(const ChunkParams& a, int slot, int& 
   return true;
 }
 
+// Two fp32 values in one 64-bit register, and the arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2f(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Two fp32 values as packed bf16 high parts and low parts.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - __low2float(h), x1 - __high2float(h));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2f(x, a, b);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+  const uint64_t h = pack2f(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u));
+  unpack2f(fma2(h, pack2f(-1.f, -1.f), x), a, b);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
+}
+__device__ __forceinline__ void split8(const uint64_t* x, uint4& hi, uint4& lo) {
+  split2(x[0], hi.x, lo.x);
+  split2(x[1], hi.y, lo.y);
+  split2(x[2], hi.z, lo.z);
+  split2(x[3], hi.w, lo.w);
 }
 __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
-  split2(x[0], x[1], hi.x, lo.x);
-  split2(x[2], x[3], hi.y, lo.y);
-  split2(x[4], x[5], hi.z, lo.z);
-  split2(x[6], x[7], hi.w, lo.w);
+  split2(pack2f(x[0], x[1]), hi.x, lo.x);
+  split2(pack2f(x[2], x[3]), hi.y, lo.y);
+  split2(pack2f(x[4], x[5]), hi.z, lo.z);
+  split2(pack2f(x[6], x[7]), hi.w, lo.w);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -123,33 +156,60 @@ __device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t c) {
   return (r >> 3) * 512u + (r & 7) * 64u + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+// Four chained products D (+)= A B of a converged warp behind one elect (16 of K each; AS and
+// BS bytes from one to the next): the first accumulates if `acc`, the others always.
+template <uint32_t AS, uint32_t BS>
+__device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u64 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
+      "add.u64 a2, a1, %5;\n\tadd.u64 b2, b1, %6;\n\t"
+      "add.u64 a3, a2, %5;\n\tadd.u64 b3, b2, %6;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS >> 4), "n"(BS >> 4)
+      : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// gc of a chunk's rows 2 lane, 2 lane + 1 (one warp), in log2 units, as a float and what
-// the float misses of the double sum: decays between neighbours stay exact after a steep
-// drop.  g below -120 already is e^g = 0.  Rows past the end have g = 0.
+// A sum kept as a float and what the float misses (the pair is good to about 2^-46).
+__device__ __forceinline__ void add_pairs(float& h, float& l, float h2, float l2) {
+  const float s = h + h2, b = s - h, e = ((h - (s - b)) + (h2 - b)) + (l + l2);
+  h = s + e;
+  l = e - (h - s);
+}
+// gc of a chunk's rows 2 lane, 2 lane + 1 (one warp), in log2 units, as such pairs: decays
+// between neighbours stay exact after a steep drop.  g below -120 already is e^g = 0.  Rows
+// past the end have g = 0.
 __device__ __forceinline__ void gate_scan(const Params& p, long tok, int rows, int hv, int lane, float (&hi)[2],
                                           float (&lo)[2]) {
   const int i0 = 2 * lane;
   float g0 = i0 < rows ? p.g[(tok + i0) * p.HV + hv] : 0.f, g1 = i0 + 1 < rows ? p.g[(tok + i0 + 1) * p.HV + hv] : 0.f;
   g0 = g0 < -120.f ? -120.f : g0;
   g1 = g1 < -120.f ? -120.f : g1;
-  const double d0 = 1.4426950408889634 * g0, d1 = 1.4426950408889634 * g1;
-  double run = d0 + d1;
+  constexpr float kL = 1.44269502f, kLlow = 1.92596299e-8f;  // log2 e and its rest
+  const float h0 = g0 * kL, l0 = fmaf(g0, kL, -h0) + g0 * kLlow, h1 = g1 * kL, l1 = fmaf(g1, kL, -h1) + g1 * kLlow;
+  float h = h0, l = l0;
+  add_pairs(h, l, h1, l1);                    // the lane's two rows
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const double up = __shfl_up_sync(0xFFFFFFFFu, run, s);
-    if (lane >= s) run += up;
+    const float uh = __shfl_up_sync(0xFFFFFFFFu, h, s), ul = __shfl_up_sync(0xFFFFFFFFu, l, s);
+    if (lane >= s) add_pairs(h, l, uh, ul);
   }
-  const double r0 = run - d1;
-  hi[0] = static_cast<float>(r0);
-  hi[1] = static_cast<float>(run);
-  lo[0] = static_cast<float>(r0 - static_cast<double>(hi[0]));
-  lo[1] = static_cast<float>(run - static_cast<double>(hi[1]));
+  hi[1] = h;
+  lo[1] = l;
+  add_pairs(h, l, -h1, -l1);
+  hi[0] = h;
+  lo[0] = l;
 }
 
 }  // namespace gdr
