@@ -297,10 +297,11 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ chain ---
-// One CTA per (sequence, value head, N value columns): the columns of S never meet.  Warps
-// 0-7 hold the state in fp32 registers (warp w: key dims 32 (w % 4) + lane, half w / 4 of
-// the columns) and do everything between the products, warp 8 issues the products, warp 9
-// loads the chunks two ahead (TMA tiles of k, q and v, the record by bulk copy).  Per chunk:
+// One CTA per (sequence, value head, N value columns): the columns of S never meet.  N / 4
+// warps hold the state in fp32 registers (warp w: key dims 32 (w % 4) + lane, columns
+// 16 (w / 4) ..) and do everything between the products; of three more one issues the
+// products, one loads the chunks two ahead (TMA tiles of k, q and v, the record by bulk
+// copy), one stores results from their staging.  Per chunk:
 //   1. D1 = [k; q] S      M = 128, K = key dims       lanes 0-63: k S, 64-127: q S
 //   2. D2 = [T; R] Y      M = 128, K = 64             lanes 0-63: vn,  64-127: R Y
 //   3. D3 = k^T (E vn)    M = 128 key dims, K = 64    S = gamma S + D3 in registers
@@ -322,23 +323,36 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
 // with the transposed operands read from the same tiles (MN-major), so M is 128 where only
 // 64 lanes are wanted: the other lanes' atom is some other tile and nobody reads them.
 namespace chain {
-constexpr int NT = 320;
+constexpr int groups(int N) { return N / 16; }           // of 16 columns: a quadrant's warps each take one
+constexpr int warps(int N) { return 4 * groups(N); }     // that hold the state; then products, loads, stores
+constexpr int threads(int N) { return 32 * (warps(N) + 3); }
 enum Mode { FORWARD, SAVE, REVERSE };
 template <int K, int N, Mode MODE>
 struct Lay {
+  static constexpr bool BWD = MODE != FORWARD;
   static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : C;    // REVERSE: rows 64-127 hold scale G do
-  // a stage: [k; q] tiles at 0, then
-  static constexpr uint32_t REC = (K / 64) * kTileBytes;          // the record
-  static constexpr uint32_t VS = REC + kRecBytes;                 // v (or do): 64 rows x N
-  static constexpr uint32_t STAGE = VS + C * N * 2;
-  static constexpr uint32_t S = 2 * STAGE;                        // S parts: K-rows of 2 N columns
+  // a stage: [k; q] tiles at 0, then the record's row factors, v (or do), 64 rows x N; and
+  // FORWARD [T; R] (the others keep one buffer of it: it is free from step 2 to the next)
+  static constexpr uint32_t FAC = (K / 64) * kTileBytes;
+  static constexpr uint32_t VS = FAC + 1024;
+  static constexpr uint32_t TT = VS + C * N * 2;
+  static constexpr uint32_t STAGE = BWD ? TT : TT + 2 * kTileBytes;
+  static constexpr uint32_t TT1 = 2 * STAGE;
+  static constexpr uint32_t S = TT1 + (BWD ? 2 * kTileBytes : 0); // S parts: K-rows of 2 N columns
   static constexpr uint32_t Y = S + 128 * 2 * N * 2;              // Y, then E vn
-  static constexpr uint32_t BAR = Y + YROWS * 2 * N * 2;
-  static constexpr uint32_t SMEM = BAR + 128 + 1024;
+  // on the way to memory: o (64 rows x N bf16), or vn (z) in two parts and S in fp32
+  static constexpr uint32_t OUT = Y + YROWS * 2 * N * 2;
+  static constexpr uint32_t SF = OUT + (BWD ? 2 * C * 128 : C * N * 2);
+  static constexpr uint32_t BAR = SF + (BWD ? K * 256 : 0);
+  static constexpr uint32_t SLACK = 832;                          // for the base's alignment
+  static constexpr uint32_t SMEM = BAR + 192 + SLACK;
   static constexpr uint32_t LBO_S = 128 * 128, LBO_Y = YROWS * 128;   // between 64-column atoms
-  static constexpr uint32_t TX = MODE == SAVE ? (K / 64) * 8192 + 2 * 8192 + 1024 + C * N * 2 : STAGE;
+  static constexpr uint32_t TX = (MODE == SAVE ? (K / 64) * 8192 : (K / 64) * kTileBytes) + 1024 + C * N * 2 +
+                                 (BWD ? 0 : 2 * kTileBytes);
+  static_assert(SMEM <= 232448, "shared memory");
 };
-enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, D1, D2, D3, SREADY, YREADY, VREADY, QREADY, DRAIN, NBAR };
+enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, TFULL, TFREE, D1, D2, D3, SREADY, YREADY, VREADY, QREADY, SFREADY, OUTREADY, OUTFREE,
+       DRAIN, NBAR };
 }  // namespace chain
 
 // CPT values of a row (in pairs) as the two parts of a 2 N-column operand (c0: first column).
@@ -357,21 +371,21 @@ __device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, 
     }
   }
 }
-// The same as the two parts of a 64-row operand image in memory.
-template <int CPT>
-__device__ __forceinline__ void put_image(uint8_t* hi, uint8_t* lo, int row, int c0, const uint64_t (&x)[CPT / 2]) {
-#pragma unroll
-  for (int j = 0; j < CPT / 8; ++j) {
-    uint4 h, l;
-    split8(x + 4 * j, h, l);
-    *reinterpret_cast<uint4*>(hi + sw128(row, (c0 >> 3) + j)) = h;
-    *reinterpret_cast<uint4*>(lo + sw128(row, (c0 >> 3) + j)) = l;
-  }
-}
 __device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
   float a, b;
   unpack2f(x, a, b);
   return pack_bf16(a, b);
+}
+// CPT values of a row as bf16: to the staging tile (its TMA store takes whole chunks), or
+// straight to memory.
+template <int N, int CPT>
+__device__ __forceinline__ void put_tile(uint8_t* tile, int row, int c0, const uint64_t (&x)[CPT / 2]) {
+#pragma unroll
+  for (int j = 0; j < CPT / 8; ++j) {
+    const uint32_t ch = (c0 >> 3) + j;
+    *reinterpret_cast<uint4*>(tile + (N == 32 ? sw64(row, ch) : sw128(row, ch))) =
+        make_uint4(pack_pair(x[4 * j]), pack_pair(x[4 * j + 1]), pack_pair(x[4 * j + 2]), pack_pair(x[4 * j + 3]));
+  }
 }
 template <int CPT>
 __device__ __forceinline__ void put_bf16(void* out, size_t at, const uint64_t (&x)[CPT / 2]) {
@@ -380,15 +394,6 @@ __device__ __forceinline__ void put_bf16(void* out, size_t at, const uint64_t (&
   for (int j = 0; j < CPT / 8; ++j)
     *reinterpret_cast<uint4*>(op + 8 * j) =
         make_uint4(pack_pair(x[4 * j]), pack_pair(x[4 * j + 1]), pack_pair(x[4 * j + 2]), pack_pair(x[4 * j + 3]));
-}
-// (32-byte aligned: the workspace only)
-__device__ __forceinline__ void st_global_v8(float* p, const uint64_t* x) {
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) unpack2f(x[j], f[2 * j], f[2 * j + 1]);
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
-               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-               : "memory");
 }
 template <int CPT>
 __device__ __forceinline__ void tmem_ld(uint32_t t, float (&x)[CPT]) {
@@ -410,8 +415,13 @@ template <int K, int N, chain::Mode MODE>
 __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkParams& a, int V, int block, uint8_t* raw) {
   using L = chain::Lay<K, N, MODE>;
   using namespace chain;
-  constexpr int CPT = N / 2, H2 = CPT / 2;
-  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  constexpr int CPT = 16, H2 = CPT / 2, NW = warps(N);
+  const uint32_t shift = (1024u - (smem_u32(raw) & 1023u)) & 1023u;  // 0: nothing lies before the dynamic part
+  uint8_t* sm = raw + shift;
+  if (shift > L::SLACK) {
+    if (threadIdx.x == 0) atomicOr(a.p.status, kStatusTimeout);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
   volatile uint32_t* failed = tslot + 1;
@@ -427,13 +437,13 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   const auto chunk = [&](int n) { return MODE == REVERSE ? nch - 1 - n : n; };  // of step n
   if (tid == 0) {
     for (int b = 0; b < NBAR; ++b)
-      mbar_init(&bars[b], b == SREADY ? 8 : (b == YREADY || b == VREADY || b == QREADY) ? 4 : 1);
+      mbar_init(&bars[b], b == SREADY || b == SFREADY ? NW : b == YREADY || b == VREADY || b == QREADY || b == OUTREADY ? NW / 2 : 1);
     *failed = 0u;
     fence_mbar_init();
   }
   constexpr uint32_t TCOLS = N == 32 ? 256 : 512;
   constexpr uint32_t TD2 = 2 * N, TD3 = 4 * N, TD2R = 6 * N;
-  if (warp == 8) {
+  if (warp == NW) {
     tmem_alloc(tslot, TCOLS);
     tmem_relinquish();
   }
@@ -443,9 +453,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   const uint32_t tmem = *tslot;
   // waits of a whole warp; false once the CTA has failed
   auto wait = [&](int b, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[b], parity))) return true;
-    const bool ok = *failed == 0u && mbar_wait(&bars[b], parity, a.wait_ns);
-    if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
     if (lane == 0 && *failed == 0u) {
       atomicOr(p.status, kStatusTimeout);
       *failed = 1u;
@@ -457,81 +465,144 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     if (lane == 0) mbar_arrive(&bars[b]);
   };
 
-  if (warp == 9) {
+  if (warp == NW + 1) {
     // ---------------------------------------------------------------- loads ---
-    int n = 0;
-    for (; n < nch; ++n) {
-      // a stage's readers are done once the next chunk's products may start (EMPTY)
-      if (n >= 2 && !wait(EMPTY0 + (n & 1), ((n >> 1) - 1) & 1)) break;
+    auto record = [&](int n) { return a.rec + (static_cast<size_t>(slot0 + chunk(n)) * p.HV + hv) * kRecBytes; };
+    auto load = [&](int n) {
       if (lane == 0) {
         uint8_t* st = sm + (n & 1) * L::STAGE;
         uint64_t* full = &bars[FULL0 + (n & 1)];
         const int tok = static_cast<int>(tok0 + C * static_cast<long>(chunk(n)));
-        const uint8_t* rec = a.rec + (static_cast<size_t>(slot0 + chunk(n)) * p.HV + hv) * kRecBytes;
         mbar_arrive_expect_tx_relaxed(full, L::TX);
 #pragma unroll
         for (int b = 0; b < K / 64; ++b) {
           tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
           if (MODE != SAVE) tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
         }
-        if (MODE == SAVE) {
-          bulk_load(st + L::REC, rec, 8192, full);
-          bulk_load(st + L::REC + kTileBytes, rec + kTileBytes, 8192, full);
-          bulk_load(st + L::REC + kRecFactors, rec + kRecFactors, 1024, full);
-        } else {
-          bulk_load(st + L::REC, rec, kRecBytes, full);
-        }
+        bulk_load(st + L::FAC, record(n) + kRecFactors, 1024, full);
+        if (MODE == FORWARD) bulk_load(st + L::TT, record(n), 2 * kTileBytes, full);
         tma_load_3d(st + L::VS, &maps.v, full, v0, hv, tok);
       }
       __syncwarp();
+    };
+    auto load_t = [&](int n) {  // the one buffer of [T; R]: T alone for SAVE
+      if (lane == 0) {
+        mbar_arrive_expect_tx_relaxed(&bars[TFULL], MODE == SAVE ? 16384 : 2 * kTileBytes);
+        bulk_load(sm + L::TT1, record(n), MODE == SAVE ? 8192 : 2 * kTileBytes, &bars[TFULL]);
+        if (MODE == SAVE) bulk_load(sm + L::TT1 + kTileBytes, record(n) + kTileBytes, 8192, &bars[TFULL]);
+      }
+      __syncwarp();
+    };
+    int nf = 0, nt = 0;   // loads issued
+    for (; nf < 2 && nf < nch; ++nf) load(nf);
+    if (MODE != FORWARD && nch > 0) load_t(nt++);
+    for (int n = 1; n < nch; ++n) {
+      if (MODE != FORWARD) {                       // free once step 2 of the chunk before is done
+        if (!wait(TFREE, (n - 1) & 1)) break;
+        load_t(nt++);
+      }
+      if (nf < nch) {                              // a stage's readers are done once the next chunk's products start
+        if (!wait(EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        load(nf++);
+      }
     }
-    // what was issued lands before the CTA gives up its memory (the last two may not have
-    // been waited for by anybody if the chain failed)
-    for (int m = n < 2 ? 0 : n - 2; m < n; ++m) mbar_wait(&bars[FULL0 + (m & 1)], (m >> 1) & 1, kDrainNs);
-  } else if (warp == 8) {
+    // what was issued lands before the CTA gives up its memory (the last may not have been
+    // waited for by anybody if the chain failed)
+    for (int m = nf < 2 ? 0 : nf - 2; m < nf; ++m) mbar_wait(&bars[FULL0 + (m & 1)], (m >> 1) & 1, kDrainNs);
+    if (nt > 0) mbar_wait(&bars[TFULL], (nt - 1) & 1, kDrainNs);
+  } else if (warp == NW) {
     // ------------------------------------------------------------- products ---
     const uint32_t sb = smem_u32(sm);
     constexpr uint32_t id2n = idesc_f16kind(128, 2 * N) | IDESC_B_MN_MAJOR;   // both parts of B
     constexpr uint32_t idn = idesc_f16kind(128, N == 32 ? 2 * N : N) | IDESC_B_MN_MAJOR;  // the high part (N = 32: both)
     const uint64_t ds = sdesc(sb + L::S, L::LBO_S, 1024, 2), dy = sdesc(sb + L::Y, L::LBO_Y, 1024, 2);
+    // four products, 16 of K each, AS and BS bytes apart.  Only FORWARD writes them out: the
+    // backward's code then no longer fits the instruction cache beside the other warps' (its
+    // warps waited for instructions 3.5 cycles of every 9 that they did not wait for data)
+    auto issue = [&](uint32_t d, uint64_t aa, uint64_t bb, uint32_t idesc, uint32_t acc, uint32_t as) {
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s, aa += as >> 4, bb += 2048 >> 4, acc = 1u) umma_f16_warp(d, aa, bb, idesc, acc);
+    };
     for (int n = 0; n < nch; ++n) {
-      const uint32_t ph = n & 1, st = sb + ph * L::STAGE;
+      const uint32_t ph = n & 1, st = sb + ph * L::STAGE, tt = MODE == FORWARD ? st + L::TT : sb + L::TT1;
       const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2);
-      const uint64_t dt = MODE == REVERSE ? sdesc(st + L::REC, kTileBytes, 1024, 2) : sdesc_sw128(st + L::REC);
+      const uint64_t dt = MODE == REVERSE ? sdesc(tt, kTileBytes, 1024, 2) : sdesc_sw128(tt);
       if (!wait(FULL0 + (n & 1), (n >> 1) & 1)) break;
       if (!wait(SREADY, ph)) break;
       tc_fence_after();
+      if (MODE == FORWARD) {
 #pragma unroll
-      for (int b = 0; b < K / 64; ++b)
-        umma4<32, 2048>(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0);
+        for (int b = 0; b < K / 64; ++b)
+          umma4<32, 2048>(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0);
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < K / 64; ++b) issue(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0, 32);
+      }
       umma_commit_warp(&bars[D1]);
       if (n > 0 && lane == 0) mbar_arrive(&bars[EMPTY0 + ((n - 1) & 1)]);
       __syncwarp();
+      if (MODE != FORWARD && !wait(TFULL, ph)) break;
       if (MODE == REVERSE) {
         if (!wait(QREADY, ph)) break;
         tc_fence_after();
         const uint64_t dd = sdesc(st + L::VS, 8192, 1024, 2);
         constexpr uint32_t idr = idesc_f16kind(128, N) | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;
         // R^T do, the two parts of R (rows 64-127 of the record's tiles); q^T (scale G do)
-        umma4<2048, 2048>(tmem + TD2R, dt + (8192 >> 4), dd, idr, 0u);
-        umma4<2048, 2048>(tmem + TD2R, dt + ((kTileBytes + 8192) >> 4), dd, idr, 1u);
-        umma4<2048, 2048>(tmem + TD3, dkt + (8192 >> 4), dy + (8192 >> 4), id2n | IDESC_A_MN_MAJOR, 0u);
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) issue(tmem + TD2R, dt + ((8192 + h * kTileBytes) >> 4), dd, idr, h, 2048);
+        issue(tmem + TD3, dkt + (8192 >> 4), dy + (8192 >> 4), id2n | IDESC_A_MN_MAJOR, 0u, 2048);
       }
       if (!wait(YREADY, ph)) break;
       tc_fence_after();
       constexpr uint32_t am = MODE == REVERSE ? IDESC_A_MN_MAJOR : 0u;
       constexpr uint32_t as = MODE == REVERSE ? 2048 : 32;   // bytes of 16 of K in [T; R]
-      umma4<as, 2048>(tmem + TD2, dt, dy, id2n | am, 0u);
-      umma4<as, 2048>(tmem + TD2, dt + (kTileBytes >> 4), dy, idn | am, 1u);
+      if (MODE == FORWARD) {
+        umma4<as, 2048>(tmem + TD2, dt, dy, id2n | am, 0u);
+        umma4<as, 2048>(tmem + TD2, dt + (kTileBytes >> 4), dy, idn | am, 1u);
+      } else {
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) issue(tmem + TD2, dt + (h * kTileBytes >> 4), dy, (h ? idn : id2n) | am, h, as);
+      }
       umma_commit_warp(&bars[D2]);
+      if (MODE != FORWARD) umma_commit_warp(&bars[TFREE]);
       if (!wait(VREADY, ph)) break;
       tc_fence_after();
-      umma4<2048, 2048>(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, MODE == REVERSE);
+      if (MODE == FORWARD) umma4<2048, 2048>(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, 0u);
+      else issue(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, MODE == REVERSE, 2048);
       umma_commit_warp(&bars[D3]);
     }
     // what is in flight ends before the CTA gives up its memory
     umma_commit_warp(&bars[DRAIN]);
     mbar_wait(&bars[DRAIN], 0, kDrainNs);
+  } else if (warp == NW + 2) {
+    // --------------------------------------------------------------- stores ---
+    for (int n = 0; n < nch; ++n) {
+      const int c = chunk(n);
+      const size_t cu = static_cast<size_t>(slot0 + c) * p.HV + hv;
+      if (MODE != FORWARD) {
+        if (!wait(SFREADY, n & 1)) break;
+        if (lane == 0) {
+          bulk_store((MODE == SAVE ? a.states : a.dstates) + cu * K * V + (v0 >> 6) * (K * 64), sm + L::SF, K * 256);
+          bulk_commit();
+        }
+        __syncwarp();
+      }
+      if (!wait(OUTREADY, n & 1)) break;
+      if (lane == 0) {
+        if (MODE != FORWARD) {
+          uint8_t* img = (MODE == SAVE ? a.vn : a.z) + cu * (4 * C * static_cast<size_t>(V)) + (v0 >> 6) * 8192;
+          bulk_store(img, sm + L::OUT, 8192);
+          bulk_store(img + 2 * C * static_cast<size_t>(V), sm + L::OUT + 8192, 8192);
+        } else if (C * c + C <= len) {
+          tma_store_3d(&maps.o, sm + L::OUT, v0, hv, static_cast<int>(tok0 + C * static_cast<long>(c)));
+        }
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&bars[OUTFREE]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_read();
   } else {
     // ------------------------------------------ state, Y, vn (z), output ---
     const int quad = warp & 3, c0 = (warp >> 2) * CPT;
@@ -556,16 +627,10 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     for (int n = 0; n < nch; ++n) {
       const uint32_t ph = n & 1;
       uint8_t* st = sm + ph * L::STAGE;
-      const float* fac = reinterpret_cast<const float*>(st + L::REC + kRecFactors);
+      const float* fac = reinterpret_cast<const float*>(st + L::FAC);
       const int c = chunk(n);
       const size_t tok = static_cast<size_t>(tok0 + C * static_cast<long>(c) + i);
       const bool live = C * c + i < len, whole = C * c + C <= len;  // this row; every row of the chunk
-      if (MODE != FORWARD && r < K) {
-        float* img = (MODE == SAVE ? a.states : a.dstates) +
-                     ((static_cast<size_t>(slot0 + c) * p.HV + hv) * K + r) * V + v0 + c0;
-#pragma unroll
-        for (int j = 0; j < CPT / 8; ++j) st_global_v8(img + 8 * j, s + 4 * j);
-      }
       if (!(good = wait(FULL0 + (n & 1), (n >> 1) & 1))) break;
       const float row = fac[i];
       const uint64_t gamma = pack2f(fac[192], fac[192]);
@@ -573,13 +638,26 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       // rows past the sequence's end hold the next one's tokens, whatever they are: every
       // operand that meets them in a sum over tokens has them zeroed first
       auto clear_row = [&](uint8_t* tile) {
-#pragma unroll
-        for (int b = 0; b < K / 64; ++b)
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4*>(tile + b * kTileBytes + sw128(i, ch)) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int ch = 0; ch < 8 * (K / 64); ++ch)
+          *reinterpret_cast<uint4*>(tile + (ch >> 3) * kTileBytes + sw128(i, ch & 7)) = make_uint4(0, 0, 0, 0);
       };
-      uint64_t x[H2], y[H2], o[MODE == FORWARD ? H2 : 1];
+      auto put_state = [&]() {  // S (dS') in fp32 to its staging; rows of 16 chunks, swizzled
+        if (n > 0 && !wait(OUTFREE, (n - 1) & 1)) return false;
+        if (r < K) {
+#pragma unroll
+          for (int j = 0; j < CPT / 4; ++j) {
+            float4 t;
+            unpack2f(s[2 * j], t.x, t.y);
+            unpack2f(s[2 * j + 1], t.z, t.w);
+            *reinterpret_cast<float4*>(sm + L::SF + r * 256 + ((((c0 >> 2) + j) ^ (r & 7)) << 4)) = t;
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(SFREADY);
+        return true;
+      };
+      uint64_t x[H2], y[H2];
       auto load_v = [&](uint64_t (&out)[H2], float f) {  // f times this thread's values of v (do)
         const uint64_t ff = pack2f(f, f);
 #pragma unroll
@@ -630,16 +708,17 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         fence_proxy_async_smem();
         tc_fence_before();
         arrive(VREADY);
-        if (MODE != FORWARD) {
-          uint8_t* img = (MODE == SAVE ? a.vn : a.z) +
-                         (static_cast<size_t>(slot0 + c) * p.HV + hv) * (4 * C * static_cast<size_t>(V)) + (v0 >> 6) * 8192;
-          put_image<CPT>(img, img + 2 * C * static_cast<size_t>(V), i, c0, x);
-        }
-        if (MODE == REVERSE && live) {
-          const uint64_t bb = pack2f(be, be);
+        if (MODE != FORWARD) {  // while step 3 runs: S, and vn (z) as it is, in two parts
+          if (!(good = put_state())) break;
 #pragma unroll
-          for (int j = 0; j < H2; ++j) y[j] = mul2(bb, x[j]);
-          put_bf16<CPT>(a.dv, orow, y);
+          for (int j = 0; j < CPT / 8; ++j) {
+            uint4 h, l;
+            split8(x + 4 * j, h, l);
+            *reinterpret_cast<uint4*>(sm + L::OUT + sw128(i, (c0 >> 3) + j)) = h;
+            *reinterpret_cast<uint4*>(sm + L::OUT + 8192 + sw128(i, (c0 >> 3) + j)) = l;
+          }
+          fence_proxy_async_smem();
+          arrive(OUTREADY);
         }
       } else if (MODE == FORWARD) {
         const uint64_t f = pack2f(p.scale * row, p.scale * row);
@@ -650,7 +729,14 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         tc_fence_after();
         tmem_ld_parts<N, CPT>(tl + TD2, y);
 #pragma unroll
-        for (int j = 0; j < H2; ++j) o[j] = fma2(f, x[j], y[j]);
+        for (int j = 0; j < H2; ++j) x[j] = fma2(f, x[j], y[j]);
+        // through shared memory: a row a thread straight to memory, the stores would take the
+        // load/store unit 500 to 1300 cycles a chunk from the warps on the way to step 3
+        if (n > 0 && !(good = wait(OUTFREE, (n - 1) & 1))) break;
+        if (whole) put_tile<N, CPT>(sm + L::OUT, i, c0, x);
+        else if (live) put_bf16<CPT>(p.out, orow, x);
+        fence_proxy_async_smem();
+        arrive(OUTREADY);
       } else if (MODE == REVERSE) {
         load_v(x, p.scale * row);
         if (!whole && !live) {
@@ -664,6 +750,9 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         put_parts<N, CPT>(sm + L::Y, L::LBO_Y, 64 + i, c0, x);
         fence_proxy_async_smem();
         arrive(QREADY);
+        if (!(good = put_state())) break;
+      } else if (!(good = put_state())) {
+        break;
       }
       if (!(good = wait(D3, ph))) break;
       tc_fence_after();
@@ -674,10 +763,6 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(SREADY);
-      // the output only now: its stores, a row a thread, would hold up the other warps'
-      // shared-memory stores on the way to step 3 (250 of 3340 cycles a chunk)
-      if constexpr (MODE == FORWARD)
-        if (!isk && live) put_bf16<CPT>(p.out, orow, o);
     }
     if (good && final && r < K) {
 #pragma unroll
@@ -691,14 +776,14 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == NW) {
     tc_fence_after();
     tmem_dealloc(tmem, TCOLS);
   }
 }
 
 template <int K, int N>
-__global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a,
+__global__ void __launch_bounds__(chain::threads(N), 1) gdr_chain_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a,
                                                                  int V) {
   extern __shared__ __align__(16) uint8_t raw[];
   chain_body<K, N, chain::FORWARD>(maps, a, V, blockIdx.x, raw);
@@ -707,7 +792,7 @@ __global__ void __launch_bounds__(chain::NT, 1) gdr_chain_kernel(const __grid_co
 // The backward's two chains in one launch: even blocks SAVE (maps: v), odd blocks REVERSE
 // (maps_r: d_out).  They share nothing but the records, so they run side by side.
 template <int K>
-__global__ void __launch_bounds__(chain::NT, 1) gdr_chains_kernel(const __grid_constant__ ChainMaps maps,
+__global__ void __launch_bounds__(chain::threads(64), 1) gdr_chains_kernel(const __grid_constant__ ChainMaps maps,
                                                                   const __grid_constant__ ChainMaps maps_r,
                                                                   const ChunkParams a, int V) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -765,7 +850,7 @@ cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cud
   constexpr uint32_t bytes = chain::Lay<K, N, chain::FORWARD>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(gdr_chain_kernel<K, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  gdr_chain_kernel<K, N><<<static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / N), chain::NT, bytes, st>>>(maps, a, V);
+  gdr_chain_kernel<K, N><<<static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / N), chain::threads(N), bytes, st>>>(maps, a, V);
   return cudaGetLastError();
 }
 
@@ -775,7 +860,7 @@ cudaError_t launch_chains(const ChainMaps& maps, const ChainMaps& maps_r, const 
   static_assert(bytes >= chain::Lay<K, 64, chain::SAVE>::SMEM, "shared memory of the two chains");
   cudaError_t e = cudaFuncSetAttribute(gdr_chains_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  gdr_chains_kernel<K><<<2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / 64), chain::NT, bytes, st>>>(maps, maps_r, a, V);
+  gdr_chains_kernel<K><<<2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / 64), chain::threads(64), bytes, st>>>(maps, maps_r, a, V);
   return cudaGetLastError();
 }
 
@@ -806,7 +891,7 @@ cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long w
   ChainMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   if (!make_map(&maps.q, p.q, K, p.H, tokens, 64) || !make_map(&maps.k, p.k, K, p.H, tokens, 64) ||
-      !make_map(&maps.v, p.v, V, p.HV, tokens, N))
+      !make_map(&maps.v, p.v, V, p.HV, tokens, N) || !make_map(&maps.o, p.out, V, p.HV, tokens, N))
     return cudaErrorInvalidValue;
   cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
   if (e != cudaSuccess) return e;

@@ -41,8 +41,8 @@ struct ChunkParams {
   Params p;
   uint8_t* rec;       // [slots, HV] records
   // backward: what the chains leave for the gradient kernel, per (slot, hv)
-  float* states;      // S entering the chunk [K, V]
-  float* dstates;     // dS' leaving it
+  float* states;      // S entering the chunk: [V / 64][K rows][16 chunks of 4, chunk ^= row & 7]
+  float* dstates;     // dS' leaving it, likewise
   uint8_t* vn;        // vn as an operand image: [2 parts][V / 64][64 rows][64] bf16
   uint8_t* z;         // z, same layout
   const void* dout;   // [tokens, HV, V] bf16
@@ -61,6 +61,7 @@ struct ChunkParams {
 struct ChainMaps {
   CUtensorMap q, k;   // boxes of 64 dims x 64 tokens
   CUtensorMap v;      // forward: v, reverse: d_out; boxes of N columns x 64 tokens
+  CUtensorMap o;      // forward: out, likewise
 };
 
 // First slot of a sequence's chunks.  Packed sequences: floor(tok0 / 64) + seq leaves room
@@ -173,6 +174,18 @@ __device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS >> 4), "n"(BS >> 4)
       : "memory");
+}
+
+// Wait for a barrier's phase, giving up after `limit_ns` or once *failed is set.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* failed) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns || *failed != 0u) return false;
+  }
+  return true;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -10,7 +10,7 @@
 //     dgc   = scale G q . (do S^T) + q . (A k) + k . (B k) - k . (A^T q + B^T k)
 //             - G beta k . (z S^T) - t,                      t  = E k . (vn dS'^T)
 //     dgl   = sum t + gamma <S, dS'>   (of the chunk's last gc);  dg = suffix sums of dgc
-// (dv = beta z is written by the reverse chain.)  A row's decay gradient is what the row's
+// dv = beta z.  A row's decay gradient is what the row's
 // products say: the gate multiplies whole rows, so every sum over D's entries is a dot of q
 // or k with a product that dq or dk need anyway.  A's diagonal has D = 1 and would enter
 // dgc twice with opposite signs; it stays out of the products and is added to dq and dk in
@@ -23,8 +23,8 @@
 //
 // One CTA of 256 threads per (chunk, value head).  Products on tcgen05 with M = 128: rows
 // 0-63 belong to q's side (do; A), rows 64-127 to k's side (z, vn; B), stacked in shared
-// memory so that one instruction serves both, and thread (lane r, half h) of the CTA owns
-// row r and half of the key dims throughout.
+// memory so that one instruction serves both, and thread (lane r, quarter h) of the CTA owns
+// row r and a quarter of the key dims throughout.
 #include "gdr_chunk.cuh"
 
 namespace kda {
@@ -32,7 +32,7 @@ namespace gdr {
 namespace {
 
 namespace grad {
-constexpr int NT = 256;
+constexpr int NT = 512;
 // 64-row pieces of 8 KB in each 64-column block of V; neighbours make 128-row operands
 // (the first four of block 0 later hold the third part of dS', 2 x 128 rows at most)
 enum { P_DO, P_ZH, P_ZERO, P_ZL, P_VL, P_VH, PIECES };
@@ -40,31 +40,71 @@ constexpr uint32_t BLOCK = PIECES * 8192;
 template <int K, int V>
 struct Lay {
   static constexpr uint32_t VB = V / 64;
-  static constexpr uint32_t S = VB * BLOCK;               // S parts; later A;B low, high parts and [q; k]
+  static constexpr uint32_t S = VB * BLOCK;               // S; later the A;B parts (low, high) and [q; k]
   static constexpr uint32_t CLO = S, CHI = S + kTileBytes, QK = S + 2 * kTileBytes;
-  static constexpr uint32_t PART = VB * K * 128;          // bytes of one part of S
-  static constexpr uint32_t DS = S + 65536;               // dS' parts; later the partial sums
-  static constexpr uint32_t X = DS + 2 * PART;            // gc high, low, beta, A's diagonal, warp sums
-  static constexpr uint32_t BAR = X + (4 * C + 8) * 4;
+  static constexpr uint32_t MAT = VB * K * 256;           // bytes of S or dS', fp32 or two parts
+  static constexpr uint32_t DS = S + 65536;               // dS'; later the partial sums
+  static constexpr uint32_t X = DS + MAT;                 // gc high, low, beta, A's diagonal, z . v, warp sums
+  static constexpr uint32_t BAR = X + (5 * C + 16) * 4;
   static constexpr uint32_t SMEM = BAR + 64 + 1024;
 };
 static_assert(Lay<128, 128>::SMEM <= 232448, "shared memory");
 enum { LD_A = 0, LD_S, LD_D, LD_QK, M1, M2, M3, NBAR };
 constexpr uint32_t E1 = 0, E2 = 128, E3 = 256, E4 = 320, E5A = 448, E5B = 256;  // TMEM columns
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// A matrix from fp32 rows (256 bytes, 16-byte chunks swizzled by the row) into its two bf16
+// parts in place: 8 rows are 2048 bytes of fp32, and one 1024-byte swizzle atom of each
+// part.  A warp takes 8 rows at a time; lane: row lane / 4, columns 8 q and 8 (q + 4) with
+// q = lane % 4.  `f(x, m)` sees the values and the 8-column chunk's number.
+template <class F>
+__device__ __forceinline__ void parts_in_place(uint8_t* mat, int groups, int warp, int lane, const F& f) {
+  const int row = lane >> 2, q = lane & 3;
+#pragma unroll 1
+  for (int g = warp; g < groups; g += NT / 32) {
+    uint8_t* at = mat + g * 2048;
+    float x[2][8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = 2 * q + (e & 1) + 8 * (e >> 1);
+      const float4 u = *reinterpret_cast<const float4*>(at + row * 256 + ((c ^ row) << 4));
+      float* d = x[e >> 1] + 4 * (e & 1);
+      d[0] = u.x; d[1] = u.y; d[2] = u.z; d[3] = u.w;
+    }
+    uint4 h[2], l[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      split8(x[e], h[e], l[e]);
+      f(x[e], h[e], l[e], g, row, q + 4 * e);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      *reinterpret_cast<uint4*>(at + row * 128 + (((q + 4 * e) ^ row) << 4)) = h[e];
+      *reinterpret_cast<uint4*>(at + 1024 + row * 128 + (((q + 4 * e) ^ row) << 4)) = l[e];
+    }
+  }
+}
 }  // namespace grad
 
+// Code that runs once per CTA is bound by instruction fetch, so everything here is small
+// loops: with the conversions, products and epilogue unrolled the same kernel took 207 us for
+// 2048 chunks and heads.
 template <int K, int V>
 __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
   using L = grad::Lay<K, V>;
   using namespace grad;
-  constexpr int VB = V / 64, KB = K / 64, DPT = K / 2;
+  constexpr int VB = V / 64, KB = K / 64, DPT = K / 4;
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   float* gh = reinterpret_cast<float*>(sm + L::X);
   float* gl = gh + C;
   float* bs = gl + C;
   float* diag = bs + C;
-  float* wsum = diag + C;
+  float* zvs = diag + C;
+  float* wsum = zvs + C;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
   const Params& p = a.p;
@@ -77,6 +117,7 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
   if (warp == 0) {
     if (lane == 0) {
       for (int b = 0; b < NBAR; ++b) mbar_init(&bars[b], 1);
+      tslot[1] = 0u;
       fence_mbar_init();
       const uint8_t* z = a.z + unit * (4 * C * V);
       const uint8_t* vn = a.vn + unit * (4 * C * V);
@@ -89,10 +130,10 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
         bulk_load(blk + P_VH * 8192, vn + b * 8192, 8192, &bars[LD_A]);
         bulk_load(blk + P_VL * 8192, vn + 2 * C * V + b * 8192, 8192, &bars[LD_A]);
       }
-      mbar_arrive_expect_tx_relaxed(&bars[LD_S], 2 * L::PART);
-      bulk_load(sm + L::S, a.states + unit * (K * V), 2 * L::PART, &bars[LD_S]);
-      mbar_arrive_expect_tx_relaxed(&bars[LD_D], 2 * L::PART);
-      bulk_load(sm + L::DS, a.dstates + unit * (K * V), 2 * L::PART, &bars[LD_D]);
+      mbar_arrive_expect_tx_relaxed(&bars[LD_S], L::MAT);
+      bulk_load(sm + L::S, a.states + unit * (K * V), L::MAT, &bars[LD_S]);
+      mbar_arrive_expect_tx_relaxed(&bars[LD_D], L::MAT);
+      bulk_load(sm + L::DS, a.dstates + unit * (K * V), L::MAT, &bars[LD_D]);
     }
     __syncwarp();
     tmem_alloc(tslot, 512);
@@ -115,148 +156,97 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot, sb = smem_u32(sm);
+  volatile uint32_t* never = tslot + 1;   // (zero)
   // a wait that runs out records the timeout and then drains: the work waited for is this
   // CTA's own copies and products, and its memory may not go before they are done
   auto wait = [&](int b) {
-    if (!mbar_wait(&bars[b], 0, a.wait_ns)) {
+#pragma unroll 1
+    for (uint64_t limit = a.wait_ns; !wait_phase(&bars[b], 0, limit, never) && limit != ~0ull; limit = limit == kDrainNs ? ~0ull : kDrainNs)
       atomicOr(p.status, kStatusTimeout);
-      mbar_wait(&bars[b], 0, kDrainNs);
-    }
     __syncwarp();
   };
-  const auto dk_ = [&](uint32_t off) { return sdesc_sw128(sb + off); };  // K-major operand
+  const auto kmaj = [&](uint32_t off) { return sdesc_sw128(sb + off); };             // rows of 128 bytes
+  const auto mat = [&](uint32_t off) { return sdesc_sw128(sb + off, 2048); };        // a part of S or dS'
+  constexpr uint32_t id1 = idesc_f16kind(128, K), id3 = idesc_f16kind(128, 64);
 
-  // ---- the products that need no k or q
+  // ---- [do; z] vn^T
   wait(LD_A);
   if (warp == 0) {
-    constexpr uint32_t id3 = idesc_f16kind(128, 64);
-    uint32_t acc = 0;
-#pragma unroll
-    for (int b = 0; b < VB; ++b)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint64_t o = (b * BLOCK + s * 32) >> 4;
-        umma_f16_warp(tmem + E3, dk_(P_DO * 8192) + o, dk_(P_VH * 8192) + o, id3, acc);
-        umma_f16_warp(tmem + E3, dk_(P_DO * 8192) + o, dk_(P_VL * 8192) + o, id3, 1u);
-        umma_f16_warp(tmem + E3, dk_(P_ZERO * 8192) + o, dk_(P_VH * 8192) + o, id3, 1u);
-        acc = 1;
-      }
+#pragma unroll 1
+    for (int b = 0; b < VB; ++b) {
+      const uint64_t o = b * BLOCK >> 4;
+      umma4<32, 32>(tmem + E3, kmaj(P_DO * 8192) + o, kmaj(P_VH * 8192) + o, id3, b > 0);
+      umma4<32, 32>(tmem + E3, kmaj(P_DO * 8192) + o, kmaj(P_VL * 8192) + o, id3, 1u);
+      umma4<32, 32>(tmem + E3, kmaj(P_ZERO * 8192) + o, kmaj(P_VH * 8192) + o, id3, 1u);
+    }
     umma_commit_warp(&bars[M1]);
   }
-  // ---- S and dS' from fp32 into operand parts, in place; <S, dS'> on the way
-  constexpr int NU = K * V / 8 / NT;                       // 8-value chunks of a thread
-  uint32_t d3[NU][4];
+  // ---- S into its parts; <S, dS'> on the way
+  wait(LD_S);
+  wait(LD_D);
   {
-    float s[NU][8], d[NU][8], dot = 0.f;
-    // (d3: the third part of dS', put in place of do and z once their products are done)
-    wait(LD_S);
-    wait(LD_D);
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const float4* ps = reinterpret_cast<const float4*>(sm + L::S + (tid + NT * u) * 32);
-      const float4* pd = reinterpret_cast<const float4*>(sm + L::DS + (tid + NT * u) * 32);
-      const float4 s0 = ps[0], s1 = ps[1], d0 = pd[0], d1 = pd[1];
-      s[u][0] = s0.x; s[u][1] = s0.y; s[u][2] = s0.z; s[u][3] = s0.w;
-      s[u][4] = s1.x; s[u][5] = s1.y; s[u][6] = s1.z; s[u][7] = s1.w;
-      d[u][0] = d0.x; d[u][1] = d0.y; d[u][2] = d0.z; d[u][3] = d0.w;
-      d[u][4] = d1.x; d[u][5] = d1.y; d[u][6] = d1.z; d[u][7] = d1.w;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dot = fmaf(s[u][e], d[u][e], dot);
-    }
+    float dot = 0.f;
+    parts_in_place(sm + L::S, L::MAT / 2048, warp, lane, [&](const float (&x)[8], uint4, uint4, int g, int row, int m) {
+      const uint8_t* at = sm + L::DS + g * 2048 + row * 256;
+      const float4 u = *reinterpret_cast<const float4*>(at + (((2 * m) ^ row) << 4));
+      const float4 w = *reinterpret_cast<const float4*>(at + (((2 * m + 1) ^ row) << 4));
+      dot = fmaf(x[0], u.x, fmaf(x[1], u.y, fmaf(x[2], u.z, fmaf(x[3], u.w, dot))));
+      dot = fmaf(x[4], w.x, fmaf(x[5], w.y, fmaf(x[6], w.z, fmaf(x[7], w.w, dot))));
+    });
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
     if (lane == 0) wsum[warp] = dot;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const int c = tid + NT * u, dim = c / (V / 8), ch = c % (V / 8);
-      const uint32_t o = (ch >> 3) * (K * 128) + sw128(dim, ch & 7);
-      uint4 h, l;
-      split8(s[u], h, l);
-      *reinterpret_cast<uint4*>(sm + L::S + o) = h;
-      *reinterpret_cast<uint4*>(sm + L::S + L::PART + o) = l;
-      split8(d[u], h, l);
-      *reinterpret_cast<uint4*>(sm + L::DS + o) = h;
-      *reinterpret_cast<uint4*>(sm + L::DS + L::PART + o) = l;
-      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        d3[u][e] = pack_bf16(d[u][2 * e] - __uint_as_float(hw[e] << 16) - __uint_as_float(lw[e] << 16),
-                             d[u][2 * e + 1] - __uint_as_float(hw[e] & 0xFFFF0000u) - __uint_as_float(lw[e] & 0xFFFF0000u));
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
   }
+  fence_proxy_async_smem();
+  __syncthreads();
+  // ---- [do; z] S^T
   if (warp == 0) {
-    constexpr uint32_t id1 = idesc_f16kind(128, K);
-    uint32_t acc = 0;
-#pragma unroll
-    for (int b = 0; b < VB; ++b)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint64_t o = (b * BLOCK + s * 32) >> 4, os = (b * K * 128 + s * 32) >> 4;
-        umma_f16_warp(tmem + E1, dk_(P_DO * 8192) + o, dk_(L::S) + os, id1, acc);
-        umma_f16_warp(tmem + E1, dk_(P_DO * 8192) + o, dk_(L::S + L::PART) + os, id1, 1u);
-        umma_f16_warp(tmem + E1, dk_(P_ZERO * 8192) + o, dk_(L::S) + os, id1, 1u);
-        acc = 1;
-      }
+#pragma unroll 1
+    for (int b = 0; b < VB; ++b) {
+      const uint64_t o = b * BLOCK >> 4, os = b * K * 256 >> 4;
+      umma4<32, 32>(tmem + E1, kmaj(P_DO * 8192) + o, mat(L::S) + os, id1, b > 0);
+      umma4<32, 32>(tmem + E1, kmaj(P_DO * 8192) + o, mat(L::S + 1024) + os, id1, 1u);
+      umma4<32, 32>(tmem + E1, kmaj(P_ZERO * 8192) + o, mat(L::S) + os, id1, 1u);
+    }
     umma_commit_warp(&bars[M2]);
-    acc = 0;
-#pragma unroll
-    for (int b = 0; b < VB; ++b)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint64_t o = (b * BLOCK + s * 32) >> 4, os = (b * K * 128 + s * 32) >> 4;
-        umma_f16_warp(tmem + E2, dk_(P_VL * 8192) + o, dk_(L::DS) + os, id1, acc);
-        umma_f16_warp(tmem + E2, dk_(P_VL * 8192) + o, dk_(L::DS + L::PART) + os, id1, 1u);
-        umma_f16_warp(tmem + E2, dk_(P_ZL * 8192) + o, dk_(L::DS) + os, id1, 1u);
-        umma_f16_warp(tmem + E2, dk_(P_ZL * 8192) + o, dk_(L::DS + L::PART) + os, id1, 1u);
-        acc = 1;
-      }
   }
-  // ---- z . v, while they run
-  const int r = 32 * (warp & 3) + lane, half = warp >> 2, i = r & 63;
+  // ---- while it runs: z . v, and dv = beta z, a row's 16-byte chunks on neighbouring threads
+  const int r = 32 * (warp & 3) + lane, part = warp >> 2, i = r & 63;
   const bool kside = r >= 64, live = i < rows;
+  {
+    constexpr int CH = V / 8;                              // 16-byte chunks of a row
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v);
+    __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(a.dv);
+#pragma unroll 1
+    for (int n = tid; n < C * CH; n += NT) {
+      const int rw = n / CH, ch = n % CH;
+      const uint8_t* at = sm + (ch >> 3) * BLOCK + sw128(rw, ch & 7);
+      const uint4 uh = *reinterpret_cast<const uint4*>(at + P_ZH * 8192), ul = *reinterpret_cast<const uint4*>(at + P_ZL * 8192);
+      const size_t o = (static_cast<size_t>(tok0 + rw) * p.HV + hv) * V + 8 * ch;
+      const uint4 uv = rw < rows ? *reinterpret_cast<const uint4*>(v + o) : make_uint4(0, 0, 0, 0);
+      const uint32_t h[4] = {uh.x, uh.y, uh.z, uh.w}, l[4] = {ul.x, ul.y, ul.z, ul.w}, w[4] = {uv.x, uv.y, uv.z, uv.w};
+      const float b = bs[rw];
+      uint32_t out[4];
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z0 = lo16(h[e]) + lo16(l[e]), z1 = hi16(h[e]) + hi16(l[e]);
+        dot = fmaf(z0, lo16(w[e]), fmaf(z1, hi16(w[e]), dot));
+        out[e] = pack_bf16(b * z0, b * z1);
+      }
+      if (rw < rows) *reinterpret_cast<uint4*>(dv + o) = make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+      for (int m = CH / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
+      if (ch == 0) zvs[rw] = dot;
+    }
+  }
   const float hi = gh[i], lo = gl[i], be = bs[i];
   const float bsafe = fabsf(be) < 1e-20f ? 1e-20f : be;
   const float row = ex2(hi), tail = ex2((gh[63] - hi) + (gl[63] - lo));
-  float zv = 0.f;
-  if (kside && live) {
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (static_cast<size_t>(tok0 + i) * p.HV + hv) * V;
-#pragma unroll
-    for (int c = 0; c < V / 16; ++c) {
-      const int col = half * (V / 16) + c;                // 16-byte chunk of the row
-      const uint8_t* blk = sm + (col >> 3) * BLOCK;
-      const uint4 uh = *reinterpret_cast<const uint4*>(blk + P_ZH * 8192 + sw128(i, col & 7));
-      const uint4 ul = *reinterpret_cast<const uint4*>(blk + P_ZL * 8192 + sw128(i, col & 7));
-      const uint4 uv = *reinterpret_cast<const uint4*>(v + 8 * col);
-      const uint32_t h[4] = {uh.x, uh.y, uh.z, uh.w}, l[4] = {ul.x, ul.y, ul.z, ul.w}, w[4] = {uv.x, uv.y, uv.z, uv.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        zv = fmaf(__uint_as_float(h[e] << 16) + __uint_as_float(l[e] << 16), __uint_as_float(w[e] << 16), zv);
-        zv = fmaf(__uint_as_float(h[e] & 0xFFFF0000u) + __uint_as_float(l[e] & 0xFFFF0000u),
-                  __uint_as_float(w[e] & 0xFFFF0000u), zv);
-      }
-    }
-  }
-  // ---- A and B, strictly lower, as [A; B] operand parts
   const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   wait(M1);
+  wait(M2);          // S, do and z are no longer read by products
   tc_fence_after();
-  float x[32];
-  tmem_ld32(tl + E3 + 32 * half, x);
-  tmem_ld_wait();
-  {
-    const float f = kside ? -bsafe : p.scale;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int c = 32 * half + j;
-      if (!kside && c == i) diag[i] = live ? f * x[j] : 0.f;
-      x[j] = (live && c < i) ? f * x[j] * ex2((hi - gh[c]) + (lo - gl[c])) : 0.f;
-    }
-  }
-  wait(M2);          // S is no longer read by products
-  __syncthreads();
   if (tid == 0) {
     mbar_arrive_expect_tx_relaxed(&bars[LD_QK], KB * kTileBytes);
 #pragma unroll
@@ -265,74 +255,92 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
       tma_load_3d(sm + L::QK + b * kTileBytes + 8192, &maps.k, &bars[LD_QK], 64 * b, hk, static_cast<int>(tok0));
     }
   }
+  // ---- A and B, strictly lower, as [A; B] operand parts
+  {
+    const float f = kside ? -bsafe : p.scale;
+    {
+      const int c0 = 16 * part;
+      float x[16];
+      tmem_ld16(tl + E3 + c0, x);
+      tmem_ld_wait();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint4 h, l;
-    split8(x + 8 * j, h, l);
-    *reinterpret_cast<uint4*>(sm + L::CHI + sw128(r, 4 * half + j)) = h;
-    *reinterpret_cast<uint4*>(sm + L::CLO + sw128(r, 4 * half + j)) = l;
-  }
+      for (int j = 0; j < 16; ++j) {
+        const int c = c0 + j;
+        if (!kside && c == i) diag[i] = live ? f * x[j] : 0.f;
+        x[j] = (live && c < i) ? f * x[j] * ex2((hi - gh[c]) + (lo - gl[c])) : 0.f;
+      }
 #pragma unroll
-  for (int u = 0; u < NU; ++u) {
-    const int c = tid + NT * u, dim = c / (V / 8), ch = c % (V / 8);
-    *reinterpret_cast<uint4*>(sm + (ch >> 3) * (K * 128) + sw128(dim, ch & 7)) = make_uint4(d3[u][0], d3[u][1], d3[u][2], d3[u][3]);
+      for (int j = 0; j < 2; ++j) {
+        uint4 ph, pl;
+        split8(x + 8 * j, ph, pl);
+        *reinterpret_cast<uint4*>(sm + L::CHI + sw128(r, (c0 >> 3) + j)) = ph;
+        *reinterpret_cast<uint4*>(sm + L::CLO + sw128(r, (c0 >> 3) + j)) = pl;
+      }
+    }
   }
+  __syncthreads();   // z . v and dv have read z
+  // ---- dS' into three parts, the third in place of do and z
+  parts_in_place(sm + L::DS, L::MAT / 2048, warp, lane, [&](const float (&x)[8], uint4 h, uint4 l, int g, int rw, int m) {
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+    uint32_t t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      t[e] = pack_bf16(x[2 * e] - lo16(hw[e]) - lo16(lw[e]), x[2 * e + 1] - hi16(hw[e]) - hi16(lw[e]));
+    const int vb = g / (K / 8), dim = (g % (K / 8)) * 8 + rw;
+    *reinterpret_cast<uint4*>(sm + vb * (K * 128) + sw128(dim, m)) = make_uint4(t[0], t[1], t[2], t[3]);
+  });
   wait(LD_QK);
-  if (!live && half == 0) {  // rows past the sequence's end: other tokens, of any value
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<uint4*>(sm + L::QK + b * kTileBytes + sw128(r, c)) = make_uint4(0, 0, 0, 0);
+  if (!live && part == 0) {  // rows past the sequence's end: other tokens, of any value
+#pragma unroll 1
+    for (int c = 0; c < 8 * KB; ++c)
+      *reinterpret_cast<uint4*>(sm + L::QK + (c >> 3) * kTileBytes + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  // ---- [A; B] k and A^T q + B^T k (the latter in lanes 64-127: the first atom of M is the
-  // neighbouring tile, whose lanes nobody reads)
+  // ---- vn dS'^T, [A; B] k and A^T q + B^T k (the last in lanes 64-127: the first atom of M is
+  // the neighbouring tile, whose lanes nobody reads)
   if (warp == 0) {
     tc_fence_after();
-    constexpr uint32_t id4 = idesc_f16kind(128, K) | IDESC_B_MN_MAJOR;
-    constexpr uint32_t id5 = idesc_f16kind(128, 64) | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;
-#pragma unroll
-    for (int b = 0; b < VB; ++b)
-#pragma unroll
-      for (int s = 0; s < 4; ++s)  // vn (third part of dS')^T
-        umma_f16_warp(tmem + E2, dk_(P_VL * 8192) + ((b * BLOCK + s * 32) >> 4), dk_(0) + ((b * K * 128 + s * 32) >> 4),
-                      idesc_f16kind(128, K), 1u);
-    const uint64_t bk = sdesc(sb + L::QK + 8192, kTileBytes, 1024, 2), bq = sdesc(sb + L::QK, kTileBytes, 1024, 2);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      umma_f16_warp(tmem + E4, dk_(L::CHI) + (s * 32 >> 4), bk + (s * 2048 >> 4), id4, s > 0);
-      umma_f16_warp(tmem + E4, dk_(L::CLO) + (s * 32 >> 4), bk + (s * 2048 >> 4), id4, 1u);
+#pragma unroll 1
+    for (int b = 0; b < VB; ++b) {
+      const uint64_t o = b * BLOCK >> 4, os = b * K * 256 >> 4;
+      umma4<32, 32>(tmem + E2, kmaj(P_VL * 8192) + o, mat(L::DS) + os, id1, b > 0);
+      umma4<32, 32>(tmem + E2, kmaj(P_VL * 8192) + o, mat(L::DS + 1024) + os, id1, 1u);
+      umma4<32, 32>(tmem + E2, kmaj(P_ZL * 8192) + o, mat(L::DS) + os, id1, 1u);
+      umma4<32, 32>(tmem + E2, kmaj(P_ZL * 8192) + o, mat(L::DS + 1024) + os, id1, 1u);
+      umma4<32, 32>(tmem + E2, kmaj(P_VL * 8192) + o, kmaj(b * K * 128), id1, 1u);
     }
+    constexpr uint32_t id4 = id1 | IDESC_B_MN_MAJOR, id5 = id3 | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;
+    const uint64_t bk = sdesc(sb + L::QK + 8192, kTileBytes, 1024, 2), bq = sdesc(sb + L::QK, kTileBytes, 1024, 2);
+    umma4<32, 2048>(tmem + E4, kmaj(L::CHI), bk, id4, 0u);
+    umma4<32, 2048>(tmem + E4, kmaj(L::CLO), bk, id4, 1u);
     const uint64_t ah = sdesc(sb + L::CLO, kTileBytes, 1024, 2), al = sdesc(sb + L::CLO - kTileBytes, kTileBytes, 1024, 2);
-#pragma unroll
+#pragma unroll 1
     for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint64_t o = s * 2048 >> 4, ob = (b * kTileBytes + s * 2048) >> 4;
-        umma_f16_warp(tmem + (b ? E5B : E5A), ah + o, bq + ob, id5, s > 0);
-        umma_f16_warp(tmem + (b ? E5B : E5A), al + o, bq + ob, id5, 1u);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t o = h * 8192 >> 4, ob = (b * kTileBytes + h * 8192) >> 4;
+        umma4<2048, 2048>(tmem + (b ? E5B : E5A), ah + o, bq + ob, id5, h);
+        umma4<2048, 2048>(tmem + (b ? E5B : E5A), al + o, bq + ob, id5, 1u);
       }
     umma_commit_warp(&bars[M3]);
   }
   wait(M3);
   tc_fence_after();
   // ---- rows of dq and dk, and their dots
-  float dgc = 0.f, t = 0.f, db = zv;
+  float dgc = 0.f, t = 0.f, db = 0.f;
   {
     const float dg_ = diag[i], f1 = kside ? -row * be : p.scale * row;
     float a1 = 0.f, a2 = 0.f, a4 = 0.f, a5 = 0.f;
     const size_t orow = static_cast<size_t>(tok0 + i);
     const bool grouped = p.HV != p.H;
-#pragma unroll
+#pragma unroll 1
     for (int d0 = 0; d0 < DPT; d0 += 16) {
-      const int d = half * DPT + d0;
-      float e1[16], e4[16], out[16], own[16], oth[16];
+      const int d = part * DPT + d0;
+      float e1[16], e4[16], out[16], own[16];
       tmem_ld16(tl + E1 + d, e1);
       tmem_ld16(tl + E4 + d, e4);
-      tmem_ld_wait();
       const uint8_t* tile = sm + L::QK + (d >> 6) * kTileBytes;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -341,17 +349,18 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
         const uint32_t wo[4] = {uo.x, uo.y, uo.z, uo.w}, wt[4] = {ut.x, ut.y, ut.z, ut.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          own[8 * c + 2 * e] = __uint_as_float(wo[e] << 16);
-          own[8 * c + 2 * e + 1] = __uint_as_float(wo[e] & 0xFFFF0000u);
-          oth[8 * c + 2 * e] = __uint_as_float(wt[e] << 16);
-          oth[8 * c + 2 * e + 1] = __uint_as_float(wt[e] & 0xFFFF0000u);
+          own[8 * c + 2 * e] = lo16(wo[e]);
+          own[8 * c + 2 * e + 1] = hi16(wo[e]);
+          out[8 * c + 2 * e] = dg_ * lo16(wt[e]);
+          out[8 * c + 2 * e + 1] = dg_ * hi16(wt[e]);
         }
       }
+      tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         a1 = fmaf(own[j], e1[j], a1);
         a4 = fmaf(own[j], e4[j], a4);
-        out[j] = fmaf(f1, e1[j], fmaf(dg_, oth[j], e4[j]));
+        out[j] = fmaf(f1, e1[j], out[j] + e4[j]);
       }
       if (kside) {
         tmem_ld16(tl + E2 + d, e1);
@@ -385,18 +394,19 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
       if (kside) {
         t = tail * a2;
         dgc = a4 - a5 + f1 * a1 - t;
-        db += a4 / bsafe - row * a1;
+        db = a4 / bsafe - row * a1;
+        if (part == 0) db += zvs[i];
       } else {
         dgc = f1 * a1 + a4;
       }
     }
   }
   // ---- the rows' shares of dg and dbeta (over dS', whose products are done)
-  float* sg = reinterpret_cast<float*>(sm + L::DS);  // [2 halves][128] dgc, then t, then dbeta
-  sg[half * 128 + r] = dgc;
+  float* sg = reinterpret_cast<float*>(sm + L::DS);  // [4 quarters][128] dgc, then t, then dbeta
+  sg[part * 128 + r] = dgc;
   if (kside) {
-    sg[256 + half * 64 + i] = t;
-    sg[384 + half * 64 + i] = db;
+    sg[512 + part * 64 + i] = t;
+    sg[768 + part * 64 + i] = db;
   }
   tc_fence_before();
   __syncthreads();
@@ -405,14 +415,16 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
     tmem_dealloc(tmem, 512);
   }
   if (warp == 1) {
-    float sd = lane < 8 ? wsum[lane] : 0.f, st = 0.f;
+    float sd = lane < NT / 32 ? wsum[lane] : 0.f, st = 0.f, b0 = 0.f, b1 = 0.f;
     float g0 = 0.f, g1 = 0.f;
     const int i0 = 2 * lane;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 4; ++h) {
       g0 += sg[h * 128 + i0] + sg[h * 128 + 64 + i0];
       g1 += sg[h * 128 + i0 + 1] + sg[h * 128 + 64 + i0 + 1];
-      st += sg[256 + h * 64 + i0] + sg[256 + h * 64 + i0 + 1];
+      st += sg[512 + h * 64 + i0] + sg[512 + h * 64 + i0 + 1];
+      b0 += sg[768 + h * 64 + i0];
+      b1 += sg[768 + h * 64 + i0 + 1];
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
@@ -429,11 +441,11 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
     const size_t o = static_cast<size_t>(tok0 + i0) * p.HV + hv;
     if (i0 < rows) {
       a.dg[o] = run + last;
-      a.dbeta[o] = sg[384 + i0] + sg[448 + i0];
+      a.dbeta[o] = b0;
     }
     if (i0 + 1 < rows) {
       a.dg[o + p.HV] = run - g0 + last;
-      a.dbeta[o + p.HV] = sg[384 + i0 + 1] + sg[448 + i0 + 1];
+      a.dbeta[o + p.HV] = b1;
     }
   }
 }
