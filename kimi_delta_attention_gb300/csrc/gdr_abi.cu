@@ -129,9 +129,9 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
   if (z.ns == 0) return KDA_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint32_t* status = static_cast<uint32_t*>(workspace);
-  if (cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
   const kda::gdr::Params p{q, k, v, g, beta, initial_state, cu_seqlens, out, final_state, status, scale, s->T,
                            s->H, s->HV, static_cast<int>(z.ns)};
+  if (!chunked(s, z) && cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
   const cudaError_t e =
       chunked(s, z) ? kda::gdr::launch_chunk_fwd(p, chunk_part(workspace), wait_limit_ns(), s->K, s->V, cs)
                     : kda::gdr::launch_recurrent(p, s->K, s->V, s->io_dtype == KDA_BF16, cs);
@@ -187,8 +187,8 @@ kda_status kda_gdr_bwd(const kda_shape* s, const void* q, const void* k, const v
   if (z.ns == 0) return KDA_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint32_t* status = static_cast<uint32_t*>(workspace);
-  if (cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
   if (z.tokens == 0) {  // no tokens: the state's gradient passes through
+    if (cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
     if (!d_initial_state) return KDA_OK;
     const cudaError_t e = d_final_state ? cudaMemcpyAsync(d_initial_state, d_final_state, z.state, cudaMemcpyDeviceToDevice, cs)
                                         : cudaMemsetAsync(d_initial_state, 0, z.state, cs);

@@ -90,7 +90,9 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int seq, rows;
   long tok;
-  if (!find_chunk(a, slot, seq, tok, rows)) return;
+  if (blockIdx.x == 0 && tid == 0) *p.status = 0u;
+  if (!find_chunk(a, nullptr, slot, seq, tok, rows)) return;
+  bool ok = true;                                // this thread's waits
   if (warp == 0) {
     if (lane == 0) {
       mbar_init(&bar[0], 1);
@@ -125,14 +127,13 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now: a block of the next kernel that shares this SM takes its TMEM after this one's
+  let_next_kernel_start();
   const uint32_t tmem = *tslot;
-  bool ok = true;
   if (warp == 0) {
     ok = mbar_wait(&bar[0], 0, a.wait_ns);
-    if (!__all_sync(0xFFFFFFFFu, ok)) {
-      if (lane == 0) atomicOr(p.status, kStatusTimeout);
-      mbar_wait(&bar[0], 0, kDrainNs);
-    }
+    if (!ok) mbar_wait(&bar[0], 0, kDrainNs);
+    __syncwarp();
     const uint64_t d = sdesc_sw128(smem_u32(sm));
 #pragma unroll
     for (int s = 0; s < K / 16; ++s) {
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
   const bool isq = tid >= 64;
   const float hi = gh[i], lo = gl[i], be = bs[i];
   if (!mbar_wait(&bar[1], 0, a.wait_ns)) {
-    atomicOr(p.status, kStatusTimeout);
+    ok = false;
     mbar_wait(&bar[1], 0, kDrainNs);
   }
   tc_fence_after();
@@ -285,8 +286,10 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
     fac[i] = ex2(hi);
     fac[64 + i] = ex2((gh[63] - hi) + (gl[63] - lo));
     fac[128 + i] = be;
-    if (i == 63) fac[192] = ex2(hi);
+    if (i == 63) fac[kRecGamma] = ex2(hi);
   }
+  ok = __syncthreads_and(ok);
+  if (tid == 0) fac[kRecFailed] = ok ? 0.f : 1.f;
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
@@ -432,7 +435,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long tok0;
   int len;
-  seq_tokens(p.cu, p.T, p.num_seqs, p.status, seq, tok0, len);
+  const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
   const int nch = num_chunks(len), slot0 = first_slot(a, seq, tok0);
   const auto chunk = [&](int n) { return MODE == REVERSE ? nch - 1 - n : n; };  // of step n
   if (tid == 0) {
@@ -451,6 +454,9 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  wait_for_previous_kernel();  // the records, the cleared status
+  let_next_kernel_start();
+  if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
   // waits of a whole warp; false once the CTA has failed
   auto wait = [&](int b, uint32_t parity) {
     if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
@@ -632,8 +638,9 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       const size_t tok = static_cast<size_t>(tok0 + C * static_cast<long>(c) + i);
       const bool live = C * c + i < len, whole = C * c + C <= len;  // this row; every row of the chunk
       if (!(good = wait(FULL0 + (n & 1), (n >> 1) & 1))) break;
+      if (tid == 0 && fac[kRecFailed] != 0.f) atomicOr(p.status, kStatusTimeout);
       const float row = fac[i];
-      const uint64_t gamma = pack2f(fac[192], fac[192]);
+      const uint64_t gamma = pack2f(fac[kRecGamma], fac[kRecGamma]);
       const size_t orow = (tok * p.HV + hv) * V + v0 + c0;
       // rows past the sequence's end hold the next one's tokens, whatever they are: every
       // operand that meets them in a sum over tokens has them zeroed first
@@ -839,29 +846,25 @@ int sm_count() {
 
 template <int K>
 cudaError_t launch_prep(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(gdr_prep_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep::SMEM);
-  if (e != cudaSuccess) return e;
-  gdr_prep_kernel<K><<<static_cast<unsigned>(a.slots) * a.p.HV, prep::NT, prep::SMEM, st>>>(maps, a);
-  return cudaGetLastError();
+  static LaunchState state;
+  return launch_kernel(state, gdr_prep_kernel<K>, static_cast<unsigned>(a.slots) * a.p.HV, prep::NT, prep::SMEM, false, st,
+                       maps, a);
 }
 
 template <int K, int N>
 cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cudaStream_t st) {
-  constexpr uint32_t bytes = chain::Lay<K, N, chain::FORWARD>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(gdr_chain_kernel<K, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  gdr_chain_kernel<K, N><<<static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / N), chain::threads(N), bytes, st>>>(maps, a, V);
-  return cudaGetLastError();
+  static LaunchState state;
+  return launch_kernel(state, gdr_chain_kernel<K, N>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / N),
+                       chain::threads(N), chain::Lay<K, N, chain::FORWARD>::SMEM, true, st, maps, a, V);
 }
 
 template <int K>
 cudaError_t launch_chains(const ChainMaps& maps, const ChainMaps& maps_r, const ChunkParams& a, int V, cudaStream_t st) {
   constexpr uint32_t bytes = chain::Lay<K, 64, chain::REVERSE>::SMEM;   // the larger of the two
   static_assert(bytes >= chain::Lay<K, 64, chain::SAVE>::SMEM, "shared memory of the two chains");
-  cudaError_t e = cudaFuncSetAttribute(gdr_chains_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  gdr_chains_kernel<K><<<2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / 64), chain::threads(64), bytes, st>>>(maps, maps_r, a, V);
-  return cudaGetLastError();
+  static LaunchState state;
+  return launch_kernel(state, gdr_chains_kernel<K>, 2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / 64),
+                       chain::threads(64), bytes, true, st, maps, maps_r, a, V);
 }
 
 }  // namespace

@@ -32,10 +32,13 @@ constexpr unsigned long long kDrainNs = 2000000000ull; // limit for work already
 
 // Record of one (chunk, value head), written by the preparation and read by the chains:
 // [T; R] as two K-major, 128-byte-swizzled bf16 tiles of 128 rows x 64 (high, then low
-// parts), then per-row factors (fp32): G, E, beta, gamma.
+// parts), then per-row factors (fp32): G, E, beta, gamma, and a word that is not zero where
+// the preparation ran out of time.  (The preparation is the call's first kernel and clears
+// the status word, so it reports through the record; the kernels after it report directly.)
 constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kRecFactors = 2 * kTileBytes;
 constexpr uint32_t kRecBytes = kRecFactors + 1024;
+constexpr int kRecGamma = 192, kRecFailed = 193;       // indices among the factors
 
 struct ChunkParams {
   Params p;
@@ -72,7 +75,7 @@ __device__ __forceinline__ int first_slot(const ChunkParams& a, int seq, long to
 __device__ __forceinline__ int num_chunks(int len) { return (len + C - 1) >> 6; }
 
 // The sequence and chunk of a slot; false where the slot holds no chunk.
-__device__ __forceinline__ bool find_chunk(const ChunkParams& a, int slot, int& seq, long& tok, int& rows) {
+__device__ __forceinline__ bool find_chunk(const ChunkParams& a, uint32_t* status, int slot, int& seq, long& tok, int& rows) {
   long tok0;
   int len, m;
   if (a.p.cu == nullptr) {
@@ -88,7 +91,7 @@ __device__ __forceinline__ bool find_chunk(const ChunkParams& a, int slot, int& 
       else hi = mid - 1;
     }
     seq = lo;
-    if (!seq_tokens(a.p.cu, a.p.T, a.p.num_seqs, a.p.status, seq, tok0, len)) return false;
+    if (!seq_tokens(a.p.cu, a.p.T, a.p.num_seqs, status, seq, tok0, len)) return false;
     m = slot - first_slot(a, seq, tok0);
   }
   if (m < 0 || m >= num_chunks(len)) return false;
@@ -176,6 +179,12 @@ __device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32
       : "memory");
 }
 
+// A kernel of a call starts while the one before it still runs: before it touches what that
+// one wrote it waits for its end, and it lets the next one start once all its blocks have
+// started and taken their TMEM (a waiting block must not hold what a running one needs).
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Wait for a barrier's phase, giving up after `limit_ns` or once *failed is set.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* failed) {
   uint64_t t0 = 0;
@@ -223,6 +232,35 @@ __device__ __forceinline__ void gate_scan(const Params& p, long tok, int rows, i
   add_pairs(h, l, -h1, -l1);
   hi[0] = h;
   lo[0] = l;
+}
+
+// Launch a kernel, as a dependent of the stream's previous one where `after` says so; its
+// shared-memory limit is raised on its first launch on a device.
+struct LaunchState {
+  bool raised[64] = {};
+};
+template <class... P, class... A>
+cudaError_t launch_kernel(LaunchState& state, void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, bool after,
+                          cudaStream_t st, const A&... args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !state.raised[dev]) {  // (a race raises it twice, to the same value)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) state.raised[dev] = true;
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace gdr

@@ -112,13 +112,14 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int seq, rows;
   long tok0;
-  if (!find_chunk(a, slot, seq, tok0, rows)) return;
+  if (!find_chunk(a, nullptr, slot, seq, tok0, rows)) return;
   const size_t unit = static_cast<size_t>(slot) * p.HV + hv;
   if (warp == 0) {
     if (lane == 0) {
       for (int b = 0; b < NBAR; ++b) mbar_init(&bars[b], 1);
       tslot[1] = 0u;
       fence_mbar_init();
+      wait_for_previous_kernel();  // the chains' results; all other threads meet them behind this one's copies
       const uint8_t* z = a.z + unit * (4 * C * V);
       const uint8_t* vn = a.vn + unit * (4 * C * V);
       mbar_arrive_expect_tx_relaxed(&bars[LD_A], VB * 5 * 8192);
@@ -469,11 +470,9 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float* dqs, const 
 
 template <int K, int V>
 cudaError_t launch(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
-  constexpr uint32_t bytes = grad::Lay<K, V>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(gdr_grad_kernel<K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  gdr_grad_kernel<K, V><<<static_cast<unsigned>(a.slots) * a.p.HV, grad::NT, bytes, st>>>(maps, a);
-  return cudaGetLastError();
+  static LaunchState state;
+  return launch_kernel(state, gdr_grad_kernel<K, V>, static_cast<unsigned>(a.slots) * a.p.HV, grad::NT, grad::Lay<K, V>::SMEM,
+                       true, st, maps, a);
 }
 
 }  // namespace

@@ -142,3 +142,28 @@ def test_refusals():
     refused(lambda: kda.kda_gdr_bwd(*args, d_final_state=x["ds"].bfloat16()))
     refused(lambda: kda.kda_gdr_bwd(*args, scale=0.0))
     refused(lambda: kda.kda_gdr_bwd(*args, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")), 6)
+
+
+@pytest.mark.parametrize("limit", ["1", "1000"])
+def test_wait_limit(limit, monkeypatch):
+    """A wait limit too short for the kernels' copies: the calls complete, with their result or
+    a reported timeout, and the next calls are right."""
+    x = make((2, 400), 2, 4, 128, 128, seed=49, grads=True)
+    d = cuda(x)
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    fws = torch.empty(kda.kda_gdr_fwd_workspace_size(kda.make_shape(d["q"], d["v"])), dtype=torch.uint8, device="cuda")
+    bws = torch.empty(kda.kda_gdr_bwd_workspace_size(kda.make_shape(d["q"], d["v"])), dtype=torch.uint8, device="cuda")
+    fwd = lambda: kda.kda_gdr_fwd(*args, d["scale"], initial_state=d["s0"], workspace=fws)
+    bwd = lambda: kda.kda_gdr_bwd(*args, d["do"], d["scale"], initial_state=d["s0"], d_final_state=d["ds"], workspace=bws)
+    ref_f, ref_b = fwd(), bwd()
+    torch.cuda.synchronize()
+    monkeypatch.setenv("KDA_WAIT_LIMIT_NS", limit)
+    got = fwd()
+    status = kda.kda_read_device_status(fws)
+    assert status in (0, 5) and (status == 5 or all(torch.equal(s, t) for s, t in zip(ref_f, got)))
+    got = bwd()
+    status = kda.kda_read_device_status(bws)
+    assert status in (0, 5) and (status == 5 or all(torch.equal(s, t) for s, t in zip(ref_b, got)))
+    monkeypatch.delenv("KDA_WAIT_LIMIT_NS")
+    assert all(torch.equal(s, t) for s, t in zip(ref_f, fwd())) and kda.kda_read_device_status(fws) == 0
+    assert all(torch.equal(s, t) for s, t in zip(ref_b, bwd())) and kda.kda_read_device_status(bws) == 0
