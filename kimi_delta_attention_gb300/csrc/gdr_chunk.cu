@@ -110,8 +110,9 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
     tmem_relinquish();
   }
   if (warp == 1) {
-    float h[2], l[2];
-    gate_scan(p, tok, rows, hv, lane, h, l);
+    float g[2], h[2], l[2];
+    load_gate(p.g, p, tok, rows, hv, lane, g);
+    gate_scan(g[0], g[1], lane, h, l);
     gh[2 * lane] = h[0];
     gh[2 * lane + 1] = h[1];
     gl[2 * lane] = l[0];
@@ -526,8 +527,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     // backward's code then no longer fits the instruction cache beside the other warps' (its
     // warps waited for instructions 3.5 cycles of every 9 that they did not wait for data)
     auto issue = [&](uint32_t d, uint64_t aa, uint64_t bb, uint32_t idesc, uint32_t acc, uint32_t as) {
-#pragma unroll 1
-      for (int s = 0; s < 4; ++s, aa += as >> 4, bb += 2048 >> 4, acc = 1u) umma_f16_warp(d, aa, bb, idesc, acc);
+      umma4_loop(d, aa, as, bb, 2048, idesc, acc);
     };
     for (int n = 0; n < nch; ++n) {
       const uint32_t ph = n & 1, st = sb + ph * L::STAGE, tt = MODE == FORWARD ? st + L::TT : sb + L::TT1;
@@ -833,17 +833,6 @@ bool make_map(CUtensorMap* m, const void* base, int dim, int heads, long tokens,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  static int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-      return 152;
-    return v;
-  }();
-  return n;
-}
-
 template <int K>
 cudaError_t launch_prep(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
   static LaunchState state;
@@ -938,7 +927,9 @@ cudaError_t launch_chunk_bwd(const Params& p, const void* dout, const float* dfi
       !make_map(&maps.v, p.v, V, p.HV, tokens, 64))
     return cudaErrorInvalidValue;
   maps_r = maps;
-  if (!make_map(&maps_r.v, dout, V, p.HV, tokens, 64)) return cudaErrorInvalidValue;
+  if (!make_map(&maps_r.v, dout, V, p.HV, tokens, 64) || !make_map(&maps_r.o, dq, K, p.H, tokens, 64) ||
+      !make_map(&maps_r.o2, dk, K, p.H, tokens, 64))
+    return cudaErrorInvalidValue;
   cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
   if (e != cudaSuccess) return e;
   e = K == 128 ? launch_chains<128>(maps, maps_r, a, V, st) : launch_chains<64>(maps, maps_r, a, V, st);

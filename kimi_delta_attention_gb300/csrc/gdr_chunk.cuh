@@ -64,7 +64,8 @@ struct ChunkParams {
 struct ChainMaps {
   CUtensorMap q, k;   // boxes of 64 dims x 64 tokens
   CUtensorMap v;      // forward: v, reverse: d_out; boxes of N columns x 64 tokens
-  CUtensorMap o;      // forward: out, likewise
+  CUtensorMap o;      // forward: out, likewise; gradients without grouped heads: dq and (o2) dk, as q and k
+  CUtensorMap o2;
 };
 
 // First slot of a sequence's chunks.  Packed sequences: floor(tok0 / 64) + seq leaves room
@@ -179,6 +180,13 @@ __device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32
       : "memory");
 }
 
+// The same in a loop, for kernels whose code must stay small.
+__device__ __forceinline__ void umma4_loop(uint32_t d, uint64_t a, uint32_t as, uint64_t b, uint32_t bs, uint32_t idesc,
+                                           uint32_t acc) {
+#pragma unroll 1
+  for (int s = 0; s < 4; ++s, a += as >> 4, b += bs >> 4, acc = 1u) umma_f16_warp(d, a, b, idesc, acc);
+}
+
 // A kernel of a call starts while the one before it still runs: before it touches what that
 // one wrote it waits for its end, and it lets the next one start once all its blocks have
 // started and taken their TMEM (a waiting block must not hold what a running one needs).
@@ -203,6 +211,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A lane's two rows of g or beta; zero past the end.
+__device__ __forceinline__ void load_gate(const float* x, const Params& p, long tok, int rows, int hv, int lane, float (&v)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) v[e] = 2 * lane + e < rows ? x[(tok + 2 * lane + e) * p.HV + hv] : 0.f;
+}
 // A sum kept as a float and what the float misses (the pair is good to about 2^-46).
 __device__ __forceinline__ void add_pairs(float& h, float& l, float h2, float l2) {
   const float s = h + h2, b = s - h, e = ((h - (s - b)) + (h2 - b)) + (l + l2);
@@ -210,12 +223,8 @@ __device__ __forceinline__ void add_pairs(float& h, float& l, float h2, float l2
   l = e - (h - s);
 }
 // gc of a chunk's rows 2 lane, 2 lane + 1 (one warp), in log2 units, as such pairs: decays
-// between neighbours stay exact after a steep drop.  g below -120 already is e^g = 0.  Rows
-// past the end have g = 0.
-__device__ __forceinline__ void gate_scan(const Params& p, long tok, int rows, int hv, int lane, float (&hi)[2],
-                                          float (&lo)[2]) {
-  const int i0 = 2 * lane;
-  float g0 = i0 < rows ? p.g[(tok + i0) * p.HV + hv] : 0.f, g1 = i0 + 1 < rows ? p.g[(tok + i0 + 1) * p.HV + hv] : 0.f;
+// between neighbours stay exact after a steep drop.  g below -120 already is e^g = 0.
+__device__ __forceinline__ void gate_scan(float g0, float g1, int lane, float (&hi)[2], float (&lo)[2]) {
   g0 = g0 < -120.f ? -120.f : g0;
   g1 = g1 < -120.f ? -120.f : g1;
   constexpr float kL = 1.44269502f, kLlow = 1.92596299e-8f;  // log2 e and its rest
@@ -232,6 +241,17 @@ __device__ __forceinline__ void gate_scan(const Params& p, long tok, int rows, i
   add_pairs(h, l, -h1, -l1);
   hi[0] = h;
   lo[0] = l;
+}
+
+inline int sm_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      return 152;
+    return v;
+  }();
+  return n;
 }
 
 // Launch a kernel, as a dependent of the stream's previous one where `after` says so; its
