@@ -415,6 +415,27 @@ __device__ __forceinline__ void tmem_ld_parts(uint32_t t, uint64_t (&x)[CPT / 2]
   for (int j = 0; j < CPT / 2; ++j) x[j] = add2(pack2f(a[2 * j], a[2 * j + 1]), pack2f(b[2 * j], b[2 * j + 1]));
 }
 
+// The sequence a chain takes: packed sequences start the longest first (by rank, ties by
+// index), for the grid to end together.  Any lengths, valid or not, give every rank once.
+constexpr int kRanked = 256;                              // more sequences than that come in their own order
+__device__ __forceinline__ int ranked_sequence(const Params& p, int rank, volatile uint32_t* slot) {
+  if (p.cu == nullptr || p.num_seqs == 1 || p.num_seqs > kRanked) return rank;
+  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
+    const unsigned len = static_cast<unsigned>(p.cu[s + 1]) - static_cast<unsigned>(p.cu[s]);
+    unsigned last = p.cu[0];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < p.num_seqs; ++j) {
+      const unsigned next = p.cu[j + 1], l = next - last;
+      before += l > len || (l == len && j < s);
+      last = next;
+    }
+    if (before == rank) *slot = s;
+  }
+  __syncthreads();
+  return static_cast<int>(*slot);
+}
+
 template <int K, int N, chain::Mode MODE>
 __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkParams& a, int V, int block, uint8_t* raw) {
   using L = chain::Lay<K, N, MODE>;
@@ -432,7 +453,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   const Params& p = a.p;
   const int slices = V / N;
   const int unit = block / slices, v0 = (block % slices) * N;
-  const int seq = unit / p.HV, hv = unit % p.HV, hk = hv / (p.HV / p.H);
+  const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long tok0;
   int len;

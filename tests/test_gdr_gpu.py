@@ -51,6 +51,26 @@ def test_forward(shape, io, state):
     check(S, S_ref, "state")
 
 
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("state", [False, True])
+def test_forward_more_chains_than_processors(K, V, state):
+    x = make([70, 0, 193, 1, 64], 8, 32, K, V, state=state, seed=21)
+    o, S = forward(x)
+    o_ref, S_ref = reference(x)
+    check(o, o_ref, "o")
+    check(S, S_ref, "state")
+
+
+@pytest.mark.parametrize("count", [200, 300])
+def test_forward_hundreds_of_sequences(count):
+    """Sequences start the longest first, up to a count; every one is done once either way."""
+    x = make([i * 7 % 5 if i % 50 else 90 for i in range(count)], 1, 1, 128, 128, state=True, seed=22)
+    o, S = forward(x)
+    o_ref, S_ref = reference(x)
+    check(o, o_ref, "o")
+    check(S, S_ref, "state")
+
+
 @pytest.mark.parametrize("gate", ["none", "strong", "cliff"])
 def test_forward_gates(gate):
     x = make((1, 300), 2, 4, 128, 128, gate=gate, seed=5)
