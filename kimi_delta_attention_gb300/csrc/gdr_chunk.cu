@@ -817,6 +817,326 @@ __global__ void __launch_bounds__(chain::threads(N), 1) gdr_chain_kernel(const _
   chain_body<K, N, chain::FORWARD>(maps, a, V, blockIdx.x, raw);
 }
 
+// ------------------------------------------------- chain, 128 columns wide ---
+// The same recurrence turned over, for calls with more (sequence, value head) pairs than
+// the SMs can take in slices: one CTA per pair, lane = value column, everything transposed:
+//   1. D1 = S^T [k; q]^T    M = 128 columns of S, N = 64 + 64 tokens, K = key dims
+//   2. D2 = Y^T [T; R]^T    N = 64 + 64 tokens, K = 64 tokens
+//   3. D3 = (E vn)^T k      N = key dims, K = 64
+// S, Y and E vn are the A operands and lie in TMEM (two bf16 parts, each a product of its own
+// that adds to the same accumulator), so a product reads only its B operand from shared
+// memory, nothing is staged there in parts, and all 16 warps run one and the same code in
+// all three steps (a thread: one column, 16 tokens or K / 4 key dims) -- against the
+// 64-column slices, whose two halves run different code.
+namespace wide {
+constexpr int NW = 16, THREADS = 32 * (NW + 3);
+constexpr uint32_t TS = 0, TD1 = 128, TD3 = TD1, TY = 256, TV = 320, TD2 = 384;   // TMEM columns: all 512
+template <int K>
+struct Lay {
+  static constexpr uint32_t FAC = (K / 64) * kTileBytes;          // a stage: [k; q], row factors, v (two boxes), [T; R]
+  static constexpr uint32_t VS = FAC + 1024;
+  static constexpr uint32_t TT = VS + 2 * 8192;
+  static constexpr uint32_t STAGE = TT + 2 * kTileBytes;
+  static constexpr uint32_t OUT = 2 * STAGE;                      // o: two boxes of 64 rows x 64
+  static constexpr uint32_t BAR = OUT + 2 * 8192;
+  static constexpr uint32_t SLACK = 832;
+  static constexpr uint32_t SMEM = BAR + 192 + SLACK;
+  static constexpr uint32_t TX = STAGE;
+  static_assert(SMEM <= 232448 && STAGE % 1024 == 0, "shared memory");
+};
+enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, D1, D1Q, D2, D2R, D3, SREADY, YREADY, VREADY, OUTREADY, OUTFREE, DRAIN, NBAR };
+
+// CNT values as the two parts of an A operand in TMEM (pairs: one column).
+template <int CNT>
+__device__ __forceinline__ void parts_to_tmem(uint32_t hi, uint32_t lo, const uint64_t (&x)[CNT / 2]) {
+  uint32_t h[CNT / 2], l[CNT / 2];
+#pragma unroll
+  for (int j = 0; j < CNT / 2; ++j) split2(x[j], h[j], l[j]);
+  if constexpr (CNT == 16) {
+    tmem_st8u(hi, h);
+    tmem_st8u(lo, l);
+  } else {
+    tmem_st16u(hi, h);
+    tmem_st16u(lo, l);
+  }
+  tmem_st_wait();
+}
+}  // namespace wide
+
+template <int K>
+__global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  using L = wide::Lay<K>;
+  using namespace wide;
+  constexpr int V = 128, DPT = K / 4;              // key dims of a thread's share of S
+  const uint32_t shift = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
+  uint8_t* sm = raw + shift;
+  if (shift > L::SLACK) {
+    if (threadIdx.x == 0) atomicOr(a.p.status, kStatusTimeout);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
+  volatile uint32_t* failed = tslot + 1;
+  const Params& p = a.p;
+  const int unit = blockIdx.x, hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long tok0;
+  int len;
+  const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
+  const int nch = num_chunks(len), slot0 = first_slot(a, seq, tok0);
+  if (tid == 0) {
+    for (int b = 0; b < NBAR; ++b) mbar_init(&bars[b], b >= SREADY && b <= OUTREADY ? NW : 1);
+    *failed = 0u;
+    fence_mbar_init();
+  }
+  if (warp == NW) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  wait_for_previous_kernel();  // the records, the cleared status
+  let_next_kernel_start();
+  if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
+  auto wait = [&](int b, uint32_t parity) {        // of a whole warp; false once the CTA has failed
+    if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
+    if (lane == 0 && *failed == 0u) {
+      atomicOr(p.status, kStatusTimeout);
+      *failed = 1u;
+    }
+    return false;
+  };
+  auto arrive = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[b]);
+  };
+
+  if (warp == NW + 1) {
+    // ---------------------------------------------------------------- loads ---
+    auto load = [&](int n) {
+      if (lane == 0) {
+        uint8_t* st = sm + (n & 1) * L::STAGE;
+        uint64_t* full = &bars[FULL0 + (n & 1)];
+        const int tok = static_cast<int>(tok0 + C * static_cast<long>(n));
+        const uint8_t* rec = a.rec + (static_cast<size_t>(slot0 + n) * p.HV + hv) * kRecBytes;
+        mbar_arrive_expect_tx_relaxed(full, L::TX);
+#pragma unroll
+        for (int b = 0; b < K / 64; ++b) {
+          tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
+          tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
+        }
+        bulk_load(st + L::FAC, rec + kRecFactors, 1024, full);
+        tma_load_3d(st + L::VS, &maps.v, full, 0, hv, tok);
+        tma_load_3d(st + L::VS + 8192, &maps.v, full, 64, hv, tok);
+        bulk_load(st + L::TT, rec, 2 * kTileBytes, full);
+      }
+      __syncwarp();
+    };
+    int nf = 0;
+    for (; nf < 2 && nf < nch; ++nf) load(nf);
+    for (int n = 1; n < nch && nf < nch; ++n) {    // a stage's readers are done once the next chunk's products start
+      if (!wait(EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+      load(nf++);
+    }
+    for (int m = nf < 2 ? 0 : nf - 2; m < nf; ++m) mbar_wait(&bars[FULL0 + (m & 1)], (m >> 1) & 1, kDrainNs);
+  } else if (warp == NW) {
+    // ------------------------------------------------------------- products ---
+    const uint32_t sb = smem_u32(sm);
+    constexpr uint32_t id64 = idesc_f16kind(128, 64), idk = idesc_f16kind(128, K) | IDESC_B_MN_MAJOR;
+    constexpr uint32_t row[4] = {0, 2, 4, 6}, col[4] = {0, 128, 256, 384};   // 16 of K, in 16 bytes
+    auto s_times = [&](uint32_t d, uint64_t b) {   // both parts of S^T times 64 rows of [k; q]
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int kb = 0; kb < K / 64; ++kb)
+          umma_ts_chain<4>(d, tmem + TS + h * (K / 2) + 32 * kb, b + (kb * kTileBytes >> 4), row, id64, h + kb > 0);
+    };
+    auto y_times = [&](uint32_t d, uint64_t b) {   // Y^T times 64 rows of [T; R]: high high, high low, low high
+      umma_ts_chain<4>(d, tmem + TY, b, row, id64, 0u);
+      umma_ts_chain<4>(d, tmem + TY, b + (kTileBytes >> 4), row, id64, 1u);
+      umma_ts_chain<4>(d, tmem + TY + 32, b, row, id64, 1u);
+    };
+    for (int n = 0; n < nch; ++n) {
+      const uint32_t ph = n & 1, st = sb + ph * L::STAGE;
+      const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2), dt = sdesc_sw128(st + L::TT);
+      if (!wait(FULL0 + (n & 1), (n >> 1) & 1)) break;
+      if (!wait(SREADY, ph)) break;
+      tc_fence_after();
+      s_times(tmem + TD1, dkq);
+      umma_commit_warp(&bars[D1]);
+      if (n > 0 && lane == 0) mbar_arrive(&bars[EMPTY0 + ((n - 1) & 1)]);
+      __syncwarp();
+      s_times(tmem + TD1 + 64, dkq + (8192 >> 4));
+      umma_commit_warp(&bars[D1Q]);
+      if (!wait(YREADY, ph)) break;
+      tc_fence_after();
+      y_times(tmem + TD2, dt);
+      umma_commit_warp(&bars[D2]);
+      y_times(tmem + TD2 + 64, dt + (8192 >> 4));
+      umma_commit_warp(&bars[D2R]);
+      if (!wait(VREADY, ph)) break;
+      tc_fence_after();
+      umma_ts_chain<4>(tmem + TD3, tmem + TV, dkt, col, idk, 0u);
+      umma_ts_chain<4>(tmem + TD3, tmem + TV + 32, dkt, col, idk, 1u);
+      umma_commit_warp(&bars[D3]);
+    }
+    umma_commit_warp(&bars[DRAIN]);                // what is in flight ends before the CTA gives up its memory
+    mbar_wait(&bars[DRAIN], 0, kDrainNs);
+  } else if (warp == NW + 2) {
+    // --------------------------------------------------------------- stores ---
+    for (int n = 0; n < nch; ++n) {
+      if (!wait(OUTREADY, n & 1)) break;
+      if (lane == 0) {
+        if (C * n + C <= len) {
+          const int tok = static_cast<int>(tok0 + C * static_cast<long>(n));
+          tma_store_3d(&maps.o, sm + L::OUT, 0, hv, tok);
+          tma_store_3d(&maps.o, sm + L::OUT + 8192, 64, hv, tok);
+          bulk_commit();
+        }
+        bulk_wait_read();
+        mbar_arrive(&bars[OUTFREE]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_read();
+  } else {
+    // ------------------------------------------ state, Y, vn, output ---
+    const int quad = warp & 3, grp = warp >> 2, t0 = 16 * grp, d0 = DPT * grp;
+    const int col = 32 * quad + lane;              // TMEM lane: value column
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    const uint32_t ts = tl + TS + d0 / 2, ty = tl + TY + t0 / 2, tv = tl + TV + t0 / 2;
+    // element (token t0 + j, column) of a 64-token tile of two boxes
+    const uint32_t toff = (col >> 6) * 8192 + t0 * 128 + (col & 7) * 2, tch = ((col & 63) >> 3) << 4;
+    const auto at = [&](int j) { return toff + j * 128 + (tch ^ ((j & 7) << 4)); };
+    const size_t soff = ((static_cast<size_t>(seq) * p.HV + hv) * K + d0) * V + col;
+    uint64_t s[DPT / 2];
+#pragma unroll
+    for (int j = 0; j < DPT / 2; ++j)
+      s[j] = p.s0 ? pack2f(p.s0[soff + 2 * j * V], p.s0[soff + (2 * j + 1) * V]) : 0ull;
+    parts_to_tmem<DPT>(ts, ts + K / 2, s);
+    tc_fence_before();
+    arrive(SREADY);
+    const uint64_t scale = pack2f(p.scale, p.scale);
+    bool good = true;
+    for (int n = 0; n < nch; ++n) {
+      const uint32_t ph = n & 1;
+      uint8_t* st = sm + ph * L::STAGE;
+      const float* fac = reinterpret_cast<const float*>(st + L::FAC);
+      const int rows = len - C * n;                // of the chunk, from the first; 64 and more: all
+      if (!(good = wait(FULL0 + (n & 1), (n >> 1) & 1))) break;
+      if (tid == 0 && fac[kRecFailed] != 0.f) atomicOr(p.status, kStatusTimeout);
+      uint64_t y[8], o[8];
+      float x[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {                // v, whatever rows past the end hold
+        const uint32_t u = *reinterpret_cast<const uint16_t*>(st + L::VS + at(2 * j));
+        const uint32_t w = *reinterpret_cast<const uint16_t*>(st + L::VS + at(2 * j + 1));
+        y[j] = pack2f(__uint_as_float(u << 16), __uint_as_float(w << 16));
+      }
+      if (!(good = wait(D1, ph))) break;
+      tc_fence_after();
+      tmem_ld16(tl + TD1 + t0, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {                // beta (v - G k S)
+        const float2 g = *reinterpret_cast<const float2*>(fac + t0 + 2 * j), be = *reinterpret_cast<const float2*>(fac + 128 + t0 + 2 * j);
+        float v0, v1;
+        unpack2f(y[j], v0, v1);
+        y[j] = mul2(pack2f(be.x, be.y), pack2f(fmaf(-g.x, x[2 * j], v0), fmaf(-g.y, x[2 * j + 1], v1)));
+      }
+      if (rows < C) {                              // rows past the end: zero wherever a sum over tokens meets them
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float v0, v1;
+          unpack2f(y[j], v0, v1);
+          y[j] = pack2f(t0 + 2 * j < rows ? v0 : 0.f, t0 + 2 * j + 1 < rows ? v1 : 0.f);
+        }
+        if (tid < C && tid >= rows) {
+#pragma unroll 1
+          for (int ch = 0; ch < 8 * (K / 64); ++ch)
+            *reinterpret_cast<uint4*>(st + (ch >> 3) * kTileBytes + sw128(tid, ch & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      parts_to_tmem<16>(ty, ty + 32, y);
+      tc_fence_before();
+      arrive(YREADY);
+      if (!(good = wait(D1Q, ph))) break;          // while step 2 runs: scale G q S
+      tc_fence_after();
+      tmem_ld16(tl + TD1 + 64 + t0, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 g = *reinterpret_cast<const float2*>(fac + t0 + 2 * j);
+        o[j] = mul2(scale, mul2(pack2f(g.x, g.y), pack2f(x[2 * j], x[2 * j + 1])));
+      }
+      if (!(good = wait(D2, ph))) break;
+      tc_fence_after();
+      tmem_ld16(tl + TD2 + t0, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 e = *reinterpret_cast<const float2*>(fac + 64 + t0 + 2 * j);
+        y[j] = mul2(pack2f(e.x, e.y), pack2f(x[2 * j], x[2 * j + 1]));
+      }
+      parts_to_tmem<16>(tv, tv + 32, y);
+      tc_fence_before();
+      arrive(VREADY);
+      if (!(good = wait(D2R, ph))) break;          // while step 3 runs: the output
+      tc_fence_after();
+      tmem_ld16(tl + TD2 + 64 + t0, x);
+      tmem_ld_wait();
+      if (n > 0 && !(good = wait(OUTFREE, (n - 1) & 1))) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t u = pack_pair(add2(o[j], pack2f(x[2 * j], x[2 * j + 1])));
+        if (rows >= C) {
+          *reinterpret_cast<uint16_t*>(sm + L::OUT + at(2 * j)) = static_cast<uint16_t>(u);
+          *reinterpret_cast<uint16_t*>(sm + L::OUT + at(2 * j + 1)) = static_cast<uint16_t>(u >> 16);
+        } else {
+          uint16_t* op = static_cast<uint16_t*>(p.out) +
+                         (static_cast<size_t>(tok0 + C * static_cast<long>(n) + t0 + 2 * j) * p.HV + hv) * V + col;
+          if (t0 + 2 * j < rows) op[0] = static_cast<uint16_t>(u);
+          if (t0 + 2 * j + 1 < rows) op[static_cast<size_t>(p.HV) * V] = static_cast<uint16_t>(u >> 16);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive(OUTREADY);
+      const float gm = fac[kRecGamma];
+      const uint64_t gamma = pack2f(gm, gm);
+      if (!(good = wait(D3, ph))) break;
+      tc_fence_after();
+      float z[DPT];
+      tmem_ld<DPT>(tl + TD3 + d0, z);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < DPT / 2; ++j) s[j] = fma2(gamma, s[j], pack2f(z[2 * j], z[2 * j + 1]));
+      parts_to_tmem<DPT>(ts, ts + K / 2, s);
+      tc_fence_before();
+      arrive(SREADY);
+    }
+    if (good && p.sfin) {
+#pragma unroll
+      for (int j = 0; j < DPT / 2; ++j) {
+        float u, w;
+        unpack2f(s[j], u, w);
+        p.sfin[soff + 2 * j * V] = u;
+        p.sfin[soff + (2 * j + 1) * V] = w;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == NW) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // The backward's two chains in one launch: even blocks SAVE (maps: v), odd blocks REVERSE
 // (maps_r: d_out).  They share nothing but the records, so they run side by side.
 template <int K>
@@ -869,6 +1189,13 @@ cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cud
 }
 
 template <int K>
+cudaError_t launch_wide(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
+  static LaunchState state;
+  return launch_kernel(state, gdr_wide_kernel<K>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV, wide::THREADS, wide::Lay<K>::SMEM,
+                       true, st, maps, a);
+}
+
+template <int K>
 cudaError_t launch_chains(const ChainMaps& maps, const ChainMaps& maps_r, const ChunkParams& a, int V, cudaStream_t st) {
   constexpr uint32_t bytes = chain::Lay<K, 64, chain::REVERSE>::SMEM;   // the larger of the two
   static_assert(bytes >= chain::Lay<K, 64, chain::SAVE>::SMEM, "shared memory of the two chains");
@@ -908,6 +1235,7 @@ cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long w
     return cudaErrorInvalidValue;
   cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
   if (e != cudaSuccess) return e;
+  if (N == 64 && V == 128) return K == 128 ? launch_wide<128>(maps, a, st) : launch_wide<64>(maps, a, st);
   if (K == 128) return N == 32 ? launch_chain<128, 32>(maps, a, V, st) : launch_chain<128, 64>(maps, a, V, st);
   return N == 32 ? launch_chain<64, 32>(maps, a, V, st) : launch_chain<64, 64>(maps, a, V, st);
 }
