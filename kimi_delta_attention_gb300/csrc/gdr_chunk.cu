@@ -11,26 +11,27 @@ namespace {
 
 // ------------------------------------------------------------ preparation ---
 // One CTA of 128 threads per (chunk, value head).  [k; q] k^T is one product of M = 128
-// (rows 0-63: k, 64-127: q), read back a row a thread into M and P (fp32, shared memory).
-// Then X (I + M) = [I; P] for the 128 rows X = [T; R], R = P T, in 16-column blocks from the
-// last to the first:
-//     X_J = ([I; P]_J - sum over L > J of X_L M_LJ) T_JJ
-// with T_JJ, the inverse of the diagonal block, by substitution (a row a thread), and the
-// block products on warp-level TF32 tensor instructions, each operand in two TF32 parts
-// (2^-20).  A row block of 16 needs no other: a warp walks its row blocks alone.
-// What bounds it is instruction fetch: written out straight (the solves unrolled into
-// registers), the code ran once per CTA at an instruction a cycle and SM, 47 us for 2048
-// chunks and heads by plain substitution, 87 us with these same block products unrolled.
-// So the block product is one small loop body and its operands stay in shared memory.
+// (rows 0-63: k, 64-127: q), read back a row a thread: M to shared memory in fp32, P as an
+// operand in two bf16 parts.  T = (I + M)^-1 in blocks of 16: the diagonal ones by
+// substitution (a row a thread), the others by
+//     [A 0; B D]^-1 = [A^-1 0; -D^-1 B A^-1  D^-1],
+// first within the 32-row halves, then between them: 16 block products of a depth of 6, on
+// warp-level TF32 tensor instructions, each operand in two TF32 parts (2^-20).  R = P T is a
+// product of tcgen05 again (P's and T's parts: high high, high low, low high; on blocks of 16
+// it took 20 more block products).
+// What bounds it is instruction fetch and issue: written out straight (the solves unrolled
+// into registers), the code ran once per CTA at an instruction a cycle and SM, 47 us for 2048
+// chunks and heads by plain substitution, 87 us with block products unrolled; so the block
+// product is one small loop body and its operands stay in shared memory.
 namespace prep {
 constexpr int NT = 128;
-constexpr uint32_t LDM = 68;                           // floats between rows of M, P and X: no bank conflicts
-// [k; q] tiles at 0; then X (128 rows, rows 64-127 start as P) over them; then the record's image
-constexpr uint32_t OFF_M = 128 * LDM * 4;
+constexpr uint32_t LDM = 68;                           // floats between rows of M and T: no bank conflicts
+// [k; q] tiles at 0, then the record's image over them (T in rows 0-63; in 64-127 first P, then R)
+constexpr uint32_t OFF_M = kRecBytes;
 constexpr uint32_t OFF_GC = OFF_M + C * LDM * 4;       // gc high parts, low parts (log2), beta, block factors
 constexpr uint32_t OFF_BAR = OFF_GC + 4 * C * 4;
 constexpr uint32_t SMEM = OFF_BAR + 64 + 1024;
-static_assert(OFF_M >= kRecBytes && OFF_M >= 2 * kTileBytes, "the record's image and the tiles fit");
+static_assert(OFF_M >= 2 * kTileBytes, "the tiles fit");
 
 // Two TF32 parts by truncation (the low 13 bits cleared).
 __device__ __forceinline__ void tf32_parts(float x, uint32_t& h, uint32_t& l) {
@@ -71,20 +72,27 @@ __device__ __forceinline__ void block_mma(float (&acc)[2][4], const float* x, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] += cross[n][e];
 }
+__device__ __forceinline__ void block_put(float* x, const float (&acc)[2][4], float f, int lane) {
+  x += (lane >> 2) * LDM + 2 * (lane & 3);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    *reinterpret_cast<float2*>(x + 8 * n) = make_float2(f * acc[n][0], f * acc[n][1]);
+    *reinterpret_cast<float2*>(x + 8 * n + 8 * LDM) = make_float2(f * acc[n][2], f * acc[n][3]);
+  }
+}
 }  // namespace prep
 
 template <int K>
 __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  float* xs = reinterpret_cast<float*>(sm);
   float* ms = reinterpret_cast<float*>(sm + prep::OFF_M);
   float* gh = reinterpret_cast<float*>(sm + prep::OFF_GC);
   float* gl = gh + C;
   float* bs = gl + C;
   float* cf = bs + C;                             // e^{gc of the 16-block's last row - gc_j}
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + prep::OFF_BAR);  // [0]: tiles; [1]: product
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 2);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + prep::OFF_BAR);  // [0]: tiles; [1], [2]: products
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 3);
   const Params& p = a.p;
   const int slot = blockIdx.x / p.HV, hv = blockIdx.x % p.HV, hk = hv / (p.HV / p.H);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -97,6 +105,7 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
     if (lane == 0) {
       mbar_init(&bar[0], 1);
       mbar_init(&bar[1], 1);
+      mbar_init(&bar[2], 1);
       fence_mbar_init();
       mbar_arrive_expect_tx_relaxed(&bar[0], (K / 64) * kTileBytes);
 #pragma unroll
@@ -158,7 +167,6 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
     const uint32_t t = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const float f = i < rows ? (isq ? p.scale : be) : 0.f;   // rows past the sequence's end: M = P = 0
     const int last = isq ? i : i - 1, own = i >> 4;          // columns 0 .. last of the row are not zero
-    float* dst = (isq ? xs + C * prep::LDM : ms) + i * prep::LDM;  // P over the tiles
     const int blocks = 2 + 2 * (warp & 1);                   // (rows 0-31 end in column 31)
 #pragma unroll 1
     for (int b = 0; b < blocks; ++b) {
@@ -178,109 +186,109 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 16; ++j) y[j] = i < rows ? y[j] * (fb * cf[16 * b + j]) : 0.f;
       }
+      if (isq) {                                             // P over the tiles, as an operand
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint4 h, l;
+          split8(y + 8 * c, h, l);
+          *reinterpret_cast<uint4*>(sm + sw128(tid, 2 * b + c)) = h;
+          *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, 2 * b + c)) = l;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(ms + i * prep::LDM + 16 * b + 4 * j) =
+              make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+      }
+    }
+    if (warp == 2) {                                         // (the rest of P's rows 0-31)
+#pragma unroll
+      for (int c = 4; c < 8; ++c) {
+        *reinterpret_cast<uint4*>(sm + sw128(tid, c)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, c)) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  if (warp < 2) {                                  // rows 32 warp ..: a half of I + M, of one warp alone
+    __syncwarp();
+    {                                              // row i of its diagonal block inverted, in the block's place
+      const int rr = tid & 15;
+      float* mb = ms + (tid & ~15) * (prep::LDM + 1);
+      float x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = j == rr ? 1.f : 0.f;
+#pragma unroll
+      for (int l = 15; l >= 1; --l)
+#pragma unroll
+        for (int j = 0; 4 * j < l; ++j) {
+          const float4 r = *reinterpret_cast<const float4*>(mb + l * prep::LDM + 4 * j);
+          x[4 * j] = fmaf(-x[l], r.x, x[4 * j]);
+          if (4 * j + 1 < l) x[4 * j + 1] = fmaf(-x[l], r.y, x[4 * j + 1]);
+          if (4 * j + 2 < l) x[4 * j + 2] = fmaf(-x[l], r.z, x[4 * j + 2]);
+          if (4 * j + 3 < l) x[4 * j + 3] = fmaf(-x[l], r.w, x[4 * j + 3]);
+        }
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4*>(dst + 16 * b + 4 * j) = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+        *reinterpret_cast<float4*>(mb + rr * prep::LDM + 4 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      __syncwarp();
+    }
+    float* ha = ms + 32 * warp * (prep::LDM + 1);  // [A 0; B D] of 16-row blocks: B A^-1, then -D^-1 of it
+    float* hb = ha + 16 * prep::LDM;
+#pragma unroll 1
+    for (int n = 0; n < 2; ++n) {
+      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      prep::block_mma(acc, n ? hb + 16 : hb, prep::LDM, n ? hb : ha, prep::LDM, lane);
+      __syncwarp();
+      prep::block_put(hb, acc, n ? -1.f : 1.f, lane);
+      __syncwarp();
     }
   }
   tc_fence_before();
-  __syncthreads();  // M and P are in shared memory, the accumulator is read
-  if (warp == 0) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 64);
-  }
-  if (warp < 2) {   // T_JJ: row i of its block of I + M inverted, in the block's place
-    const int rr = tid & 15;
-    float* mb = ms + (tid & ~15) * prep::LDM + (tid & ~15);
-    float x[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = j == rr ? 1.f : 0.f;
-#pragma unroll
-    for (int l = 15; l >= 1; --l)
-#pragma unroll
-      for (int j = 0; 4 * j < l; ++j) {
-        const float4 r = *reinterpret_cast<const float4*>(mb + l * prep::LDM + 4 * j);
-        x[4 * j] = fmaf(-x[l], r.x, x[4 * j]);
-        if (4 * j + 1 < l) x[4 * j + 1] = fmaf(-x[l], r.y, x[4 * j + 1]);
-        if (4 * j + 2 < l) x[4 * j + 2] = fmaf(-x[l], r.z, x[4 * j + 2]);
-        if (4 * j + 3 < l) x[4 * j + 3] = fmaf(-x[l], r.w, x[4 * j + 3]);
-      }
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(mb + rr * prep::LDM + 4 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-  }
-  __syncthreads();
-  // row blocks (0-3 of T, 4-7 of R), shared out so that every warp has 8 to 10 of the 37
-  // block products
-  {
-    const int turn = (warp + blockIdx.x) & 3, g = lane >> 2, t = lane & 3;
-    uint32_t tasks = turn == 0 ? 0x7u : turn == 1 ? 0x03u : turn == 2 ? 0x56u : 0x412u;
-    const int count = turn == 0 ? 1 : turn == 3 ? 3 : 2;
+  __syncthreads();  // the halves are done, P is written, the accumulator is read
+  {                 // the same between the halves, a block a warp; B A^-1 in the unused upper right
+    const int I = warp >> 1, J = warp & 1;
+    float* upper = ms + 32;
 #pragma unroll 1
-    for (int q = 0; q < count; ++q, tasks >>= 4) {
-      const int rb = tasks & 7, I = rb & 3;
-      float* xr = xs + 16 * rb * prep::LDM;
+    for (int n = 0; n < 2; ++n) {
+      const float* x = ms + (32 + 16 * I) * prep::LDM + (n ? 32 : 0);
+      const float* y = (n ? upper : ms) + 16 * J;
+      const int from = n ? 0 : J, to = n ? I : 1;
+      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 1
-      for (int J = I; J >= 0; --J) {
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 1
-        for (int L = I; L > J; --L)
-          prep::block_mma(acc, xr + 16 * L, prep::LDM, ms + 16 * L * prep::LDM + 16 * J, prep::LDM, lane);
-        float* xj = xr + 16 * J + g * prep::LDM + 2 * t;
-        const float* tb = ms + 16 * J * (prep::LDM + 1);
-        if (rb < 4 && J == I) {                    // T's diagonal block
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            *reinterpret_cast<float2*>(xj + 8 * n) = *reinterpret_cast<const float2*>(tb + g * prep::LDM + 8 * n + 2 * t);
-            *reinterpret_cast<float2*>(xj + 8 * n + 8 * prep::LDM) =
-                *reinterpret_cast<const float2*>(tb + (g + 8) * prep::LDM + 8 * n + 2 * t);
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float2 u = make_float2(0.f, 0.f), w = u;
-            if (rb >= 4) {
-              u = *reinterpret_cast<const float2*>(xj + 8 * n);
-              w = *reinterpret_cast<const float2*>(xj + 8 * n + 8 * prep::LDM);
-            }
-            *reinterpret_cast<float2*>(xj + 8 * n) = make_float2(u.x - acc[n][0], u.y - acc[n][1]);
-            *reinterpret_cast<float2*>(xj + 8 * n + 8 * prep::LDM) = make_float2(w.x - acc[n][2], w.y - acc[n][3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-          }
-          __syncwarp();
-          prep::block_mma(acc, xr + 16 * J, prep::LDM, tb, prep::LDM, lane);
-          __syncwarp();
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            *reinterpret_cast<float2*>(xj + 8 * n) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2*>(xj + 8 * n + 8 * prep::LDM) = make_float2(acc[n][2], acc[n][3]);
-          }
-        }
-        __syncwarp();
-      }
+      for (int l = from; l <= to; ++l) prep::block_mma(acc, x + 16 * l, prep::LDM, y + 16 * l * prep::LDM, prep::LDM, lane);
+      prep::block_put(n ? ms + (32 + 16 * I) * prep::LDM + 16 * J : upper + 16 * I * prep::LDM + 16 * J, acc, n ? -1.f : 1.f, lane);
+      __syncthreads();
     }
   }
-  __syncthreads();
-  // rows of X to the record's image, over them
-  {
-    float y[C];
-    const int own = i >> 4;                        // columns past the row's own block are zero
+  {                 // T to the record's image, half a row a thread
+    const int own = i >> 4, half = tid >> 6;       // columns past the row's own block are zero
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float4 u = (j >> 2) <= own ? *reinterpret_cast<const float4*>(xs + tid * prep::LDM + 4 * j)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-      y[4 * j] = u.x; y[4 * j + 1] = u.y; y[4 * j + 2] = u.z; y[4 * j + 3] = u.w;
-    }
-    __syncthreads();
+    for (int c = 0; c < 4; ++c) {
+      const int ch = 4 * half + c;
+      float y[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+      for (int j = 0; j < 2; ++j) {
+        const float4 u = (ch >> 1) <= own ? *reinterpret_cast<const float4*>(ms + i * prep::LDM + 8 * ch + 4 * j)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        y[4 * j] = u.x; y[4 * j + 1] = u.y; y[4 * j + 2] = u.z; y[4 * j + 3] = u.w;
+      }
       uint4 h, l;
-      split8(y + 8 * c, h, l);
-      *reinterpret_cast<uint4*>(sm + sw128(tid, c)) = h;
-      *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, c)) = l;
+      split8(y, h, l);
+      *reinterpret_cast<uint4*>(sm + sw128(i, ch)) = h;
+      *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(i, ch)) = l;
     }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (warp == 0) {  // R = P T in lanes 64-127 (0-63: T's rows times T, read by nobody)
+    tc_fence_after();
+    const uint64_t dp = sdesc_sw128(smem_u32(sm)), dt = sdesc(smem_u32(sm), kTileBytes, 1024, 2);
+    constexpr uint32_t id = idesc_f16kind(128, 64) | IDESC_B_MN_MAJOR;
+#pragma unroll 1
+    for (int n = 0; n < 3; ++n)
+      umma4<32, 2048>(tmem, dp + (n == 2 ? kTileBytes >> 4 : 0u), dt + (n == 1 ? kTileBytes >> 4 : 0u), id, n > 0);
+    umma_commit_warp(&bar[2]);
   }
   float* fac = reinterpret_cast<float*>(sm + kRecFactors);
   if (!isq) {
@@ -289,7 +297,32 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
     fac[128 + i] = be;
     if (i == 63) fac[kRecGamma] = ex2(hi);
   }
+  if (!mbar_wait(&bar[2], 0, a.wait_ns)) {
+    ok = false;
+    mbar_wait(&bar[2], 0, kDrainNs);
+  }
+  tc_fence_after();
+  if (isq) {
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      float y[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + 32 * b, y);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint4 h, l;
+        split8(y + 8 * c, h, l);
+        *reinterpret_cast<uint4*>(sm + sw128(tid, 4 * b + c)) = h;
+        *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, 4 * b + c)) = l;
+      }
+    }
+  }
+  tc_fence_before();
   ok = __syncthreads_and(ok);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
   if (tid == 0) fac[kRecFailed] = ok ? 0.f : 1.f;
   fence_proxy_async_smem();
   __syncthreads();
@@ -818,35 +851,75 @@ __global__ void __launch_bounds__(chain::threads(N), 1) gdr_chain_kernel(const _
 }
 
 // ------------------------------------------------- chain, 128 columns wide ---
-// The same recurrence turned over, for calls with more (sequence, value head) pairs than
-// the SMs can take in slices: one CTA per pair, lane = value column, everything transposed:
+// The same recurrence turned over, for V = 128 where the slices of 32 columns do not fit the
+// SMs at once, and in the backward: one CTA per pair, lane = value column, all transposed:
 //   1. D1 = S^T [k; q]^T    M = 128 columns of S, N = 64 + 64 tokens, K = key dims
 //   2. D2 = Y^T [T; R]^T    N = 64 + 64 tokens, K = 64 tokens
 //   3. D3 = (E vn)^T k      N = key dims, K = 64
 // S, Y and E vn are the A operands and lie in TMEM (two bf16 parts, each a product of its own
 // that adds to the same accumulator), so a product reads only its B operand from shared
 // memory, nothing is staged there in parts, and all 16 warps run one and the same code in
-// all three steps (a thread: one column, 16 tokens or K / 4 key dims) -- against the
+// all three steps (a warp: 32 columns, 16 tokens or K / 4 key dims) -- against the
 // 64-column slices, whose two halves run different code.
+//
+// SAVE leaves out the q and R halves.  REVERSE:
+//   1. D1 = dS'^T k^T
+//   2. D2 = do^T R (do from shared memory as it is; it does not wait for step 1) + (E D1)^T T
+//   3. D3 = (scale G do)^T q (issued with step 2's) - (G beta z)^T k
 namespace wide {
 constexpr int NW = 16, THREADS = 32 * (NW + 3);
-constexpr uint32_t TS = 0, TD1 = 128, TD3 = TD1, TY = 256, TV = 320, TD2 = 384;   // TMEM columns: all 512
-template <int K>
+using chain::Mode;
+template <int K, Mode MODE>
 struct Lay {
+  static constexpr bool BWD = MODE != chain::FORWARD;
+  // TMEM columns, all 512.  FORWARD: D1 has a q half, D3 lies over D1; REVERSE: z's operand over Y's
+  static constexpr uint32_t TS = 0, TD1 = 128, TY = 256, TV = MODE == chain::REVERSE ? TY : 320, TW = 320,
+                            TD2 = BWD ? 192 : 384, TD3 = BWD ? 384 : TD1;
   static constexpr uint32_t FAC = (K / 64) * kTileBytes;          // a stage: [k; q], row factors, v (two boxes), [T; R]
   static constexpr uint32_t VS = FAC + 1024;
   static constexpr uint32_t TT = VS + 2 * 8192;
-  static constexpr uint32_t STAGE = TT + 2 * kTileBytes;
-  static constexpr uint32_t OUT = 2 * STAGE;                      // o: two boxes of 64 rows x 64
-  static constexpr uint32_t BAR = OUT + 2 * 8192;
+  static constexpr uint32_t STAGE = BWD ? TT : TT + 2 * kTileBytes;  // (the others keep one buffer of [T; R])
+  static constexpr uint32_t TT1 = 2 * STAGE;
+  static constexpr uint32_t OUT = TT1 + (BWD ? 2 * kTileBytes : 0);  // o: two boxes of 64 rows x 64; or vn (z) in two parts
+  static constexpr uint32_t SF = OUT + (BWD ? 4 : 2) * 8192;         // S (dS') in fp32
+  static constexpr uint32_t BAR = SF + (BWD ? K * 512 : 0);
   static constexpr uint32_t SLACK = 832;
   static constexpr uint32_t SMEM = BAR + 192 + SLACK;
-  static constexpr uint32_t TX = STAGE;
+  static constexpr uint32_t TX = (MODE == chain::SAVE ? (K / 64) * 8192 : (K / 64) * kTileBytes) + 1024 + 2 * 8192 +
+                                 (BWD ? 0 : 2 * kTileBytes);
   static_assert(SMEM <= 232448 && STAGE % 1024 == 0, "shared memory");
 };
-enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, D1, D1Q, D2, D2R, D3, SREADY, YREADY, VREADY, OUTREADY, OUTFREE, DRAIN, NBAR };
+enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, TFULL, TFREE, D1, D1Q, D2, D2R, D3, SREADY, YREADY, VREADY, QREADY, SFREADY, OUTREADY,
+       SFFREE, OUTFREE, DRAIN, NBAR };
+static_assert(NBAR * 8 + 12 <= 192, "barriers, the TMEM address, the failure flag, the sequence");
 
-// CNT values as the two parts of an A operand in TMEM (pairs: one column).
+// A thread's 16 values of a [32 columns, 16 tokens] block, in pairs of neighbouring tokens: pair
+// 4 h + 2 m + r is column 16 h + 8 r + lane / 4, tokens 8 m + 2 (lane % 4) and one on -- the
+// fragments of the 16-lane TMEM accesses and of transposed 8 x 8 tiles in shared memory.  With
+// a column a thread instead, v and o took 16 16-bit accesses a thread and the row factors 8
+// each (here 2).
+__device__ __forceinline__ void block_ld(uint32_t t, uint64_t (&x)[8]) {
+  float u[16];
+  tmem_ld_16x256b_x2(t, u);
+  tmem_ld_16x256b_x2(t + (16u << 16), u + 8);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = pack2f(u[2 * j], u[2 * j + 1]);
+}
+// ... as the two parts of an A operand, the low part's columns 32 on
+__device__ __forceinline__ void block_parts(uint32_t t, const uint64_t (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split2(x[4 * h + j], a[j], b[j]);
+    tmem_st_16x128b_x2(t + (static_cast<uint32_t>(16 * h) << 16), a[0], a[1], a[2], a[3]);
+    tmem_st_16x128b_x2(t + (static_cast<uint32_t>(16 * h) << 16) + 32, b[0], b[1], b[2], b[3]);
+  }
+  tmem_st_wait();
+}
+
+// CNT values of a lane as the two parts of an A operand in TMEM (pairs: one column).
 template <int CNT>
 __device__ __forceinline__ void parts_to_tmem(uint32_t hi, uint32_t lo, const uint64_t (&x)[CNT / 2]) {
   uint32_t h[CNT / 2], l[CNT / 2];
@@ -863,12 +936,12 @@ __device__ __forceinline__ void parts_to_tmem(uint32_t hi, uint32_t lo, const ui
 }
 }  // namespace wide
 
-template <int K>
-__global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  using L = wide::Lay<K>;
+template <int K, chain::Mode MODE>
+__device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkParams& a, int unit, uint8_t* raw) {
+  using L = wide::Lay<K, MODE>;
   using namespace wide;
-  constexpr int V = 128, DPT = K / 4;              // key dims of a thread's share of S
+  using namespace chain;
+  constexpr int NW = wide::NW, V = 128, DPT = K / 4;   // DPT: key dims of a thread's share of S
   const uint32_t shift = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
   uint8_t* sm = raw + shift;
   if (shift > L::SLACK) {
@@ -876,17 +949,18 @@ __global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + wide::NBAR);
   volatile uint32_t* failed = tslot + 1;
   const Params& p = a.p;
-  const int unit = blockIdx.x, hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
+  const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long tok0;
   int len;
   const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
   const int nch = num_chunks(len), slot0 = first_slot(a, seq, tok0);
+  const auto chunk = [&](int n) { return MODE == REVERSE ? nch - 1 - n : n; };  // of step n
   if (tid == 0) {
-    for (int b = 0; b < NBAR; ++b) mbar_init(&bars[b], b >= SREADY && b <= OUTREADY ? NW : 1);
+    for (int b = 0; b < wide::NBAR; ++b) mbar_init(&bars[b], b >= wide::SREADY && b <= wide::OUTREADY ? NW : 1);
     *failed = 0u;
     fence_mbar_init();
   }
@@ -916,32 +990,49 @@ __global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid
 
   if (warp == NW + 1) {
     // ---------------------------------------------------------------- loads ---
+    auto record = [&](int n) { return a.rec + (static_cast<size_t>(slot0 + chunk(n)) * p.HV + hv) * kRecBytes; };
     auto load = [&](int n) {
       if (lane == 0) {
         uint8_t* st = sm + (n & 1) * L::STAGE;
-        uint64_t* full = &bars[FULL0 + (n & 1)];
-        const int tok = static_cast<int>(tok0 + C * static_cast<long>(n));
-        const uint8_t* rec = a.rec + (static_cast<size_t>(slot0 + n) * p.HV + hv) * kRecBytes;
+        uint64_t* full = &bars[wide::FULL0 + (n & 1)];
+        const int tok = static_cast<int>(tok0 + C * static_cast<long>(chunk(n)));
         mbar_arrive_expect_tx_relaxed(full, L::TX);
 #pragma unroll
         for (int b = 0; b < K / 64; ++b) {
           tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
-          tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
+          if (MODE != SAVE) tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
         }
-        bulk_load(st + L::FAC, rec + kRecFactors, 1024, full);
+        bulk_load(st + L::FAC, record(n) + kRecFactors, 1024, full);
         tma_load_3d(st + L::VS, &maps.v, full, 0, hv, tok);
         tma_load_3d(st + L::VS + 8192, &maps.v, full, 64, hv, tok);
-        bulk_load(st + L::TT, rec, 2 * kTileBytes, full);
+        if (MODE == FORWARD) bulk_load(st + L::TT, record(n), 2 * kTileBytes, full);
       }
       __syncwarp();
     };
-    int nf = 0;
+    auto load_t = [&](int n) {  // the one buffer of [T; R]: T alone for SAVE
+      if (lane == 0) {
+        mbar_arrive_expect_tx_relaxed(&bars[wide::TFULL], MODE == SAVE ? 16384 : 2 * kTileBytes);
+        bulk_load(sm + L::TT1, record(n), MODE == SAVE ? 8192 : 2 * kTileBytes, &bars[wide::TFULL]);
+        if (MODE == SAVE) bulk_load(sm + L::TT1 + kTileBytes, record(n) + kTileBytes, 8192, &bars[wide::TFULL]);
+      }
+      __syncwarp();
+    };
+    int nf = 0, nt = 0;   // loads issued
     for (; nf < 2 && nf < nch; ++nf) load(nf);
-    for (int n = 1; n < nch && nf < nch; ++n) {    // a stage's readers are done once the next chunk's products start
-      if (!wait(EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
-      load(nf++);
+    if (MODE != FORWARD && nch > 0) load_t(nt++);
+    for (int n = 1; n < nch; ++n) {
+      if (MODE != FORWARD) {                       // free once step 2 of the chunk before is done
+        if (!wait(wide::TFREE, (n - 1) & 1)) break;
+        load_t(nt++);
+      }
+      if (nf < nch) {                              // a stage's readers are done once the next chunk's products start
+        if (!wait(wide::EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        load(nf++);
+      }
     }
-    for (int m = nf < 2 ? 0 : nf - 2; m < nf; ++m) mbar_wait(&bars[FULL0 + (m & 1)], (m >> 1) & 1, kDrainNs);
+    // what was issued lands before the CTA gives up its memory
+    for (int m = nf < 2 ? 0 : nf - 2; m < nf; ++m) mbar_wait(&bars[wide::FULL0 + (m & 1)], (m >> 1) & 1, kDrainNs);
+    if (nt > 0) mbar_wait(&bars[wide::TFULL], (nt - 1) & 1, kDrainNs);
   } else if (warp == NW) {
     // ------------------------------------------------------------- products ---
     const uint32_t sb = smem_u32(sm);
@@ -952,180 +1043,273 @@ __global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int kb = 0; kb < K / 64; ++kb)
-          umma_ts_chain<4>(d, tmem + TS + h * (K / 2) + 32 * kb, b + (kb * kTileBytes >> 4), row, id64, h + kb > 0);
+          umma_ts_chain<4>(d, tmem + L::TS + h * (K / 2) + 32 * kb, b + (kb * kTileBytes >> 4), row, id64, h + kb > 0);
     };
     auto y_times = [&](uint32_t d, uint64_t b) {   // Y^T times 64 rows of [T; R]: high high, high low, low high
-      umma_ts_chain<4>(d, tmem + TY, b, row, id64, 0u);
-      umma_ts_chain<4>(d, tmem + TY, b + (kTileBytes >> 4), row, id64, 1u);
-      umma_ts_chain<4>(d, tmem + TY + 32, b, row, id64, 1u);
+      constexpr uint32_t id = MODE == REVERSE ? id64 | IDESC_B_MN_MAJOR : id64, acc = MODE == REVERSE;
+      umma_ts_chain<4>(d, tmem + L::TY, b, MODE == REVERSE ? col : row, id, acc);
+      umma_ts_chain<4>(d, tmem + L::TY, b + (kTileBytes >> 4), MODE == REVERSE ? col : row, id, 1u);
+      umma_ts_chain<4>(d, tmem + L::TY + 32, b, MODE == REVERSE ? col : row, id, 1u);
+    };
+    auto into_state = [&](uint32_t at, uint64_t b, uint32_t acc) {  // both parts of a [columns, tokens] operand times rows of q or k
+      umma_ts_chain<4>(tmem + L::TD3, tmem + at, b, col, idk, acc);
+      umma_ts_chain<4>(tmem + L::TD3, tmem + at + 32, b, col, idk, 1u);
     };
     for (int n = 0; n < nch; ++n) {
-      const uint32_t ph = n & 1, st = sb + ph * L::STAGE;
-      const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2), dt = sdesc_sw128(st + L::TT);
-      if (!wait(FULL0 + (n & 1), (n >> 1) & 1)) break;
-      if (!wait(SREADY, ph)) break;
+      const uint32_t ph = n & 1, st = sb + ph * L::STAGE, tt = MODE == FORWARD ? st + L::TT : sb + L::TT1;
+      const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2);
+      const uint64_t dt = MODE == REVERSE ? sdesc(tt, kTileBytes, 1024, 2) : sdesc_sw128(tt);
+      if (!wait(wide::FULL0 + (n & 1), (n >> 1) & 1)) break;
+      if (!wait(wide::SREADY, ph)) break;
       tc_fence_after();
-      s_times(tmem + TD1, dkq);
-      umma_commit_warp(&bars[D1]);
-      if (n > 0 && lane == 0) mbar_arrive(&bars[EMPTY0 + ((n - 1) & 1)]);
+      s_times(tmem + L::TD1, dkq);
+      umma_commit_warp(&bars[wide::D1]);
+      if (n > 0 && lane == 0) mbar_arrive(&bars[wide::EMPTY0 + ((n - 1) & 1)]);
       __syncwarp();
-      s_times(tmem + TD1 + 64, dkq + (8192 >> 4));
-      umma_commit_warp(&bars[D1Q]);
-      if (!wait(YREADY, ph)) break;
+      if (MODE == FORWARD) {
+        s_times(tmem + L::TD1 + 64, dkq + (8192 >> 4));
+        umma_commit_warp(&bars[wide::D1Q]);
+      } else if (!wait(wide::TFULL, ph)) {
+        break;
+      }
+      if (MODE == REVERSE) {
+        if (!wait(wide::QREADY, ph)) break;
+        tc_fence_after();
+        const uint64_t dd = sdesc(st + L::VS, 8192, 1024, 2);
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+          umma4<2048, 2048>(tmem + L::TD2, dd, dt + ((8192 + h * kTileBytes) >> 4), id64 | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR, h);
+        into_state(L::TW, dkt + (8192 >> 4), 0u);
+      }
+      if (!wait(wide::YREADY, ph)) break;
       tc_fence_after();
-      y_times(tmem + TD2, dt);
-      umma_commit_warp(&bars[D2]);
-      y_times(tmem + TD2 + 64, dt + (8192 >> 4));
-      umma_commit_warp(&bars[D2R]);
-      if (!wait(VREADY, ph)) break;
+      y_times(tmem + L::TD2, dt);
+      umma_commit_warp(&bars[wide::D2]);
+      if (MODE == FORWARD) {
+        y_times(tmem + L::TD2 + 64, dt + (8192 >> 4));
+        umma_commit_warp(&bars[wide::D2R]);
+      } else {
+        umma_commit_warp(&bars[wide::TFREE]);
+      }
+      if (!wait(wide::VREADY, ph)) break;
       tc_fence_after();
-      umma_ts_chain<4>(tmem + TD3, tmem + TV, dkt, col, idk, 0u);
-      umma_ts_chain<4>(tmem + TD3, tmem + TV + 32, dkt, col, idk, 1u);
-      umma_commit_warp(&bars[D3]);
+      into_state(L::TV, dkt, MODE == REVERSE);
+      umma_commit_warp(&bars[wide::D3]);
     }
-    umma_commit_warp(&bars[DRAIN]);                // what is in flight ends before the CTA gives up its memory
-    mbar_wait(&bars[DRAIN], 0, kDrainNs);
+    umma_commit_warp(&bars[wide::DRAIN]);          // what is in flight ends before the CTA gives up its memory
+    mbar_wait(&bars[wide::DRAIN], 0, kDrainNs);
   } else if (warp == NW + 2) {
     // --------------------------------------------------------------- stores ---
     for (int n = 0; n < nch; ++n) {
-      if (!wait(OUTREADY, n & 1)) break;
+      const int c = chunk(n);
+      const size_t cu = static_cast<size_t>(slot0 + c) * p.HV + hv;
+      if (MODE != FORWARD) {
+        if (!wait(wide::SFREADY, n & 1)) break;
+        if (lane == 0) {
+          bulk_store((MODE == SAVE ? a.states : a.dstates) + cu * K * V, sm + L::SF, K * V * 4);
+          bulk_commit();
+          bulk_wait_read();
+          mbar_arrive(&bars[wide::SFFREE]);
+        }
+        __syncwarp();
+      }
+      if (!wait(wide::OUTREADY, n & 1)) break;
       if (lane == 0) {
-        if (C * n + C <= len) {
-          const int tok = static_cast<int>(tok0 + C * static_cast<long>(n));
+        if (MODE != FORWARD) {
+          bulk_store((MODE == SAVE ? a.vn : a.z) + cu * (4 * C * V), sm + L::OUT, 4 * C * V);
+        } else if (C * c + C <= len) {
+          const int tok = static_cast<int>(tok0 + C * static_cast<long>(c));
           tma_store_3d(&maps.o, sm + L::OUT, 0, hv, tok);
           tma_store_3d(&maps.o, sm + L::OUT + 8192, 64, hv, tok);
-          bulk_commit();
         }
+        bulk_commit();
         bulk_wait_read();
-        mbar_arrive(&bars[OUTFREE]);
+        mbar_arrive(&bars[wide::OUTFREE]);
       }
       __syncwarp();
     }
     if (lane == 0) bulk_wait_read();
   } else {
-    // ------------------------------------------ state, Y, vn, output ---
+    // ------------------------------------------ state, Y, vn (z), output ---
     const int quad = warp & 3, grp = warp >> 2, t0 = 16 * grp, d0 = DPT * grp;
     const int col = 32 * quad + lane;              // TMEM lane: value column
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    const uint32_t ts = tl + TS + d0 / 2, ty = tl + TY + t0 / 2, tv = tl + TV + t0 / 2;
-    // element (token t0 + j, column) of a 64-token tile of two boxes
-    const uint32_t toff = (col >> 6) * 8192 + t0 * 128 + (col & 7) * 2, tch = ((col & 63) >> 3) << 4;
-    const auto at = [&](int j) { return toff + j * 128 + (tch ^ ((j & 7) << 4)); };
+    const uint32_t ts = tl + L::TS + d0 / 2;
+    // this thread's row of the block's 8 x 8 tiles (its first 16 columns; the others: ^ 32)
+    const uint32_t toff = (quad >> 1) * 8192 + (t0 / 8 + (lane >> 4)) * 1024 + (lane & 7) * 128 +
+                          ((4 * (quad & 1) + ((lane >> 3) & 1)) ^ (lane & 7)) * 16;
+    const int tk = t0 + 2 * (lane & 3);            // pair j: tokens tk + 8 ((j >> 1) & 1) and one on
     const size_t soff = ((static_cast<size_t>(seq) * p.HV + hv) * K + d0) * V + col;
+    const float* first = MODE == REVERSE ? a.dfin : p.s0;
+    float* final = MODE == FORWARD ? p.sfin : MODE == REVERSE ? a.ds0 : nullptr;
     uint64_t s[DPT / 2];
 #pragma unroll
     for (int j = 0; j < DPT / 2; ++j)
-      s[j] = p.s0 ? pack2f(p.s0[soff + 2 * j * V], p.s0[soff + (2 * j + 1) * V]) : 0ull;
+      s[j] = first ? pack2f(first[soff + 2 * j * V], first[soff + (2 * j + 1) * V]) : 0ull;
     parts_to_tmem<DPT>(ts, ts + K / 2, s);
     tc_fence_before();
-    arrive(SREADY);
+    arrive(wide::SREADY);
     const uint64_t scale = pack2f(p.scale, p.scale);
     bool good = true;
     for (int n = 0; n < nch; ++n) {
       const uint32_t ph = n & 1;
       uint8_t* st = sm + ph * L::STAGE;
       const float* fac = reinterpret_cast<const float*>(st + L::FAC);
-      const int rows = len - C * n;                // of the chunk, from the first; 64 and more: all
-      if (!(good = wait(FULL0 + (n & 1), (n >> 1) & 1))) break;
-      if (tid == 0 && fac[kRecFailed] != 0.f) atomicOr(p.status, kStatusTimeout);
-      uint64_t y[8], o[8];
-      float x[16];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {                // v, whatever rows past the end hold
-        const uint32_t u = *reinterpret_cast<const uint16_t*>(st + L::VS + at(2 * j));
-        const uint32_t w = *reinterpret_cast<const uint16_t*>(st + L::VS + at(2 * j + 1));
-        y[j] = pack2f(__uint_as_float(u << 16), __uint_as_float(w << 16));
-      }
-      if (!(good = wait(D1, ph))) break;
-      tc_fence_after();
-      tmem_ld16(tl + TD1 + t0, x);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {                // beta (v - G k S)
-        const float2 g = *reinterpret_cast<const float2*>(fac + t0 + 2 * j), be = *reinterpret_cast<const float2*>(fac + 128 + t0 + 2 * j);
-        float v0, v1;
-        unpack2f(y[j], v0, v1);
-        y[j] = mul2(pack2f(be.x, be.y), pack2f(fmaf(-g.x, x[2 * j], v0), fmaf(-g.y, x[2 * j + 1], v1)));
-      }
-      if (rows < C) {                              // rows past the end: zero wherever a sum over tokens meets them
+      const int c = chunk(n), rows = len - C * c;  // rows of the chunk, from the first; 64 and more: all
+      uint64_t x[8], y[8], o[8];
+      // rows past the end hold the next sequence's tokens, whatever they are: zero wherever a
+      // sum over tokens meets them
+      auto zero_past_end = [&](uint64_t (&w)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float v0, v1;
-          unpack2f(y[j], v0, v1);
-          y[j] = pack2f(t0 + 2 * j < rows ? v0 : 0.f, t0 + 2 * j + 1 < rows ? v1 : 0.f);
+          unpack2f(w[j], v0, v1);
+          const int t = tk + 8 * ((j >> 1) & 1);
+          w[j] = pack2f(t < rows ? v0 : 0.f, t + 1 < rows ? v1 : 0.f);
         }
-        if (tid < C && tid >= rows) {
+      };
+      auto factors = [&](int at, uint64_t (&f)[2]) {  // of this thread's tokens
+#pragma unroll
+        for (int m = 0; m < 2; ++m) f[m] = *reinterpret_cast<const uint64_t*>(fac + at + tk + 8 * m);
+      };
+      auto put_block = [&](uint8_t* tile, const uint32_t (&w)[8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          stmatrix_x4_trans(smem_u32(tile + (toff ^ (32 * h))), w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+      };
+      uint64_t fg[2], fe[2], fb[2];                // G, E, beta
+      if (!(good = wait(wide::FULL0 + (n & 1), (n >> 1) & 1))) break;
+      if (tid == 0 && fac[kRecFailed] != 0.f) atomicOr(p.status, kStatusTimeout);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {                // v (do)
+        uint32_t u[4];
+        ldmatrix_x4_trans(smem_u32(st + L::VS + (toff ^ (32 * h))), u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[4 * h + j] = pack2f(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+      }
+      factors(0, fg);
+      factors(64, fe);
+      factors(128, fb);
+      if (rows < C) {
+        if (tid < (MODE == REVERSE ? 3 * C : C) && (tid & 63) >= rows) {  // rows of k, of q, of do
+          uint8_t* tile = tid < 2 * C ? st : st + L::VS;
+          const uint32_t step = tid < 2 * C ? kTileBytes : 8192u;
+          const int row = tid < 2 * C ? tid : tid - 2 * C, chunks = tid < 2 * C ? 8 * (K / 64) : 16;
 #pragma unroll 1
-          for (int ch = 0; ch < 8 * (K / 64); ++ch)
-            *reinterpret_cast<uint4*>(st + (ch >> 3) * kTileBytes + sw128(tid, ch & 7)) = make_uint4(0, 0, 0, 0);
+          for (int ch = 0; ch < chunks; ++ch)
+            *reinterpret_cast<uint4*>(tile + (ch >> 3) * step + sw128(row, ch & 7)) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
-      parts_to_tmem<16>(ty, ty + 32, y);
-      tc_fence_before();
-      arrive(YREADY);
-      if (!(good = wait(D1Q, ph))) break;          // while step 2 runs: scale G q S
-      tc_fence_after();
-      tmem_ld16(tl + TD1 + 64 + t0, x);
-      tmem_ld_wait();
+      if (MODE == REVERSE) {                       // scale G do
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 g = *reinterpret_cast<const float2*>(fac + t0 + 2 * j);
-        o[j] = mul2(scale, mul2(pack2f(g.x, g.y), pack2f(x[2 * j], x[2 * j + 1])));
+        for (int j = 0; j < 8; ++j) y[j] = mul2(mul2(scale, fg[(j >> 1) & 1]), y[j]);
+        if (rows < C) zero_past_end(y);
+        block_parts(tl + L::TW + t0 / 2, y);
+        tc_fence_before();
+        arrive(wide::QREADY);
       }
-      if (!(good = wait(D2, ph))) break;
+      if (!(good = wait(wide::D1, ph))) break;
       tc_fence_after();
-      tmem_ld16(tl + TD2 + t0, x);
-      tmem_ld_wait();
+      block_ld(tl + L::TD1 + t0, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 e = *reinterpret_cast<const float2*>(fac + 64 + t0 + 2 * j);
-        y[j] = mul2(pack2f(e.x, e.y), pack2f(x[2 * j], x[2 * j + 1]));
+        if (MODE == REVERSE) {                     // E k dS'
+          y[j] = mul2(fe[(j >> 1) & 1], x[j]);
+        } else {                                   // beta (v - G k S)
+          float v0, v1, x0, x1, g0, g1;
+          unpack2f(y[j], v0, v1);
+          unpack2f(x[j], x0, x1);
+          unpack2f(fg[(j >> 1) & 1], g0, g1);
+          y[j] = mul2(fb[(j >> 1) & 1], pack2f(fmaf(-g0, x0, v0), fmaf(-g1, x1, v1)));
+        }
       }
-      parts_to_tmem<16>(tv, tv + 32, y);
+      if (rows < C) zero_past_end(y);
+      block_parts(tl + L::TY + t0 / 2, y);
       tc_fence_before();
-      arrive(VREADY);
-      if (!(good = wait(D2R, ph))) break;          // while step 3 runs: the output
+      arrive(wide::YREADY);
+      if (MODE == FORWARD) {                       // while step 2 runs: scale G q S
+        if (!(good = wait(wide::D1Q, ph))) break;
+        tc_fence_after();
+        block_ld(tl + L::TD1 + 64 + t0, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = mul2(mul2(scale, fg[(j >> 1) & 1]), o[j]);
+      } else {                                     // S (dS') in fp32 to its staging: rows of 16 chunks, swizzled
+        if (n > 0 && !(good = wait(wide::SFFREE, (n - 1) & 1))) break;
+        uint8_t* sf = sm + L::SF + (col >> 6) * (K * 256) + d0 * 256 + (col & 3) * 4;
+        const uint32_t ch = ((col & 63) >> 2) << 4;
+#pragma unroll
+        for (int j = 0; j < DPT / 2; ++j) {
+          float u, w;
+          unpack2f(s[j], u, w);
+          *reinterpret_cast<float*>(sf + 2 * j * 256 + (ch ^ (((2 * j) & 7) << 4))) = u;
+          *reinterpret_cast<float*>(sf + (2 * j + 1) * 256 + (ch ^ (((2 * j + 1) & 7) << 4))) = w;
+        }
+        fence_proxy_async_smem();
+        arrive(wide::SFREADY);
+      }
+      if (!(good = wait(wide::D2, ph))) break;
       tc_fence_after();
-      tmem_ld16(tl + TD2 + 64 + t0, x);
-      tmem_ld_wait();
-      if (n > 0 && !(good = wait(OUTFREE, (n - 1) & 1))) break;
+      block_ld(tl + L::TD2 + t0, x);
+      if (MODE == REVERSE && rows < C) zero_past_end(x);  // (vn is zero there by itself: row i of T is e_i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)                  // E vn, or -G beta z
+        y[j] = MODE == REVERSE ? mul2(mul2(pack2f(-1.f, -1.f), mul2(fg[(j >> 1) & 1], fb[(j >> 1) & 1])), x[j])
+                               : mul2(fe[(j >> 1) & 1], x[j]);
+      block_parts(tl + L::TV + t0 / 2, y);
+      tc_fence_before();
+      arrive(wide::VREADY);
+      if (MODE == FORWARD) {                       // while step 3 runs: the output
+        if (!(good = wait(wide::D2R, ph))) break;
+        tc_fence_after();
+        block_ld(tl + L::TD2 + 64 + t0, x);
+      }
+      if (n > 0 && !(good = wait(wide::OUTFREE, (n - 1) & 1))) break;
+      uint32_t w[8], wl[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t u = pack_pair(add2(o[j], pack2f(x[2 * j], x[2 * j + 1])));
-        if (rows >= C) {
-          *reinterpret_cast<uint16_t*>(sm + L::OUT + at(2 * j)) = static_cast<uint16_t>(u);
-          *reinterpret_cast<uint16_t*>(sm + L::OUT + at(2 * j + 1)) = static_cast<uint16_t>(u >> 16);
-        } else {
+        if (MODE == FORWARD) w[j] = pack_pair(add2(o[j], x[j]));
+        else split2(x[j], w[j], wl[j]);            // vn (z) as it is, in two parts
+      }
+      if (MODE != FORWARD) {
+        put_block(sm + L::OUT, w);
+        put_block(sm + L::OUT + 16384, wl);
+      } else if (rows >= C) {
+        put_block(sm + L::OUT, w);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int t = tk + 8 * ((j >> 1) & 1);
           uint16_t* op = static_cast<uint16_t*>(p.out) +
-                         (static_cast<size_t>(tok0 + C * static_cast<long>(n) + t0 + 2 * j) * p.HV + hv) * V + col;
-          if (t0 + 2 * j < rows) op[0] = static_cast<uint16_t>(u);
-          if (t0 + 2 * j + 1 < rows) op[static_cast<size_t>(p.HV) * V] = static_cast<uint16_t>(u >> 16);
+                         (static_cast<size_t>(tok0 + C * static_cast<long>(c) + t) * p.HV + hv) * V + 32 * quad + 16 * (j >> 2) +
+                         8 * (j & 1) + (lane >> 2);
+          if (t < rows) op[0] = static_cast<uint16_t>(w[j]);
+          if (t + 1 < rows) op[static_cast<size_t>(p.HV) * V] = static_cast<uint16_t>(w[j] >> 16);
         }
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      arrive(OUTREADY);
+      arrive(wide::OUTREADY);
       const float gm = fac[kRecGamma];
       const uint64_t gamma = pack2f(gm, gm);
-      if (!(good = wait(D3, ph))) break;
+      if (!(good = wait(wide::D3, ph))) break;
       tc_fence_after();
       float z[DPT];
-      tmem_ld<DPT>(tl + TD3 + d0, z);
+      tmem_ld<DPT>(tl + L::TD3 + d0, z);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < DPT / 2; ++j) s[j] = fma2(gamma, s[j], pack2f(z[2 * j], z[2 * j + 1]));
       parts_to_tmem<DPT>(ts, ts + K / 2, s);
       tc_fence_before();
-      arrive(SREADY);
+      arrive(wide::SREADY);
     }
-    if (good && p.sfin) {
+    if (good && final) {
 #pragma unroll
       for (int j = 0; j < DPT / 2; ++j) {
         float u, w;
         unpack2f(s[j], u, w);
-        p.sfin[soff + 2 * j * V] = u;
-        p.sfin[soff + (2 * j + 1) * V] = w;
+        final[soff + 2 * j * V] = u;
+        final[soff + (2 * j + 1) * V] = w;
       }
     }
   }
@@ -1135,6 +1319,21 @@ __global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+template <int K>
+__global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  wide_body<K, chain::FORWARD>(maps, a, blockIdx.x, raw);
+}
+
+template <int K>
+__global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_chains_kernel(const __grid_constant__ ChainMaps maps,
+                                                                          const __grid_constant__ ChainMaps maps_r,
+                                                                          const ChunkParams a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  if (blockIdx.x & 1) wide_body<K, chain::REVERSE>(maps_r, a, blockIdx.x >> 1, raw);
+  else wide_body<K, chain::SAVE>(maps, a, blockIdx.x >> 1, raw);
 }
 
 // The backward's two chains in one launch: even blocks SAVE (maps: v), odd blocks REVERSE
@@ -1191,8 +1390,16 @@ cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cud
 template <int K>
 cudaError_t launch_wide(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
   static LaunchState state;
-  return launch_kernel(state, gdr_wide_kernel<K>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV, wide::THREADS, wide::Lay<K>::SMEM,
-                       true, st, maps, a);
+  return launch_kernel(state, gdr_wide_kernel<K>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV, wide::THREADS,
+                       wide::Lay<K, chain::FORWARD>::SMEM, true, st, maps, a);
+}
+template <int K>
+cudaError_t launch_wide_chains(const ChainMaps& maps, const ChainMaps& maps_r, const ChunkParams& a, cudaStream_t st) {
+  constexpr uint32_t bytes = wide::Lay<K, chain::REVERSE>::SMEM;
+  static_assert(bytes >= wide::Lay<K, chain::SAVE>::SMEM, "shared memory of the two chains");
+  static LaunchState state;
+  return launch_kernel(state, gdr_wide_chains_kernel<K>, 2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV, wide::THREADS, bytes,
+                       true, st, maps, maps_r, a);
 }
 
 template <int K>
@@ -1281,7 +1488,8 @@ cudaError_t launch_chunk_bwd(const Params& p, const void* dout, const float* dfi
     return cudaErrorInvalidValue;
   cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
   if (e != cudaSuccess) return e;
-  e = K == 128 ? launch_chains<128>(maps, maps_r, a, V, st) : launch_chains<64>(maps, maps_r, a, V, st);
+  if (V == 128) e = K == 128 ? launch_wide_chains<128>(maps, maps_r, a, st) : launch_wide_chains<64>(maps, maps_r, a, st);
+  else e = K == 128 ? launch_chains<128>(maps, maps_r, a, V, st) : launch_chains<64>(maps, maps_r, a, V, st);
   if (e != cudaSuccess) return e;
   if ((e = launch_grads(maps_r, a, K, V, st)) != cudaSuccess || !grouped) return e;
   return launch_group_sum(static_cast<const float*>(a.dq), dq, dk, tokens, p.H, p.HV / p.H, K, st);

@@ -178,6 +178,19 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[4]
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
 }
+// The same for two 8-column groups, one after the other (r[0..3], r[4..7]).
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+               : "r"(taddr));
+}
+// 16 lanes x 128 bit, two groups of 4 columns: thread t puts r[0] to (lane t/4, column t%4), r[1]
+// to lane t/4 + 8, r[2] and r[3] to the second group likewise -- the same fragment packed to 16 bits.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // 32 lanes x 32 bit, 32 consecutive columns per thread, stored to TMEM.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
@@ -468,6 +481,14 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 template <int N>
 __device__ __forceinline__ void bulk_wait_group_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// Four 8 x 8 tiles of 16-bit elements, transposed: thread t gets elements (2 (t%4), t/4) and
+// (2 (t%4) + 1, t/4) of tile n in r[n]; thread t's address is that of row t%8 of tile t/8.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
 }
 // Four 8x8 b16 matrices from m16n8-fragment registers to shared memory, transposed: row r
 // of the stored matrix i is column r of the fragment, written at the address lane 8 i + r gives.

@@ -54,6 +54,11 @@ def test_gradients(shape, state):
     compare(make(state=state, seed=41, grads=True, **shape))
 
 
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64)])
+def test_gradients_of_many_sequences(K, V):
+    compare(make([i * 7 % 5 if i % 50 else 90 for i in range(200)], 1, 2, K, V, state=True, seed=51, grads=True))
+
+
 @pytest.mark.parametrize("gate", ["none", "strong", "cliff"])
 def test_gradients_gates(gate):
     compare(make((1, 200), 1, 2, 128, 128, gate=gate, seed=42, grads=True))
