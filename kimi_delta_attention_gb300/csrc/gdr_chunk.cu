@@ -26,12 +26,17 @@ namespace {
 namespace prep {
 constexpr int NT = 128;
 constexpr uint32_t LDM = 68;                           // floats between rows of M and T: no bank conflicts
-// [k; q] tiles at 0, then the record's image over them (T in rows 0-63; in 64-127 first P, then R)
-constexpr uint32_t OFF_M = kRecBytes;
-constexpr uint32_t OFF_GC = OFF_M + C * LDM * 4;       // gc high parts, low parts (log2), beta, block factors
-constexpr uint32_t OFF_BAR = OFF_GC + 4 * C * 4;
+// [k; q] tiles at 0; over them, in 64-row tiles of an operand's high and low part, P, then R; and
+// between these M, 32 rows each, then T.  So six CTAs share an SM (with M apart from the tiles, four).
+constexpr uint32_t HALF_M = 32 * LDM * 4;
+constexpr uint32_t OFF_T = 0, OFF_P = 9216, PART = 17408;  // low parts: PART on; rows 32-63 of M: likewise
+constexpr uint32_t OFF_GC = 2 * PART;                  // gc high parts, low parts (log2), beta, block factors; then the record's row factors
+constexpr uint32_t OFF_BAR = OFF_GC + 1024;
 constexpr uint32_t SMEM = OFF_BAR + 64 + 1024;
-static_assert(OFF_M >= 2 * kTileBytes, "the tiles fit");
+static_assert(OFF_GC >= 2 * kTileBytes && HALF_M <= OFF_P && OFF_P + 8192 <= PART && OFF_P >= 8192, "the tiles fit");
+__device__ __forceinline__ float* row_of_m(uint8_t* sm, int r) {
+  return reinterpret_cast<float*>(sm + (r >= 32 ? PART : 0)) + (r & 31) * LDM;
+}
 
 // Two TF32 parts by truncation (the low 13 bits cleared).
 __device__ __forceinline__ void tf32_parts(float x, uint32_t& h, uint32_t& l) {
@@ -83,10 +88,9 @@ __device__ __forceinline__ void block_put(float* x, const float (&acc)[2][4], fl
 }  // namespace prep
 
 template <int K>
-__global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
+__global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  float* ms = reinterpret_cast<float*>(sm + prep::OFF_M);
   float* gh = reinterpret_cast<float*>(sm + prep::OFF_GC);
   float* gl = gh + C;
   float* bs = gl + C;
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
   // row i of D in log2: gc_i - gc_j; the factors of the row
   const int i = tid & 63;
   const bool isq = tid >= 64;
-  const float hi = gh[i], lo = gl[i], be = bs[i];
+  const float hi = gh[i], lo = gl[i], be = bs[i], end_hi = gh[63], end_lo = gl[63];
   if (!mbar_wait(&bar[1], 0, a.wait_ns)) {
     ok = false;
     mbar_wait(&bar[1], 0, kDrainNs);
@@ -191,21 +195,21 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
         for (int c = 0; c < 2; ++c) {
           uint4 h, l;
           split8(y + 8 * c, h, l);
-          *reinterpret_cast<uint4*>(sm + sw128(tid, 2 * b + c)) = h;
-          *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, 2 * b + c)) = l;
+          *reinterpret_cast<uint4*>(sm + prep::OFF_P + sw128(i, 2 * b + c)) = h;
+          *reinterpret_cast<uint4*>(sm + prep::OFF_P + prep::PART + sw128(i, 2 * b + c)) = l;
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(ms + i * prep::LDM + 16 * b + 4 * j) =
+          *reinterpret_cast<float4*>(prep::row_of_m(sm, i) + 16 * b + 4 * j) =
               make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
       }
     }
     if (warp == 2) {                                         // (the rest of P's rows 0-31)
 #pragma unroll
       for (int c = 4; c < 8; ++c) {
-        *reinterpret_cast<uint4*>(sm + sw128(tid, c)) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, c)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(sm + prep::OFF_P + sw128(i, c)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(sm + prep::OFF_P + prep::PART + sw128(i, c)) = make_uint4(0, 0, 0, 0);
       }
     }
   }
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
     __syncwarp();
     {                                              // row i of its diagonal block inverted, in the block's place
       const int rr = tid & 15;
-      float* mb = ms + (tid & ~15) * (prep::LDM + 1);
+      float* mb = prep::row_of_m(sm, tid & ~15) + (tid & ~15);
       float x[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] = j == rr ? 1.f : 0.f;
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
         *reinterpret_cast<float4*>(mb + rr * prep::LDM + 4 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
       __syncwarp();
     }
-    float* ha = ms + 32 * warp * (prep::LDM + 1);  // [A 0; B D] of 16-row blocks: B A^-1, then -D^-1 of it
+    float* ha = prep::row_of_m(sm, 32 * warp) + 32 * warp;  // [A 0; B D] of 16-row blocks: B A^-1, then -D^-1 of it
     float* hb = ha + 16 * prep::LDM;
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
@@ -248,52 +252,54 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
   __syncthreads();  // the halves are done, P is written, the accumulator is read
   {                 // the same between the halves, a block a warp; B A^-1 in the unused upper right
     const int I = warp >> 1, J = warp & 1;
-    float* upper = ms + 32;
+    float* top = prep::row_of_m(sm, 0);
+    float* low = prep::row_of_m(sm, 32);
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
-      const float* x = ms + (32 + 16 * I) * prep::LDM + (n ? 32 : 0);
-      const float* y = (n ? upper : ms) + 16 * J;
+      const float* x = low + 16 * I * prep::LDM + (n ? 32 : 0);
+      const float* y = top + 16 * J + (n ? 32 : 0);
       const int from = n ? 0 : J, to = n ? I : 1;
       float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 1
       for (int l = from; l <= to; ++l) prep::block_mma(acc, x + 16 * l, prep::LDM, y + 16 * l * prep::LDM, prep::LDM, lane);
-      prep::block_put(n ? ms + (32 + 16 * I) * prep::LDM + 16 * J : upper + 16 * I * prep::LDM + 16 * J, acc, n ? -1.f : 1.f, lane);
+      prep::block_put((n ? low : top + 32) + 16 * I * prep::LDM + 16 * J, acc, n ? -1.f : 1.f, lane);
       __syncthreads();
     }
   }
-  {                 // T to the record's image, half a row a thread
+  {                 // T as an operand over M, half a row a thread
     const int own = i >> 4, half = tid >> 6;       // columns past the row's own block are zero
+    float y[32];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c4 = 8 * half + j;
+      const float4 u = (c4 >> 2) <= own ? *reinterpret_cast<const float4*>(prep::row_of_m(sm, i) + 4 * c4)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      y[4 * j] = u.x; y[4 * j + 1] = u.y; y[4 * j + 2] = u.z; y[4 * j + 3] = u.w;
+    }
+    __syncthreads();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int ch = 4 * half + c;
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 u = (ch >> 1) <= own ? *reinterpret_cast<const float4*>(ms + i * prep::LDM + 8 * ch + 4 * j)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-        y[4 * j] = u.x; y[4 * j + 1] = u.y; y[4 * j + 2] = u.z; y[4 * j + 3] = u.w;
-      }
       uint4 h, l;
-      split8(y, h, l);
-      *reinterpret_cast<uint4*>(sm + sw128(i, ch)) = h;
-      *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(i, ch)) = l;
+      split8(y + 8 * c, h, l);
+      *reinterpret_cast<uint4*>(sm + prep::OFF_T + sw128(i, 4 * half + c)) = h;
+      *reinterpret_cast<uint4*>(sm + prep::OFF_T + prep::PART + sw128(i, 4 * half + c)) = l;
     }
   }
   fence_proxy_async_smem();
   __syncthreads();
-  if (warp == 0) {  // R = P T in lanes 64-127 (0-63: T's rows times T, read by nobody)
+  if (warp == 0) {  // R = P T in lanes 64-127 (0-63: of whatever lies before P, read by nobody)
     tc_fence_after();
-    const uint64_t dp = sdesc_sw128(smem_u32(sm)), dt = sdesc(smem_u32(sm), kTileBytes, 1024, 2);
+    const uint64_t dp = sdesc_sw128(smem_u32(sm) + prep::OFF_P - 8192), dt = sdesc(smem_u32(sm) + prep::OFF_T, 8192, 1024, 2);
     constexpr uint32_t id = idesc_f16kind(128, 64) | IDESC_B_MN_MAJOR;
 #pragma unroll 1
     for (int n = 0; n < 3; ++n)
-      umma4<32, 2048>(tmem, dp + (n == 2 ? kTileBytes >> 4 : 0u), dt + (n == 1 ? kTileBytes >> 4 : 0u), id, n > 0);
+      umma4<32, 2048>(tmem, dp + (n == 2 ? prep::PART >> 4 : 0u), dt + (n == 1 ? prep::PART >> 4 : 0u), id, n > 0);
     umma_commit_warp(&bar[2]);
   }
-  float* fac = reinterpret_cast<float*>(sm + kRecFactors);
+  float* fac = gh;
   if (!isq) {
     fac[i] = ex2(hi);
-    fac[64 + i] = ex2((gh[63] - hi) + (gl[63] - lo));
+    fac[64 + i] = ex2((end_hi - hi) + (end_lo - lo));
     fac[128 + i] = be;
     if (i == 63) fac[kRecGamma] = ex2(hi);
   }
@@ -312,8 +318,8 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
       for (int c = 0; c < 4; ++c) {
         uint4 h, l;
         split8(y + 8 * c, h, l);
-        *reinterpret_cast<uint4*>(sm + sw128(tid, 4 * b + c)) = h;
-        *reinterpret_cast<uint4*>(sm + kTileBytes + sw128(tid, 4 * b + c)) = l;
+        *reinterpret_cast<uint4*>(sm + prep::OFF_P + sw128(i, 4 * b + c)) = h;
+        *reinterpret_cast<uint4*>(sm + prep::OFF_P + prep::PART + sw128(i, 4 * b + c)) = l;
       }
     }
   }
@@ -327,7 +333,13 @@ __global__ void __launch_bounds__(prep::NT, 4) gdr_prep_kernel(const __grid_cons
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
-    bulk_store(a.rec + (static_cast<size_t>(slot) * p.HV + hv) * kRecBytes, sm, kRecBytes);
+    uint8_t* rec = a.rec + (static_cast<size_t>(slot) * p.HV + hv) * kRecBytes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      bulk_store(rec + h * kTileBytes, sm + prep::OFF_T + h * prep::PART, 8192);
+      bulk_store(rec + h * kTileBytes + 8192, sm + prep::OFF_P + h * prep::PART, 8192);
+    }
+    bulk_store(rec + kRecFactors, fac, 1024);
     bulk_commit();
     bulk_wait_read();
   }
