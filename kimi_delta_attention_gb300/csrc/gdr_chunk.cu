@@ -30,7 +30,7 @@ constexpr uint32_t LDM = 68;                           // floats between rows of
 // between these M, 32 rows each, then T.  So six CTAs share an SM (with M apart from the tiles, four).
 constexpr uint32_t HALF_M = 32 * LDM * 4;
 constexpr uint32_t OFF_T = 0, OFF_P = 9216, PART = 17408;  // low parts: PART on; rows 32-63 of M: likewise
-constexpr uint32_t OFF_GC = 2 * PART;                  // gc high parts, low parts (log2), beta, block factors; then the record's row factors
+constexpr uint32_t OFF_GC = 2 * PART;                  // -gc high parts, low parts (log2), beta, block factors; then the record's row factors
 constexpr uint32_t OFF_BAR = OFF_GC + 1024;
 constexpr uint32_t SMEM = OFF_BAR + 64 + 1024;
 static_assert(OFF_GC >= 2 * kTileBytes && HALF_M <= OFF_P && OFF_P + 8192 <= PART && OFF_P >= 8192, "the tiles fit");
@@ -91,7 +91,7 @@ template <int K>
 __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  float* gh = reinterpret_cast<float*>(sm + prep::OFF_GC);
+  float* gh = reinterpret_cast<float*>(sm + prep::OFF_GC);   // -gc
   float* gl = gh + C;
   float* bs = gl + C;
   float* cf = bs + C;                             // e^{gc of the 16-block's last row - gc_j}
@@ -126,10 +126,10 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
     float g[2], h[2], l[2];
     load_gate(p.g, p, tok, rows, hv, lane, g);
     gate_scan(g[0], g[1], lane, h, l);
-    gh[2 * lane] = h[0];
-    gh[2 * lane + 1] = h[1];
-    gl[2 * lane] = l[0];
-    gl[2 * lane + 1] = l[1];
+    gh[2 * lane] = -h[0];
+    gh[2 * lane + 1] = -h[1];
+    gl[2 * lane] = -l[0];
+    gl[2 * lane + 1] = -l[1];
     const float eh = __shfl_sync(0xFFFFFFFFu, h[1], lane | 7), el = __shfl_sync(0xFFFFFFFFu, l[1], lane | 7);
     cf[2 * lane] = ex2((eh - h[0]) + (el - l[0]));
     cf[2 * lane + 1] = ex2((eh - h[1]) + (el - l[1]));
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
   let_next_kernel_start();
   const uint32_t tmem = *tslot;
   if (warp == 0) {
-    ok = mbar_wait(&bar[0], 0, a.wait_ns);
-    if (!ok) mbar_wait(&bar[0], 0, kDrainNs);
+    ok = mbar_wait_sleep(&bar[0], 0, a.wait_ns);
+    if (!ok) mbar_wait_sleep(&bar[0], 0, kDrainNs);
     __syncwarp();
     const uint64_t d = sdesc_sw128(smem_u32(sm));
 #pragma unroll
@@ -159,36 +159,48 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
   // row i of D in log2: gc_i - gc_j; the factors of the row
   const int i = tid & 63;
   const bool isq = tid >= 64;
-  const float hi = gh[i], lo = gl[i], be = bs[i], end_hi = gh[63], end_lo = gl[63];
-  if (!mbar_wait(&bar[1], 0, a.wait_ns)) {
+  const float hi = -gh[i], lo = -gl[i], be = bs[i], end_hi = -gh[63], end_lo = -gl[63];
+  if (!mbar_wait_sleep(&bar[1], 0, a.wait_ns)) {
     ok = false;
-    mbar_wait(&bar[1], 0, kDrainNs);
+    mbar_wait_sleep(&bar[1], 0, kDrainNs);
   }
   tc_fence_after();
-  // M and P.  D_ij = e^{gc_i - gc_j} directly in the row's own 16-block; before it through
-  // the block's last row, as two factors <= 1, one per row and block, one per column
+  // M and P.  D_ij = e^{gc_i - gc_j} directly in the last two 16-blocks of the warp's rows;
+  // before them through the block's last row, as two factors <= 1, one per row and block, one
+  // per column
   {
     const uint32_t t = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const float f = i < rows ? (isq ? p.scale : be) : 0.f;   // rows past the sequence's end: M = P = 0
-    const int last = isq ? i : i - 1, own = i >> 4;          // columns 0 .. last of the row are not zero
+    const int last = isq ? i : i - 1;                        // columns 0 .. last of the row are not zero
     const int blocks = 2 + 2 * (warp & 1);                   // (rows 0-31 end in column 31)
 #pragma unroll 1
     for (int b = 0; b < blocks; ++b) {
       float y[16];
       tmem_ld16(t + 16 * b, y);
-      tmem_ld_wait();
-      const float* ch = gh + 16 * b;
+      const uint64_t hh = pack2f(hi, hi), ll = pack2f(lo, lo);
+      uint64_t d[8];
       if (b >= blocks - 2) {                                 // a block of some of the warp's rows
-        const float fb = f * ex2(fminf((hi - ch[15]) + (lo - gl[16 * b + 15]), 0.f));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float d = b == own ? f * ex2((hi - ch[j]) + (lo - gl[16 * b + j])) : fb * cf[16 * b + j];
-          y[j] = (16 * b + j <= last && i < rows) ? y[j] * d : 0.f;
+        for (int j = 0; j < 8; ++j) {                        // (gh, gl hold -gc)
+          const uint64_t at = add2(add2(hh, *reinterpret_cast<const uint64_t*>(gh + 16 * b + 2 * j)),
+                                   add2(ll, *reinterpret_cast<const uint64_t*>(gl + 16 * b + 2 * j)));
+          float d0, d1;
+          unpack2f(at, d0, d1);
+          d[j] = pack2f(ex2(d0), ex2(d1));
         }
       } else {
-        const float fb = f * ex2((hi - ch[15]) + (lo - gl[16 * b + 15]));
+        const float e = ex2((hi + gh[16 * b + 15]) + (lo + gl[16 * b + 15]));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = i < rows ? y[j] * (fb * cf[16 * b + j]) : 0.f;
+        for (int j = 0; j < 8; ++j) d[j] = mul2(pack2f(e, e), *reinterpret_cast<const uint64_t*>(cf + 16 * b + 2 * j));
+      }
+      tmem_ld_wait();
+      const int end = i < rows ? last - 16 * b : -1;         // columns 0 .. end of the block are not zero
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float d0, d1;
+        unpack2f(mul2(mul2(pack2f(f, f), d[j]), pack2f(y[2 * j], y[2 * j + 1])), d0, d1);
+        y[2 * j] = 2 * j <= end ? d0 : 0.f;
+        y[2 * j + 1] = 2 * j + 1 <= end ? d1 : 0.f;
       }
       if (isq) {                                             // P over the tiles, as an operand
 #pragma unroll
@@ -303,9 +315,9 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
     fac[128 + i] = be;
     if (i == 63) fac[kRecGamma] = ex2(hi);
   }
-  if (!mbar_wait(&bar[2], 0, a.wait_ns)) {
+  if (!mbar_wait_sleep(&bar[2], 0, a.wait_ns)) {
     ok = false;
-    mbar_wait(&bar[2], 0, kDrainNs);
+    mbar_wait_sleep(&bar[2], 0, kDrainNs);
   }
   tc_fence_after();
   if (isq) {
