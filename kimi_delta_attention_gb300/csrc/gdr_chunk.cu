@@ -874,6 +874,335 @@ __global__ void __launch_bounds__(chain::threads(N), 1) gdr_chain_kernel(const _
   chain_body<K, N, chain::FORWARD>(maps, a, V, blockIdx.x, raw);
 }
 
+// ------------------------------------------------- chain, 32 columns thin ---
+// The forward where one CTA per 32 value columns fits the SMs: few sequences, all latency.
+// The same three steps as above, but the products over tokens are of M = 64, the rows that
+// the recurrence waits for (k S, T Y) first and the output's (q S, R Y) behind them, in the
+// shadow of what follows.  M = 64 puts 16 rows into each quadrant of TMEM, so the work
+// between the products lies on all four parts of the SM, on one code path, in fragments of
+// 8 x 8 tiles (v, Y, E vn and o move by tile accesses): a thread holds 8 values of a block.
+// What the recurrence does not wait for is done where a warp waits for a product: a chunk's
+// output while step 2 of the next runs, the next chunk's v and factors while step 3 runs.
+namespace thin {
+constexpr int N = 32, NW = 8, THREADS = 32 * (NW + 3);
+// TMEM columns: both parts' products, 2 x 32 each; q S and R Y twice, for chunks in turn
+constexpr uint32_t TK = 0, TD3 = 0, TT = 64, TQ = 128, TR = 256, TURN = 64;
+template <int K>
+struct Lay {
+  static constexpr uint32_t FAC = (K / 64) * kTileBytes;          // a stage of three: [k; q], row factors, v
+  static constexpr uint32_t VS = FAC + 1024;
+  static constexpr uint32_t STAGE = VS + C * N * 2;
+  static constexpr uint32_t TT = 3 * STAGE;                       // [T; R], of two
+  static constexpr uint32_t S = TT + 2 * 2 * kTileBytes;          // rows of 2 x 32 columns, high and low parts
+  static constexpr uint32_t Y = S + 128 * 128;
+  static constexpr uint32_t VN = Y + C * 128;                     // E vn
+  static constexpr uint32_t OUT = VN + C * 128;
+  static constexpr uint32_t BAR = OUT + C * N * 2;
+  static constexpr uint32_t SLACK = 832;
+  static constexpr uint32_t SMEM = BAR + 192 + SLACK;
+  static_assert(SMEM <= 232448 && STAGE % 1024 == 0, "shared memory");
+};
+enum { FULL = 0, EMPTY = 3, TFULL = 6, TFREE = 8, D1 = 10, D2, D3, SREADY, YREADY, VREADY, OUTREADY, OUTFREE, DRAIN, NBAR };
+// 16 rows x 16 columns of a result, the two parts' products added: pair 2 m + r is row
+// lane / 4 + 8 r, columns 8 m + 2 (lane % 4) and one on
+__device__ __forceinline__ void frag_ld(uint32_t t, uint64_t (&x)[4]) {
+  uint32_t a[2][4], b[2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    tmem_ld_16x256b(t + 8 * m, a[m]);
+    tmem_ld_16x256b(t + N + 8 * m, b[m]);
+  }
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    x[j] = add2(pack2f(__uint_as_float(a[j >> 1][2 * (j & 1)]), __uint_as_float(a[j >> 1][2 * (j & 1) + 1])),
+                pack2f(__uint_as_float(b[j >> 1][2 * (j & 1)]), __uint_as_float(b[j >> 1][2 * (j & 1) + 1])));
+}
+}  // namespace thin
+
+template <int K>
+__global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a,
+                                                                   int V) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  using L = thin::Lay<K>;
+  using namespace thin;
+  const uint32_t shift = (1024u - (smem_u32(raw) & 1023u)) & 1023u;
+  uint8_t* sm = raw + shift;
+  if (shift > L::SLACK) {
+    if (threadIdx.x == 0) atomicOr(a.p.status, kStatusTimeout);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
+  volatile uint32_t* failed = tslot + 1;
+  const Params& p = a.p;
+  const int slices = V / N, unit = blockIdx.x / slices, v0 = (blockIdx.x % slices) * N;
+  const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long tok0;
+  int len;
+  const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
+  const int nch = num_chunks(len), slot0 = first_slot(a, seq, tok0);
+  if (tid == 0) {
+    for (int b = 0; b < NBAR; ++b) mbar_init(&bars[b], b >= SREADY && b <= OUTREADY ? NW : 1);
+    *failed = 0u;
+    fence_mbar_init();
+  }
+  if (warp == NW) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  wait_for_previous_kernel();  // the records, the cleared status
+  let_next_kernel_start();
+  if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
+  auto wait = [&](int b, uint32_t parity) {        // of a whole warp; false once the CTA has failed
+    if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
+    if (lane == 0 && *failed == 0u) {
+      atomicOr(p.status, kStatusTimeout);
+      *failed = 1u;
+    }
+    return false;
+  };
+  auto arrive = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[b]);
+  };
+
+  if (warp == NW + 1) {
+    // ---------------------------------------------------------------- loads ---
+    auto record = [&](int n) { return a.rec + (static_cast<size_t>(slot0 + n) * p.HV + hv) * kRecBytes; };
+    auto load = [&](int n) {
+      if (lane == 0) {
+        uint8_t* st = sm + (n % 3) * L::STAGE;
+        uint64_t* full = &bars[FULL + n % 3];
+        const int tok = static_cast<int>(tok0 + C * static_cast<long>(n));
+        mbar_arrive_expect_tx_relaxed(full, L::STAGE);
+#pragma unroll
+        for (int b = 0; b < K / 64; ++b) {
+          tma_load_3d(st + b * kTileBytes, &maps.k, full, 64 * b, hk, tok);
+          tma_load_3d(st + b * kTileBytes + 8192, &maps.q, full, 64 * b, hk, tok);
+        }
+        bulk_load(st + L::FAC, record(n) + kRecFactors, 1024, full);
+        tma_load_3d(st + L::VS, &maps.v, full, v0, hv, tok);
+      }
+      __syncwarp();
+    };
+    auto load_t = [&](int n) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx_relaxed(&bars[TFULL + (n & 1)], 2 * kTileBytes);
+        bulk_load(sm + L::TT + (n & 1) * 2 * kTileBytes, record(n), 2 * kTileBytes, &bars[TFULL + (n & 1)]);
+      }
+      __syncwarp();
+    };
+    int nf = 0, nt = 0;
+    for (; nf < 3 && nf < nch; ++nf) {
+      load(nf);
+      if (nf < 2) load_t(nt++);
+    }
+    for (int n = 1; n < nch; ++n) {
+      if (nt < nch) {                              // free once step 2 of the chunk before is done
+        if (!wait(TFREE + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        load_t(nt++);
+      }
+      if (nf < nch) {                              // a stage's readers are done once the next chunk's products start
+        if (!wait(EMPTY + (n - 1) % 3, ((n - 1) / 3) & 1)) break;
+        load(nf++);
+      }
+    }
+    // what was issued lands before the CTA gives up its memory
+    for (int m = nf < 3 ? 0 : nf - 3; m < nf; ++m) mbar_wait(&bars[FULL + m % 3], (m / 3) & 1, kDrainNs);
+    for (int m = nt < 2 ? 0 : nt - 2; m < nt; ++m) mbar_wait(&bars[TFULL + (m & 1)], (m >> 1) & 1, kDrainNs);
+  } else if (warp == NW) {
+    // ------------------------------------------------------------- products ---
+    const uint32_t sb = smem_u32(sm);
+    constexpr uint32_t id64 = idesc_f16kind(64, 2 * N) | IDESC_B_MN_MAJOR;
+    constexpr uint32_t idk = idesc_f16kind(128, 2 * N) | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;  // (K = 64: the other lanes' rows are some other tile)
+    const uint64_t ds = sdesc(sb + L::S, 128 * 128, 1024, 2), dy = sdesc(sb + L::Y, C * 128, 1024, 2), dv = sdesc(sb + L::VN, C * 128, 1024, 2);
+    auto times_s = [&](uint32_t d, uint64_t rows) {
+#pragma unroll
+      for (int b = 0; b < K / 64; ++b) umma4<32, 2048>(d, rows + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id64, b > 0);
+    };
+    auto times_y = [&](uint32_t d, uint64_t rows) {  // high and low parts of T or R
+      umma4<32, 2048>(d, rows, dy, id64, 0u);
+      umma4<32, 2048>(d, rows + (kTileBytes >> 4), dy, id64, 1u);
+    };
+    for (int n = 0; n < nch; ++n) {
+      const uint32_t ph = n & 1, st = sb + (n % 3) * L::STAGE;
+      const uint64_t dkq = sdesc_sw128(st), dkt = sdesc(st, kTileBytes, 1024, 2), dt = sdesc_sw128(sb + L::TT + ph * 2 * kTileBytes);
+      if (!wait(FULL + n % 3, (n / 3) & 1)) break;
+      if (!wait(SREADY, ph)) break;
+      tc_fence_after();
+      times_s(tmem + TK, dkq);
+      umma_commit_warp(&bars[D1]);
+      if (n > 0 && lane == 0) mbar_arrive(&bars[EMPTY + (n - 1) % 3]);
+      __syncwarp();
+      times_s(tmem + TQ + TURN * ph, dkq + (8192 >> 4));
+      if (!wait(TFULL + ph, (n >> 1) & 1)) break;
+      if (!wait(YREADY, ph)) break;
+      tc_fence_after();
+      times_y(tmem + thin::TT, dt);
+      umma_commit_warp(&bars[D2]);
+      times_y(tmem + TR + TURN * ph, dt + (8192 >> 4));
+      umma_commit_warp(&bars[TFREE + ph]);
+      if (!wait(VREADY, ph)) break;
+      tc_fence_after();
+      umma4<2048, 2048>(tmem + TD3, dkt, dv, idk, 0u);
+      umma_commit_warp(&bars[D3]);
+    }
+    umma_commit_warp(&bars[DRAIN]);                // what is in flight ends before the CTA gives up its memory
+    mbar_wait(&bars[DRAIN], 0, kDrainNs);
+  } else if (warp == NW + 2) {
+    // --------------------------------------------------------------- stores ---
+    for (int n = 0; n < nch; ++n) {
+      if (!wait(OUTREADY, n & 1)) break;
+      if (lane == 0) {
+        if (C * n + C <= len) {
+          tma_store_3d(&maps.o, sm + L::OUT, v0, hv, static_cast<int>(tok0 + C * static_cast<long>(n)));
+          bulk_commit();
+        }
+        bulk_wait_read();
+        mbar_arrive(&bars[OUTFREE]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_read();
+  } else {
+    // ------------------------------------------ state, Y, vn, output ---
+    const int quad = warp & 3, cg = warp >> 2, c0 = 16 * cg;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + c0;
+    // S: a key dim a thread, 16 columns
+    const int r = 32 * quad + lane;
+    const size_t soff = ((static_cast<size_t>(seq) * p.HV + hv) * K + r) * V + v0 + c0;
+    // tokens: rows i, i + 8; and the row of this thread's address in tile accesses
+    const int i = 16 * quad + (lane >> 2), ir = 16 * quad + (lane & 15), ch = 2 * cg + (lane >> 4);
+    const uint32_t in_v = sw64(ir, ch), in_y = sw128(ir, ch), in_ylow = sw128(ir, 4 + ch);
+    uint64_t s[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 t = p.s0 && r < K ? *reinterpret_cast<const float4*>(p.s0 + soff + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      s[2 * j] = pack2f(t.x, t.y);
+      s[2 * j + 1] = pack2f(t.z, t.w);
+    }
+    put_parts<N, 16>(sm + L::S, 0, r, c0, s);
+    fence_proxy_async_smem();
+    arrive(SREADY);
+    uint64_t x[4], y[4], bv[4], fe[2], fo[2], fy[2], gamma = 0;  // of the chunk: beta v, E, scale G, -beta G
+    uint32_t w[4], wl[4];
+    auto fetch = [&](int n) {                      // a chunk's v and factors
+      if (!wait(FULL + n % 3, (n / 3) & 1)) return false;
+      uint8_t* st = sm + (n % 3) * L::STAGE;
+      const float* fac = reinterpret_cast<const float*>(st + L::FAC);
+      if (tid == 0 && fac[kRecFailed] != 0.f) atomicOr(p.status, kStatusTimeout);
+      ldmatrix_x4(smem_u32(st + L::VS + in_v), w);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float g = fac[i + 8 * e], tail = fac[64 + i + 8 * e], be = fac[128 + i + 8 * e];
+        fe[e] = pack2f(tail, tail);
+        fo[e] = pack2f(p.scale * g, p.scale * g);
+        fy[e] = pack2f(-be * g, -be * g);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          bv[2 * m + e] = mul2(pack2f(be, be), pack2f(__uint_as_float(w[2 * m + e] << 16), __uint_as_float(w[2 * m + e] & 0xFFFF0000u)));
+      }
+      gamma = pack2f(fac[kRecGamma], fac[kRecGamma]);
+      // rows past the end hold the next sequence's tokens, whatever they are: zero wherever a
+      // sum over tokens meets them
+      if (tid < C && tid >= len - C * n) {
+#pragma unroll 1
+        for (int c = 0; c < 8 * (K / 64); ++c)
+          *reinterpret_cast<uint4*>(st + (c >> 3) * kTileBytes + sw128(tid, c & 7)) = make_uint4(0, 0, 0, 0);
+      }
+      return true;
+    };
+    auto put_y = [&](uint8_t* tile) {              // y as an operand's two parts
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split2(y[j], w[j], wl[j]);
+      stmatrix_x4(smem_u32(tile + in_y), w);
+      stmatrix_x4(smem_u32(tile + in_ylow), wl);
+      fence_proxy_async_smem();
+      tc_fence_before();
+    };
+    uint64_t fo_last[2];
+    auto output = [&](int n) {                     // of a chunk whose step 3 is done, and so its products
+      frag_ld(tl + TQ + TURN * (n & 1), y);
+      frag_ld(tl + TR + TURN * (n & 1), x);
+      if (n > 0 && !wait(OUTFREE, (n - 1) & 1)) return false;
+      const int rows = len - C * n;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = pack_pair(fma2(fo_last[j & 1], y[j], x[j]));
+        const int row = i + 8 * (j & 1);
+        if (rows < C && row < rows)
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) +
+                                       (static_cast<size_t>(tok0 + C * static_cast<long>(n) + row) * p.HV + hv) * V + v0 + c0 +
+                                       8 * (j >> 1) + 2 * (lane & 3)) = w[j];
+      }
+      if (rows >= C) stmatrix_x4(smem_u32(sm + L::OUT + in_v), w);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive(OUTREADY);
+      return true;
+    };
+    bool good = nch == 0 || fetch(0);
+    for (int n = 0; n < nch && good; ++n) {
+      const uint32_t ph = n & 1;
+      const int rows = len - C * n;                // of the chunk, from the first; 64 and more: all
+      if (!(good = wait(D1, ph))) break;
+      tc_fence_after();
+      frag_ld(tl + TK, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                // beta (v - G k S)
+        y[j] = fma2(fy[j & 1], x[j], bv[j]);
+        if (i + 8 * (j & 1) >= rows) y[j] = 0;
+      }
+      put_y(sm + L::Y);
+      arrive(YREADY);
+      if (n > 0 && !(good = output(n - 1))) break;
+      fo_last[0] = fo[0];
+      fo_last[1] = fo[1];
+      if (!(good = wait(D2, ph))) break;
+      tc_fence_after();
+      frag_ld(tl + thin::TT, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = mul2(fe[j & 1], x[j]);   // E vn
+      put_y(sm + L::VN);
+      arrive(VREADY);
+      const uint64_t gm = gamma;
+      if (n + 1 < nch && !(good = fetch(n + 1))) break;
+      if (!(good = wait(D3, ph))) break;
+      tc_fence_after();
+      uint64_t z[8];
+      tmem_ld_parts<N, 16>(tl + TD3, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = fma2(gm, s[j], z[j]);
+      put_parts<N, 16>(sm + L::S, 0, r, c0, s);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive(SREADY);
+    }
+    if (good && nch > 0) good = output(nch - 1);
+    if (good && p.sfin && r < K) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float4 t;
+        unpack2f(s[2 * j], t.x, t.y);
+        unpack2f(s[2 * j + 1], t.z, t.w);
+        *reinterpret_cast<float4*>(p.sfin + soff + 4 * j) = t;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == NW) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // ------------------------------------------------- chain, 128 columns wide ---
 // The same recurrence turned over, for V = 128 where the slices of 32 columns do not fit the
 // SMs at once, and in the backward: one CTA per pair, lane = value column, all transposed:
@@ -1412,6 +1741,13 @@ cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cud
 }
 
 template <int K>
+cudaError_t launch_thin(const ChainMaps& maps, const ChunkParams& a, int V, cudaStream_t st) {
+  static LaunchState state;
+  return launch_kernel(state, gdr_thin_kernel<K>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / thin::N), thin::THREADS,
+                       thin::Lay<K>::SMEM, true, st, maps, a, V);
+}
+
+template <int K>
 cudaError_t launch_wide(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
   static LaunchState state;
   return launch_kernel(state, gdr_wide_kernel<K>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV, wide::THREADS,
@@ -1467,8 +1803,8 @@ cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long w
   cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
   if (e != cudaSuccess) return e;
   if (N == 64 && V == 128) return K == 128 ? launch_wide<128>(maps, a, st) : launch_wide<64>(maps, a, st);
-  if (K == 128) return N == 32 ? launch_chain<128, 32>(maps, a, V, st) : launch_chain<128, 64>(maps, a, V, st);
-  return N == 32 ? launch_chain<64, 32>(maps, a, V, st) : launch_chain<64, 64>(maps, a, V, st);
+  if (N == 32) return K == 128 ? launch_thin<128>(maps, a, V, st) : launch_thin<64>(maps, a, V, st);
+  return K == 128 ? launch_chain<128, 64>(maps, a, V, st) : launch_chain<64, 64>(maps, a, V, st);
 }
 
 // Bytes of a backward's intermediates per (slot, value head): the record, S and dS', vn and z.
