@@ -537,14 +537,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   let_next_kernel_start();
   if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
   // waits of a whole warp; false once the CTA has failed
-  auto wait = [&](int b, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
-    if (lane == 0 && *failed == 0u) {
-      atomicOr(p.status, kStatusTimeout);
-      *failed = 1u;
-    }
-    return false;
-  };
+  auto wait = [&](int b, uint32_t parity) { return wait_warp(&bars[b], parity, a.wait_ns, failed, p.status); };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[b]);
@@ -959,14 +952,7 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
   wait_for_previous_kernel();  // the records, the cleared status
   let_next_kernel_start();
   if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
-  auto wait = [&](int b, uint32_t parity) {        // of a whole warp; false once the CTA has failed
-    if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
-    if (lane == 0 && *failed == 0u) {
-      atomicOr(p.status, kStatusTimeout);
-      *failed = 1u;
-    }
-    return false;
-  };
+  auto wait = [&](int b, uint32_t parity) { return wait_warp(&bars[b], parity, a.wait_ns, failed, p.status); };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[b]);
@@ -1328,14 +1314,7 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
   wait_for_previous_kernel();  // the records, the cleared status
   let_next_kernel_start();
   if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
-  auto wait = [&](int b, uint32_t parity) {        // of a whole warp; false once the CTA has failed
-    if (__all_sync(0xFFFFFFFFu, wait_phase(&bars[b], parity, a.wait_ns, failed))) return true;
-    if (lane == 0 && *failed == 0u) {
-      atomicOr(p.status, kStatusTimeout);
-      *failed = 1u;
-    }
-    return false;
-  };
+  auto wait = [&](int b, uint32_t parity) { return wait_warp(&bars[b], parity, a.wait_ns, failed, p.status); };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[b]);

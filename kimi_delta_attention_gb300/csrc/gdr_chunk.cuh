@@ -208,6 +208,23 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint6
   return true;
 }
 
+// The same by a whole warp of a CTA that reports its failure once.  What a wait needs after its
+// first look is one function for all of them: written out at every wait, this code alone
+// pushed the others out of the instruction cache.
+static __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* failed,
+                                         uint32_t* status) {
+  if (__all_sync(0xFFFFFFFFu, wait_phase(bar, parity, limit_ns, failed))) return true;
+  if ((threadIdx.x & 31) == 0 && *failed == 0u) {
+    atomicOr(status, kStatusTimeout);
+    *failed = 1u;
+  }
+  return false;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* failed,
+                                          uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || wait_longer(bar, parity, limit_ns, failed, status);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
