@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 3);
   const Params& p = a.p;
   const int slot = blockIdx.x / p.HV, hv = blockIdx.x % p.HV, hk = hv / (p.HV / p.H);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   int seq, rows;
   long tok;
   if (blockIdx.x == 0 && tid == 0) *p.status = 0u;
@@ -150,10 +150,8 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
     __syncwarp();
     const uint64_t d = sdesc_sw128(smem_u32(sm));
 #pragma unroll
-    for (int s = 0; s < K / 16; ++s) {
-      const uint64_t o = ((s >> 2) * kTileBytes + (s & 3) * 32) >> 4;
-      umma_f16_warp(tmem, d + o, d + o, idesc_f16kind(128, 64), s > 0 ? 1u : 0u);
-    }
+    for (int b = 0; b < K / 64; ++b)
+      umma4<32, 32>(tmem, d + (b * kTileBytes >> 4), d + (b * kTileBytes >> 4), idesc_f16kind(128, 64), b > 0);
     umma_commit_warp(&bar[1]);
   }
   // row i of D in log2: gc_i - gc_j; the factors of the row
@@ -511,7 +509,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   const int slices = V / N;
   const int unit = block / slices, v0 = (block % slices) * N;
   const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   long tok0;
   int len;
   const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
@@ -931,7 +929,7 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
   const Params& p = a.p;
   const int slices = V / N, unit = blockIdx.x / slices, v0 = (blockIdx.x % slices) * N;
   const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   long tok0;
   int len;
   const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
@@ -1292,7 +1290,7 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
   volatile uint32_t* failed = tslot + 1;
   const Params& p = a.p;
   const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   long tok0;
   int len;
   const bool in_order = seq_tokens(p.cu, p.T, p.num_seqs, nullptr, seq, tok0, len);
@@ -1369,23 +1367,22 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
     // ------------------------------------------------------------- products ---
     const uint32_t sb = smem_u32(sm);
     constexpr uint32_t id64 = idesc_f16kind(128, 64), idk = idesc_f16kind(128, K) | IDESC_B_MN_MAJOR;
-    constexpr uint32_t row[4] = {0, 2, 4, 6}, col[4] = {0, 128, 256, 384};   // 16 of K, in 16 bytes
     auto s_times = [&](uint32_t d, uint64_t b) {   // both parts of S^T times 64 rows of [k; q]
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int kb = 0; kb < K / 64; ++kb)
-          umma_ts_chain<4>(d, tmem + L::TS + h * (K / 2) + 32 * kb, b + (kb * kTileBytes >> 4), row, id64, h + kb > 0);
+          umma_ts4<32>(d, tmem + L::TS + h * (K / 2) + 32 * kb, b + (kb * kTileBytes >> 4), id64, h + kb > 0);
     };
     auto y_times = [&](uint32_t d, uint64_t b) {   // Y^T times 64 rows of [T; R]: high high, high low, low high
-      constexpr uint32_t id = MODE == REVERSE ? id64 | IDESC_B_MN_MAJOR : id64, acc = MODE == REVERSE;
-      umma_ts_chain<4>(d, tmem + L::TY, b, MODE == REVERSE ? col : row, id, acc);
-      umma_ts_chain<4>(d, tmem + L::TY, b + (kTileBytes >> 4), MODE == REVERSE ? col : row, id, 1u);
-      umma_ts_chain<4>(d, tmem + L::TY + 32, b, MODE == REVERSE ? col : row, id, 1u);
+      constexpr uint32_t id = MODE == REVERSE ? id64 | IDESC_B_MN_MAJOR : id64, acc = MODE == REVERSE, step = MODE == REVERSE ? 2048 : 32;
+      umma_ts4<step>(d, tmem + L::TY, b, id, acc);
+      umma_ts4<step>(d, tmem + L::TY, b + (kTileBytes >> 4), id, 1u);
+      umma_ts4<step>(d, tmem + L::TY + 32, b, id, 1u);
     };
     auto into_state = [&](uint32_t at, uint64_t b, uint32_t acc) {  // both parts of a [columns, tokens] operand times rows of q or k
-      umma_ts_chain<4>(tmem + L::TD3, tmem + at, b, col, idk, acc);
-      umma_ts_chain<4>(tmem + L::TD3, tmem + at + 32, b, col, idk, 1u);
+      umma_ts4<2048>(tmem + L::TD3, tmem + at, b, idk, acc);
+      umma_ts4<2048>(tmem + L::TD3, tmem + at + 32, b, idk, 1u);
     };
     for (int n = 0; n < nch; ++n) {
       const uint32_t ph = n & 1, st = sb + ph * L::STAGE, tt = MODE == FORWARD ? st + L::TT : sb + L::TT1;

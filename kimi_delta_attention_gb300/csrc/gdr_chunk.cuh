@@ -164,23 +164,34 @@ __device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t c) {
   return (r >> 3) * 512u + (r & 7) * 64u + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Four chained products D (+)= A B of a converged warp behind one elect (16 of K each; AS and
-// BS bytes from one to the next): the first accumulates if `acc`, the others always.
+// A real branch to one lane of a converged warp: a predicate on every product and its
+// operands' way into uniform registers cost 27 instructions a product, the branch 8.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+// The warp's number, known to the compiler as the same for all its lanes.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+
+// Four chained products D (+)= A B (16 of K each; AS and BS bytes from one to the next) of a
+// converged warp: the first accumulates if `acc`, the others always.
 template <uint32_t AS, uint32_t BS>
 __device__ __forceinline__ void umma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "add.u64 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
-      "add.u64 a2, a1, %5;\n\tadd.u64 b2, b1, %6;\n\t"
-      "add.u64 a3, a2, %5;\n\tadd.u64 b3, b2, %6;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS >> 4), "n"(BS >> 4)
-      : "memory");
+  if (elect_one()) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) umma_f16(d, a + s * (AS >> 4), b + s * (BS >> 4), idesc, s ? 1u : acc);
+  }
+  __syncwarp();
+}
+// The same with A in tensor memory (8 columns are 16 of K).
+template <uint32_t BS>
+__device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (elect_one()) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) umma_f16_ts(d, a + 8 * s, b + s * (BS >> 4), idesc, s ? 1u : acc);
+  }
+  __syncwarp();
 }
 
 // The same in a loop, for kernels whose code must stay small.

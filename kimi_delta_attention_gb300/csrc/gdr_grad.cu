@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
     int u;
   };
   Upcoming* upcoming = reinterpret_cast<Upcoming*>(wsum + 16);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
 
   Unit cur;
   int u = next_unit(a, blockIdx.x, units, cur);
