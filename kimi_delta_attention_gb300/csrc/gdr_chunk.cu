@@ -592,11 +592,9 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     constexpr uint32_t id2n = idesc_f16kind(128, 2 * N) | IDESC_B_MN_MAJOR;   // both parts of B
     constexpr uint32_t idn = idesc_f16kind(128, N == 32 ? 2 * N : N) | IDESC_B_MN_MAJOR;  // the high part (N = 32: both)
     const uint64_t ds = sdesc(sb + L::S, L::LBO_S, 1024, 2), dy = sdesc(sb + L::Y, L::LBO_Y, 1024, 2);
-    // four products, 16 of K each, AS and BS bytes apart.  Only FORWARD writes them out: the
-    // backward's code then no longer fits the instruction cache beside the other warps' (its
-    // warps waited for instructions 3.5 cycles of every 9 that they did not wait for data)
     auto issue = [&](uint32_t d, uint64_t aa, uint64_t bb, uint32_t idesc, uint32_t acc, uint32_t as) {
-      umma4_loop(d, aa, as, bb, 2048, idesc, acc);
+      if (as == 32) umma4<32, 2048>(d, aa, bb, idesc, acc);
+      else umma4<2048, 2048>(d, aa, bb, idesc, acc);
     };
     for (int n = 0; n < nch; ++n) {
       const uint32_t ph = n & 1, st = sb + ph * L::STAGE, tt = MODE == FORWARD ? st + L::TT : sb + L::TT1;
@@ -605,14 +603,8 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       if (!wait(FULL0 + (n & 1), (n >> 1) & 1)) break;
       if (!wait(SREADY, ph)) break;
       tc_fence_after();
-      if (MODE == FORWARD) {
 #pragma unroll
-        for (int b = 0; b < K / 64; ++b)
-          umma4<32, 2048>(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0);
-      } else {
-#pragma unroll 1
-        for (int b = 0; b < K / 64; ++b) issue(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0, 32);
-      }
+      for (int b = 0; b < K / 64; ++b) issue(tmem, dkq + (b * kTileBytes >> 4), ds + (b * 8192 >> 4), id2n, b > 0, 32);
       umma_commit_warp(&bars[D1]);
       if (n > 0 && lane == 0) mbar_arrive(&bars[EMPTY0 + ((n - 1) & 1)]);
       __syncwarp();
@@ -623,7 +615,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         const uint64_t dd = sdesc(st + L::VS, 8192, 1024, 2);
         constexpr uint32_t idr = idesc_f16kind(128, N) | IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR;
         // R^T do, the two parts of R (rows 64-127 of the record's tiles); q^T (scale G do)
-#pragma unroll 1
+#pragma unroll
         for (uint32_t h = 0; h < 2; ++h) issue(tmem + TD2R, dt + ((8192 + h * kTileBytes) >> 4), dd, idr, h, 2048);
         issue(tmem + TD3, dkt + (8192 >> 4), dy + (8192 >> 4), id2n | IDESC_A_MN_MAJOR, 0u, 2048);
       }
@@ -631,19 +623,13 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       tc_fence_after();
       constexpr uint32_t am = MODE == REVERSE ? IDESC_A_MN_MAJOR : 0u;
       constexpr uint32_t as = MODE == REVERSE ? 2048 : 32;   // bytes of 16 of K in [T; R]
-      if (MODE == FORWARD) {
-        umma4<as, 2048>(tmem + TD2, dt, dy, id2n | am, 0u);
-        umma4<as, 2048>(tmem + TD2, dt + (kTileBytes >> 4), dy, idn | am, 1u);
-      } else {
-#pragma unroll 1
-        for (uint32_t h = 0; h < 2; ++h) issue(tmem + TD2, dt + (h * kTileBytes >> 4), dy, (h ? idn : id2n) | am, h, as);
-      }
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h) issue(tmem + TD2, dt + (h * kTileBytes >> 4), dy, (h ? idn : id2n) | am, h, as);
       umma_commit_warp(&bars[D2]);
       if (MODE != FORWARD) umma_commit_warp(&bars[TFREE]);
       if (!wait(VREADY, ph)) break;
       tc_fence_after();
-      if (MODE == FORWARD) umma4<2048, 2048>(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, 0u);
-      else issue(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, MODE == REVERSE, 2048);
+      issue(tmem + TD3, dkt, dy, id2n | IDESC_A_MN_MAJOR, MODE == REVERSE, 2048);
       umma_commit_warp(&bars[D3]);
     }
     // what is in flight ends before the CTA gives up its memory

@@ -194,13 +194,6 @@ __device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint64_t b, uin
   __syncwarp();
 }
 
-// The same in a loop, for kernels whose code must stay small.
-__device__ __forceinline__ void umma4_loop(uint32_t d, uint64_t a, uint32_t as, uint64_t b, uint32_t bs, uint32_t idesc,
-                                           uint32_t acc) {
-#pragma unroll 1
-  for (int s = 0; s < 4; ++s, a += as >> 4, b += bs >> 4, acc = 1u) umma_f16_warp(d, a, b, idesc, acc);
-}
-
 // A kernel of a call starts while the one before it still runs: before it touches what that
 // one wrote it waits for its end, and it lets the next one start once all its blocks have
 // started and taken their TMEM (a waiting block must not hold what a running one needs).
