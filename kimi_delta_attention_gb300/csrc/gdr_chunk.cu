@@ -22,7 +22,9 @@ namespace {
 // What bounds it is instruction fetch and issue: written out straight (the solves unrolled
 // into registers), the code ran once per CTA at an instruction a cycle and SM, 47 us for 2048
 // chunks and heads by plain substitution, 87 us with block products unrolled; so the block
-// product is one small loop body and its operands stay in shared memory.
+// product is one small loop body and its operands stay in shared memory.  Now 31 us for those
+// 2048 (K = 128), 275 us for 23424 of packed sequences: 1.9 instructions a cycle and SM, 6600 a
+// chunk and head; it writes 33 KB each.
 namespace prep {
 constexpr int NT = 128;
 constexpr uint32_t LDM = 68;                           // floats between rows of M and T: no bank conflicts
@@ -356,8 +358,7 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ chain ---
-// One CTA per (sequence, value head, N value columns): the columns of S never meet.  N / 4
-// warps hold the state in fp32 registers (warp w: key dims 32 (w % 4) + lane, columns
+// For V = 64: one CTA per (sequence, value head).  16 warps hold the state in fp32 registers (warp w: key dims 32 (w % 4) + lane, columns
 // 16 (w / 4) ..) and do everything between the products; of three more one issues the
 // products, one loads the chunks two ahead (TMA tiles of k, q and v, the record by bulk
 // copy), one stores results from their staging.  Per chunk:
@@ -368,7 +369,10 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
 // and low parts of S, Y and E vn lie side by side as 2 N columns of one operand (their
 // products land in 2 N columns and are added when read), so that a product is one
 // instruction per 16 of K: the chain is bound by the latency of these three steps, not by
-// the tensor cores' rate.
+// the tensor cores' rate.  (In all chains the code between the products has to stay small:
+// it does not fit the first instruction caches, and every warp's wait, branch and product
+// issue that was made shorter showed at once -- the products' issue behind one branch, for
+// one, took 124 us of a forward to 118.)
 //
 // SAVE is the same recurrence for the backward: no output (the q and R rows are not
 // loaded; what lies in their place only meets lanes that nobody reads); the state entering
@@ -382,11 +386,9 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
 // with the transposed operands read from the same tiles (MN-major), so M is 128 where only
 // 64 lanes are wanted: the other lanes' atom is some other tile and nobody reads them.
 namespace chain {
-constexpr int groups(int N) { return N / 16; }           // of 16 columns: a quadrant's warps each take one
-constexpr int warps(int N) { return 4 * groups(N); }     // that hold the state; then products, loads, stores
-constexpr int threads(int N) { return 32 * (warps(N) + 3); }
+constexpr int N = 64, NW = N / 4, THREADS = 32 * (NW + 3);   // NW warps hold the state; then products, loads, stores
 enum Mode { FORWARD, SAVE, REVERSE };
-template <int K, int N, Mode MODE>
+template <int K, Mode MODE>
 struct Lay {
   static constexpr bool BWD = MODE != FORWARD;
   static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : C;    // REVERSE: rows 64-127 hold scale G do
@@ -414,20 +416,17 @@ enum { FULL0 = 0, FULL1, EMPTY0, EMPTY1, TFULL, TFREE, D1, D2, D3, SREADY, YREAD
        DRAIN, NBAR };
 }  // namespace chain
 
-// CPT values of a row (in pairs) as the two parts of a 2 N-column operand (c0: first column).
-template <int N, int CPT>
-__device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, int c0, const uint64_t (&x)[CPT / 2]) {
+// 16 values of a row (in pairs) as the two parts of a 2 N-column operand (c0: first column; lbo:
+// between its 64-column atoms).
+template <int N>
+__device__ __forceinline__ void put_parts(uint8_t* base, uint32_t lbo, int row, int c0, const uint64_t (&x)[8]) {
 #pragma unroll
-  for (int j = 0; j < CPT / 8; ++j) {
+  for (int j = 0; j < 2; ++j) {
     uint4 h, l;
     split8(x + 4 * j, h, l);
-    if constexpr (N == 32) {
-      *reinterpret_cast<uint4*>(base + sw128(row, (c0 >> 3) + j)) = h;
-      *reinterpret_cast<uint4*>(base + sw128(row, 4 + (c0 >> 3) + j)) = l;
-    } else {
-      *reinterpret_cast<uint4*>(base + sw128(row, (c0 >> 3) + j)) = h;
-      *reinterpret_cast<uint4*>(base + lbo + sw128(row, (c0 >> 3) + j)) = l;
-    }
+    *reinterpret_cast<uint4*>(base + sw128(row, (c0 >> 3) + j)) = h;
+    if constexpr (N == 32) *reinterpret_cast<uint4*>(base + sw128(row, 4 + (c0 >> 3) + j)) = l;   // both in one 128-byte row
+    else *reinterpret_cast<uint4*>(base + lbo + sw128(row, (c0 >> 3) + j)) = l;
   }
 }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
@@ -435,39 +434,30 @@ __device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
   unpack2f(x, a, b);
   return pack_bf16(a, b);
 }
-// CPT values of a row as bf16: to the staging tile (its TMA store takes whole chunks), or
+// 16 values of a row as bf16: to the staging tile (its TMA store takes whole chunks), or
 // straight to memory.
-template <int N, int CPT>
-__device__ __forceinline__ void put_tile(uint8_t* tile, int row, int c0, const uint64_t (&x)[CPT / 2]) {
+__device__ __forceinline__ void put_tile(uint8_t* tile, int row, int c0, const uint64_t (&x)[8]) {
 #pragma unroll
-  for (int j = 0; j < CPT / 8; ++j) {
-    const uint32_t ch = (c0 >> 3) + j;
-    *reinterpret_cast<uint4*>(tile + (N == 32 ? sw64(row, ch) : sw128(row, ch))) =
+  for (int j = 0; j < 2; ++j)
+    *reinterpret_cast<uint4*>(tile + sw128(row, (c0 >> 3) + j)) =
         make_uint4(pack_pair(x[4 * j]), pack_pair(x[4 * j + 1]), pack_pair(x[4 * j + 2]), pack_pair(x[4 * j + 3]));
-  }
 }
-template <int CPT>
-__device__ __forceinline__ void put_bf16(void* out, size_t at, const uint64_t (&x)[CPT / 2]) {
+__device__ __forceinline__ void put_bf16(void* out, size_t at, const uint64_t (&x)[8]) {
   __nv_bfloat16* op = static_cast<__nv_bfloat16*>(out) + at;
 #pragma unroll
-  for (int j = 0; j < CPT / 8; ++j)
+  for (int j = 0; j < 2; ++j)
     *reinterpret_cast<uint4*>(op + 8 * j) =
         make_uint4(pack_pair(x[4 * j]), pack_pair(x[4 * j + 1]), pack_pair(x[4 * j + 2]), pack_pair(x[4 * j + 3]));
 }
-template <int CPT>
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&x)[CPT]) {
-  if constexpr (CPT == 16) tmem_ld16(t, x);
-  else tmem_ld32(t, x);
-}
 // x = the sum of the two parts' products
-template <int N, int CPT>
-__device__ __forceinline__ void tmem_ld_parts(uint32_t t, uint64_t (&x)[CPT / 2]) {
-  float a[CPT], b[CPT];
-  tmem_ld<CPT>(t, a);
-  tmem_ld<CPT>(t + N, b);
+template <int N>
+__device__ __forceinline__ void tmem_ld_parts(uint32_t t, uint64_t (&x)[8]) {
+  float a[16], b[16];
+  tmem_ld16(t, a);
+  tmem_ld16(t + N, b);
   tmem_ld_wait();
 #pragma unroll
-  for (int j = 0; j < CPT / 2; ++j) x[j] = add2(pack2f(a[2 * j], a[2 * j + 1]), pack2f(b[2 * j], b[2 * j + 1]));
+  for (int j = 0; j < 8; ++j) x[j] = add2(pack2f(a[2 * j], a[2 * j + 1]), pack2f(b[2 * j], b[2 * j + 1]));
 }
 
 // The sequence a chain takes: packed sequences start the longest first (by rank, ties by
@@ -491,11 +481,11 @@ __device__ __forceinline__ int ranked_sequence(const Params& p, int rank, volati
   return static_cast<int>(*slot);
 }
 
-template <int K, int N, chain::Mode MODE>
-__device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkParams& a, int V, int block, uint8_t* raw) {
-  using L = chain::Lay<K, N, MODE>;
+template <int K, chain::Mode MODE>
+__device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkParams& a, int unit, uint8_t* raw) {
+  using L = chain::Lay<K, MODE>;
   using namespace chain;
-  constexpr int CPT = 16, H2 = CPT / 2, NW = warps(N);
+  constexpr int CPT = 16, H2 = CPT / 2, V = N;
   const uint32_t shift = (1024u - (smem_u32(raw) & 1023u)) & 1023u;  // 0: nothing lies before the dynamic part
   uint8_t* sm = raw + shift;
   if (shift > L::SLACK) {
@@ -506,8 +496,6 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + NBAR);
   volatile uint32_t* failed = tslot + 1;
   const Params& p = a.p;
-  const int slices = V / N;
-  const int unit = block / slices, v0 = (block % slices) * N;
   const int hv = unit % p.HV, hk = hv / (p.HV / p.H), seq = ranked_sequence(p, unit / p.HV, tslot + 2);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   long tok0;
@@ -521,10 +509,9 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     *failed = 0u;
     fence_mbar_init();
   }
-  constexpr uint32_t TCOLS = N == 32 ? 256 : 512;
   constexpr uint32_t TD2 = 2 * N, TD3 = 4 * N, TD2R = 6 * N;
   if (warp == NW) {
-    tmem_alloc(tslot, TCOLS);
+    tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -557,7 +544,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         }
         bulk_load(st + L::FAC, record(n) + kRecFactors, 1024, full);
         if (MODE == FORWARD) bulk_load(st + L::TT, record(n), 2 * kTileBytes, full);
-        tma_load_3d(st + L::VS, &maps.v, full, v0, hv, tok);
+        tma_load_3d(st + L::VS, &maps.v, full, 0, hv, tok);
       }
       __syncwarp();
     };
@@ -590,7 +577,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     // ------------------------------------------------------------- products ---
     const uint32_t sb = smem_u32(sm);
     constexpr uint32_t id2n = idesc_f16kind(128, 2 * N) | IDESC_B_MN_MAJOR;   // both parts of B
-    constexpr uint32_t idn = idesc_f16kind(128, N == 32 ? 2 * N : N) | IDESC_B_MN_MAJOR;  // the high part (N = 32: both)
+    constexpr uint32_t idn = idesc_f16kind(128, N) | IDESC_B_MN_MAJOR;        // the high part
     const uint64_t ds = sdesc(sb + L::S, L::LBO_S, 1024, 2), dy = sdesc(sb + L::Y, L::LBO_Y, 1024, 2);
     auto issue = [&](uint32_t d, uint64_t aa, uint64_t bb, uint32_t idesc, uint32_t acc, uint32_t as) {
       if (as == 32) umma4<32, 2048>(d, aa, bb, idesc, acc);
@@ -643,7 +630,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       if (MODE != FORWARD) {
         if (!wait(SFREADY, n & 1)) break;
         if (lane == 0) {
-          bulk_store((MODE == SAVE ? a.states : a.dstates) + cu * K * V + (v0 >> 6) * (K * 64), sm + L::SF, K * 256);
+          bulk_store((MODE == SAVE ? a.states : a.dstates) + cu * K * V, sm + L::SF, K * 256);
           bulk_commit();
         }
         __syncwarp();
@@ -651,11 +638,10 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       if (!wait(OUTREADY, n & 1)) break;
       if (lane == 0) {
         if (MODE != FORWARD) {
-          uint8_t* img = (MODE == SAVE ? a.vn : a.z) + cu * (4 * C * static_cast<size_t>(V)) + (v0 >> 6) * 8192;
-          bulk_store(img, sm + L::OUT, 8192);
-          bulk_store(img + 2 * C * static_cast<size_t>(V), sm + L::OUT + 8192, 8192);
+          uint8_t* img = (MODE == SAVE ? a.vn : a.z) + cu * (4 * C * V);
+          bulk_store(img, sm + L::OUT, 2 * 8192);
         } else if (C * c + C <= len) {
-          tma_store_3d(&maps.o, sm + L::OUT, v0, hv, static_cast<int>(tok0 + C * static_cast<long>(c)));
+          tma_store_3d(&maps.o, sm + L::OUT, 0, hv, static_cast<int>(tok0 + C * static_cast<long>(c)));
         }
         bulk_commit();
         bulk_wait_read();
@@ -669,7 +655,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     const int quad = warp & 3, c0 = (warp >> 2) * CPT;
     const int r = 32 * quad + lane;                  // TMEM lane: key dim of S, row of [k; q]
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + c0;
-    const size_t soff = ((static_cast<size_t>(seq) * p.HV + hv) * K + r) * V + v0 + c0;
+    const size_t soff = ((static_cast<size_t>(seq) * p.HV + hv) * K + r) * V + c0;
     const bool isk = quad < 2;                       // token rows of k; else rows r - 64 of q
     const int i = r & 63;
     const float* first = MODE == REVERSE ? a.dfin : p.s0;
@@ -681,7 +667,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       s[2 * j] = pack2f(t.x, t.y);
       s[2 * j + 1] = pack2f(t.z, t.w);
     }
-    put_parts<N, CPT>(sm + L::S, L::LBO_S, r, c0, s);
+    put_parts<N>(sm + L::S, L::LBO_S, r, c0, s);
     fence_proxy_async_smem();
     arrive(SREADY);
     bool good = true;
@@ -696,7 +682,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       if (tid == 0 && fac[kRecFailed] != 0.f) atomicOr(p.status, kStatusTimeout);
       const float row = fac[i];
       const uint64_t gamma = pack2f(fac[kRecGamma], fac[kRecGamma]);
-      const size_t orow = (tok * p.HV + hv) * V + v0 + c0;
+      const size_t orow = (tok * p.HV + hv) * V + c0;
       // rows past the sequence's end hold the next one's tokens, whatever they are: every
       // operand that meets them in a sum over tokens has them zeroed first
       auto clear_row = [&](uint8_t* tile) {
@@ -725,7 +711,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
 #pragma unroll
         for (int j = 0; j < CPT / 8; ++j) {
           const uint32_t ch = (c0 >> 3) + j;
-          const uint4 u = *reinterpret_cast<const uint4*>(st + L::VS + (N == 32 ? sw64(i, ch) : sw128(i, ch)));
+          const uint4 u = *reinterpret_cast<const uint4*>(st + L::VS + sw128(i, ch));
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -739,7 +725,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         const uint64_t ff1 = pack2f(f1, f1), ff2 = pack2f(f2, f2);
         if (!(good = wait(D1, ph))) break;
         tc_fence_after();
-        tmem_ld_parts<N, CPT>(tl, x);
+        tmem_ld_parts<N>(tl, x);
 #pragma unroll
         for (int j = 0; j < H2; ++j) x[j] = MODE == REVERSE ? mul2(ff1, x[j]) : fma2(ff1, x[j], y[j]);
         if (!whole && !live) {
@@ -747,16 +733,16 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
           for (int j = 0; j < H2; ++j) x[j] = 0;
           if (warp < 4) clear_row(st);
         }
-        put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, x);
+        put_parts<N>(sm + L::Y, L::LBO_Y, i, c0, x);
         fence_proxy_async_smem();
         tc_fence_before();
         arrive(YREADY);
         if (!(good = wait(D2, ph))) break;
         tc_fence_after();
-        tmem_ld_parts<N, CPT>(tl + TD2, x);
+        tmem_ld_parts<N>(tl + TD2, x);
         if (MODE == REVERSE) {
           float t[CPT];
-          tmem_ld<CPT>(tl + TD2R, t);
+          tmem_ld16(tl + TD2R, t);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < H2; ++j) x[j] = add2(x[j], pack2f(t[2 * j], t[2 * j + 1]));
@@ -766,7 +752,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
           if (MODE == REVERSE && !live) x[j] = 0;   // (vn is zero there by itself: row i of T is e_i)
           y[j] = mul2(ff2, x[j]);
         }
-        put_parts<N, CPT>(sm + L::Y, L::LBO_Y, i, c0, y);
+        put_parts<N>(sm + L::Y, L::LBO_Y, i, c0, y);
         fence_proxy_async_smem();
         tc_fence_before();
         arrive(VREADY);
@@ -786,17 +772,17 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
         const uint64_t f = pack2f(p.scale * row, p.scale * row);
         if (!(good = wait(D1, ph))) break;
         tc_fence_after();
-        tmem_ld_parts<N, CPT>(tl, x);
+        tmem_ld_parts<N>(tl, x);
         if (!(good = wait(D2, ph))) break;
         tc_fence_after();
-        tmem_ld_parts<N, CPT>(tl + TD2, y);
+        tmem_ld_parts<N>(tl + TD2, y);
 #pragma unroll
         for (int j = 0; j < H2; ++j) x[j] = fma2(f, x[j], y[j]);
         // through shared memory: a row a thread straight to memory, the stores would take the
         // load/store unit 500 to 1300 cycles a chunk from the warps on the way to step 3
         if (n > 0 && !(good = wait(OUTFREE, (n - 1) & 1))) break;
-        if (whole) put_tile<N, CPT>(sm + L::OUT, i, c0, x);
-        else if (live) put_bf16<CPT>(p.out, orow, x);
+        if (whole) put_tile(sm + L::OUT, i, c0, x);
+        else if (live) put_bf16(p.out, orow, x);
         fence_proxy_async_smem();
         arrive(OUTREADY);
       } else if (MODE == REVERSE) {
@@ -809,7 +795,7 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
           for (int j = 0; j < CPT / 8; ++j)
             *reinterpret_cast<uint4*>(st + L::VS + sw128(i, (c0 >> 3) + j)) = make_uint4(0, 0, 0, 0);
         }
-        put_parts<N, CPT>(sm + L::Y, L::LBO_Y, 64 + i, c0, x);
+        put_parts<N>(sm + L::Y, L::LBO_Y, 64 + i, c0, x);
         fence_proxy_async_smem();
         arrive(QREADY);
         if (!(good = put_state())) break;
@@ -818,10 +804,10 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
       }
       if (!(good = wait(D3, ph))) break;
       tc_fence_after();
-      tmem_ld_parts<N, CPT>(tl + TD3, x);
+      tmem_ld_parts<N>(tl + TD3, x);
 #pragma unroll
       for (int j = 0; j < H2; ++j) s[j] = fma2(gamma, s[j], x[j]);
-      put_parts<N, CPT>(sm + L::S, L::LBO_S, r, c0, s);
+      put_parts<N>(sm + L::S, L::LBO_S, r, c0, s);
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(SREADY);
@@ -840,15 +826,14 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   __syncthreads();
   if (warp == NW) {
     tc_fence_after();
-    tmem_dealloc(tmem, TCOLS);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-template <int K, int N>
-__global__ void __launch_bounds__(chain::threads(N), 1) gdr_chain_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a,
-                                                                 int V) {
+template <int K>
+__global__ void __launch_bounds__(chain::THREADS, 1) gdr_chain_kernel(const __grid_constant__ ChainMaps maps, const ChunkParams a) {
   extern __shared__ __align__(16) uint8_t raw[];
-  chain_body<K, N, chain::FORWARD>(maps, a, V, blockIdx.x, raw);
+  chain_body<K, chain::FORWARD>(maps, a, blockIdx.x, raw);
 }
 
 // ------------------------------------------------- chain, 32 columns thin ---
@@ -859,7 +844,12 @@ __global__ void __launch_bounds__(chain::threads(N), 1) gdr_chain_kernel(const _
 // between the products lies on all four parts of the SM, on one code path, in fragments of
 // 8 x 8 tiles (v, Y, E vn and o move by tile accesses): a thread holds 8 values of a block.
 // What the recurrence does not wait for is done where a warp waits for a product: a chunk's
-// output while step 2 of the next runs, the next chunk's v and factors while step 3 runs.
+// output while step 2 of the next runs, the next chunk's v and factors while step 3 runs
+// (with two stages instead of three, the loads came too late for that: 158 us where it is
+// 130; eight further warps for the output were no faster).
+// 90 us for 4096 tokens, 32 heads of 128: 1.4 us a chunk, of it about 0.8 in the three
+// products' latency, the rest in the hand-over between warps.  [k; q] S as one product of
+// M = 128, the k rows on two of the four parts of the SM, took 110 us.
 namespace thin {
 constexpr int N = 32, NW = 8, THREADS = 32 * (NW + 3);
 // TMEM columns: both parts' products, 2 x 32 each; q S and R Y twice, for chunks in turn
@@ -1057,7 +1047,7 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
       s[2 * j] = pack2f(t.x, t.y);
       s[2 * j + 1] = pack2f(t.z, t.w);
     }
-    put_parts<N, 16>(sm + L::S, 0, r, c0, s);
+    put_parts<N>(sm + L::S, 0, r, c0, s);
     fence_proxy_async_smem();
     arrive(SREADY);
     uint64_t x[4], y[4], bv[4], fe[2], fo[2], fy[2], gamma = 0;  // of the chunk: beta v, E, scale G, -beta G
@@ -1146,10 +1136,10 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
       if (!(good = wait(D3, ph))) break;
       tc_fence_after();
       uint64_t z[8];
-      tmem_ld_parts<N, 16>(tl + TD3, z);
+      tmem_ld_parts<N>(tl + TD3, z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] = fma2(gm, s[j], z[j]);
-      put_parts<N, 16>(sm + L::S, 0, r, c0, s);
+      put_parts<N>(sm + L::S, 0, r, c0, s);
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(SREADY);
@@ -1184,6 +1174,12 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
 // memory, nothing is staged there in parts, and all 16 warps run one and the same code in
 // all three steps (a warp: 32 columns, 16 tokens or K / 4 key dims) -- against the
 // 64-column slices, whose two halves run different code.
+//
+// 380 us for 16 packed sequences (46402 tokens, 32 heads, 23424 chunks and heads), 2.5 us a
+// chunk: the products are 1.3 us of it at the tensor cores' rate (each fp32 operand counts
+// twice), the rest is the work between them, one after the other.  64-column slices took
+// 650.  Splitting the steps' operands in halves, products over the first while the second
+// is made, did not help (687 us a call for 680): both then fight for tensor memory.
 //
 // SAVE leaves out the q and R halves.  REVERSE:
 //   1. D1 = dS'^T k^T
@@ -1610,7 +1606,8 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
       if (!(good = wait(wide::D3, ph))) break;
       tc_fence_after();
       float z[DPT];
-      tmem_ld<DPT>(tl + L::TD3 + d0, z);
+      if constexpr (DPT == 16) tmem_ld16(tl + L::TD3 + d0, z);
+      else tmem_ld32(tl + L::TD3 + d0, z);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < DPT / 2; ++j) s[j] = fma2(gamma, s[j], pack2f(z[2 * j], z[2 * j + 1]));
@@ -1654,12 +1651,12 @@ __global__ void __launch_bounds__(wide::THREADS, 1) gdr_wide_chains_kernel(const
 // The backward's two chains in one launch: even blocks SAVE (maps: v), odd blocks REVERSE
 // (maps_r: d_out).  They share nothing but the records, so they run side by side.
 template <int K>
-__global__ void __launch_bounds__(chain::threads(64), 1) gdr_chains_kernel(const __grid_constant__ ChainMaps maps,
+__global__ void __launch_bounds__(chain::THREADS, 1) gdr_chains_kernel(const __grid_constant__ ChainMaps maps,
                                                                   const __grid_constant__ ChainMaps maps_r,
-                                                                  const ChunkParams a, int V) {
+                                                                  const ChunkParams a) {
   extern __shared__ __align__(16) uint8_t raw[];
-  if (blockIdx.x & 1) chain_body<K, 64, chain::REVERSE>(maps_r, a, V, blockIdx.x >> 1, raw);
-  else chain_body<K, 64, chain::SAVE>(maps, a, V, blockIdx.x >> 1, raw);
+  if (blockIdx.x & 1) chain_body<K, chain::REVERSE>(maps_r, a, blockIdx.x >> 1, raw);
+  else chain_body<K, chain::SAVE>(maps, a, blockIdx.x >> 1, raw);
 }
 
 // ------------------------------------------------------------------- host ---
@@ -1695,11 +1692,11 @@ cudaError_t launch_prep(const ChainMaps& maps, const ChunkParams& a, cudaStream_
                        maps, a);
 }
 
-template <int K, int N>
-cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, int V, cudaStream_t st) {
+template <int K>
+cudaError_t launch_chain(const ChainMaps& maps, const ChunkParams& a, cudaStream_t st) {
   static LaunchState state;
-  return launch_kernel(state, gdr_chain_kernel<K, N>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / N),
-                       chain::threads(N), chain::Lay<K, N, chain::FORWARD>::SMEM, true, st, maps, a, V);
+  return launch_kernel(state, gdr_chain_kernel<K>, static_cast<unsigned>(a.p.num_seqs) * a.p.HV, chain::THREADS,
+                       chain::Lay<K, chain::FORWARD>::SMEM, true, st, maps, a);
 }
 
 template <int K>
@@ -1725,12 +1722,12 @@ cudaError_t launch_wide_chains(const ChainMaps& maps, const ChainMaps& maps_r, c
 }
 
 template <int K>
-cudaError_t launch_chains(const ChainMaps& maps, const ChainMaps& maps_r, const ChunkParams& a, int V, cudaStream_t st) {
-  constexpr uint32_t bytes = chain::Lay<K, 64, chain::REVERSE>::SMEM;   // the larger of the two
-  static_assert(bytes >= chain::Lay<K, 64, chain::SAVE>::SMEM, "shared memory of the two chains");
+cudaError_t launch_chains(const ChainMaps& maps, const ChainMaps& maps_r, const ChunkParams& a, cudaStream_t st) {
+  constexpr uint32_t bytes = chain::Lay<K, chain::REVERSE>::SMEM;   // the larger of the two
+  static_assert(bytes >= chain::Lay<K, chain::SAVE>::SMEM, "shared memory of the two chains");
   static LaunchState state;
-  return launch_kernel(state, gdr_chains_kernel<K>, 2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV * (V / 64),
-                       chain::threads(64), bytes, true, st, maps, maps_r, a, V);
+  return launch_kernel(state, gdr_chains_kernel<K>, 2u * static_cast<unsigned>(a.p.num_seqs) * a.p.HV,
+                       chain::THREADS, bytes, true, st, maps, maps_r, a);
 }
 
 }  // namespace
@@ -1754,8 +1751,10 @@ cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long w
   a.wait_ns = wait_ns;
   a.chunks = (p.T + C - 1) / C;
   a.slots = static_cast<int>(chunk_slots(tokens, p.num_seqs, p.cu != nullptr, p.T));
-  // 32 columns a CTA while those CTAs fit the SMs at once (the chain's steps are latency, so
-  // more CTAs are free); else 64.
+  // Thin chains, 32 columns a CTA, while they fit the SMs at once: a step is latency, and more
+  // CTAs are free (4096 tokens, V = 128, 32 pairs: 119 us, wide 180).  Beyond that a pair's
+  // whole V in one CTA (64 pairs: wide 205, thin 226; 128 pairs: 256 and 432; V = 64, 128 pairs:
+  // 247 and 272).
   const int N = static_cast<long>(p.num_seqs) * p.HV * (V / 32) <= sm_count() ? 32 : 64;
   ChainMaps maps;
   std::memset(&maps, 0, sizeof(maps));
@@ -1766,7 +1765,7 @@ cudaError_t launch_chunk_fwd(const Params& p, uint8_t* rec, unsigned long long w
   if (e != cudaSuccess) return e;
   if (N == 64 && V == 128) return K == 128 ? launch_wide<128>(maps, a, st) : launch_wide<64>(maps, a, st);
   if (N == 32) return K == 128 ? launch_thin<128>(maps, a, V, st) : launch_thin<64>(maps, a, V, st);
-  return K == 128 ? launch_chain<128, 64>(maps, a, V, st) : launch_chain<64, 64>(maps, a, V, st);
+  return K == 128 ? launch_chain<128>(maps, a, st) : launch_chain<64>(maps, a, st);
 }
 
 // Bytes of a backward's intermediates per (slot, value head): the record, S and dS', vn and z.
@@ -1810,8 +1809,9 @@ cudaError_t launch_chunk_bwd(const Params& p, const void* dout, const float* dfi
     return cudaErrorInvalidValue;
   cudaError_t e = K == 128 ? launch_prep<128>(maps, a, st) : launch_prep<64>(maps, a, st);
   if (e != cudaSuccess) return e;
+  // (4096 tokens, 32 pairs: 439 us wide when 64-column slices, on twice the SMs, took 453)
   if (V == 128) e = K == 128 ? launch_wide_chains<128>(maps, maps_r, a, st) : launch_wide_chains<64>(maps, maps_r, a, st);
-  else e = K == 128 ? launch_chains<128>(maps, maps_r, a, V, st) : launch_chains<64>(maps, maps_r, a, V, st);
+  else e = K == 128 ? launch_chains<128>(maps, maps_r, a, st) : launch_chains<64>(maps, maps_r, a, st);
   if (e != cudaSuccess) return e;
   if ((e = launch_grads(maps_r, a, K, V, st)) != cudaSuccess || !grouped) return e;
   return launch_group_sum(static_cast<const float*>(a.dq), dq, dk, tokens, p.H, p.HV / p.H, K, st);

@@ -21,10 +21,15 @@
 // dots t every later dg sums up, takes dS' in three parts (dg off by 2.9e-6 in a model of
 // the arithmetic, 4.3e-6 with two; the largest of small cases 5.7e-6 and 9.9e-6).
 //
-// One CTA of 256 threads per (chunk, value head).  Products on tcgen05 with M = 128: rows
+// One CTA of 512 threads an SM, walking over the (chunk, value head) pairs.  Products on tcgen05 with M = 128: rows
 // 0-63 belong to q's side (do; A), rows 64-127 to k's side (z, vn; B), stacked in shared
 // memory so that one instruction serves both, and thread (lane r, quarter h) of the CTA owns
 // row r and a quarter of the key dims throughout.
+// 190 us for 2048 chunks and heads (K = V = 128).  A unit takes 27000 cycles for 33000
+// instructions: it is a chain of phases (loads, S and dS' into their parts, three groups of
+// products, the rows of dq and dk) of which only the loads overlap with their neighbours, and
+// these only where shared memory is free again (224 KB a unit: none to spare).  The loads are
+// not the bound: started half a unit apart on half of the SMs, it took as long.
 #include "gdr_chunk.cuh"
 
 namespace kda {
