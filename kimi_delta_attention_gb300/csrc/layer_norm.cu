@@ -116,6 +116,16 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float* red, int t) {
   }
 }
 
+// A 16-byte vector to shared memory without passing through registers; the issuing thread
+// alone reads it, so waiting for its own groups is all it needs.
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
 // One row per TPR threads, NV vectors of VEC values a thread (vector j of thread t at
 // column VEC (t + TPR j)).  A block walks over rows with its columns' weights in registers
 // (read per row they were 4 times the row's own bytes from L2: 65 us for 16384 rows of 4096
@@ -213,13 +223,16 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_kernel(const Params p) {
     y[c] = from_f32<IO>(fmaf((to_f32(x[c]) - mu) * r, p.w ? p.w[c] : 1.f, p.b ? p.b[c] : 0.f));
 }
 
-// Backward: the block's rows are blockIdx.x G + group, then every gridDim.x G further, the
-// next row's loads in flight; a thread meets the same columns in every row, so its share of
-// dw and db stays in registers.  The groups' shares are added in their order and written
-// once, as the block's part of [blocks, D].
-template <typename IO, int VEC, int NV, int TPR, int NT>
+// Backward: the block's rows are blockIdx.x G + group, then every gridDim.x G further; a
+// thread meets the same columns in every row, so its share of dw and db stays in registers.
+// The groups' shares are added in their order and written once, as the block's part of
+// [blocks, D].  The rows to come are on their way in a ring in shared memory of RING rows a
+// group, each thread's own vectors (RING = 0, for rows that are not vectors: the next row's
+// in registers; with these alone 32 KB an SM were in flight, 77 us for 16384 rows of 4096).
+template <typename IO, int VEC, int NV, int TPR, int NT, int RING>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(const Params p) {
   constexpr int G = NT / TPR;
+  extern __shared__ __align__(16) uint4 ring[];   // [RING][2 NV][NT]
   __shared__ float red[2][2 * (NT / 32)];
   __shared__ float share[G > 1 ? TPR * 16 : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -232,14 +245,21 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
   }
   Raw<IO, VEC> rx[NV], ry[NV];
   float mu, r;
-  auto fetch = [&](long row) {
+  const long step = static_cast<long>(gridDim.x) * G;
+  long base = static_cast<long>(blockIdx.x) * G;
+  auto fetch = [&](long row, int slot) {
     const bool live = row < p.rows;
     const IO* x = static_cast<const IO*>(p.x) + row * p.ldx;
     const IO* dy = static_cast<const IO*>(p.dy) + row * p.lddy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = VEC * (t + TPR * j);
-      if (live && c < p.D) {
+      if constexpr (RING > 0) {
+        if (live && c < p.D) {
+          copy_async(&ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x], x + c);
+          copy_async(&ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x], dy + c);
+        }
+      } else if (live && c < p.D) {
         rx[j].load(x + c);
         ry[j].load(dy + c);
       } else {
@@ -247,22 +267,35 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
         ry[j].zero();
       }
     }
-    mu = live ? p.mean[row] : 0.f;
-    r = live ? p.rstd[row] : 0.f;
+    if constexpr (RING > 0) copies_close();
   };
-  const long step = static_cast<long>(gridDim.x) * G;
-  long base = static_cast<long>(blockIdx.x) * G;
-  int buf = 0;
-  fetch(base + grp);
+  auto stats = [&](long row) {
+    mu = row < p.rows ? p.mean[row] : 0.f;
+    r = row < p.rows ? p.rstd[row] : 0.f;
+  };
+  int buf = 0, slot = 0;
+  if constexpr (RING > 0) {
+#pragma unroll
+    for (int n = 0; n < RING; ++n) fetch(base + grp + n * step, n);
+  } else {
+    fetch(base + grp, 0);
+  }
+  stats(base + grp);
   for (; base < p.rows; base += step) {
     const long row = base + grp;
     float xh[NV][VEC], a[NV][VEC], s[2] = {0.f, 0.f};
     const float rr = r;
+    if constexpr (RING > 0) copies_wait<RING - 1>();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      const bool in = VEC * (t + TPR * j) < p.D;   // (past D, xh is 0 for the sums)
+      if constexpr (RING > 0) {
+        const bool there = in && row < p.rows;
+        rx[j].u = there ? ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x] : make_uint4(0, 0, 0, 0);
+        ry[j].u = there ? ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x] : make_uint4(0, 0, 0, 0);
+      }
       rx[j].to(xh[j]);
       ry[j].to(a[j]);
-      const bool in = VEC * (t + TPR * j) < p.D;   // (past D, xh is 0 for the sums)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float h = in ? (xh[j][e] - mu) * r : 0.f, d = a[j][e];
@@ -274,7 +307,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
         s[1] = fmaf(a[j][e], h, s[1]);
       }
     }
-    fetch(row + step);
+    fetch(row + (RING > 0 ? RING : 1) * step, slot);
+    stats(row + step);
+    if (++slot >= RING) slot = 0;
     row_sum<TPR>(s, red[buf] + grp * (2 * TPR / 32), t);
     buf ^= 1;
     const float c0 = s[0] / p.D, c1 = s[1] / p.D;
@@ -392,9 +427,23 @@ int threads_per_row(int D) {
 template <typename IO, int VEC, int TPR, bool BWD>
 void launch_tpr(const Params& p, int grid, cudaStream_t st) {
   constexpr int NT = TPR < 256 ? 256 : TPR, NV = 16 / VEC;
-  if constexpr (BWD)
-    layer_norm_bwd_kernel<IO, VEC, NV, TPR, NT><<<grid, NT, 0, st>>>(p);
-  else
+  if constexpr (BWD) {
+    // as many rows, up to 4, as 192 KB an SM hold
+    constexpr size_t row = 2 * static_cast<size_t>(NV) * NT * 16, fit = 192 * 1024 / (row * (NT == 256 ? 2 : 1));
+    constexpr int RING = VEC == 1 ? 0 : fit < 4 ? fit : 4;
+    constexpr size_t bytes = RING * row;
+    if constexpr (RING > 0) {
+      static bool raised[64] = {};       // (a race raises it twice, to the same value)
+      int dev = 0;
+      cudaGetDevice(&dev);
+      if (dev < 0 || dev >= 64 || !raised[dev]) {
+        cudaFuncSetAttribute(layer_norm_bwd_kernel<IO, VEC, NV, TPR, NT, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+        if (dev >= 0 && dev < 64) raised[dev] = true;
+      }
+    }
+    layer_norm_bwd_kernel<IO, VEC, NV, TPR, NT, RING><<<grid, NT, bytes, st>>>(p);
+  } else
     layer_norm_kernel<IO, VEC, NV, TPR, NT><<<grid, NT, 0, st>>>(p);
 }
 
