@@ -6,8 +6,9 @@
 // Both passes are bound by HBM: 2 and 3 passes over the rows.  A row stays in the registers
 // of its threads between the sums and the result, so it is read once.  The second moment is
 // taken around the mean already known (no cancellation of large squares); all sums are fp32.
-// 16384 rows of 4096 bf16: forward 45 us (268 MB, 88 % of the copy bandwidth), backward 77 us
-// and 6 for the sums over its blocks (403 MB, 77 %: between two rows it waits for a block's sums).
+// 16384 rows of 4096 bf16: forward 45 us (268 MB, 88 % of the copy bandwidth), backward 80 us
+// with the sums over its blocks, a call among others (403 MB, 75 %; of it 4 in the second
+// kernel, and between two rows a block waits for its sums).
 #include <cstddef>
 #include <cstdint>
 
@@ -114,6 +115,29 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float* red, int t) {
       x[i] = s;
     }
   }
+}
+
+// Two fp32 values in one 64-bit register, and the arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // A 16-byte vector to shared memory without passing through registers; the issuing thread
@@ -228,7 +252,8 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_kernel(const Params p) {
 // The groups' shares are added in their order and written once, as the block's part of
 // [blocks, D].  The rows to come are on their way in a ring in shared memory of RING rows a
 // group, each thread's own vectors (RING = 0, for rows that are not vectors: the next row's
-// in registers; with these alone 32 KB an SM were in flight, 77 us for 16384 rows of 4096).
+// in registers; with these alone 32 KB an SM were in flight, a call of 16384 rows of 4096 took
+// 88 us, with the ring 84).  The arithmetic is in pairs of values (84 -> 82).
 template <typename IO, int VEC, int NV, int TPR, int NT, int RING>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(const Params p) {
   constexpr int G = NT / TPR;
@@ -236,12 +261,18 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
   __shared__ float red[2][2 * (NT / 32)];
   __shared__ float share[G > 1 ? TPR * 16 : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  float dw[NV][VEC], db[NV][VEC], w[NV][VEC];
+  // a thread's 16 values in pairs: value n = VEC j + e is element e of vector j
+  constexpr int NP = NV * VEC / 2;
+  uint64_t dw[NP], db[NP], w[NP];
+  {
+    float v[NV][VEC];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    load_param<VEC>(w[j], p.w, VEC * (t + TPR * j), p.D, 1.f);
+    for (int j = 0; j < NV; ++j) load_param<VEC>(v[j], p.w, VEC * (t + TPR * j), p.D, 1.f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
+    for (int n = 0; n < NP; ++n) {
+      w[n] = pair(v[2 * n / VEC][2 * n % VEC], v[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+      dw[n] = db[n] = 0ull;
+    }
   }
   Raw<IO, VEC> rx[NV], ry[NV];
   float mu, r;
@@ -283,30 +314,42 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
   stats(base + grp);
   for (; base < p.rows; base += step) {
     const long row = base + grp;
-    float xh[NV][VEC], a[NV][VEC], s[2] = {0.f, 0.f};
+    float vx[NV][VEC], vy[NV][VEC];
     const float rr = r;
     if constexpr (RING > 0) copies_wait<RING - 1>();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = VEC * (t + TPR * j) < p.D;   // (past D, xh is 0 for the sums)
+      const bool in = VEC * (t + TPR * j) < p.D;
       if constexpr (RING > 0) {
         const bool there = in && row < p.rows;
         rx[j].u = there ? ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x] : make_uint4(0, 0, 0, 0);
         ry[j].u = there ? ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x] : make_uint4(0, 0, 0, 0);
       }
-      rx[j].to(xh[j]);
-      ry[j].to(a[j]);
+      rx[j].to(vx[j]);
+      ry[j].to(vy[j]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float h = in ? (xh[j][e] - mu) * r : 0.f, d = a[j][e];
-        dw[j][e] = fmaf(d, h, dw[j][e]);
-        db[j][e] += d;
-        xh[j][e] = h;
-        a[j][e] = d * w[j][e];
-        s[0] += a[j][e];
-        s[1] = fmaf(a[j][e], h, s[1]);
+      for (int e = 0; e < VEC; ++e) vx[j][e] = in ? vx[j][e] : mu;   // (past D, xh is 0 for the sums)
+    }
+    uint64_t xh[NP], a[NP], s0 = 0ull, s1 = 0ull;
+    {
+      const uint64_t mm = pair(-mu, -mu), r2 = pair(r, r);
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        const uint64_t x = pair(vx[2 * n / VEC][2 * n % VEC], vx[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+        const uint64_t d = pair(vy[2 * n / VEC][2 * n % VEC], vy[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+        xh[n] = mul2(add2(x, mm), r2);
+        dw[n] = fma2(d, xh[n], dw[n]);
+        db[n] = add2(db[n], d);
+        a[n] = mul2(d, w[n]);
+        s0 = add2(s0, a[n]);
+        s1 = fma2(a[n], xh[n], s1);
       }
     }
+    float s[2], half;
+    unpair(s0, s[0], half);
+    s[0] += half;
+    unpair(s1, s[1], half);
+    s[1] += half;
     fetch(row + (RING > 0 ? RING : 1) * step, slot);
     stats(row + step);
     if (++slot >= RING) slot = 0;
@@ -315,19 +358,22 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     const float c0 = s[0] / p.D, c1 = s[1] / p.D;
     if (row < p.rows && p.y) {
       IO* dx = static_cast<IO*>(p.y) + row * p.D;
+      const uint64_t n0 = pair(-c0, -c0), n1 = pair(-c1, -c1), r2 = pair(rr, rr);
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        unpair(mul2(r2, fma2(xh[n], n1, add2(a[n], n0))), vx[2 * n / VEC][2 * n % VEC], vx[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = VEC * (t + TPR * j);
-        if (c < p.D) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) a[j][e] = rr * (a[j][e] - c0 - xh[j][e] * c1);
-          Raw<IO, VEC>::store(dx + c, a[j]);
-        }
+        if (c < p.D) Raw<IO, VEC>::store(dx + c, vx[j]);
       }
     }
   }
-  auto write = [&](float (&x)[NV][VEC], float* part) {
+  auto write = [&](const uint64_t (&sums)[NP], float* part) {
     if (!part) return;
+    float x[NV][VEC];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) unpair(sums[n], x[2 * n / VEC][2 * n % VEC], x[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
     for (int g = 0; g < G; ++g) {
       if (grp == g) {
 #pragma unroll
@@ -347,6 +393,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
       if (G > 1) __syncthreads();
     }
   };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   write(dw, p.pw);
   write(db, p.pb);
 }
@@ -391,6 +438,7 @@ __global__ void __launch_bounds__(1024) layer_norm_parts_kernel(const float* pw,
   const float* src = blockIdx.y == 0 ? pw : pb;
   float* dst = blockIdx.y == 0 ? dw : db;
   if (!dst) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts: this kernel starts under the one that writes them
   float s = 0.f;
   if (c < D) {
 #pragma unroll 8
@@ -512,8 +560,20 @@ cudaError_t launch_bwd(const void* x, long ldx, const void* dy, long lddy, const
     if (bf16) launch_io<__nv_bfloat16, true>(p, grid, st);
     else launch_io<float, true>(p, grid, st);
   }
-  if (dw || db)
-    layer_norm_parts_kernel<<<dim3((D + 31) / 32, 2), 1024, 0, st>>>(pw, pb, dw, db, rows > 0 ? grid : 0, D);
+  if (dw || db) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((D + 31) / 32, 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = rows > 0 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, layer_norm_parts_kernel, static_cast<const float*>(pw), static_cast<const float*>(pb),
+                                             dw, db, rows > 0 ? grid : 0, D);
+    if (e != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 
