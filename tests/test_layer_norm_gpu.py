@@ -70,6 +70,25 @@ def test_forward_and_backward(rows, D, io, affine):
     close(db, gb, "dbias")
 
 
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(9001, 256), (4003, 1024), (2501, 4096), (1201, 8192), (907, 16384)])
+def test_gradients_of_many_rows(rows, D, io):
+    """Several rows a block, and more than are in flight at once; each sum over the rows is a chain
+    of at most 10 rows, 32 groups and 10 parts, then a tree of 5: below the bound above."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, D, generator=gen, device="cuda").to(io)
+    dy = torch.randn(rows, D, generator=gen, device="cuda").to(io)
+    w = 1 + 0.3 * torch.randn(D, generator=gen, device="cuda")
+    _, mean, rstd = kda.kda_layer_norm_fwd(x, w, None, EPS)
+    dx, dw, db = kda.kda_layer_norm_bwd(x, dy, w, mean, rstd)
+    _, m_ref, r_ref = ref_fwd(x, None, None)
+    xh, d = (x.double() - m_ref[:, None]) * r_ref[:, None], dy.double()
+    a = d * w.double()
+    close(dx, r_ref[:, None] * (a - a.mean(-1, keepdim=True) - xh * (a * xh).mean(-1, keepdim=True)), "dx")
+    close(dw, (d * xh).sum(0), "dweight")
+    close(db, d.sum(0), "dbias")
+
+
 def test_large_mean():
     """The variance is taken around the mean: a mean of 1000 and a deviation of 1."""
     x = torch.randn(8, 2048, device="cuda") + 1000
