@@ -140,11 +140,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// A 16-byte vector to shared memory without passing through registers; the issuing thread
-// alone reads it, so waiting for its own groups is all it needs.
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src)
-               : "memory");
+// 16 or 4 bytes to shared memory without passing through registers; the issuing thread alone
+// reads them, so waiting for its own groups is all it needs.
+template <typename T>
+__device__ __forceinline__ void copy_async(T* dst, const void* src) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (sizeof(T) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -251,13 +253,15 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_kernel(const Params p) {
 // thread meets the same columns in every row, so its share of dw and db stays in registers.
 // The groups' shares are added in their order and written once, as the block's part of
 // [blocks, D].  The rows to come are on their way in a ring in shared memory of RING rows a
-// group, each thread's own vectors (RING = 0, for rows that are not vectors: the next row's
+// group, each thread's own vectors or elements (RING = 0, for single bf16 elements: the next row's
 // in registers; with these alone 32 KB an SM were in flight, a call of 16384 rows of 4096 took
 // 88 us, with the ring 84).  The arithmetic is in pairs of values (84 -> 82).
 template <typename IO, int VEC, int NV, int TPR, int NT, int RING>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(const Params p) {
   constexpr int G = NT / TPR;
-  extern __shared__ __align__(16) uint4 ring[];   // [RING][2 NV][NT]
+  using Slot = decltype(Raw<IO, VEC>::u);
+  extern __shared__ __align__(16) uint4 dynamic[];
+  Slot* ring = reinterpret_cast<Slot*>(dynamic);  // [RING][2 NV][NT]
   __shared__ float red[2][2 * (NT / 32)];
   __shared__ float share[G > 1 ? TPR * 16 : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -322,8 +326,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
       const bool in = VEC * (t + TPR * j) < p.D;
       if constexpr (RING > 0) {
         const bool there = in && row < p.rows;
-        rx[j].u = there ? ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x] : make_uint4(0, 0, 0, 0);
-        ry[j].u = there ? ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x] : make_uint4(0, 0, 0, 0);
+        rx[j].u = there ? ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x] : Slot{};
+        ry[j].u = there ? ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x] : Slot{};
       }
       rx[j].to(vx[j]);
       ry[j].to(vy[j]);
@@ -477,8 +481,8 @@ void launch_tpr(const Params& p, int grid, cudaStream_t st) {
   constexpr int NT = TPR < 256 ? 256 : TPR, NV = 16 / VEC;
   if constexpr (BWD) {
     // as many rows, up to 4, as 192 KB an SM hold
-    constexpr size_t row = 2 * static_cast<size_t>(NV) * NT * 16, fit = 192 * 1024 / (row * (NT == 256 ? 2 : 1));
-    constexpr int RING = VEC == 1 ? 0 : fit < 4 ? fit : 4;
+    constexpr size_t row = 2 * static_cast<size_t>(NV) * NT * sizeof(Raw<IO, VEC>), fit = 192 * 1024 / (row * (NT == 256 ? 2 : 1));
+    constexpr int RING = sizeof(Raw<IO, VEC>) == 2 ? 0 : fit < 4 ? fit : 4;
     constexpr size_t bytes = RING * row;
     if constexpr (RING > 0) {
       static bool raised[64] = {};       // (a race raises it twice, to the same value)
