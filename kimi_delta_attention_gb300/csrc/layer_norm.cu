@@ -6,8 +6,8 @@
 // Both passes are bound by HBM: 2 and 3 passes over the rows.  A row stays in the registers
 // of its threads between the sums and the result, so it is read once.  The second moment is
 // taken around the mean already known (no cancellation of large squares); all sums are fp32.
-// 16384 rows of 4096 bf16: forward 45 us (268 MB, 88 % of the copy bandwidth), backward 80 us
-// with the sums over its blocks, a call among others (403 MB, 75 %; of it 4 in the second
+// 16384 rows of 4096 bf16, a call among others: forward 47 us (268 MB, 85 % of the copy
+// bandwidth), backward 80 us with the sums over its blocks (403 MB, 75 %; of it 4 in the second
 // kernel, and between two rows a block waits for its sums).
 #include <cstddef>
 #include <cstdint>
@@ -155,10 +155,15 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // One row per TPR threads, NV vectors of VEC values a thread (vector j of thread t at
 // column VEC (t + TPR j)).  A block walks over rows with its columns' weights in registers
 // (read per row they were 4 times the row's own bytes from L2: 65 us for 16384 rows of 4096
-// in bf16) and the next row's loads in flight over the two sums of this one.
-template <typename IO, int VEC, int NV, int TPR, int NT>
+// in bf16) and the rows to come on their way in a ring in shared memory of RING rows a group,
+// each thread's own vectors or elements (RING = 0, for single bf16 elements, and 49 us for 47
+// with vectors too: the next row's in registers).
+template <typename IO, int VEC, int NV, int TPR, int NT, int RING>
 __global__ void __launch_bounds__(NT) layer_norm_kernel(const Params p) {
   constexpr int G = NT / TPR;
+  using Slot = decltype(Raw<IO, VEC>::u);
+  extern __shared__ __align__(16) uint4 dynamic[];
+  Slot* ring = reinterpret_cast<Slot*>(dynamic);  // [RING][NV][NT]
   __shared__ float red[2][NT / 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   float* rd[2] = {red[0] + grp * (TPR / 32), red[1] + grp * (TPR / 32)};
@@ -170,28 +175,44 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const Params p) {
     load_param<VEC>(b[j], p.b, c, p.D, 0.f);
   }
   Raw<IO, VEC> raw[NV];
-  auto fetch = [&](long row) {
+  auto fetch = [&](long row, int slot) {
     const IO* x = static_cast<const IO*>(p.x) + row * p.ldx;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = VEC * (t + TPR * j);
-      if (row < p.rows && c < p.D) raw[j].load(x + c);
-      else raw[j].zero();
+      if constexpr (RING > 0) {
+        if (row < p.rows && c < p.D) copy_async(&ring[(slot * NV + j) * NT + threadIdx.x], x + c);
+      } else if (row < p.rows && c < p.D) {
+        raw[j].load(x + c);
+      } else {
+        raw[j].zero();
+      }
     }
+    if constexpr (RING > 0) copies_close();
   };
   const long step = static_cast<long>(gridDim.x) * G;
   long base = static_cast<long>(blockIdx.x) * G;
-  fetch(base + grp);
+  int slot = 0;
+  if constexpr (RING > 0) {
+#pragma unroll
+    for (int n = 0; n < RING; ++n) fetch(base + grp + n * step, n);
+  } else {
+    fetch(base + grp, 0);
+  }
   for (; base < p.rows; base += step) {  // (the whole block: row_sum has block barriers)
     const long row = base + grp;
     float a[NV][VEC], s[1] = {0.f};
+    if constexpr (RING > 0) copies_wait<RING - 1>();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if constexpr (RING > 0)
+        raw[j].u = VEC * (t + TPR * j) < p.D && row < p.rows ? ring[(slot * NV + j) * NT + threadIdx.x] : Slot{};
       raw[j].to(a[j]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += a[j][e];
     }
-    fetch(row + step);
+    fetch(row + (RING > 0 ? RING : 1) * step, slot);
+    if (++slot >= RING) slot = 0;
     row_sum<TPR>(s, rd[0], t);
     const float mu = s[0] / p.D;
     s[0] = 0.f;
@@ -252,10 +273,8 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_kernel(const Params p) {
 // Backward: the block's rows are blockIdx.x G + group, then every gridDim.x G further; a
 // thread meets the same columns in every row, so its share of dw and db stays in registers.
 // The groups' shares are added in their order and written once, as the block's part of
-// [blocks, D].  The rows to come are on their way in a ring in shared memory of RING rows a
-// group, each thread's own vectors or elements (RING = 0, for single bf16 elements: the next row's
-// in registers; with these alone 32 KB an SM were in flight, a call of 16384 rows of 4096 took
-// 88 us, with the ring 84).  The arithmetic is in pairs of values (84 -> 82).
+// [blocks, D].  The ring is the forward's (with the next row's loads in registers alone 32 KB an
+// SM were in flight, a call of 16384 rows of 4096 took 88 us, with the ring 84).  The arithmetic is in pairs of values (84 -> 82).
 template <typename IO, int VEC, int NV, int TPR, int NT, int RING>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(const Params p) {
   constexpr int G = NT / TPR;
@@ -479,24 +498,24 @@ int threads_per_row(int D) {
 template <typename IO, int VEC, int TPR, bool BWD>
 void launch_tpr(const Params& p, int grid, cudaStream_t st) {
   constexpr int NT = TPR < 256 ? 256 : TPR, NV = 16 / VEC;
-  if constexpr (BWD) {
-    // as many rows, up to 4, as 192 KB an SM hold
-    constexpr size_t row = 2 * static_cast<size_t>(NV) * NT * sizeof(Raw<IO, VEC>), fit = 192 * 1024 / (row * (NT == 256 ? 2 : 1));
-    constexpr int RING = sizeof(Raw<IO, VEC>) == 2 ? 0 : fit < 4 ? fit : 4;
-    constexpr size_t bytes = RING * row;
-    if constexpr (RING > 0) {
-      static bool raised[64] = {};       // (a race raises it twice, to the same value)
-      int dev = 0;
-      cudaGetDevice(&dev);
-      if (dev < 0 || dev >= 64 || !raised[dev]) {
-        cudaFuncSetAttribute(layer_norm_bwd_kernel<IO, VEC, NV, TPR, NT, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(bytes));
-        if (dev >= 0 && dev < 64) raised[dev] = true;
-      }
+  // the ring: as many rows, up to 4, as 192 KB an SM hold
+  constexpr size_t row = (BWD ? 2 : 1) * static_cast<size_t>(NV) * NT * sizeof(Raw<IO, VEC>);
+  constexpr size_t fit = 192 * 1024 / (row * (NT > 256 ? 1 : BWD ? 2 : 3));
+  constexpr int RING = sizeof(Raw<IO, VEC>) == 2 ? 0 : fit < 4 ? fit : 4;
+  constexpr size_t bytes = RING * row;
+  void (*kernel)(Params);
+  if constexpr (BWD) kernel = layer_norm_bwd_kernel<IO, VEC, NV, TPR, NT, RING>;
+  else kernel = layer_norm_kernel<IO, VEC, NV, TPR, NT, RING>;
+  if constexpr (bytes > 40 * 1024) {
+    static bool raised[64] = {};       // (a race raises it twice, to the same value)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !raised[dev]) {
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+      if (dev >= 0 && dev < 64) raised[dev] = true;
     }
-    layer_norm_bwd_kernel<IO, VEC, NV, TPR, NT, RING><<<grid, NT, bytes, st>>>(p);
-  } else
-    layer_norm_kernel<IO, VEC, NV, TPR, NT><<<grid, NT, 0, st>>>(p);
+  }
+  kernel<<<grid, NT, bytes, st>>>(p);
 }
 
 template <typename IO, int VEC, bool BWD>
