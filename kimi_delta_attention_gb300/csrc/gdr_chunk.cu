@@ -1522,6 +1522,12 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
         tc_fence_before();
         arrive(wide::QREADY);
       }
+      if (MODE != REVERSE) {                       // beta v, -beta G
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = mul2(fb[(j >> 1) & 1], y[j]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) fb[m] = mul2(pack2f(-1.f, -1.f), mul2(fb[m], fg[m]));
+      }
       if (!(good = wait(wide::D1, ph))) break;
       tc_fence_after();
       block_ld(tl + L::TD1 + t0, x);
@@ -1529,12 +1535,8 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
       for (int j = 0; j < 8; ++j) {
         if (MODE == REVERSE) {                     // E k dS'
           y[j] = mul2(fe[(j >> 1) & 1], x[j]);
-        } else {                                   // beta (v - G k S)
-          float v0, v1, x0, x1, g0, g1;
-          unpack2f(y[j], v0, v1);
-          unpack2f(x[j], x0, x1);
-          unpack2f(fg[(j >> 1) & 1], g0, g1);
-          y[j] = mul2(fb[(j >> 1) & 1], pack2f(fmaf(-g0, x0, v0), fmaf(-g1, x1, v1)));
+        } else {                                   // beta v - (beta G) k S
+          y[j] = fma2(fb[(j >> 1) & 1], x[j], y[j]);
         }
       }
       if (rows < C) zero_past_end(y);
