@@ -1177,7 +1177,7 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
 // all three steps (a warp: 32 columns, 16 tokens or K / 4 key dims) -- against the
 // 64-column slices, whose two halves run different code.
 //
-// 380 us for 16 packed sequences (46402 tokens, 32 heads, 23424 chunks and heads), 2.5 us a
+// 370 us for 16 packed sequences (46402 tokens, 32 heads, 23424 chunks and heads), 2.4 us a
 // chunk: the products are 1.3 us of it at the tensor cores' rate (each fp32 operand counts
 // twice), the rest is the work between them, one after the other.  64-column slices took
 // 650.  Splitting the steps' operands in halves, products over the first while the second

@@ -25,7 +25,7 @@
 // 0-63 belong to q's side (do; A), rows 64-127 to k's side (z, vn; B), stacked in shared
 // memory so that one instruction serves both, and thread (lane r, quarter h) of the CTA owns
 // row r and a quarter of the key dims throughout.
-// 190 us for 2048 chunks and heads (K = V = 128).  A unit takes 27000 cycles for 33000
+// 188 us for 2048 chunks and heads (K = V = 128).  A unit takes 27000 cycles for 33000
 // instructions: it is a chain of phases (loads, S and dS' into their parts, three groups of
 // products, the rows of dq and dk) of which only the loads overlap with their neighbours, and
 // these only where shared memory is free again (224 KB a unit: none to spare).  The loads are

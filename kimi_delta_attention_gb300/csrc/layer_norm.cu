@@ -6,9 +6,9 @@
 // Both passes are bound by HBM: 2 and 3 passes over the rows.  A row stays in the registers
 // of its threads between the sums and the result, so it is read once.  The second moment is
 // taken around the mean already known (no cancellation of large squares); all sums are fp32.
-// 16384 rows of 4096 bf16, a call among others: forward 47 us (268 MB, 85 % of the copy
-// bandwidth), backward 80 us with the sums over its blocks (403 MB, 75 %; of it 4 in the second
-// kernel, and between two rows a block waits for its sums).
+// 16384 rows of 4096 bf16: forward 44 us (268 MB, 90 % of the copy bandwidth), backward 72 us
+// (403 MB, 83 %: between two rows a block waits for its sums) and 6 for the sums over its
+// blocks; calls among others take 46 and 80.
 #include <cstddef>
 #include <cstdint>
 
@@ -141,12 +141,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // 16 or 4 bytes to shared memory without passing through registers; the issuing thread alone
-// reads them, so waiting for its own groups is all it needs.
+// reads them, so waiting for its own groups is all it needs.  Zeros where there is nothing to
+// copy (nothing is read then).
 template <typename T>
-__device__ __forceinline__ void copy_async(T* dst, const void* src) {
-  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (sizeof(T) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async(T* dst, const void* src, bool there) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)), bytes = there ? sizeof(T) : 0;
+  if constexpr (sizeof(T) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -156,8 +159,8 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // column VEC (t + TPR j)).  A block walks over rows with its columns' weights in registers
 // (read per row they were 4 times the row's own bytes from L2: 65 us for 16384 rows of 4096
 // in bf16) and the rows to come on their way in a ring in shared memory of RING rows a group,
-// each thread's own vectors or elements (RING = 0, for single bf16 elements, and 49 us for 47
-// with vectors too: the next row's in registers).
+// each thread's own vectors or elements (RING = 0, for single bf16 elements, and 49 us a call for
+// 46 with vectors too: the next row's in registers).
 template <typename IO, int VEC, int NV, int TPR, int NT, int RING>
 __global__ void __launch_bounds__(NT) layer_norm_kernel(const Params p) {
   constexpr int G = NT / TPR;
@@ -181,7 +184,8 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const Params p) {
     for (int j = 0; j < NV; ++j) {
       const int c = VEC * (t + TPR * j);
       if constexpr (RING > 0) {
-        if (row < p.rows && c < p.D) copy_async(&ring[(slot * NV + j) * NT + threadIdx.x], x + c);
+        const bool there = row < p.rows && c < p.D;
+        copy_async(&ring[(slot * NV + j) * NT + threadIdx.x], there ? x + c : static_cast<const IO*>(p.x), there);
       } else if (row < p.rows && c < p.D) {
         raw[j].load(x + c);
       } else {
@@ -205,8 +209,7 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const Params p) {
     if constexpr (RING > 0) copies_wait<RING - 1>();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (RING > 0)
-        raw[j].u = VEC * (t + TPR * j) < p.D && row < p.rows ? ring[(slot * NV + j) * NT + threadIdx.x] : Slot{};
+      if constexpr (RING > 0) raw[j].u = ring[(slot * NV + j) * NT + threadIdx.x];
       raw[j].to(a[j]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += a[j][e];
@@ -309,10 +312,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     for (int j = 0; j < NV; ++j) {
       const int c = VEC * (t + TPR * j);
       if constexpr (RING > 0) {
-        if (live && c < p.D) {
-          copy_async(&ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x], x + c);
-          copy_async(&ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x], dy + c);
-        }
+        const bool there = live && c < p.D;
+        copy_async(&ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x], there ? x + c : static_cast<const IO*>(p.x), there);
+        copy_async(&ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x], there ? dy + c : static_cast<const IO*>(p.dy), there);
       } else if (live && c < p.D) {
         rx[j].load(x + c);
         ry[j].load(dy + c);
@@ -342,16 +344,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     if constexpr (RING > 0) copies_wait<RING - 1>();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = VEC * (t + TPR * j) < p.D;
       if constexpr (RING > 0) {
-        const bool there = in && row < p.rows;
-        rx[j].u = there ? ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x] : Slot{};
-        ry[j].u = there ? ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x] : Slot{};
+        rx[j].u = ring[(slot * 2 * NV + 2 * j) * NT + threadIdx.x];
+        ry[j].u = ring[(slot * 2 * NV + 2 * j + 1) * NT + threadIdx.x];
       }
       rx[j].to(vx[j]);
-      ry[j].to(vy[j]);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) vx[j][e] = in ? vx[j][e] : mu;   // (past D, xh is 0 for the sums)
+      ry[j].to(vy[j]);   // (0 past D, which keeps these columns out of every sum)
     }
     uint64_t xh[NP], a[NP], s0 = 0ull, s1 = 0ull;
     {
