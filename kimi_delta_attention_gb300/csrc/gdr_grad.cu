@@ -517,7 +517,6 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
             const int d = part * DPT + 8 * n;
             *reinterpret_cast<uint4*>(sm + L::QK + (d >> 6) * kTileBytes + sw128(r, (d & 63) >> 3)) = packed[n];
           }
-          fence_proxy_async_smem();
         } else if (live) {
           __nv_bfloat16* op = static_cast<__nv_bfloat16*>(kside ? a.dk : a.dq) + (orow * p.H + hk) * K + part * DPT;
 #pragma unroll
@@ -538,6 +537,9 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
     sg[part * 128 + r] = dgc;
     sg[512 + part * 128 + r] = t;
     if (kside) sg[1024 + part * 64 + i] = db;
+    // every thread's use of the exchange rows and of [q; k] comes before the copies that follow:
+    // the next unit's S over both, and dq and dk from [q; k]
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {

@@ -172,3 +172,23 @@ def test_wait_limit(limit, monkeypatch):
     monkeypatch.delenv("KDA_WAIT_LIMIT_NS")
     assert all(torch.equal(s, t) for s, t in zip(ref_f, fwd())) and kda.kda_read_device_status(fws) == 0
     assert all(torch.equal(s, t) for s, t in zip(ref_b, bwd())) and kda.kda_read_device_status(bws) == 0
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 64), (128, 64)])
+@pytest.mark.parametrize("H,HV", [(4, 8), (8, 8)])
+def test_gradients_unit_after_unit(K, V, H, HV):
+    """More (chunk, value head) pairs than processors, most chunks partial: a CTA's buffers pass from one
+    pair to the next.  Against 64 bits, and each sequence's bits are those of a call of its own,
+    where no CTA meets a second pair."""
+    seqs = [70, 1, 64, 33] * 8
+    x = make(seqs, H, HV, K, V, state=True, seed=52, grads=True)
+    got = backward(x)
+    for name, a, ref in zip(NAMES, got, reference(x, NAMES)):
+        check(a, ref, "d" + name)
+    at = 0
+    for i, n in enumerate(seqs[:8]):
+        one = {m: t[:, at:at + n].contiguous() if m in ("q", "k", "v", "g", "beta", "do") else t for m, t in x.items()}
+        one.update(cu=None, s0=x["s0"][i:i + 1], ds=x["ds"][i:i + 1])
+        alone = backward(one)
+        assert all(torch.equal(s[:, at:at + n], t) for s, t in zip(got[:5], alone[:5])) and torch.equal(got[5][i:i + 1], alone[5])
+        at += n
