@@ -4,10 +4,10 @@
 
 Layer norm, projections (torch matrix products), the delta rule and the output projection,
 with a residual.  ``layer_norm`` and ``gated_delta_rule`` are autograd functions over the
-library's forward and backward; ``GatedDeltaLayer`` trains with them, and serves with the
-chunked forward for a prompt and the recurrent step for each token after it, the requests'
-states in one pool.  The command trains a layer for some steps on synthetic data, then
-serves the same tokens and compares.
+library's forward and backward (first derivatives; a second one raises); ``GatedDeltaLayer``
+trains with them, and serves with the chunked forward for a prompt and the recurrent step for
+each token after it, the requests' states in one pool.  The command trains a layer for some
+steps on synthetic data, then serves the same tokens and compares.
 """
 from __future__ import annotations
 
@@ -15,6 +15,7 @@ import argparse
 
 import torch
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import _gdr
 
@@ -28,6 +29,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -50,6 +52,7 @@ class _GatedDeltaRule(torch.autograd.Function):
         return o, state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dstate):
         q, k, v, g, beta, s0, cu = ctx.saved_tensors
         grads = _gdr.kda_gdr_bwd(q, k, v, g, beta, do.contiguous(), ctx.scale, initial_state=s0, cu_seqlens=cu,
