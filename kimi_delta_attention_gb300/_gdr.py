@@ -13,11 +13,10 @@ import functools
 import torch
 
 from . import _lib
-from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _check, load_library
+from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, load_library
 
 _IO = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _f32 = torch.float32
-_empty, _empty_like = torch.empty, torch.empty_like
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -36,20 +35,10 @@ def _maybe(name, t, dtype, shape, index):
     return None if t is None else _need(name, t, dtype, shape, index)
 
 
-def _keep(made, stream, index):
-    """Blocks allocated on the current stream's pool but used on another stream must not be
-    handed out again before that stream is done with them."""
-    other = torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
-    for t in made:
-        if t is not None:
-            t.record_stream(other)
-
-
-def _run(fn, index, made, stream, *args):
-    """fn(*args, stream) on device `index`; `made`: tensors allocated for the call."""
-    current = _raw_stream(index)
+def _run(fn, index, stream, *args):
+    """fn(*args, stream) on device `index` (stream None: its current one)."""
     if stream is None:
-        stream = current
+        stream = _raw_stream(index)
     if index == _current_device():
         code = fn(*args, stream)
     else:
@@ -57,8 +46,6 @@ def _run(fn, index, made, stream, *args):
             code = fn(*args, stream)
     if code:
         _check(code)
-    if stream != current:
-        _keep(made, stream, index)
 
 
 @functools.lru_cache(maxsize=256)
@@ -98,16 +85,14 @@ def _workspace_bytes(name, *sizes):
     return int(getattr(load_library(), name)(_shape(*sizes))) or 256
 
 
-def _workspace(workspace, name, shape, index, made):
-    """The caller's workspace, or one of the size that `name` gives for the shape: (address, bytes)."""
+def _workspace(workspace, name, shape, index, empty):
+    """The caller's workspace, or one of the size that `name` gives for the shape: (tensor, bytes)."""
     if workspace is None:
         n = _workspace_bytes(name, shape.B, shape.T, shape.H, shape.HV, shape.K, shape.V, shape.num_seqs, shape.io_dtype)
-        workspace = _empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
-        made.append(workspace)
-        return workspace.data_ptr(), n
+        return empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise KdaError(1, f"workspace must be contiguous on cuda:{index}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def kda_gdr_fwd_workspace_size(shape: KdaShape) -> int:
@@ -121,20 +106,18 @@ def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=Non
     int32 (packed sequences, B = 1).  Returns (o [B,T,HV,V], final_state or None)."""
     lib, shape, addr, states, index, scale = _rule_args(q, k, v, g, beta, scale, cu_seqlens)
     s0 = _maybe("initial_state", initial_state, _f32, states, index)
-    made = []
+    empty, empty_like = _allocators(stream, index)
     if out is None:
-        out = _empty_like(v)
-        made.append(out)
+        out = empty_like(v)
     else:
         _need("out", out, v.dtype, v.shape, index)
     if final_state is not None:
         _need("final_state", final_state, _f32, states, index)
     elif output_final_state:
-        final_state = _empty(states, dtype=_f32, device=q.device)
-        made.append(final_state)
-    ws, n = _workspace(workspace, "kda_gdr_fwd_workspace_size", shape, index, made)
-    _run(lib.kda_gdr_fwd, index, made, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), out.data_ptr(),
-         _ptr_or_none(final_state), ws, n)
+        final_state = empty(states, dtype=_f32, device=q.device)
+    ws, n = _workspace(workspace, "kda_gdr_fwd_workspace_size", shape, index, empty)
+    _run(lib.kda_gdr_fwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), out.data_ptr(),
+         _ptr_or_none(final_state), ws.data_ptr(), n)
     return out, final_state
 
 
@@ -151,12 +134,12 @@ def kda_gdr_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seql
     s0 = _maybe("initial_state", initial_state, _f32, states, index)
     do = _need("d_out", d_out, v.dtype, v.shape, index)
     dfin = _maybe("d_final_state", d_final_state, _f32, states, index)
-    dq, dk, dv, dg, dbeta = _empty_like(q), _empty_like(k), _empty_like(v), _empty_like(g), _empty_like(beta)
-    ds0 = _empty(states, dtype=_f32, device=q.device) if output_d_initial_state else None
-    made = [dq, dk, dv, dg, dbeta, ds0]
-    ws, n = _workspace(workspace, "kda_gdr_bwd_workspace_size", shape, index, made)
-    _run(lib.kda_gdr_bwd, index, made, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), do, dfin, dq.data_ptr(),
-         dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr_or_none(ds0), ws, n)
+    empty, empty_like = _allocators(stream, index)
+    dq, dk, dv, dg, dbeta = empty_like(q), empty_like(k), empty_like(v), empty_like(g), empty_like(beta)
+    ds0 = empty(states, dtype=_f32, device=q.device) if output_d_initial_state else None
+    ws, n = _workspace(workspace, "kda_gdr_bwd_workspace_size", shape, index, empty)
+    _run(lib.kda_gdr_bwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), do, dfin, dq.data_ptr(),
+         dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr_or_none(ds0), ws.data_ptr(), n)
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -174,15 +157,14 @@ def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stat
         n = state.shape[0]
         states = (n, *states[1:])
     st = _need("state", state, _f32, states, index)
-    made = []
+    empty, empty_like = _allocators(stream, index)
     if out is None:
-        out = _empty_like(v)
-        made.append(out)
+        out = empty_like(v)
     else:
         _need("out", out, v.dtype, v.shape, index)
     if status is not None and (status.get_device() != index or status.numel() * status.element_size() < 4):
         raise KdaError(1, f"status must hold 4 bytes on cuda:{index}")
-    _run(lib.kda_gdr_step, index, made, stream, shape, *addr, scale, st, at, n, out.data_ptr(), _ptr_or_none(status))
+    _run(lib.kda_gdr_step, index, stream, shape, *addr, scale, st, at, n, out.data_ptr(), _ptr_or_none(status))
     return out
 
 
@@ -206,18 +188,16 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, output_sta
     rows, D, ld = _rows("x", x)
     index = x.get_device()
     w, b = _maybe("weight", weight, _f32, (D,), index), _maybe("bias", bias, _f32, (D,), index)
-    made = []
+    empty, empty_like = _allocators(stream, index)
     if out is None:
-        out = _empty(x.shape, dtype=x.dtype, device=x.device)
-        made.append(out)
+        out = empty(x.shape, dtype=x.dtype, device=x.device)
     else:
         _need("out", out, x.dtype, x.shape, index)
     mean = rstd = None
     if output_stats:
-        mean = _empty(x.shape[:-1], dtype=_f32, device=x.device)
-        rstd = _empty_like(mean)
-        made += [mean, rstd]
-    _run(lib.kda_layer_norm_fwd, index, made, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, w, b, eps, out.data_ptr(),
+        mean = empty(x.shape[:-1], dtype=_f32, device=x.device)
+        rstd = empty_like(mean)
+    _run(lib.kda_layer_norm_fwd, index, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, w, b, eps, out.data_ptr(),
          _ptr_or_none(mean), _ptr_or_none(rstd))
     return out, mean, rstd
 
@@ -244,18 +224,17 @@ def kda_layer_norm_bwd(x, dy, weight, mean, rstd, output_dx=True, output_dweight
     lead = x.shape[:-1]
     w = _maybe("weight", weight, _f32, (D,), index)
     mu, rs = _need("mean", mean, _f32, lead, index), _need("rstd", rstd, _f32, lead, index)
-    dx = _empty(x.shape, dtype=x.dtype, device=x.device) if output_dx else None
-    dw = _empty(D, dtype=_f32, device=x.device) if output_dweight else None
-    db = _empty(D, dtype=_f32, device=x.device) if output_dbias else None
-    made = [dx, dw, db]
+    empty, _ = _allocators(stream, index)
+    dx = empty(x.shape, dtype=x.dtype, device=x.device) if output_dx else None
+    dw = empty(D, dtype=_f32, device=x.device) if output_dweight else None
+    db = empty(D, dtype=_f32, device=x.device) if output_dbias else None
     if workspace is None:
         n = _norm_workspace_bytes(rows, D)
-        workspace = _empty(n, dtype=torch.uint8, device=x.device)
-        made.append(workspace)
+        workspace = empty(n, dtype=torch.uint8, device=x.device)
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise KdaError(1, f"workspace must be contiguous on cuda:{index}")
         n = workspace.numel() * workspace.element_size()
-    _run(lib.kda_layer_norm_bwd, index, made, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, dy.data_ptr(), ldy, w, mu, rs,
+    _run(lib.kda_layer_norm_bwd, index, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, dy.data_ptr(), ldy, w, mu, rs,
          _ptr_or_none(dx), _ptr_or_none(dw), _ptr_or_none(db), workspace.data_ptr(), n)
     return dx, dw, db

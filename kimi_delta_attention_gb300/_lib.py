@@ -8,6 +8,7 @@ is no fallback: if the library is missing the call fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -127,6 +128,25 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         if path is None:
             _lib = lib
         return lib
+
+
+def _allocators(stream, index):
+    """torch.empty and torch.empty_like for a call that runs on the raw `stream` (None: the
+    current one) of CUDA device `index`.  On another stream than the current one, a block comes
+    from that stream's pool: one of the current stream's pool may still be read there by work
+    the caller has enqueued.  The caller reads it on the current stream as a rule, so it is not
+    handed out again before that stream is done with it either."""
+    if stream is None or stream == torch._C._cuda_getCurrentRawStream(index):
+        return torch.empty, torch.empty_like
+    here, there = torch.cuda.current_stream(index), torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
+
+    def place(make, *args, **kw):
+        with torch.cuda.stream(there):
+            t = make(*args, **kw)
+        t.record_stream(here)
+        return t
+
+    return functools.partial(place, torch.empty), functools.partial(place, torch.empty_like)
 
 
 def kda_status_string(code: int) -> str:
