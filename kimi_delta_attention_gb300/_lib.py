@@ -219,30 +219,20 @@ def _forward_on_device(lib, entry, q, k, v, g, beta, scale, initial_state, cu_se
         scale = K ** -0.5
     NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
     HV, V = v.shape[2], v.shape[3]
-    made = []  # tensors allocated here, on the current stream's pool
+    empty, empty_like = _allocators(stream, q.get_device())
     if out is None:
-        out = torch.empty_like(v)
-        made.append(out)
+        out = empty_like(v)
     if final_state is None and output_final_state:
-        final_state = torch.empty((NS, HV, K, V), dtype=torch.float32, device=q.device)
-        made.append(final_state)
+        final_state = empty((NS, HV, K, V), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(kda_chunk_fwd_workspace_size(shape), dtype=torch.uint8, device=q.device)
-        made.append(workspace)
-    current = torch.cuda.current_stream(q.device).cuda_stream
+        workspace = empty(kda_chunk_fwd_workspace_size(shape), dtype=torch.uint8, device=q.device)
     if stream is None:
-        stream = current
+        stream = torch.cuda.current_stream(q.device).cuda_stream
     code = getattr(lib, entry)(
         ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.c_float(scale),
         _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state), _ptr(workspace),
         ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream))
     _check(code)
-    if made and stream != current:
-        # the work runs on another stream: the caching allocator must not hand these blocks
-        # (the temporary workspace above all) to the current stream before that work is done
-        other = torch.cuda.ExternalStream(stream, device=q.device)
-        for t in made:
-            t.record_stream(other)
     return out, final_state
 
 
@@ -284,10 +274,11 @@ def kda_chunk_fwd_static_scratch(q, k, v, g, beta, scale=None, initial_state=Non
             scale = K ** -0.5
         NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
         HV, V = v.shape[2], v.shape[3]
+        empty, empty_like = _allocators(stream, q.get_device())
         if out is None:
-            out = torch.empty_like(v)
+            out = empty_like(v)
         if final_state is None and output_final_state:
-            final_state = torch.empty((NS, HV, K, V), dtype=torch.float32, device=q.device)
+            final_state = empty((NS, HV, K, V), dtype=torch.float32, device=q.device)
         if stream is None:
             stream = torch.cuda.current_stream(q.device).cuda_stream
         status = ctypes.c_void_p()
@@ -311,7 +302,7 @@ def kda_decode(q, k, v, g, beta, state, scale=None, out=None, stream=None):
         if scale is None:
             scale = q.shape[3] ** -0.5
         if out is None:
-            out = torch.empty_like(v)
+            out = _allocators(stream, q.get_device())[1](v)
         if stream is None:
             stream = torch.cuda.current_stream(q.device).cuda_stream
         _check(lib.kda_decode(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -340,28 +331,20 @@ def kda_chunk_fwd_gated(q, k, v, g_raw, beta_raw, A_log, dt_bias, gate="bounded"
             scale = K ** -0.5
         NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
         HV, V = v.shape[2], v.shape[3]
-        made = []
+        empty, empty_like = _allocators(stream, q.get_device())
         if out is None:
-            out = torch.empty_like(v)
-            made.append(out)
+            out = empty_like(v)
         if final_state is None and output_final_state:
-            final_state = torch.empty((NS, HV, K, V), dtype=torch.float32, device=q.device)
-            made.append(final_state)
+            final_state = empty((NS, HV, K, V), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(kda_chunk_fwd_workspace_size(shape), dtype=torch.uint8, device=q.device)
-            made.append(workspace)
-        current = torch.cuda.current_stream(q.device).cuda_stream
+            workspace = empty(kda_chunk_fwd_workspace_size(shape), dtype=torch.uint8, device=q.device)
         if stream is None:
-            stream = current
+            stream = torch.cuda.current_stream(q.device).cuda_stream
         gs = KdaGate(GATE_KINDS[gate], A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound))
         _check(lib.kda_chunk_fwd_gated(
             ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw), _ptr(beta_raw), ctypes.byref(gs),
             ctypes.c_float(scale), _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
             _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream)))
-        if made and stream != current:
-            other = torch.cuda.ExternalStream(stream, device=q.device)
-            for t in made:
-                t.record_stream(other)
     return out, final_state
 
 
@@ -376,12 +359,13 @@ def kda_chunk_states(q, k, v, g, beta, initial_state=None, h=None, final_state=N
         shape = make_shape(q, v)
         B, T, H, K = q.shape
         HV, V = v.shape[2], v.shape[3]
+        empty, _ = _allocators(stream, q.get_device())
         if h is None:
-            h = torch.empty((B, HV, (T + 63) // 64, K, V), dtype=torch.bfloat16, device=q.device)
+            h = empty((B, HV, (T + 63) // 64, K, V), dtype=torch.bfloat16, device=q.device)
         if final_state is None and output_final_state:
-            final_state = torch.empty((B, HV, K, V), dtype=torch.float32, device=q.device)
+            final_state = empty((B, HV, K, V), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(kda_chunk_fwd_workspace_size(shape), dtype=torch.uint8, device=q.device)
+            workspace = empty(kda_chunk_fwd_workspace_size(shape), dtype=torch.uint8, device=q.device)
         if stream is None:
             stream = torch.cuda.current_stream(q.device).cuda_stream
         _check(lib.kda_chunk_states(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -399,10 +383,11 @@ def kda_chunk_output(q, k, v, g, beta, h, scale=None, out=None, workspace=None, 
         shape = make_shape(q, v)
         if scale is None:
             scale = q.shape[3] ** -0.5
+        empty, empty_like = _allocators(stream, q.get_device())
         if out is None:
-            out = torch.empty_like(v)
+            out = empty_like(v)
         if workspace is None:
-            workspace = torch.empty(256, dtype=torch.uint8, device=q.device)
+            workspace = empty(256, dtype=torch.uint8, device=q.device)
         if stream is None:
             stream = torch.cuda.current_stream(q.device).cuda_stream
         _check(lib.kda_chunk_output(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -434,27 +419,21 @@ def kda_backward(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seq
             scale = K ** -0.5
         NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
         HV, V = v.shape[2], v.shape[3]
+        empty, _ = _allocators(stream, q.get_device())
         f32 = dict(dtype=torch.float32, device=q.device)
-        dq = torch.empty(q.shape, **f32)
-        dk = torch.empty(k.shape, **f32)
-        dv = torch.empty(v.shape, **f32)
-        dg = torch.empty(g.shape, **f32)
-        dbeta = torch.empty(beta.shape, **f32)
-        ds0 = torch.empty((NS, HV, K, V), **f32) if output_d_initial_state else None
-        made = [dq, dk, dv, dg, dbeta] + ([ds0] if ds0 is not None else [])
+        dq = empty(q.shape, **f32)
+        dk = empty(k.shape, **f32)
+        dv = empty(v.shape, **f32)
+        dg = empty(g.shape, **f32)
+        dbeta = empty(beta.shape, **f32)
+        ds0 = empty((NS, HV, K, V), **f32) if output_d_initial_state else None
         if workspace is None:
-            workspace = torch.empty(kda_backward_workspace_size(shape), dtype=torch.uint8, device=q.device)
-            made.append(workspace)
-        current = torch.cuda.current_stream(q.device).cuda_stream
+            workspace = empty(kda_backward_workspace_size(shape), dtype=torch.uint8, device=q.device)
         if stream is None:
-            stream = current
+            stream = torch.cuda.current_stream(q.device).cuda_stream
         _check(lib.kda_backward(
             ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.c_float(scale),
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_out), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(dg), _ptr(dbeta), _ptr(ds0), _ptr(workspace),
             ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream)))
-        if stream != current:
-            other = torch.cuda.ExternalStream(stream, device=q.device)
-            for t in made:
-                t.record_stream(other)
     return dq, dk, dv, dg, dbeta, ds0
