@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import _lib
-from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, load_library
+from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _written, load_library
 
 _IO = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _f32 = torch.float32
@@ -107,6 +107,7 @@ def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=Non
     lib, shape, addr, states, index, scale = _rule_args(q, k, v, g, beta, scale, cu_seqlens)
     s0 = _maybe("initial_state", initial_state, _f32, states, index)
     empty, empty_like = _allocators(stream, index)
+    given = (out, final_state)
     if out is None:
         out = empty_like(v)
     else:
@@ -118,6 +119,7 @@ def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=Non
     ws, n = _workspace(workspace, "kda_gdr_fwd_workspace_size", shape, index, empty)
     _run(lib.kda_gdr_fwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), out.data_ptr(),
          _ptr_or_none(final_state), ws.data_ptr(), n)
+    _written(*given)
     return out, final_state
 
 
@@ -158,6 +160,7 @@ def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stat
         states = (n, *states[1:])
     st = _need("state", state, _f32, states, index)
     empty, empty_like = _allocators(stream, index)
+    given = (state, out, status)
     if out is None:
         out = empty_like(v)
     else:
@@ -165,6 +168,7 @@ def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stat
     if status is not None and (status.get_device() != index or status.numel() * status.element_size() < 4):
         raise KdaError(1, f"status must hold 4 bytes on cuda:{index}")
     _run(lib.kda_gdr_step, index, stream, shape, *addr, scale, st, at, n, out.data_ptr(), _ptr_or_none(status))
+    _written(*given)
     return out
 
 
@@ -189,6 +193,7 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, output_sta
     index = x.get_device()
     w, b = _maybe("weight", weight, _f32, (D,), index), _maybe("bias", bias, _f32, (D,), index)
     empty, empty_like = _allocators(stream, index)
+    given = out
     if out is None:
         out = empty(x.shape, dtype=x.dtype, device=x.device)
     else:
@@ -199,6 +204,7 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, output_sta
         rstd = empty_like(mean)
     _run(lib.kda_layer_norm_fwd, index, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, w, b, eps, out.data_ptr(),
          _ptr_or_none(mean), _ptr_or_none(rstd))
+    _written(given)
     return out, mean, rstd
 
 

@@ -149,6 +149,14 @@ def _allocators(stream, index):
     return functools.partial(place, torch.empty), functools.partial(place, torch.empty_like)
 
 
+def _written(*tensors):
+    """The caller's own tensors that a call has written: autograd may hold them saved, and sees
+    by their version that they changed."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def kda_status_string(code: int) -> str:
     return load_library().kda_status_string(int(code)).decode()
 
@@ -220,6 +228,7 @@ def _forward_on_device(lib, entry, q, k, v, g, beta, scale, initial_state, cu_se
     NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
     HV, V = v.shape[2], v.shape[3]
     empty, empty_like = _allocators(stream, q.get_device())
+    given = (out, final_state)
     if out is None:
         out = empty_like(v)
     if final_state is None and output_final_state:
@@ -233,6 +242,7 @@ def _forward_on_device(lib, entry, q, k, v, g, beta, scale, initial_state, cu_se
         _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state), _ptr(workspace),
         ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream))
     _check(code)
+    _written(*given)
     return out, final_state
 
 
@@ -275,6 +285,7 @@ def kda_chunk_fwd_static_scratch(q, k, v, g, beta, scale=None, initial_state=Non
         NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
         HV, V = v.shape[2], v.shape[3]
         empty, empty_like = _allocators(stream, q.get_device())
+        given = (out, final_state)
         if out is None:
             out = empty_like(v)
         if final_state is None and output_final_state:
@@ -287,6 +298,7 @@ def kda_chunk_fwd_static_scratch(q, k, v, g, beta, scale=None, initial_state=Non
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state), ctypes.c_void_p(stream),
             ctypes.byref(status))
         _check(code)
+        _written(*given)
     return out, final_state, status.value
 
 
@@ -301,12 +313,14 @@ def kda_decode(q, k, v, g, beta, state, scale=None, out=None, stream=None):
         shape = make_shape(q, v)
         if scale is None:
             scale = q.shape[3] ** -0.5
+        given = (state, out)
         if out is None:
             out = _allocators(stream, q.get_device())[1](v)
         if stream is None:
             stream = torch.cuda.current_stream(q.device).cuda_stream
         _check(lib.kda_decode(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                               ctypes.c_float(scale), _ptr(state), _ptr(out), ctypes.c_void_p(stream)))
+        _written(*given)
     return out
 
 
@@ -332,6 +346,7 @@ def kda_chunk_fwd_gated(q, k, v, g_raw, beta_raw, A_log, dt_bias, gate="bounded"
         NS = q.shape[0] if cu_seqlens is None else shape.num_seqs
         HV, V = v.shape[2], v.shape[3]
         empty, empty_like = _allocators(stream, q.get_device())
+        given = (out, final_state)
         if out is None:
             out = empty_like(v)
         if final_state is None and output_final_state:
@@ -345,6 +360,7 @@ def kda_chunk_fwd_gated(q, k, v, g_raw, beta_raw, A_log, dt_bias, gate="bounded"
             ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw), _ptr(beta_raw), ctypes.byref(gs),
             ctypes.c_float(scale), _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
             _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream)))
+        _written(*given)
     return out, final_state
 
 
@@ -360,6 +376,7 @@ def kda_chunk_states(q, k, v, g, beta, initial_state=None, h=None, final_state=N
         B, T, H, K = q.shape
         HV, V = v.shape[2], v.shape[3]
         empty, _ = _allocators(stream, q.get_device())
+        given = (h, final_state)
         if h is None:
             h = empty((B, HV, (T + 63) // 64, K, V), dtype=torch.bfloat16, device=q.device)
         if final_state is None and output_final_state:
@@ -372,6 +389,7 @@ def kda_chunk_states(q, k, v, g, beta, initial_state=None, h=None, final_state=N
                                     _ptr(initial_state), _ptr(h), _ptr(final_state), _ptr(workspace),
                                     ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                     ctypes.c_void_p(stream)))
+        _written(*given)
     return h, final_state
 
 
@@ -384,6 +402,7 @@ def kda_chunk_output(q, k, v, g, beta, h, scale=None, out=None, workspace=None, 
         if scale is None:
             scale = q.shape[3] ** -0.5
         empty, empty_like = _allocators(stream, q.get_device())
+        given = out
         if out is None:
             out = empty_like(v)
         if workspace is None:
@@ -394,6 +413,7 @@ def kda_chunk_output(q, k, v, g, beta, h, scale=None, out=None, workspace=None, 
                                     ctypes.c_float(scale), _ptr(h), _ptr(out), _ptr(workspace),
                                     ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                     ctypes.c_void_p(stream)))
+        _written(given)
     return out
 
 
