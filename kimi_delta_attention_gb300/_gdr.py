@@ -95,16 +95,36 @@ def _workspace(workspace, name, shape, index, empty):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _check_status(status, index):
+    if status is not None and (status.get_device() != index or status.numel() * status.element_size() < 4 or
+                               not status.is_contiguous()):
+        raise KdaError(1, f"status must hold 4 bytes on cuda:{index}")
+
+
+def _add_status(status, ws, stream, index):
+    """The status bits a call leaves in its workspace's first word, added to the caller's word."""
+    word = lambda t: t.view(-1).view(torch.uint8)[:4].view(torch.int32)
+    if stream is None:
+        word(status).bitwise_or_(word(ws))
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))):
+            word(status).bitwise_or_(word(ws))
+
+
 def kda_gdr_fwd_workspace_size(shape: KdaShape) -> int:
     return int(load_library().kda_gdr_fwd_workspace_size(ctypes.byref(shape)))
 
 
 def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None, out=None, final_state=None,
-                output_final_state=True, workspace=None, stream=None):
+                output_final_state=True, workspace=None, stream=None, status=None):
     """Forward of the gated delta rule with a scalar gate.  q, k [B,T,H,K]; v [B,T,HV,V];
     g (log decay), beta [B,T,HV] fp32; initial_state [NS,HV,K,V] fp32; cu_seqlens [N+1]
-    int32 (packed sequences, B = 1).  Returns (o [B,T,HV,V], final_state or None)."""
+    int32 (packed sequences, B = 1).  status: a 4-byte tensor the caller has zeroed, to which
+    the call adds the bits of its device status (kda_read_device_status takes either it or the
+    workspace); the results of a call that reports any are not meaningful.  Returns
+    (o [B,T,HV,V], final_state or None)."""
     lib, shape, addr, states, index, scale = _rule_args(q, k, v, g, beta, scale, cu_seqlens)
+    _check_status(status, index)
     s0 = _maybe("initial_state", initial_state, _f32, states, index)
     empty, empty_like = _allocators(stream, index)
     given = (out, final_state)
@@ -120,6 +140,8 @@ def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=Non
     _run(lib.kda_gdr_fwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), out.data_ptr(),
          _ptr_or_none(final_state), ws.data_ptr(), n)
     _written(*given)
+    if status is not None and states[0] > 0:    # (a call without sequences leaves the workspace alone)
+        _add_status(status, ws, stream, index)
     return out, final_state
 
 
@@ -128,12 +150,13 @@ def kda_gdr_bwd_workspace_size(shape: KdaShape) -> int:
 
 
 def kda_gdr_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seqlens=None, d_final_state=None,
-                output_d_initial_state=True, workspace=None, stream=None):
+                output_d_initial_state=True, workspace=None, stream=None, status=None):
     """Gradients of sum <d_out, o> + <d_final_state, S_final> for kda_gdr_fwd with the same
-    arguments (bf16).  Returns (dq, dk, dv, dg, dbeta, d_initial_state): dq, dk, dv bf16,
+    arguments (bf16; status likewise).  Returns (dq, dk, dv, dg, dbeta, d_initial_state): dq, dk, dv bf16,
     the others fp32, in the inputs' shapes."""
     lib, shape, addr, states, index, scale = _rule_args(q, k, v, g, beta, scale, cu_seqlens)
     s0 = _maybe("initial_state", initial_state, _f32, states, index)
+    _check_status(status, index)
     do = _need("d_out", d_out, v.dtype, v.shape, index)
     dfin = _maybe("d_final_state", d_final_state, _f32, states, index)
     empty, empty_like = _allocators(stream, index)
@@ -142,6 +165,8 @@ def kda_gdr_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seql
     ws, n = _workspace(workspace, "kda_gdr_bwd_workspace_size", shape, index, empty)
     _run(lib.kda_gdr_bwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), do, dfin, dq.data_ptr(),
          dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr_or_none(ds0), ws.data_ptr(), n)
+    if status is not None and states[0] > 0:
+        _add_status(status, ws, stream, index)
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -165,8 +190,7 @@ def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stat
         out = empty_like(v)
     else:
         _need("out", out, v.dtype, v.shape, index)
-    if status is not None and (status.get_device() != index or status.numel() * status.element_size() < 4):
-        raise KdaError(1, f"status must hold 4 bytes on cuda:{index}")
+    _check_status(status, index)
     _run(lib.kda_gdr_step, index, stream, shape, *addr, scale, st, at, n, out.data_ptr(), _ptr_or_none(status))
     _written(*given)
     return out

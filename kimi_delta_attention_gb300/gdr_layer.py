@@ -18,6 +18,7 @@ from torch import nn
 from torch.autograd.function import once_differentiable
 
 from . import _gdr
+from ._lib import _check, kda_read_device_status
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -45,10 +46,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
 
 class _GatedDeltaRule(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, scale, initial_state, cu_seqlens):
-        o, state = _gdr.kda_gdr_fwd(q, k, v, g, beta, scale, initial_state=initial_state, cu_seqlens=cu_seqlens)
+    def forward(ctx, q, k, v, g, beta, scale, initial_state, cu_seqlens, status):
+        o, state = _gdr.kda_gdr_fwd(q, k, v, g, beta, scale, initial_state=initial_state, cu_seqlens=cu_seqlens,
+                                    status=status)
         ctx.save_for_backward(q, k, v, g, beta, initial_state, cu_seqlens)
-        ctx.scale = scale
+        ctx.scale, ctx.status = scale, status
         return o, state
 
     @staticmethod
@@ -56,13 +58,18 @@ class _GatedDeltaRule(torch.autograd.Function):
     def backward(ctx, do, dstate):
         q, k, v, g, beta, s0, cu = ctx.saved_tensors
         grads = _gdr.kda_gdr_bwd(q, k, v, g, beta, do.contiguous(), ctx.scale, initial_state=s0, cu_seqlens=cu,
-                                 d_final_state=dstate.contiguous(), output_d_initial_state=ctx.needs_input_grad[6])
-        return (*grads[:5], None, grads[5], None)
+                                 d_final_state=dstate.contiguous(), output_d_initial_state=ctx.needs_input_grad[6],
+                                 status=ctx.status)
+        return (*grads[:5], None, grads[5], None, None)
 
 
-def gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None):
-    """Differentiable gated delta rule (bf16): (o, final states)."""
-    return _GatedDeltaRule.apply(q, k, v, g, beta, scale, initial_state, cu_seqlens)
+def gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None, status=None):
+    """Differentiable gated delta rule (bf16): (o, final states).  status: a zeroed 4-byte tensor
+    to which the forward and the backward add the bits of their device status, read with
+    kda_read_device_status(status) (which waits for the device) when the caller chooses: after a
+    bounded wait that gave up or a cu_seqlens that does not end at T, results and gradients are
+    not meaningful, and nothing else tells."""
+    return _GatedDeltaRule.apply(q, k, v, g, beta, scale, initial_state, cu_seqlens, status)
 
 
 class GatedDeltaLayer(nn.Module):
@@ -90,16 +97,17 @@ class GatedDeltaLayer(nn.Module):
         return (unit(q), unit(k), v.reshape(B, T, self.value_heads, self.head_dim).contiguous(),
                 -torch.nn.functional.softplus(g.float()) / 8, torch.sigmoid(b.float()))
 
-    def forward(self, x, initial_state=None, cu_seqlens=None):
-        """(y, final states): a training pass, or a prompt's prefill under torch.no_grad()."""
-        o, state = gated_delta_rule(*self._project(x), initial_state=initial_state, cu_seqlens=cu_seqlens)
+    def forward(self, x, initial_state=None, cu_seqlens=None, status=None):
+        """(y, final states): a training pass, or a prompt's prefill under torch.no_grad();
+        status as gated_delta_rule's."""
+        o, state = gated_delta_rule(*self._project(x), initial_state=initial_state, cu_seqlens=cu_seqlens, status=status)
         return x + o.reshape(*x.shape[:2], -1) @ self.w_out, state
 
     @torch.no_grad()
-    def step(self, x, pool, slots):
+    def step(self, x, pool, slots, status=None):
         """y of T new tokens (typically 1) of each request; its state is pool[slots[b]], updated
-        in place (a negative slot: an empty row, y = x)."""
-        o = _gdr.kda_gdr_step(*(t.contiguous() for t in self._project(x)), pool, slots=slots)
+        in place (a negative slot: an empty row, y = x); status reports a slot out of range."""
+        o = _gdr.kda_gdr_step(*(t.contiguous() for t in self._project(x)), pool, slots=slots, status=status)
         return x + o.reshape(*x.shape[:2], -1) @ self.w_out
 
 
@@ -112,21 +120,23 @@ def demo(width=512, heads=4, value_heads=8, B=4, T=200, steps=20, seed=0):
     target = torch.roll(x, 3, dims=1)                    # recall the token three back
     opt = torch.optim.Adam(layer.parameters(), lr=3e-3)
     losses = []
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
     for _ in range(steps):
-        y, _ = layer(x)
+        y, _ = layer(x, status=status)
         loss = (y.float() - target.float()).square().mean()
         opt.zero_grad()
         loss.backward()
         opt.step()
         losses.append(loss.item())
     with torch.no_grad():
-        whole, _ = layer(x)
+        whole, _ = layer(x, status=status)
         prompt = T - 8
-        y, state = layer(x[:, :prompt].contiguous())
+        y, state = layer(x[:, :prompt].contiguous(), status=status)
         pool = torch.zeros(2 * B, *state.shape[1:], device="cuda")
         slots = torch.randperm(2 * B, device="cuda")[:B].to(torch.int32)
         pool[slots.long()] = state
-        served = [y] + [layer.step(x[:, t:t + 1].contiguous(), pool, slots) for t in range(prompt, T)]
+        served = [y] + [layer.step(x[:, t:t + 1].contiguous(), pool, slots, status) for t in range(prompt, T)]
+        _check(kda_read_device_status(status))
         off = (torch.cat(served, 1).float() - whole.float()).abs().max() / whole.float().abs().max()
     return losses[0], losses[-1], off.item()
 

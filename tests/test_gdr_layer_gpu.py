@@ -67,3 +67,51 @@ def test_empty_rows_pass_through():
     y = layer.step(x, pool, torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda"))
     assert torch.equal(y[1], x[1]) and torch.equal(pool[[1, 3]], before[[1, 3]])
     assert not torch.equal(pool[2], before[2]) and not torch.equal(y[0], x[0])
+
+
+def rule_inputs(T=100):
+    torch.manual_seed(3)
+    unit = lambda t: torch.nn.functional.normalize(t, dim=-1).bfloat16().requires_grad_()
+    q, k = unit(torch.randn(1, T, 2, 64, device="cuda")), unit(torch.randn(1, T, 2, 64, device="cuda"))
+    v = torch.randn(1, T, 4, 64, device="cuda").bfloat16().requires_grad_()
+    g = (-0.1 * torch.rand(1, T, 4, device="cuda")).requires_grad_()
+    return q, k, v, g, torch.rand(1, T, 4, device="cuda").requires_grad_()
+
+
+def test_status_of_the_trainable_path():
+    """A padded batch, whose cu_seqlens ends below T, is reported by the forward and by the
+    backward; sound calls leave the word alone and bits stay once they are set."""
+    x = rule_inputs()
+    cu = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, _ = gdr_layer.gated_delta_rule(*x, cu_seqlens=cu(0, 40, 100), status=status)
+    o.sum().backward()
+    assert status.item() == 0 and kda.kda_read_device_status(status) == 0
+    o, _ = gdr_layer.gated_delta_rule(*x, cu_seqlens=cu(0, 40, 90), status=status)
+    assert status.item() == 2 and kda.kda_read_device_status(status) == 7
+    status.zero_()
+    o.sum().backward()
+    assert kda.kda_read_device_status(status) == 7
+    gdr_layer.gated_delta_rule(*x, cu_seqlens=cu(0, 40, 100), status=status)
+    assert kda.kda_read_device_status(status) == 7
+    none = [t[:0] for t in x]
+    status.zero_()
+    gdr_layer.gated_delta_rule(*none, status=status)
+    assert status.item() == 0
+    side, short = torch.cuda.Stream(), cu(0, 40, 90)
+    torch.cuda.synchronize()
+    kda.kda_gdr_fwd(*[t.detach() for t in x], cu_seqlens=short, stream=side.cuda_stream, status=status)
+    side.synchronize()
+    assert kda.kda_read_device_status(status) == 7
+    with pytest.raises(kda.KdaError):
+        gdr_layer.gated_delta_rule(*x, status=torch.zeros(1, dtype=torch.int32))
+
+
+def test_status_of_a_served_layer():
+    layer = gdr_layer.GatedDeltaLayer(256, 2, 4, head_dim=64)
+    x = torch.randn(2, 1, 256, device="cuda").bfloat16()
+    pool, status = torch.zeros(3, 4, 64, 64, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    layer.step(x, pool, torch.tensor([2, -1], dtype=torch.int32, device="cuda"), status)
+    assert status.item() == 0
+    layer.step(x, pool, torch.tensor([3, 0], dtype=torch.int32, device="cuda"), status)
+    assert kda.kda_read_device_status(status) == 7
