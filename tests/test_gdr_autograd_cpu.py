@@ -3,7 +3,7 @@ formulas that, like the kernels, record no graph."""
 import pytest
 import torch
 
-from kimi_delta_attention_gb300 import _gdr, gdr_layer
+from kimi_delta_attention_gb300 import KdaError, _gdr, gdr_layer
 
 
 def norm_fwd(x, weight=None, bias=None, eps=1e-5, **kw):
@@ -53,9 +53,23 @@ def test_layer_norm_once(kernels):
 
 
 def test_rule_once(kernels):
-    q, k, v = (torch.randn(1, 3, 2, 4, requires_grad=True) for _ in range(3))
+    q, k, v = (torch.randn(1, 3, 2, 4).bfloat16().requires_grad_() for _ in range(3))
     g, beta = (torch.randn(1, 3, 2, requires_grad=True) for _ in range(2))
     o, _ = gdr_layer.gated_delta_rule(q, k, v, g, beta)
     grad, = torch.autograd.grad((o * v).sum(), v, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         grad.square().sum().backward()
+
+
+def test_rule_in_fp32_has_no_gradients(kernels):
+    """Refused where the graph would be recorded, not in the backward pass."""
+    q, k, v = (torch.randn(1, 3, 2, 4) for _ in range(3))
+    g, beta = (torch.randn(1, 3, 2) for _ in range(2))
+    o, _ = gdr_layer.gated_delta_rule(q, k, v, g, beta)
+    assert torch.equal(o, v * beta[..., None])
+    g.requires_grad_()
+    with torch.no_grad():
+        gdr_layer.gated_delta_rule(q, k, v, g, beta)
+    with pytest.raises(KdaError) as e:
+        gdr_layer.gated_delta_rule(q, k, v, g, beta)
+    assert e.value.code == 2
