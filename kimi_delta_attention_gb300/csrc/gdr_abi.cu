@@ -210,8 +210,9 @@ kda_status kda_gdr_step(const kda_shape* s, const void* q, const void* k, const 
   const kda_status st = check_shape(s, false, z);
   if (st != KDA_OK) return st;
   if (!good_scale(scale)) return KDA_ERR_INVALID_ARG;
-  if (slots ? num_slots < 0 : num_slots != 0) return KDA_ERR_INVALID_ARG;
-  if (z.ns == 0 || z.tokens == 0) return KDA_OK;
+  if (num_slots < 0) return KDA_ERR_INVALID_ARG;
+  if (z.ns == 0 || z.tokens == 0) return KDA_OK;   // (no live request: an empty `slots` has no address)
+  if (!slots && num_slots != 0) return KDA_ERR_INVALID_ARG;
   if (!state || !q || !k || !v || !g || !beta || !out) return KDA_ERR_INVALID_ARG;
   const void* ptrs16[] = {q, k, v, out, state};
   for (const void* p : ptrs16)

@@ -144,3 +144,12 @@ def test_layer_norm_backward_arguments(lib):
     assert norm_bwd(lib, ws=at(8) + 8) == 3 and norm_bwd(lib, dw=at(6) + 2) == 3
     assert norm_bwd(lib, dx=at(0)) == 1 and norm_bwd(lib, dw=at(7)) == 1 and norm_bwd(lib, ws=at(1)) == 1
     assert lib.kda_layer_norm_bwd_workspace_size(-1, 4) == 0
+
+
+def test_step_without_requests(lib):
+    """No sequences, or no tokens: nothing to do, with a pool too (an empty slots array may have
+    no address); a pool's size is checked all the same."""
+    for s in (S(B=0, T=1), S(T=0)):
+        assert step(lib, s, n=3) == 0 and step(lib, s, slots=at(9), n=3) == 0
+        assert step(lib, s, q=None, k=None, v=None, out=None, n=3) == 0
+        assert step(lib, s, n=-1) == 1

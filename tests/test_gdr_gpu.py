@@ -241,3 +241,14 @@ def test_refusals():
     refused(lambda: kda.kda_gdr_step(*args, x["s0"].bfloat16()))
     refused(lambda: kda.kda_gdr_step(*args, torch.cat([x["s0"]] * 2)))
     refused(lambda: kda.kda_gdr_step(*args, x["s0"], slots=torch.zeros(1, dtype=torch.int64, device="cuda")))
+
+
+@pytest.mark.parametrize("B,T", [(0, 1), (0, 0), (3, 0)])
+def test_step_without_requests(B, T):
+    """A serving loop without a live request: the pool keeps its bits."""
+    q = torch.empty(B, T, 2, 128, device="cuda", dtype=torch.bfloat16)
+    v, g = torch.empty(B, T, 4, 128, device="cuda", dtype=torch.bfloat16), torch.empty(B, T, 4, device="cuda")
+    pool = torch.randn(5, 4, 128, 128, device="cuda")
+    before, slots = pool.clone(), torch.arange(B, dtype=torch.int32, device="cuda")
+    o = kda.kda_gdr_step(q, q, v, g, g, pool, slots=slots)
+    assert o.shape == (B, T, 4, 128) and torch.equal(pool, before)
