@@ -414,7 +414,8 @@ KDA_API kda_status kda_layer_norm_fwd(int64_t rows, int D, kda_dtype io_dtype, c
  * Its gradients, from the forward's x, mean and rstd: dx [rows, D] io_dtype,
  * dweight and dbias [D] fp32 (each may be NULL, not all three).  The rows' sum for
  * dweight and dbias is taken in a fixed order (the same bits on every call);
- * workspace: kda_layer_norm_bwd_workspace_size(rows, D) bytes, uninitialised.
+ * workspace: kda_layer_norm_bwd_workspace_size(rows, D) bytes (of the
+ * current device, as the call's own), uninitialised.
  */
 KDA_API size_t kda_layer_norm_bwd_workspace_size(int64_t rows, int D);
 KDA_API kda_status kda_layer_norm_bwd(int64_t rows, int D, kda_dtype io_dtype, const void* x, int64_t x_stride,

@@ -233,11 +233,14 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, output_sta
 
 
 @functools.lru_cache(maxsize=256)
-def _norm_workspace_bytes(rows, D):
-    return int(load_library().kda_layer_norm_bwd_workspace_size(rows, D))
+def _norm_workspace_bytes(rows, D, index):
+    """The size on device `index` (a part for every block, and blocks go by the device's processors)."""
+    with torch.cuda.device(index):
+        return int(load_library().kda_layer_norm_bwd_workspace_size(rows, D))
 
 
 def kda_layer_norm_bwd_workspace_size(rows: int, D: int) -> int:
+    """Bytes for the current device."""
     return int(load_library().kda_layer_norm_bwd_workspace_size(rows, D))
 
 
@@ -259,7 +262,7 @@ def kda_layer_norm_bwd(x, dy, weight, mean, rstd, output_dx=True, output_dweight
     dw = empty(D, dtype=_f32, device=x.device) if output_dweight else None
     db = empty(D, dtype=_f32, device=x.device) if output_dbias else None
     if workspace is None:
-        n = _norm_workspace_bytes(rows, D)
+        n = _norm_workspace_bytes(rows, D, index)
         workspace = empty(n, dtype=torch.uint8, device=x.device)
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():

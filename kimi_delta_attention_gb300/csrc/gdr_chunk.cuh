@@ -21,6 +21,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "gdr_common.cuh"
 #include "sm103.cuh"
 
@@ -267,15 +269,15 @@ __device__ __forceinline__ void gate_scan(float g0, float g1, int lane, float (&
   lo[0] = l;
 }
 
+// Processors of the current device.
 inline int sm_count() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-      return 152;
-    return v;
-  }();
-  return n;
+  static std::atomic<int> known[64];
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+  if (dev < 64 && (v = known[dev].load(std::memory_order_relaxed)) > 0) return v;
+  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return 152;
+  if (dev < 64) known[dev].store(v, std::memory_order_relaxed);
+  return v;
 }
 
 // Launch a kernel, as a dependent of the stream's previous one where `after` says so; its
