@@ -494,7 +494,7 @@ int threads_per_row(int D) {
 // the two in flight, and every block costs a part of dw and db), 768 in the forward.
 
 template <typename IO, int VEC, int TPR, bool BWD>
-void launch_tpr(const Params& p, int grid, cudaStream_t st) {
+cudaError_t launch_tpr(const Params& p, int grid, cudaStream_t st) {
   constexpr int NT = TPR < 256 ? 256 : TPR, NV = 16 / VEC;
   // the ring: as many rows, up to 4, as 192 KB an SM hold
   constexpr size_t row = (BWD ? 2 : 1) * static_cast<size_t>(NV) * NT * sizeof(Raw<IO, VEC>);
@@ -507,17 +507,20 @@ void launch_tpr(const Params& p, int grid, cudaStream_t st) {
   if constexpr (bytes > 40 * 1024) {
     static bool raised[64] = {};       // (a race raises it twice, to the same value)
     int dev = 0;
-    cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !raised[dev]) {
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+      if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) raised[dev] = true;
     }
   }
   kernel<<<grid, NT, bytes, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename IO, int VEC, bool BWD>
-void launch_vec(const Params& p, int grid, cudaStream_t st) {
+cudaError_t launch_vec(const Params& p, int grid, cudaStream_t st) {
   switch (threads_per_row(p.D)) {
     case 32: return launch_tpr<IO, VEC, 32, BWD>(p, grid, st);
     case 64: return launch_tpr<IO, VEC, 64, BWD>(p, grid, st);
@@ -529,7 +532,7 @@ void launch_vec(const Params& p, int grid, cudaStream_t st) {
 }
 
 template <typename IO, bool BWD>
-void launch_io(const Params& p, int grid, cudaStream_t st) {
+cudaError_t launch_io(const Params& p, int grid, cudaStream_t st) {
   constexpr int E = 16 / sizeof(IO);
   auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
   const bool vec = p.D % E == 0 && p.ldx % E == 0 && al(p.x) && al(p.y) && al(p.w) && al(p.b) &&
@@ -539,11 +542,9 @@ void launch_io(const Params& p, int grid, cudaStream_t st) {
       layer_norm_bwd_wide_kernel<IO><<<grid, 1024, 0, st>>>(p);
     else
       layer_norm_wide_kernel<IO><<<static_cast<unsigned>(p.rows), 1024, 0, st>>>(p);
-  } else if (vec) {
-    launch_vec<IO, E, BWD>(p, grid, st);
-  } else {
-    launch_vec<IO, 1, BWD>(p, grid, st);
+    return cudaGetLastError();
   }
+  return vec ? launch_vec<IO, E, BWD>(p, grid, st) : launch_vec<IO, 1, BWD>(p, grid, st);
 }
 
 // Blocks for `rows` rows with at most `threads` threads an SM.
@@ -565,9 +566,7 @@ cudaError_t launch_fwd(const void* x, long ldx, const float* w, const float* b, 
                        float* rstd, long rows, int D, bool bf16, cudaStream_t st) {
   Params p{x, nullptr, w, b, y, mean, rstd, nullptr, nullptr, rows, ldx, 0, D, eps};
   const int grid = grid_for(rows, D, 768);
-  if (bf16) launch_io<__nv_bfloat16, false>(p, grid, st);
-  else launch_io<float, false>(p, grid, st);
-  return cudaGetLastError();
+  return bf16 ? launch_io<__nv_bfloat16, false>(p, grid, st) : launch_io<float, false>(p, grid, st);
 }
 
 cudaError_t launch_bwd(const void* x, long ldx, const void* dy, long lddy, const float* w, const float* mean,
@@ -578,8 +577,8 @@ cudaError_t launch_bwd(const void* x, long ldx, const void* dy, long lddy, const
   float* pb = db ? ws + static_cast<size_t>(grid) * D : nullptr;
   if (rows > 0) {
     Params p{x, dy, w, nullptr, dx, const_cast<float*>(mean), const_cast<float*>(rstd), pw, pb, rows, ldx, lddy, D, 0.f};
-    if (bf16) launch_io<__nv_bfloat16, true>(p, grid, st);
-    else launch_io<float, true>(p, grid, st);
+    const cudaError_t e = bf16 ? launch_io<__nv_bfloat16, true>(p, grid, st) : launch_io<float, true>(p, grid, st);
+    if (e != cudaSuccess) return e;
   }
   if (dw || db) {
     cudaLaunchAttribute attr;
