@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const Params p) {
       }
     }
   }
+  if constexpr (RING > 0) copies_wait<0>();   // (zeros, past the last row: they land before the block's memory goes)
 }
 
 // Rows wider than the register kernels hold: the block reads its row three times.
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
       if (G > 1) __syncthreads();
     }
   };
+  if constexpr (RING > 0) copies_wait<0>();   // (zeros, past the last row)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   write(dw, p.pw);
   write(db, p.pb);
