@@ -163,7 +163,10 @@ __global__ void __launch_bounds__(grad::NT, 1) gdr_grad_kernel(const __grid_cons
 
   Unit cur;
   int u = next_unit(a, blockIdx.x, units, cur);
-  if (u >= units) return;
+  if (u >= units) {
+    wait_for_previous_kernel();   // this kernel does not end before the chains, whatever comes after it
+    return;
+  }
   auto load = [&](const Unit& x) {  // all but S; one thread
     const size_t unit = static_cast<size_t>(x.slot) * p.HV + x.hv;
     const uint8_t* z = a.z + unit * (4 * C * V);

@@ -192,3 +192,16 @@ def test_gradients_unit_after_unit(K, V, H, HV):
         alone = backward(one)
         assert all(torch.equal(s[:, at:at + n], t) for s, t in zip(got[:5], alone[:5])) and torch.equal(got[5][i:i + 1], alone[5])
         at += n
+
+
+def test_no_sound_sequence():
+    """Bounds that leave no chunk at all: the state's gradient passes through and the status, read by
+    the next work on the stream, is there."""
+    x = cuda(make([100], 1, 2, 128, 128, seed=53, grads=True))
+    cu, status = torch.tensor([5, 100], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(20):
+        status.zero_()
+        got = kda.kda_gdr_bwd(x["q"], x["k"], x["v"], x["g"], x["beta"], x["do"], initial_state=x["s0"], cu_seqlens=cu,
+                              d_final_state=x["ds"], status=status)
+        seen = status.clone(), got[5].clone()
+        assert seen[0].item() == 2 and torch.equal(seen[1], x["ds"])
