@@ -147,8 +147,7 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
   let_next_kernel_start();
   const uint32_t tmem = *tslot;
   if (warp == 0) {
-    ok = mbar_wait_sleep(&bar[0], 0, a.wait_ns);
-    if (!ok) mbar_wait_sleep(&bar[0], 0, kDrainNs);
+    ok = wait_or_drain(&bar[0], 0, a.wait_ns);
     __syncwarp();
     const uint64_t d = sdesc_sw128(smem_u32(sm));
 #pragma unroll
@@ -160,10 +159,7 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
   const int i = tid & 63;
   const bool isq = tid >= 64;
   const float hi = -gh[i], lo = -gl[i], be = bs[i], end_hi = -gh[63], end_lo = -gl[63];
-  if (!mbar_wait_sleep(&bar[1], 0, a.wait_ns)) {
-    ok = false;
-    mbar_wait_sleep(&bar[1], 0, kDrainNs);
-  }
+  ok &= wait_or_drain(&bar[1], 0, a.wait_ns);
   tc_fence_after();
   // M and P.  D_ij = e^{gc_i - gc_j} directly in the last two 16-blocks of the warp's rows;
   // before them through the block's last row, as two factors <= 1, one per row and block, one
@@ -315,10 +311,7 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
     fac[128 + i] = be;
     if (i == 63) fac[kRecGamma] = ex2(hi);
   }
-  if (!mbar_wait_sleep(&bar[2], 0, a.wait_ns)) {
-    ok = false;
-    mbar_wait_sleep(&bar[2], 0, kDrainNs);
-  }
+  ok &= wait_or_drain(&bar[2], 0, a.wait_ns);
   tc_fence_after();
   if (isq) {
 #pragma unroll 1
@@ -525,6 +518,10 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
   if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
   // waits of a whole warp; false once the CTA has failed
   auto wait = [&](int b, uint32_t parity) { return wait_warp(&bars[b], parity, a.wait_ns, failed, p.status); };
+  // the loader's keep a short limit from the first look on
+  auto wait_load = [&](int b, uint32_t parity) {
+    return a.wait_ns < kPollNs ? wait_longer(&bars[b], parity, a.wait_ns, failed, p.status) : wait(b, parity);
+  };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[b]);
@@ -563,11 +560,11 @@ __device__ __forceinline__ void chain_body(const ChainMaps& maps, const ChunkPar
     if (MODE != FORWARD && nch > 0) load_t(nt++);
     for (int n = 1; n < nch; ++n) {
       if (MODE != FORWARD) {                       // free once step 2 of the chunk before is done
-        if (!wait(TFREE, (n - 1) & 1)) break;
+        if (!wait_load(TFREE, (n - 1) & 1)) break;
         load_t(nt++);
       }
       if (nf < nch) {                              // a stage's readers are done once the next chunk's products start
-        if (!wait(EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        if (!wait_load(EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
         load(nf++);
       }
     }
@@ -929,6 +926,10 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
   let_next_kernel_start();
   if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
   auto wait = [&](int b, uint32_t parity) { return wait_warp(&bars[b], parity, a.wait_ns, failed, p.status); };
+  // the loader's keep a short limit from the first look on
+  auto wait_load = [&](int b, uint32_t parity) {
+    return a.wait_ns < kPollNs ? wait_longer(&bars[b], parity, a.wait_ns, failed, p.status) : wait(b, parity);
+  };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[b]);
@@ -967,11 +968,11 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
     }
     for (int n = 1; n < nch; ++n) {
       if (nt < nch) {                              // free once step 2 of the chunk before is done
-        if (!wait(TFREE + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        if (!wait_load(TFREE + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
         load_t(nt++);
       }
       if (nf < nch) {                              // a stage's readers are done once the next chunk's products start
-        if (!wait(EMPTY + (n - 1) % 3, ((n - 1) / 3) & 1)) break;
+        if (!wait_load(EMPTY + (n - 1) % 3, ((n - 1) / 3) & 1)) break;
         load(nf++);
       }
     }
@@ -1297,6 +1298,10 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
   let_next_kernel_start();
   if (!in_order && tid == 0) atomicOr(p.status, kStatusBounds);
   auto wait = [&](int b, uint32_t parity) { return wait_warp(&bars[b], parity, a.wait_ns, failed, p.status); };
+  // the loader's keep a short limit from the first look on
+  auto wait_load = [&](int b, uint32_t parity) {
+    return a.wait_ns < kPollNs ? wait_longer(&bars[b], parity, a.wait_ns, failed, p.status) : wait(b, parity);
+  };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[b]);
@@ -1336,11 +1341,11 @@ __device__ __forceinline__ void wide_body(const ChainMaps& maps, const ChunkPara
     if (MODE != FORWARD && nch > 0) load_t(nt++);
     for (int n = 1; n < nch; ++n) {
       if (MODE != FORWARD) {                       // free once step 2 of the chunk before is done
-        if (!wait(wide::TFREE, (n - 1) & 1)) break;
+        if (!wait_load(wide::TFREE, (n - 1) & 1)) break;
         load_t(nt++);
       }
       if (nf < nch) {                              // a stage's readers are done once the next chunk's products start
-        if (!wait(wide::EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+        if (!wait_load(wide::EMPTY0 + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
         load(nf++);
       }
     }

@@ -202,11 +202,14 @@ __device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint64_t b, uin
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// mbarrier.try_wait may suspend a thread until the phase completes, so a limit is only looked
+// at where it returns without; a limit below this is kept by polling.
+constexpr unsigned long long kPollNs = 20000ull;
 // Wait for a barrier's phase, giving up after `limit_ns` or once *failed is set.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* failed) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
+  while (!(limit_ns < kPollNs ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
     if (now - t0 > limit_ns || *failed != 0u) return false;
@@ -229,6 +232,25 @@ static __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* failed,
                                           uint32_t* status) {
   return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || wait_longer(bar, parity, limit_ns, failed, status);
+}
+
+static __device__ __noinline__ bool wait_or_drain_longer(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (limit_ns >= kPollNs) {
+    if (mbar_wait_sleep(bar, parity, limit_ns)) return true;
+  } else {
+    const uint64_t t0 = globaltimer_ns();
+    do {
+      if (mbar_test_wait(bar, parity)) return true;
+    } while (globaltimer_ns() - t0 <= limit_ns);
+  }
+  mbar_wait_sleep(bar, parity, kDrainNs);
+  return false;
+}
+
+// A wait for work that ends by itself: false if it took longer than the limit (it has ended all
+// the same, or kDrainNs are over too).
+__device__ __forceinline__ bool wait_or_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return (limit_ns >= kPollNs && mbar_try_wait(bar, parity)) || wait_or_drain_longer(bar, parity, limit_ns);
 }
 
 __device__ __forceinline__ float ex2(float x) {
