@@ -62,3 +62,71 @@ def test_blocks_come_from_the_stream_that_writes_them(problem, name):
     again = [t for t in call(stream=torch.cuda.current_stream().cuda_stream) if t is not None]
     assert all(pool_of(t) == torch.cuda.current_stream().cuda_stream for t in again)
     assert all(torch.equal(a, b) for a, b in zip(ref, again))
+
+
+def captured(call, inputs, others):
+    """A call captured in a graph and replayed after its inputs took the values of `others`."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()                                     # (first call: set-up of the kernels)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for a, b in zip(inputs, others):
+        a.copy_(b)
+    graph.replay()
+    got = [t.clone() for t in out if t is not None]
+    for a, b in zip(inputs, others):
+        a.copy_(b)                                 # (what the call updates in place)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, (t for t in out if t is not None)))
+    for a, b in zip(inputs, others):
+        a.copy_(b)
+    ref = [t for t in call() if t is not None]
+    assert len(ref) == len(got) and all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+RULE = ("q", "k", "v", "g", "beta", "s0", "do", "ds")
+SHAPES = {"prompt": dict(seqs=(1, 37), H=4, HV=8, K=128, V=128), "thin": dict(seqs=(1, 300), H=2, HV=4, K=128, V=128),
+          "wide": dict(seqs=[70, 1, 200], H=8, HV=32, K=128, V=128), "small": dict(seqs=[300, 1, 100], H=16, HV=32, K=64, V=64)}
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_rule_in_a_graph(shape):
+    x, y = (cuda(make(seed=s, grads=True, **SHAPES[shape])) for s in (65, 66))
+    names = [n for n in RULE if x[n] is not None]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    fwd = lambda: kda.kda_gdr_fwd(*args, x["scale"], initial_state=x["s0"], cu_seqlens=x["cu"], status=status)
+    bwd = lambda: kda.kda_gdr_bwd(*args, x["do"], x["scale"], initial_state=x["s0"], cu_seqlens=x["cu"], d_final_state=x["ds"],
+                                  status=status)
+    for call in (fwd, bwd):
+        keep = [x[n].clone() for n in names]
+        captured(call, [x[n] for n in names], [y[n] for n in names])
+        for n, t in zip(names, keep):
+            x[n].copy_(t)
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_step_in_a_graph(io):
+    x, y = (cuda(make((6, 1), 2, 4, 128, 128, io=io, seed=s)) for s in (67, 68))
+    names = ["q", "k", "v", "g", "beta", "s0"]
+    slots = torch.tensor([3, -1, 0, 5, 4, 1], dtype=torch.int32, device="cuda")
+    args = [x[n] for n in names[:5]]
+    captured(lambda: (kda.kda_gdr_step(*args, x["s0"], x["scale"], slots=slots), x["s0"]),
+             [x[n] for n in names] + [slots], [y[n] for n in names] + [slots.flip(0)])
+
+
+@pytest.mark.parametrize("rows,D,io", [(24, 4096, torch.bfloat16), (3000, 1001, torch.float32), (9, 20000, torch.bfloat16)])
+def test_norm_in_a_graph(rows, D, io):
+    rn = lambda *s: torch.randn(*s, device="cuda")
+    x, dy, w, b = rn(rows, D).to(io), rn(rows, D).to(io), rn(D), rn(D)
+
+    def call():
+        y, mean, rstd = kda.kda_layer_norm_fwd(x, w, b)
+        return (y, mean, rstd, *kda.kda_layer_norm_bwd(x, dy, w, mean, rstd))
+
+    captured(call, [x, dy, w, b], [rn(rows, D).to(io), rn(rows, D).to(io), rn(D), rn(D)])
