@@ -187,3 +187,27 @@ def test_refusals():
                                            output_dbias=False))
     refused(lambda: kda.kda_layer_norm_bwd(x, x, None, mean, rstd,
                                            workspace=torch.empty(8, dtype=torch.uint8, device="cuda")), 6)
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [1, 2, 3, 4, 5, 7])
+def test_gradients_of_narrow_rows(D, io):
+    """A narrow row's dx cancels almost to nothing (D = 1: to nothing), so it is held against the
+    terms that cancel: each is good to some roundings of 2^-24, 16 in all.  The reference takes the
+    mean and rstd that the call is given."""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    x, dy = (2 * torch.randn(400, D, generator=gen, device="cuda") + 1).to(io), torch.randn(400, D, generator=gen, device="cuda").to(io)
+    w = 1 + 0.3 * torch.randn(D, generator=gen, device="cuda")
+    _, mean, rstd = kda.kda_layer_norm_fwd(x, w, None, EPS)
+    dx, dw, db = kda.kda_layer_norm_bwd(x, dy, w, mean, rstd)
+    r = rstd.double()[:, None]
+    xh, a = (x.double() - mean.double()[:, None]) * r, dy.double() * w.double()
+    c0, c1 = a.mean(-1, keepdim=True), (a * xh).mean(-1, keepdim=True)
+    ref = r * (a - c0 - xh * c1)
+    terms = r * (a.abs() + a.abs().mean(-1, keepdim=True) + xh.abs() * (a * xh).abs().mean(-1, keepdim=True))
+    bound = 16 * 2.0 ** -24 * terms + (2.0 ** -8 * ref.abs() if io == torch.bfloat16 else 0)
+    assert dx.dtype == io and ((dx.double() - ref).abs() <= bound).all()
+    if D == 1:
+        assert (dx == 0).all() and (dw == 0).all()
+    close(dw, (dy.double() * xh).sum(0), "dweight")
+    close(db, dy.double().sum(0), "dbias")
