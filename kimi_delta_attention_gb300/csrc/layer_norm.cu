@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "kda_common.cuh"
+#include "pairs.cuh"
 
 namespace kda {
 namespace ln {
@@ -115,29 +116,6 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float* red, int t) {
       x[i] = s;
     }
   }
-}
-
-// Two fp32 values in one 64-bit register, and the arithmetic on both at once.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 // 16 or 4 bytes to shared memory without passing through registers; the issuing thread alone
@@ -297,7 +275,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     for (int j = 0; j < NV; ++j) load_param<VEC>(v[j], p.w, VEC * (t + TPR * j), p.D, 1.f);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      w[n] = pair(v[2 * n / VEC][2 * n % VEC], v[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+      w[n] = pack2f(v[2 * n / VEC][2 * n % VEC], v[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
       dw[n] = db[n] = 0ull;
     }
   }
@@ -354,11 +332,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     }
     uint64_t xh[NP], a[NP], s0 = 0ull, s1 = 0ull;
     {
-      const uint64_t mm = pair(-mu, -mu), r2 = pair(r, r);
+      const uint64_t mm = pack2f(-mu, -mu), r2 = pack2f(r, r);
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
-        const uint64_t x = pair(vx[2 * n / VEC][2 * n % VEC], vx[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
-        const uint64_t d = pair(vy[2 * n / VEC][2 * n % VEC], vy[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+        const uint64_t x = pack2f(vx[2 * n / VEC][2 * n % VEC], vx[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+        const uint64_t d = pack2f(vy[2 * n / VEC][2 * n % VEC], vy[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
         xh[n] = mul2(add2(x, mm), r2);
         dw[n] = fma2(d, xh[n], dw[n]);
         db[n] = add2(db[n], d);
@@ -368,9 +346,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
       }
     }
     float s[2], half;
-    unpair(s0, s[0], half);
+    unpack2f(s0, s[0], half);
     s[0] += half;
-    unpair(s1, s[1], half);
+    unpack2f(s1, s[1], half);
     s[1] += half;
     fetch(row + (RING > 0 ? RING : 1) * step, slot);
     stats(row + step);
@@ -380,10 +358,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     const float c0 = s[0] / p.D, c1 = s[1] / p.D;
     if (row < p.rows && p.y) {
       IO* dx = static_cast<IO*>(p.y) + row * p.D;
-      const uint64_t n0 = pair(-c0, -c0), n1 = pair(-c1, -c1), r2 = pair(rr, rr);
+      const uint64_t n0 = pack2f(-c0, -c0), n1 = pack2f(-c1, -c1), r2 = pack2f(rr, rr);
 #pragma unroll
       for (int n = 0; n < NP; ++n)
-        unpair(mul2(r2, fma2(xh[n], n1, add2(a[n], n0))), vx[2 * n / VEC][2 * n % VEC], vx[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+        unpack2f(mul2(r2, fma2(xh[n], n1, add2(a[n], n0))), vx[2 * n / VEC][2 * n % VEC], vx[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = VEC * (t + TPR * j);
@@ -395,7 +373,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) layer_norm_bwd_kernel(c
     if (!part) return;
     float x[NV][VEC];
 #pragma unroll
-    for (int n = 0; n < NP; ++n) unpair(sums[n], x[2 * n / VEC][2 * n % VEC], x[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
+    for (int n = 0; n < NP; ++n) unpack2f(sums[n], x[2 * n / VEC][2 * n % VEC], x[(2 * n + 1) / VEC][(2 * n + 1) % VEC]);
     for (int g = 0; g < G; ++g) {
       if (grp == g) {
 #pragma unroll
