@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(prep::NT, 6) gdr_prep_kernel(const __grid_cons
   int seq, rows;
   long tok;
   if (blockIdx.x == 0 && tid == 0) *p.status = 0u;
-  if (!find_chunk(a, nullptr, slot, seq, tok, rows)) return;
+  if (!find_chunk(a, slot, seq, tok, rows)) return;
   bool ok = true;                                // this thread's waits
   if (warp == 0) {
     if (lane == 0) {

@@ -78,8 +78,9 @@ __device__ __forceinline__ int first_slot(const ChunkParams& a, int seq, long to
 }
 __device__ __forceinline__ int num_chunks(int len) { return (len + C - 1) >> 6; }
 
-// The sequence and chunk of a slot, by a whole warp; false where the slot holds no chunk.
-__device__ __forceinline__ bool find_chunk(const ChunkParams& a, uint32_t* status, int slot, int& seq, long& tok, int& rows) {
+// The sequence and chunk of a slot, by a whole warp; false where the slot holds no chunk
+// (bounds out of order are reported by the chains).
+__device__ __forceinline__ bool find_chunk(const ChunkParams& a, int slot, int& seq, long& tok, int& rows) {
   long tok0;
   int len, m;
   if (a.p.cu == nullptr) {
@@ -98,7 +99,7 @@ __device__ __forceinline__ bool find_chunk(const ChunkParams& a, uint32_t* statu
       hi = min(hi, lo + step);
     }
     seq = lo;
-    if (!seq_tokens(a.p.cu, a.p.T, a.p.num_seqs, status, seq, tok0, len)) return false;
+    if (!seq_tokens(a.p.cu, a.p.T, a.p.num_seqs, nullptr, seq, tok0, len)) return false;
     m = slot - first_slot(a, seq, tok0);
   }
   if (m < 0 || m >= num_chunks(len)) return false;

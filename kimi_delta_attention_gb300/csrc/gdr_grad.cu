@@ -106,7 +106,7 @@ __device__ __noinline__ int next_unit(const ChunkParams& a, int u, int units, Un
     int seq;
     x.slot = u / a.p.HV;
     x.hv = u - x.slot * a.p.HV;
-    if (find_chunk(a, nullptr, x.slot, seq, x.tok, x.rows)) break;
+    if (find_chunk(a, x.slot, seq, x.tok, x.rows)) break;
   }
   return u;
 }
