@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import _lib
-from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _written, load_library
+from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _increment_version, _written, load_library
 
 _IO = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _f32 = torch.float32
@@ -184,15 +184,15 @@ def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stat
         n = state.shape[0]
         states = (n, *states[1:])
     st = _need("state", state, _f32, states, index)
-    empty, empty_like = _allocators(stream, index)
-    given = (state, out, status)
+    written = (state,)
     if out is None:
-        out = empty_like(v)
+        out = _allocators(stream, index)[1](v)
     else:
         _need("out", out, v.dtype, v.shape, index)
+        written = (state, out)
     _check_status(status, index)
     _run(lib.kda_gdr_step, index, stream, shape, *addr, scale, st, at, n, out.data_ptr(), _ptr_or_none(status))
-    _written(*given)
+    _increment_version(written)
     return out
 
 
@@ -228,7 +228,8 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, output_sta
         rstd = empty_like(mean)
     _run(lib.kda_layer_norm_fwd, index, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, w, b, eps, out.data_ptr(),
          _ptr_or_none(mean), _ptr_or_none(rstd))
-    _written(given)
+    if given is not None:
+        _written(given)
     return out, mean, rstd
 
 

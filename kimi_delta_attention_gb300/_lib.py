@@ -130,6 +130,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         return lib
 
 
+_PLAIN = (torch.empty, torch.empty_like)
+_increment_version = torch.autograd.graph.increment_version
+
+
 def _allocators(stream, index):
     """torch.empty and torch.empty_like for a call that runs on the raw `stream` (None: the
     current one) of CUDA device `index`.  On another stream than the current one, a block comes
@@ -137,7 +141,7 @@ def _allocators(stream, index):
     the caller has enqueued.  The caller reads it on the current stream as a rule, so it is not
     handed out again before that stream is done with it either."""
     if stream is None or stream == torch._C._cuda_getCurrentRawStream(index):
-        return torch.empty, torch.empty_like
+        return _PLAIN
     here, there = torch.cuda.current_stream(index), torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
 
     def place(make, *args, **kw):
@@ -154,7 +158,7 @@ def _written(*tensors):
     by their version that they changed."""
     given = [t for t in tensors if t is not None]
     if given:
-        torch.autograd.graph.increment_version(given)
+        _increment_version(given)
 
 
 def kda_status_string(code: int) -> str:
