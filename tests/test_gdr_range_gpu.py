@@ -72,6 +72,34 @@ def gradients(x, tol, names=NAMES):
     assert status.item() == 0
 
 
+def test_single_elements():
+    """fp32 results element by element.  An element's error is the sum of a hundred and more
+    uncorrelated ones, so near to Gaussian, with F32 of the elements' size as a bound of its deviation:
+    6 deviations for a million elements, and heads and tokens differ from the whole in size by up to 3:
+    20 F32 of max(|ref|, rms)."""
+    x = cuda(make((2, 700), 2, 4, 128, 128, seed=87, grads=True))
+    _, S = kda.kda_gdr_fwd(*(x[n] for n in NAMES[:5]), x["scale"], initial_state=x["s0"])
+    got = kda.kda_gdr_bwd(*(x[n] for n in NAMES[:5]), x["do"], x["scale"], initial_state=x["s0"], d_final_state=x["ds"])
+    ref = recurrence(x, NAMES)
+    for what, a, b in (("state", S, recurrence(x)[1]), *zip(("dg", "dbeta", "ds0"), got[3:], ref[3:])):
+        rms = b.square().mean().sqrt()
+        worst = ((a.double() - b).abs() / b.abs().clamp_min(rms)).max().item()
+        assert worst <= 20 * F32, f"{what}: {worst:.2e}"
+
+
+def test_fp32_inputs_give_fp32_states():
+    """A caller who wants the states to fp32 passes fp32 q, k and v: the token recurrence.  A token
+    rounds a state three times to 2^-24 of its size and takes sums over 128 dims, trees of depth 11;
+    the gates (0.92 a token) leave some 12 tokens' errors to add up, uncorrelated:
+    (12 * (3 + 11)) ** 0.5 * 2^-24 = 7.7e-7."""
+    x = cuda(make((2, 700), 2, 4, 128, 128, seed=88))
+    full = {n: t.float() if n in "qkv" else t for n, t in x.items()}
+    o, S = kda.kda_gdr_fwd(*(full[n] for n in NAMES[:5]), x["scale"], initial_state=x["s0"])
+    o_ref, S_ref = recurrence(x)
+    off(S, S_ref, 7.7e-7, "state")
+    off(o, o_ref, 7.7e-7, "o")
+
+
 # thin chains, wide chains (more CTAs than processors), chains of V = 64
 @pytest.mark.parametrize("B,T,H,HV,K,V", [(1, 8200, 1, 1, 128, 128), (1, 6001, 2, 4, 64, 128), (1, 5000, 10, 40, 128, 128),
                                           (2, 4500, 20, 40, 128, 64)])
