@@ -346,12 +346,15 @@ KDA_API kda_status kda_chunk_fwd_static_scratch(const kda_shape* shape, const vo
  * Forward.  q, k [B, T, H, K], v, out [B, T, HV, V] io_dtype; initial_state and
  * final_state [NS, HV, K, V] fp32 or NULL; cu_seqlens as in kda_chunk_fwd;
  * final_state may be initial_state.  bf16 I/O runs in chunks of 64 tokens on the
- * tensor cores, every fp32 operand in two bf16 parts (states to about 4e-6); fp32
- * I/O runs the token recurrence.
+ * tensor cores, every fp32 operand in two bf16 parts: states come out to about 4e-6 of
+ * their norm.  fp32 I/O runs the token recurrence in fp32 (states to about 2e-7, token
+ * after token): the choice of a caller who needs the states to fp32.
  * workspace: kda_gdr_fwd_workspace_size(shape) bytes, nothing in it needs
  * initialising; its first word is the status kda_read_device_status reads
  * (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens, whose sequences are then
- * taken as empty, or KDA_ERR_DEVICE_TIMEOUT).
+ * taken as empty and their rows of out not written, or KDA_ERR_DEVICE_TIMEOUT; the
+ * results of such a call are not meaningful).  A call without sequences (B = 0) has
+ * nothing to do and leaves the workspace as it was.
  */
 KDA_API size_t kda_gdr_fwd_workspace_size(const kda_shape* shape);
 KDA_API kda_status kda_gdr_fwd(const kda_shape* shape, const void* q, const void* k, const void* v, const float* g,
@@ -372,6 +375,8 @@ KDA_API kda_status kda_gdr_fwd(const kda_shape* shape, const void* q, const void
  *   d_initial_state [NS, HV, K, V] fp32 or NULL (not written)
  *   workspace       kda_gdr_bwd_workspace_size(shape) bytes (at K = V = 128, 225 KiB a
  *                   chunk and value head), uninitialised; status as kda_gdr_fwd's
+ * The fp32 gradients come out to about 5e-6 of their norm; where the terms of dg cancel (keys
+ * all alike), to that of the terms.
  * The outputs must not overlap each other or any input.
  */
 KDA_API size_t kda_gdr_bwd_workspace_size(const kda_shape* shape);
@@ -389,7 +394,8 @@ KDA_API kda_status kda_gdr_bwd(const kda_shape* shape, const void* q, const void
  *          marks an empty row (its out is 0, no state is read or written).  The
  *          non-negative slots must differ from one another.  A slot >= num_slots is
  *          treated as empty and sets bit 1 of *status_word.
- *   num_slots  entries of the pool (0 without slots)
+ *   num_slots  entries of the pool (0 without slots).  Without sequences or tokens there
+ *          is nothing to do, whatever the pool.
  *   status_word  device word or NULL; bits are only ever added, the caller clears it
  *          (kda_read_device_status reads it: KDA_ERR_DEVICE_BOUNDS)
  */

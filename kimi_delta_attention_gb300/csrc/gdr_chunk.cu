@@ -1179,10 +1179,10 @@ __global__ void __launch_bounds__(thin::THREADS, 1) gdr_thin_kernel(const __grid
 // 64-column slices, whose two halves run different code.
 //
 // 370 us for 16 packed sequences (46402 tokens, 32 heads, 23424 chunks and heads), 2.4 us a
-// chunk: the products are 1.3 us of it at the tensor cores' rate (each fp32 operand counts
-// twice), the rest is the work between them, one after the other.  64-column slices took
-// 650.  Splitting the steps' operands in halves, products over the first while the second
-// is made, did not help (687 us a call for 680): both then fight for tensor memory.
+// chunk: the tensor pipes are active in 51 % of an SM's cycles, 1.2 us of it (each fp32 operand
+// counts twice), the rest is the work between the products, one after the other.  64-column
+// slices took 650.  Splitting the steps' operands in halves, products over the first while the
+// second is made, did not help (687 us a call for 680).
 //
 // SAVE leaves out the q and R halves.  REVERSE:
 //   1. D1 = dS'^T k^T

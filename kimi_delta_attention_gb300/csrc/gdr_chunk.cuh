@@ -13,9 +13,18 @@
 // every decay is a factor <= 1 on a row of an fp32 result; there is no range of g that the
 // form cannot take.
 //
-// Precision: q, k, v and d_out are exact bf16 operands.  Every fp32 operand (S, Y, vn, T,
-// R) is taken as two bf16 parts, high + low (2^-18 of the value is lost), and the parts'
-// products are summed in fp32; states and gates stay in fp32 registers.
+// Precision: q, k, v and d_out are exact bf16 operands; states, gates and sums are fp32.  Every
+// fp32 operand of a tensor-core product is taken as two bf16 parts, high + low (2^-18 of the
+// value is lost), and the parts' products are summed in fp32; of two such operands the product
+// of the low parts is left out (2^-18 too), but for [T; R] Y in the thin chains, where it comes
+// for nothing.  That is S with k and q, Y with T and R, E vn with k, P with T; in the backward dS'
+// with k, E (k dS') with T, R and scale G do with do and q, G beta z with k, z and vn (kept in
+// memory as two parts) with do, with each other, with S and with dS' (three parts), A and B with
+// q and k; the inverse's block products take two TF32 parts.  fp32 results come out 3e-6 to 5e-6
+// off in the 2-norm, where the same formulas in fp32 are at 2e-7 to 5e-7.  Three parts (24 bits)
+// would take half to twice as many products again and more TMEM and shared memory than there is
+// (both are full).  Beside bf16 results, 1.7e-3 off by their own rounding, it does not count; a
+// caller who wants the states to fp32 passes fp32 q, k and v, which run the token recurrence.
 #pragma once
 
 #include <cuda.h>
@@ -143,8 +152,8 @@ __device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t c) {
   return (r >> 3) * 512u + (r & 7) * 64u + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// A real branch to one lane of a converged warp: a predicate on every product and its
-// operands' way into uniform registers cost 27 instructions a product, the branch 8.
+// A real branch to one lane of a converged warp around all products of a step, where each
+// product was predicated on its own: 124 -> 118 us for a forward of 4096 tokens and 32 heads.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));

@@ -461,7 +461,10 @@ int sm_count() {
   return n;
 }
 
-constexpr int kMaxRegD = 16384;  // widest row the register kernels hold
+// Widest row that the kernels of a row in registers take.  Up to 8192 columns they hold it (but for
+// some 80 bytes a thread of single elements); above, a row takes 1024 threads, which leaves 64 registers
+// each, and the backward spills 436 to 716 bytes a thread (the forward 72 at most).
+constexpr int kMaxRegD = 16384;
 
 // Threads of a row so that each holds at most 16 values.
 int threads_per_row(int D) {
@@ -469,9 +472,6 @@ int threads_per_row(int D) {
   while (t * 16 < D) t *= 2;
   return t;
 }
-
-// Blocks: 512 threads an SM in the backward (each holds three rows' worth of values beside
-// the two in flight, and every block costs a part of dw and db), 768 in the forward.
 
 template <typename IO, int VEC, int TPR, bool BWD>
 cudaError_t launch_tpr(const Params& p, int grid, cudaStream_t st) {
@@ -527,7 +527,9 @@ cudaError_t launch_io(const Params& p, int grid, cudaStream_t st) {
   return vec ? launch_vec<IO, E, BWD>(p, grid, st) : launch_vec<IO, 1, BWD>(p, grid, st);
 }
 
-// Blocks for `rows` rows with at most `threads` threads an SM.
+// Blocks for `rows` rows with at most `threads` threads an SM: 512 in the backward (each thread
+// holds three rows' worth of values beside those in flight, and every block costs a part of dw
+// and db), 768 in the forward.
 int grid_for(long rows, int D, int threads) {
   const int tpr = D > kMaxRegD ? 1024 : threads_per_row(D);
   const int nt = tpr < 256 ? 256 : tpr, groups = nt / tpr;
