@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import _lib
-from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _increment_version, _written, load_library
+from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _increment_version, _lend, _written, load_library
 
 _IO = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _f32 = torch.float32
@@ -139,6 +139,8 @@ def kda_gdr_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=Non
     ws, n = _workspace(workspace, "kda_gdr_fwd_workspace_size", shape, index, empty)
     _run(lib.kda_gdr_fwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), out.data_ptr(),
          _ptr_or_none(final_state), ws.data_ptr(), n)
+    if stream is not None:
+        _lend(stream, index, q, k, v, g, beta, initial_state, cu_seqlens, out, final_state, ws, status)
     _written(*given)
     if status is not None and states[0] > 0:    # (a call without sequences leaves the workspace alone)
         _add_status(status, ws, stream, index)
@@ -165,6 +167,8 @@ def kda_gdr_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seql
     ws, n = _workspace(workspace, "kda_gdr_bwd_workspace_size", shape, index, empty)
     _run(lib.kda_gdr_bwd, index, stream, shape, *addr, scale, s0, _ptr_or_none(cu_seqlens), do, dfin, dq.data_ptr(),
          dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr_or_none(ds0), ws.data_ptr(), n)
+    if stream is not None:
+        _lend(stream, index, q, k, v, g, beta, initial_state, cu_seqlens, d_out, d_final_state, ws, status)
     if status is not None and states[0] > 0:
         _add_status(status, ws, stream, index)
     return dq, dk, dv, dg, dbeta, ds0
@@ -192,6 +196,8 @@ def kda_gdr_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stat
         written = (state, out)
     _check_status(status, index)
     _run(lib.kda_gdr_step, index, stream, shape, *addr, scale, st, at, n, out.data_ptr(), _ptr_or_none(status))
+    if stream is not None:
+        _lend(stream, index, q, k, v, g, beta, state, slots, out, status)
     _increment_version(written)
     return out
 
@@ -228,6 +234,8 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, output_sta
         rstd = empty_like(mean)
     _run(lib.kda_layer_norm_fwd, index, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, w, b, eps, out.data_ptr(),
          _ptr_or_none(mean), _ptr_or_none(rstd))
+    if stream is not None:
+        _lend(stream, index, x, weight, bias, out)
     if given is not None:
         _written(given)
     return out, mean, rstd
@@ -271,4 +279,6 @@ def kda_layer_norm_bwd(x, dy, weight, mean, rstd, output_dx=True, output_dweight
         n = workspace.numel() * workspace.element_size()
     _run(lib.kda_layer_norm_bwd, index, stream, rows, D, _IO[x.dtype], x.data_ptr(), ld, dy.data_ptr(), ldy, w, mu, rs,
          _ptr_or_none(dx), _ptr_or_none(dw), _ptr_or_none(db), workspace.data_ptr(), n)
+    if stream is not None:
+        _lend(stream, index, x, dy, weight, mean, rstd, workspace)
     return dx, dw, db

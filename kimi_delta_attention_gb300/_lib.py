@@ -153,6 +153,17 @@ def _allocators(stream, index):
     return functools.partial(place, torch.empty), functools.partial(place, torch.empty_like)
 
 
+def _lend(stream, index, *tensors):
+    """The tensors of a call that runs on the raw `stream`, another than the current one: a block
+    the caller gives up is not handed out again before that stream is done with it."""
+    if stream == torch._C._cuda_getCurrentRawStream(index):
+        return
+    there = torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(there)
+
+
 def _written(*tensors):
     """The caller's own tensors that a call has written: autograd may hold them saved, and sees
     by their version that they changed."""
@@ -246,6 +257,7 @@ def _forward_on_device(lib, entry, q, k, v, g, beta, scale, initial_state, cu_se
         _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state), _ptr(workspace),
         ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream))
     _check(code)
+    _lend(stream, q.get_device(), q, k, v, g, beta, initial_state, cu_seqlens, out, final_state, workspace)
     _written(*given)
     return out, final_state
 
@@ -302,6 +314,7 @@ def kda_chunk_fwd_static_scratch(q, k, v, g, beta, scale=None, initial_state=Non
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state), ctypes.c_void_p(stream),
             ctypes.byref(status))
         _check(code)
+        _lend(stream, q.get_device(), q, k, v, g, beta, initial_state, cu_seqlens, out, final_state)
         _written(*given)
     return out, final_state, status.value
 
@@ -324,6 +337,7 @@ def kda_decode(q, k, v, g, beta, state, scale=None, out=None, stream=None):
             stream = torch.cuda.current_stream(q.device).cuda_stream
         _check(lib.kda_decode(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                               ctypes.c_float(scale), _ptr(state), _ptr(out), ctypes.c_void_p(stream)))
+        _lend(stream, q.get_device(), q, k, v, g, beta, state, out)
         _written(*given)
     return out
 
@@ -364,6 +378,8 @@ def kda_chunk_fwd_gated(q, k, v, g_raw, beta_raw, A_log, dt_bias, gate="bounded"
             ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw), _ptr(beta_raw), ctypes.byref(gs),
             ctypes.c_float(scale), _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
             _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream)))
+        _lend(stream, q.get_device(), q, k, v, g_raw, beta_raw, A_log, dt_bias, initial_state, cu_seqlens, out, final_state,
+              workspace)
         _written(*given)
     return out, final_state
 
@@ -393,6 +409,7 @@ def kda_chunk_states(q, k, v, g, beta, initial_state=None, h=None, final_state=N
                                     _ptr(initial_state), _ptr(h), _ptr(final_state), _ptr(workspace),
                                     ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                     ctypes.c_void_p(stream)))
+        _lend(stream, q.get_device(), q, k, v, g, beta, initial_state, h, final_state, workspace)
         _written(*given)
     return h, final_state
 
@@ -417,6 +434,7 @@ def kda_chunk_output(q, k, v, g, beta, h, scale=None, out=None, workspace=None, 
                                     ctypes.c_float(scale), _ptr(h), _ptr(out), _ptr(workspace),
                                     ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                     ctypes.c_void_p(stream)))
+        _lend(stream, q.get_device(), q, k, v, g, beta, h, out, workspace)
         _written(given)
     return out
 
@@ -460,4 +478,5 @@ def kda_backward(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_seq
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_out), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(dg), _ptr(dbeta), _ptr(ds0), _ptr(workspace),
             ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(stream)))
+        _lend(stream, q.get_device(), q, k, v, g, beta, initial_state, cu_seqlens, d_out, d_final_state, workspace)
     return dq, dk, dv, dg, dbeta, ds0

@@ -130,3 +130,32 @@ def test_norm_in_a_graph(rows, D, io):
         return (y, mean, rstd, *kda.kda_layer_norm_bwd(x, dy, w, mean, rstd))
 
     captured(call, [x, dy, w, b], [rn(rows, D).to(io), rn(rows, D).to(io), rn(D), rn(D)])
+
+
+def test_inputs_are_kept_for_the_stream():
+    """Inputs given up after a call on a busy side stream are not handed out again before it is done."""
+    side = torch.cuda.Stream()
+    x = cuda(make((2, 100), 2, 4, 128, 128, seed=69, grads=True))
+    rule = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    rows = torch.randn(300, 512, device="cuda")
+    _, mean, rstd = kda.kda_layer_norm_fwd(rows)
+    calls = [(lambda *a, **kw: kda.kda_gdr_fwd(*a[:5], initial_state=a[5], **kw), rule + [x["s0"]]),
+             (lambda *a, **kw: kda.kda_gdr_bwd(*a[:6], initial_state=a[6], d_final_state=a[7], **kw), rule + [x["do"], x["s0"], x["ds"]]),
+             (lambda *a, **kw: (kda.kda_gdr_step(*a, **kw),), [t[:, :1].contiguous() for t in rule] + [x["s0"]]),
+             (lambda *a, **kw: kda.kda_layer_norm_fwd(*a, **kw), [rows]),
+             (lambda *a, **kw: kda.kda_layer_norm_bwd(*a[:2], None, *a[2:], **kw), [rows, rows + 1, mean, rstd])]
+    for call, tensors in calls:
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(int(2e7))            # some 10 ms
+        given = [t.clone() for t in tensors]
+        torch.cuda.current_stream().synchronize()
+        kept = {t.data_ptr() for t in given}
+        out = call(*given, stream=side.cuda_stream)
+        sizes = [(t.shape, t.dtype) for t in given]
+        del given
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d in sizes]
+        assert not kept & {t.data_ptr() for t in again}
+        side.synchronize()
+        ref = call(*[t.clone() for t in tensors])
+        assert all(torch.equal(a, b) for a, b in zip(out, ref) if a is not None)

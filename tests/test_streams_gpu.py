@@ -57,3 +57,31 @@ def test_blocks_come_from_the_stream_that_writes_them(problem, name):
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
     assert not freed & {t.data_ptr() for t in got}
     assert all(pool_of(t) == side.cuda_stream for t in got)
+
+
+def test_inputs_are_kept_for_the_stream():
+    """Inputs given up after a call on a busy side stream are not handed out again before it is done."""
+    side = torch.cuda.Stream()
+    x = W.make_inputs(2, 128, 2, 4, 128, 128, "bf16", seed=73, init_state=True).to("cuda")
+    args = [x.q, x.k, x.v, x.g, x.beta]
+    h, _ = kda.kda_chunk_states(*args)
+    calls = [(lambda *a, **kw: kda.kda_chunk_fwd(*a[:5], initial_state=a[5], **kw), args + [x.initial_state]),
+             (lambda *a, **kw: kda.kda_decode(*a, **kw), [t[:, :1].contiguous() for t in args] + [x.initial_state]),
+             (lambda *a, **kw: kda.kda_chunk_states(*a, **kw), args),
+             (lambda *a, **kw: kda.kda_chunk_output(*a, **kw), args + [h]),
+             (lambda *a, **kw: kda.kda_backward(*a, **kw), args + [x.v])]
+    for call, tensors in calls:
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(int(2e7))            # some 10 ms
+        given = [t.clone() for t in tensors]
+        torch.cuda.current_stream().synchronize()
+        kept = {t.data_ptr() for t in given}
+        out = call(*given, stream=side.cuda_stream)
+        sizes = [(t.shape, t.dtype) for t in given]
+        del given
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d in sizes]
+        assert not kept & {t.data_ptr() for t in again}
+        side.synchronize()
+        ref = call(*[t.clone() for t in tensors])
+        assert all(torch.equal(a, b) for a, b in zip(out, ref) if a is not None)
