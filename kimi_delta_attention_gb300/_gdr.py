@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import _lib
-from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _increment_version, _lend, _written, load_library
+from ._lib import KDA_BF16, KDA_F32, KdaError, KdaShape, _allocators, _check, _increment_version, _lend, _raw, _written, load_library
 
 _IO = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _f32 = torch.float32
@@ -107,7 +107,7 @@ def _add_status(status, ws, stream, index):
     if stream is None:
         word(status).bitwise_or_(word(ws))
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))):
+        with torch.cuda.stream(_raw(stream, index)):
             word(status).bitwise_or_(word(ws))
 
 

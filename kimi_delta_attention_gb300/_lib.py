@@ -134,6 +134,14 @@ _PLAIN = (torch.empty, torch.empty_like)
 _increment_version = torch.autograd.graph.increment_version
 
 
+def _raw(stream, index):
+    """The torch stream of a raw stream of CUDA device `index` (0: the legacy default stream, which
+    ExternalStream would take for no stream at all)."""
+    if stream == 0:
+        return torch.cuda.default_stream(index)
+    return torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
+
+
 def _allocators(stream, index):
     """torch.empty and torch.empty_like for a call that runs on the raw `stream` (None: the
     current one) of CUDA device `index`.  On another stream than the current one, a block comes
@@ -142,7 +150,7 @@ def _allocators(stream, index):
     handed out again before that stream is done with it either."""
     if stream is None or stream == torch._C._cuda_getCurrentRawStream(index):
         return _PLAIN
-    here, there = torch.cuda.current_stream(index), torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
+    here, there = torch.cuda.current_stream(index), _raw(stream, index)
 
     def place(make, *args, **kw):
         with torch.cuda.stream(there):
@@ -158,7 +166,7 @@ def _lend(stream, index, *tensors):
     the caller gives up is not handed out again before that stream is done with it."""
     if stream == torch._C._cuda_getCurrentRawStream(index):
         return
-    there = torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
+    there = _raw(stream, index)
     for t in tensors:
         if t is not None:
             t.record_stream(there)

@@ -159,3 +159,26 @@ def test_inputs_are_kept_for_the_stream():
         side.synchronize()
         ref = call(*[t.clone() for t in tensors])
         assert all(torch.equal(a, b) for a, b in zip(out, ref) if a is not None)
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd", "step", "norm", "norm_bwd"])
+def test_default_stream_by_its_raw_number(problem, name):
+    """stream=0 is the legacy default stream, for allocations too, whichever stream is current."""
+    call = problem[name]
+    ref = [t for t in call() if t is not None]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = [t for t in call(stream=0) if t is not None]
+        torch.cuda.synchronize()
+        assert all(pool_of(t) == 0 for t in got)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_status_on_the_default_stream():
+    x = cuda(make([100], 1, 2, 128, 128, seed=70))
+    cu, status = torch.tensor([0, 90], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        kda.kda_gdr_fwd(x["q"], x["k"], x["v"], x["g"], x["beta"], cu_seqlens=cu, stream=0, status=status)
+        torch.cuda.synchronize()
+    assert status.item() == 2
