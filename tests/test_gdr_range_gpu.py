@@ -181,3 +181,36 @@ def test_gate_gradients_against_their_terms(kind):
     size = (suffix(sum(t.square() for t in terms)) + terms[5].square().sum(-1, keepdim=True) +
             torch.exp(2 * gc[..., -1:]) * (S * dS).square().sum((-1, -2))[..., None]).sqrt()
     assert (got.double() - ref).norm() <= F32 * size.norm(), ((got.double() - ref).norm() / size.norm()).item()
+
+
+NEIGHBOURS = [dict(H=2, HV=4, K=128, V=128), dict(H=2, HV=4, K=64, V=64), dict(H=8, HV=32, K=128, V=128),
+              dict(H=8, HV=32, K=64, V=128), dict(H=16, HV=32, K=128, V=64)]
+
+
+@pytest.mark.parametrize("shape", NEIGHBOURS, ids=lambda s: "-".join(str(n) for n in s.values()))
+def test_neighbours_of_every_kernel(shape):
+    """Packed sequences full of NaN and infinities, in every input, leave the others' bits alone: thin
+    chains, wide ones, those of V = 64, and the gradients of each, behind, before and between partial chunks."""
+    seqs = [70, 33, 100, 1, 64, 129]
+    bad = [1, 3, 4]
+    x = make(seqs, state=True, seed=89, grads=True, **shape)
+    y = {n: t.clone() if torch.is_tensor(t) else t for n, t in x.items()}
+    at = torch.tensor([0] + seqs).cumsum(0).tolist()
+    keep = torch.ones(at[-1], dtype=torch.bool)
+    for i, s in enumerate(bad):
+        keep[at[s]:at[s + 1]] = False
+        for n in ("q", "k", "v", "do", "g", "beta"):
+            y[n][0, at[s]:at[s + 1]] = (float("nan"), float("inf"), -float("inf"))[i]
+        y["s0"][s], y["ds"][s] = float("inf"), float("nan")
+    rest = [s for s in range(len(seqs)) if s not in bad]
+
+    def both(x):
+        d = cuda(x)
+        args = [d[n] for n in NAMES[:5]]
+        o, S = kda.kda_gdr_fwd(*args, d["scale"], initial_state=d["s0"], cu_seqlens=d["cu"])
+        g = kda.kda_gdr_bwd(*args, d["do"], d["scale"], initial_state=d["s0"], cu_seqlens=d["cu"], d_final_state=d["ds"])
+        return [t[0, keep.cuda()] for t in (o, *g[:5])] + [S[rest], g[5][rest]]
+
+    clean, dirty = both(x), both(y)
+    assert all(torch.isfinite(t).all() for t in clean)
+    assert all(torch.equal(a, b) for a, b in zip(clean, dirty))
