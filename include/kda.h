@@ -376,7 +376,8 @@ KDA_API kda_status kda_gdr_fwd(const kda_shape* shape, const void* q, const void
  *   workspace       kda_gdr_bwd_workspace_size(shape) bytes (at K = V = 128, 225 KiB a
  *                   chunk and value head), uninitialised; status as kda_gdr_fwd's
  * The fp32 gradients come out to about 5e-6 of their norm; where the terms of dg cancel (keys
- * all alike), to that of the terms.
+ * all alike), to that of the terms.  To fp32, and for fp32 I/O: kda_backward with
+ * KDA_BACKWARD=recurrent and g repeated over the key dims (dg: the sum over them).
  * The outputs must not overlap each other or any input.
  */
 KDA_API size_t kda_gdr_bwd_workspace_size(const kda_shape* shape);

@@ -24,7 +24,8 @@
 // off in the 2-norm, where the same formulas in fp32 are at 2e-7 to 5e-7.  Three parts (24 bits)
 // would take half to twice as many products again and more TMEM and shared memory than there is
 // (both are full).  Beside bf16 results, 1.7e-3 off by their own rounding, it does not count; a
-// caller who wants the states to fp32 passes fp32 q, k and v, which run the token recurrence.
+// caller who wants the states to fp32 passes fp32 q, k and v, which run the token recurrence
+// (the gradients: kda_backward's token recurrence, with g repeated over the key dims).
 #pragma once
 
 #include <cuda.h>

@@ -68,8 +68,8 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlen
     to which the forward and the backward add the bits of their device status, read with
     kda_read_device_status(status) (which waits for the device) when the caller chooses: after a
     bounded wait that gave up or a cu_seqlens that does not end at T, results and gradients are
-    not meaningful, and nothing else tells.  fp32 q, k and v have no gradients: they raise where
-    one would be recorded."""
+    not meaningful, and nothing else tells.  fp32 q, k and v have no gradients here: they
+    raise where one would be recorded (kda_backward has them)."""
     if q.dtype != torch.bfloat16 and torch.is_grad_enabled() and any(
             t is not None and t.requires_grad for t in (q, k, v, g, beta, initial_state)):
         raise KdaError(2, "gradients of the gated delta rule need bf16 q, k and v")

@@ -100,6 +100,24 @@ def test_fp32_inputs_give_fp32_states():
     off(o, o_ref, 7.7e-7, "o")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_exact_path_for_states_and_gradients(io, monkeypatch):
+    """The library's exact-precision path takes the rule too, with the gate repeated over the key dims:
+    fp32 states and gradients of inputs of either type, token by token.  States as above; a gradient
+    has come through the states' recurrence and its own, 2 ** 0.5 * 7.7e-7; dg is a product of both,
+    twice that."""
+    monkeypatch.setenv("KDA_BACKWARD", "recurrent")
+    x = cuda(make((1, 500), 2, 4, 128, 128, io=io, seed=90, grads=True))
+    wide = x["g"][..., None].expand(*x["g"].shape, 128).contiguous()
+    args = (x["q"], x["k"], x["v"], wide, x["beta"])
+    _, S = kda.kda_recurrent_fwd(*args, x["scale"], initial_state=x["s0"])
+    off(S, recurrence(x)[1], 7.7e-7, "state")
+    got = list(kda.kda_backward(*args, x["do"], x["scale"], initial_state=x["s0"], d_final_state=x["ds"]))
+    got[3] = got[3].sum(-1)
+    for n, a, b in zip(NAMES, got, recurrence(x, NAMES)):
+        off(a, b, 2.2e-6 if n == "g" else 1.1e-6, "d" + n)
+
+
 # thin chains, wide chains (more CTAs than processors), chains of V = 64
 @pytest.mark.parametrize("B,T,H,HV,K,V", [(1, 8200, 1, 1, 128, 128), (1, 6001, 2, 4, 64, 128), (1, 5000, 10, 40, 128, 128),
                                           (2, 4500, 20, 40, 128, 64)])
