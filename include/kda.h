@@ -430,6 +430,141 @@ KDA_API kda_status kda_layer_norm_bwd(int64_t rows, int D, kda_dtype io_dtype, c
                                       const float* rstd, void* dx, float* dweight, float* dbias, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Gated linear recurrence: one state value per channel.
+ *     h_t = e^{g_t} h_{t-1} + x_t,   y_t = h_t        (per sequence and channel)
+ * the diagonal sibling of the delta rule (a state [D] where that one keeps [K, V] a head).
+ * g is a natural-log decay, at most 0 (-inf included: the state is dropped); a positive g is
+ * taken as it is as long as no product of e^g over a sequence overflows.
+ * Sequences as above: [B, T] tokens, or packed with cu_seqlens (B = 1, num_seqs >= 1).
+ * Pointers need their element's alignment only (16-byte aligned rows of D % 4 = 0 channels run
+ * the vector kernels).
+ */
+typedef struct {
+  int B, T;              /* sequences and tokens of each; packed: 1 and all tokens */
+  int D;                 /* channels */
+  int num_seqs;          /* packed sequences, else 0 */
+  kda_dtype io_dtype;    /* x, y and their gradients */
+  kda_dtype gate_dtype;  /* g and its gradient */
+} kda_glr_shape;
+
+/*
+ * Forward.  x, y [B, T, D] io_dtype; g [B, T, D] gate_dtype; initial_state (NULL: zeros) and
+ * final_state (NULL: not written) [NS, D] fp32; final_state may be initial_state.  States are
+ * fp32 throughout; y is each token's state rounded to io_dtype.
+ * workspace: kda_glr_fwd_workspace_size(shape) bytes, uninitialised; its first word is the
+ * status (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens, KDA_ERR_DEVICE_TIMEOUT; the results
+ * of such a call are not meaningful).  A call without sequences leaves it as it was.
+ */
+KDA_API size_t kda_glr_fwd_workspace_size(const kda_glr_shape* shape);
+KDA_API kda_status kda_glr_fwd(const kda_glr_shape* shape, const void* x, const void* g, const float* initial_state,
+                               const int32_t* cu_seqlens, void* y, float* final_state, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Backward: the gradients of sum_t <d_out_t, y_t> + <d_final_state, h_final> with respect to x,
+ * g and initial_state, from g and the forward's y (x is not needed).  dg_t = mu_t h_{t-1} takes
+ * h_{t-1} from y, so with bf16 y it carries that rounding (2^-8 of each value at most, as any
+ * activation kept in bf16).
+ *   d_out, dx [B, T, D] io_dtype; dg gate_dtype; d_final_state (NULL: zeros) and
+ *   d_initial_state (NULL: not written) [NS, D] fp32, which may be one array.
+ * workspace: kda_glr_bwd_workspace_size(shape), as the forward's.
+ */
+KDA_API size_t kda_glr_bwd_workspace_size(const kda_glr_shape* shape);
+KDA_API kda_status kda_glr_bwd(const kda_glr_shape* shape, const void* g, const void* y, const void* d_out,
+                               const float* initial_state, const int32_t* cu_seqlens, const float* d_final_state,
+                               void* dx, void* dg, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Step for serving: T (typically 1) new tokens of each of B sequences, states updated in place
+ * (num_seqs = 0).  state [B, D] fp32, or with slots [B] a pool [num_slots, D]; slots,
+ * num_slots and status_word as kda_gdr_step's.
+ */
+KDA_API kda_status kda_glr_step(const kda_glr_shape* shape, const void* x, const void* g, float* state,
+                                const int32_t* slots, int num_slots, void* y, uint32_t* status_word, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Group norm with an activation, channels last: x [N, L, C], a group is all L positions and
+ * C / groups neighbouring channels of a sample (L = 1: the norm of a layer's heads, token by
+ * token).
+ *     xh = (x - mean) rstd,  z = xh weight + bias,  y = act(z);  rstd = 1 / sqrt(var + eps)
+ * x, y contiguous, io_dtype; weight and bias [C] fp32 or NULL (ones, zeros); mean and rstd
+ * [N, groups] fp32 or NULL (not written); var biased.  Any sizes >= 1 with C % groups = 0;
+ * pointers need their element's alignment only.  Outputs must not overlap inputs or each other.
+ * workspace: kda_group_norm_fwd_workspace_size bytes (of the current device, as the call's own),
+ * uninitialised.
+ */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;  /* z; z / (1 + e^-z) */
+KDA_API size_t kda_group_norm_fwd_workspace_size(int64_t N, int64_t L, int C, int groups);
+KDA_API kda_status kda_group_norm_fwd(int64_t N, int64_t L, int C, int groups, kda_dtype io_dtype, kda_activation act,
+                                      const void* x, const float* weight, const float* bias, float eps, void* y,
+                                      float* mean, float* rstd, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, from the forward's x, mean and rstd: dx [N, L, C] io_dtype, dweight and dbias
+ * [C] fp32 (each may be NULL, not all three).  Every sum is taken in a fixed order (the same
+ * bits on every call); workspace: kda_group_norm_bwd_workspace_size, as the forward's.
+ */
+KDA_API size_t kda_group_norm_bwd_workspace_size(int64_t N, int64_t L, int C, int groups);
+KDA_API kda_status kda_group_norm_bwd(int64_t N, int64_t L, int C, int groups, kda_dtype io_dtype, kda_activation act,
+                                      const void* x, const void* dy, const float* weight, const float* bias,
+                                      const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * One AdamW step over many tensors (decoupled weight decay):
+ *     g = gradient * grad_scale
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, t = step.  A tensor's p is read from and written to `master` where it has one, and
+ * `param` is p rounded to param_dtype.
+ *
+ * States: state_bits 32: m and v [n] fp32.  state_bits 8: m and v [n] bytes, OCP e4m3 codes;
+ * blocks of KDA_ADAMW_BLOCK consecutive values of a tensor share an fp32 scale each, m_scale and
+ * v_scale [ceil(n / KDA_ADAMW_BLOCK)], the block's largest magnitude / 448: a value is code *
+ * scale.  Codes are rounded up or down at random in proportion (a moving average rounded to
+ * nearest stands still once a step changes it by less than half a code), by numbers that seed,
+ * step, the tensor's number and the value's place give alone; a v above 0 never gets code 0.  A
+ * value that is not finite gets the NaN code and counts for no scale; a block whose magnitudes
+ * are all below 2^-100 becomes zeros.  The step itself uses m and v before they are rounded.
+ * The rounding moves a v by up to 1/16 of itself a step, so it wanders about its mean by
+ * some 11 % at beta2 = 0.95, 25 % at 0.99 and 80 % at 0.999.
+ */
+#define KDA_ADAMW_BLOCK 256
+
+typedef struct {           /* addresses of device arrays, each with its element's alignment */
+  void* param;             /* [n] param_dtype, updated */
+  const void* grad;        /* [n] grad_dtype */
+  void* m;                 /* [n], updated */
+  void* v;                 /* [n], updated */
+  float* m_scale;          /* state_bits 8: updated; else NULL */
+  float* v_scale;
+  float* master;           /* [n] fp32, updated; or NULL */
+  int64_t n;               /* 0: nothing to do */
+  int64_t param_dtype;     /* kda_dtype */
+  int64_t grad_dtype;
+} kda_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;                /* 1, 2, ... (up to 2^31 - 1) */
+  uint64_t seed;               /* of the rounding of 8-bit states */
+  int state_bits;              /* 8 or 32 */
+  /* device words or NULL, read when the step runs (so that a captured step follows them): */
+  const int32_t* step_device;  /* in place of step */
+  const float* lr_device;      /* in place of lr */
+  const float* grad_scale;     /* multiplies every gradient; NULL: 1 */
+  const float* skip;           /* not 0: the step leaves every tensor as it is */
+} kda_adamw_config;
+
+/*
+ * `tensors` is an array of the host, read before the call returns.  What a call writes must not
+ * overlap anything else that it reads or writes.  No workspace.
+ */
+KDA_API kda_status kda_adamw_step(const kda_adamw_tensor* tensors, int count, const kda_adamw_config* config,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

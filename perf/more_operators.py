@@ -354,7 +354,7 @@ def _quantise(x, u, keep):
     up = torch.ldexp(torch.ones_like(y), 3 - e)                                     # 1 / step
     q = ((y * up + u).floor() / up).clamp(max=448.0)
     if keep:
-        q = torch.where((y > 0) & (q == 0), 2.0 ** -9, q)
+        q = torch.where((a > 0) & (q == 0), 2.0 ** -9, q)
     q = torch.where(torch.isfinite(a), q, float("nan"))
     return torch.copysign(q, x).to(torch.float8_e4m3fn), scale
 
