@@ -351,7 +351,7 @@ def _quantise(x, u, keep):
     scale = torch.where(some, top * (1.0 / 448), 0.0)
     y = a * torch.where(some, 448.0 / top, 0.0)[:, None]
     e = ((y.view(torch.int32) >> 23) - 127).clamp(-6, 8)
-    up = torch.ldexp(torch.ones_like(y), 3 - e)                                     # 1 / step
+    up = ((130 - e) << 23).view(torch.float32)                                      # 1 / step = 2^(3 - e)
     q = ((y * up + u).floor() / up).clamp(max=448.0)
     if keep:
         q = torch.where((a > 0) & (q == 0), 2.0 ** -9, q)
