@@ -6,6 +6,7 @@ package builds it in-tree and binds it with ctypes.
 from ._lib import (  # noqa: F401
     EXPORTS,
     KdaError,
+    KdaGlrShape,
     KdaShape,
     kda_backward,
     kda_backward_workspace_size,
@@ -36,4 +37,16 @@ from ._gdr import (  # noqa: F401
     kda_layer_norm_bwd_workspace_size,
     kda_layer_norm_fwd,
 )
+from ._glr import (  # noqa: F401
+    kda_glr_bwd,
+    kda_glr_bwd_workspace_size,
+    kda_glr_fwd,
+    kda_glr_fwd_workspace_size,
+    kda_glr_step,
+    kda_group_norm_bwd,
+    kda_group_norm_bwd_workspace_size,
+    kda_group_norm_fwd,
+    kda_group_norm_fwd_workspace_size,
+)
+from ._adamw import kda_adamw_step  # noqa: F401
 from .builder import build  # noqa: F401

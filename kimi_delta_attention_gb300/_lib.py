@@ -36,7 +36,10 @@ EXPORTS = ("kda_chunk_fwd", "kda_recurrent_fwd", "kda_chunk_fwd_workspace_size",
            "kda_chunk_states_size", "kda_chunk_states", "kda_chunk_output", "kda_backward_workspace_size",
            "kda_backward",
            "kda_gdr_fwd_workspace_size", "kda_gdr_fwd", "kda_gdr_bwd_workspace_size", "kda_gdr_bwd", "kda_gdr_step", "kda_layer_norm_fwd",
-           "kda_layer_norm_bwd_workspace_size", "kda_layer_norm_bwd")
+           "kda_layer_norm_bwd_workspace_size", "kda_layer_norm_bwd",
+           "kda_glr_fwd_workspace_size", "kda_glr_fwd", "kda_glr_bwd_workspace_size", "kda_glr_bwd", "kda_glr_step",
+           "kda_group_norm_fwd_workspace_size", "kda_group_norm_fwd", "kda_group_norm_bwd_workspace_size", "kda_group_norm_bwd",
+           "kda_adamw_step")
 GATE_KINDS = {"bounded": 0, "softplus": 1}
 
 
@@ -55,6 +58,18 @@ class KdaShape(ctypes.Structure):
 class KdaGate(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
                 ("lower_bound", ctypes.c_float)]
+
+
+class KdaGlrShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("num_seqs", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int)]
+
+
+class KdaAdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("state_bits", ctypes.c_int), ("step_device", ctypes.c_void_p), ("lr_device", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p), ("skip", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -125,6 +140,27 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.kda_layer_norm_bwd_workspace_size.restype = S
         lib.kda_layer_norm_bwd.argtypes = [L, I, I, P, L, P, L, P, P, P, P, P, P, P, S, P]
         lib.kda_layer_norm_bwd.restype = I
+        GS = ctypes.POINTER(KdaGlrShape)
+        for name in ("kda_glr_fwd_workspace_size", "kda_glr_bwd_workspace_size"):
+            fn = getattr(lib, name)
+            fn.argtypes = [GS]
+            fn.restype = S
+        lib.kda_glr_fwd.argtypes = [GS, P, P, P, P, P, P, P, S, P]
+        lib.kda_glr_fwd.restype = I
+        lib.kda_glr_bwd.argtypes = [GS, P, P, P, P, P, P, P, P, P, P, S, P]
+        lib.kda_glr_bwd.restype = I
+        lib.kda_glr_step.argtypes = [GS, P, P, P, P, I, P, P, P]
+        lib.kda_glr_step.restype = I
+        for name in ("kda_group_norm_fwd_workspace_size", "kda_group_norm_bwd_workspace_size"):
+            fn = getattr(lib, name)
+            fn.argtypes = [L, L, I, I]
+            fn.restype = S
+        lib.kda_group_norm_fwd.argtypes = [L, L, I, I, I, I, P, P, P, F, P, P, P, P, S, P]
+        lib.kda_group_norm_fwd.restype = I
+        lib.kda_group_norm_bwd.argtypes = [L, L, I, I, I, I, P, P, P, P, P, P, P, P, P, P, S, P]
+        lib.kda_group_norm_bwd.restype = I
+        lib.kda_adamw_step.argtypes = [ctypes.c_char_p, I, ctypes.POINTER(KdaAdamwConfig), P]
+        lib.kda_adamw_step.restype = I
         if path is None:
             _lib = lib
         return lib
