@@ -55,19 +55,19 @@ kda_status check_glr(const kda_glr_shape* s, bool packed, GlrSizes& z) {
   return KDA_OK;
 }
 
-size_t glr_bytes(const kda_glr_shape* s, const GlrSizes& z) {
-  return kda::kWorkspaceBytes + kda::glr::workspace_bytes(static_cast<long>(z.tokens), s->D, s->num_seqs > 0, s->T);
+size_t glr_bytes(const kda_glr_shape* s, const GlrSizes& z, bool backward) {
+  return kda::kWorkspaceBytes + kda::glr::workspace_bytes(static_cast<long>(z.tokens), s->D, backward, s->io_dtype == KDA_BF16);
 }
 
-size_t glr_workspace_size(const kda_glr_shape* s) {
+size_t glr_workspace_size(const kda_glr_shape* s, bool backward) {
   GlrSizes z;
-  return check_glr(s, s && s->num_seqs > 0, z) == KDA_OK ? glr_bytes(s, z) : 0;
+  return check_glr(s, s && s->num_seqs > 0, z) == KDA_OK ? glr_bytes(s, z, backward) : 0;
 }
 
 // Both directions: `ins` inputs, `outs` outputs (the last one may be the array `same`).
 kda_status run_glr(const kda_glr_shape* s, const GlrSizes& z, kda::glr::Params p, bool backward, const Span* ins, int n_ins,
                    const Span* outs, int n_outs, const void* same, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!workspace || workspace_bytes < glr_bytes(s, z)) return KDA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < glr_bytes(s, z, backward)) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return KDA_ERR_ALIGNMENT;
   const Span w{workspace, workspace_bytes};
   for (int i = 0; i < n_outs; ++i) {
@@ -123,8 +123,8 @@ bool clash(Range* r, int n) {
 
 extern "C" {
 
-size_t kda_glr_fwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s); }
-size_t kda_glr_bwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s); }
+size_t kda_glr_fwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s, false); }
+size_t kda_glr_bwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s, true); }
 
 kda_status kda_glr_fwd(const kda_glr_shape* s, const void* x, const void* g, const float* initial_state,
                        const int32_t* cu_seqlens, void* y, float* final_state, void* workspace, size_t workspace_bytes,

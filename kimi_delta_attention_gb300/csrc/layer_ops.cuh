@@ -28,7 +28,7 @@ struct Params {
   int T, D, num_seqs;   // T: tokens of a sequence (without cu)
 };
 
-size_t workspace_bytes(long tokens, int D, bool packed, int T);
+size_t workspace_bytes(long tokens, int D, bool backward, bool bf16);
 cudaError_t launch(const Params& p, bool backward, bool bf16, bool gate_bf16, cudaStream_t stream);
 
 struct StepParams {

@@ -113,6 +113,18 @@ def test_state_in_place_and_in_pieces():
     within(state, rs, es, "state")
 
 
+@pytest.mark.parametrize("lengths", [[2000, 3, 0, 900], [64] * 40, [5, 1000] * 9])
+def test_final_states_over_initial_ones(lengths):
+    """final_state may be initial_state, and d_initial_state would be d_final_state's: a sequence's end is
+    written after its start was read, tiles apart or in one tile."""
+    d = make_glr(lengths, 384, BF, F32, seed=20)
+    y, s = kda.kda_glr_fwd(d["x"], d["g"], initial_state=d["s0"], cu_seqlens=d["cu"])
+    for _ in range(10):
+        state = d["s0"].clone()
+        y2, s2 = kda.kda_glr_fwd(d["x"], d["g"], initial_state=state, cu_seqlens=d["cu"], final_state=state)
+        assert s2 is state and torch.equal(y, y2) and torch.equal(s, s2)
+
+
 def test_gradients_against_differences():
     d = make_glr([9, 6], 3, F32, F32, seed=13)
     y, _ = kda.kda_glr_fwd(d["x"], d["g"], initial_state=d["s0"], cu_seqlens=d["cu"])
