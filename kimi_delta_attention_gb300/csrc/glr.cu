@@ -10,11 +10,12 @@
 // A block takes a tile of 128 channels and 64 tokens (32 in the fp32 backward), a warp 8 of the
 // tokens with 4 channels a thread, all of them in registers from one burst of loads.  A warp's
 // tokens act on what enters them as c -> A c + H; the warps' (A, H) join through shared memory, and the
-// tiles of a channel through words in the workspace: a tile publishes its (A, H), looks back over
-// the tiles before it until one whose outgoing value is known, folds forward from there and
-// publishes its own outgoing value.  Folding always forward, whichever tile it started from, gives
-// the same bits on every call.  Tiles are taken in order by a counter, so whoever a tile waits for
-// is already running; the waits are bounded all the same.
+// tiles of a channel through words in the workspace.  16 tiles make a group: a tile publishes its
+// (A, H), reads those of its group's tiles before it and the value that enters the group, and
+// folds forward over them; the group's last tile publishes what enters the next one.  So the serial
+// part is one exchange through L2 for 1024 tokens, and every fold goes over the same terms in the
+// same order on every call.  Tiles are taken in order by a counter, so whoever a tile waits for is
+// already running; the waits are bounded all the same.
 #include "layer_ops.cuh"
 
 namespace kda {
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kChannels = 128;  // of a tile: 4 a thread
 constexpr int kWarps = 8;
-constexpr int kWindow = 32;     // tiles a look back reaches
+constexpr int kGroup = 16;      // tiles joined without an exchange from one to the next
 
 // 4 channels as they lie in memory
 template <typename T>
@@ -99,7 +100,8 @@ __device__ __forceinline__ void store_state(float* states, int seq, int c0, int 
   }
 }
 
-// A published word: (A, H) of a tile, or (kKnown, its outgoing value); kEmpty before either.
+// A published word: (A, H) of a tile, or (kKnown, its outgoing value) where nothing that enters it
+// gets through; kEmpty before.
 constexpr uint64_t kEmpty = ~0ull;
 constexpr float kKnown = -1.f;   // (an A is a product of exponentials, never below 0)
 
@@ -125,21 +127,41 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
-// The last sequence that starts at or before token t (0 .. num_seqs - 1, whatever cu holds).
-__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t) {
-  int lo = 0, hi = num_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= t) lo = mid;
-    else hi = mid;
+// The last sequence that starts at or before token t (0 .. num_seqs - 1, whatever cu holds), by a whole
+// warp: 32 probes at a time.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t, int lane) {
+  int lo = 0, n = num_seqs;                // it is among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lo + lane * step;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane * step < n && cu[at] <= t);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
   }
   return lo;
+}
+
+// Waits until a thread's 4 words are there; false where the wait gave up.
+__device__ __forceinline__ bool wait_words(uint64_t (&w)[4], const uint64_t* p, unsigned long long limit_ns, uint32_t* status) {
+  unsigned long long t0 = 0;
+  for (;;) {
+    load_words(w, p);
+    if (__all_sync(0xFFFFFFFFu, w[0] != kEmpty && w[1] != kEmpty && w[2] != kEmpty && w[3] != kEmpty)) return true;
+    const unsigned long long t = now_ns();
+    if (t0 == 0) t0 = t;
+    // (one clock for the warp: its lanes leave together)
+    const bool late = t - t0 > limit_ns || (*reinterpret_cast<volatile uint32_t*>(status) & kStatusTimeout);
+    if (__any_sync(0xFFFFFFFFu, late)) break;
+  }
+  if ((threadIdx.x & 31) == 0) atomicOr(status, kStatusTimeout);
+  return false;
 }
 
 struct Scan {
   Params p;
   int tiles, channel_tiles;      // tiles along the tokens; tiles of channels
-  uint64_t* words;               // [tiles][channel_tiles][128], or null for one tile along the tokens
+  uint64_t* words;               // [tiles][channel_tiles][128], or null for one tile along the tokens; what a
+                                 // group's last tile writes is what enters the next group
   uint32_t* counter;
 };
 
@@ -154,7 +176,8 @@ template <typename IO, typename G, bool BWD, bool VEC, int R>
 __global__ void __launch_bounds__(32 * kWarps, 2) glr_scan_kernel(const Scan s) {
   constexpr int TL = kWarps * R;
   __shared__ __align__(16) float sa[kWarps][kChannels], sh[kWarps][kChannels];
-  __shared__ uint64_t win[kWindow][kChannels];
+  __shared__ __align__(16) uint64_t win[kGroup][kChannels];
+  __shared__ uint8_t known_in[kGroup];
   __shared__ uint32_t ticket;
   __shared__ uint8_t closed_by[kWarps];
   const Params& p = s.p;
@@ -196,11 +219,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_scan_kernel(const Scan s) 
   // lane r < n: the sequence of the warp's token r, and whether the scan starts anew or ends there
   int seq = 0;
   bool starts = false, ends = false, live = false;
+  if (p.cu && n > 0) seq = find_seq(p.cu, p.num_seqs, token(BWD ? n - 1 : 0), lane);
   if (lane < n) {
     const int t = token(lane);
     bool first, last;
     if (p.cu) {
-      seq = find_seq(p.cu, p.num_seqs, t);
+      if (p.cu[seq + 1] <= t) {        // another one than that of the warp's earliest token
+        int hi = p.num_seqs;
+        while (hi - seq > 1) {
+          const int mid = (seq + hi) >> 1;
+          if (p.cu[mid] <= t) seq = mid;
+          else hi = mid;
+        }
+      }
       const int a = p.cu[seq], b = p.cu[seq + 1];
       live = a <= t && t < b;
       first = t == a;
@@ -260,10 +291,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_scan_kernel(const Scan s) 
   }
   float C[4] = {0.f, 0.f, 0.f, 0.f};       // what enters the tile
   if (s.words) {
-    uint64_t* mine = s.words + (static_cast<size_t>(tile) * s.channel_tiles + ct) * kChannels + 4 * lane;
+    const size_t row = static_cast<size_t>(s.channel_tiles) * kChannels;          // words of a tile
+    uint64_t* mine = s.words + tile * row + ct * kChannels + 4 * lane;
+    const int m = tile % kGroup;                                                  // tiles of the group before this one
+    const bool last = m == kGroup - 1;
     // the whole tile's A c + H, in the last warp
     float TA[4], TH[4];
-    bool known = pclosed || closed || tile == 0;
+    const bool known = pclosed || closed || tile == 0;
     if (warp == kWarps - 1) {
       uint64_t w4[4];
 #pragma unroll
@@ -272,48 +306,36 @@ __global__ void __launch_bounds__(32 * kWarps, 2) glr_scan_kernel(const Scan s) 
         TH[j] = closed ? H[j] : fmaf(A[j], PH[j], H[j]);
         w4[j] = word(known ? kKnown : TA[j], TH[j]);
       }
-      store_words(mine, w4);
+      if (known || !last) store_words(mine, w4);
     }
     // (uniform over the block: the tile's first token says whether anything enters)
-    const bool wanted = tile > 0 && !__syncthreads_or(warp == 0 && (m_start & 1));
-    if (wanted) {
-      const unsigned long long t0 = now_ns();
-      const size_t back = static_cast<size_t>(s.channel_tiles) * kChannels;
-      for (int reach = 0;;) {
-        // warp w reads the tile reach + w + 1 before this one
-        const int k = reach + warp;
-        uint64_t w4[4] = {kEmpty, kEmpty, kEmpty, kEmpty};
-        if (k < tile) load_words(w4, mine - (k + 1) * back);
+    if (tile > 0 && !__syncthreads_or(warp == 0 && (m_start & 1))) {
+      // the group's tiles before this one, a warp each
+      for (int k = warp; k < m; k += kWarps) {
+        uint64_t w4[4];
+        wait_words(w4, mine - (m - k) * row, p.wait_ns, p.status);
+        *reinterpret_cast<ulonglong2*>(&win[k][4 * lane]) = make_ulonglong2(w4[0], w4[1]);
+        *reinterpret_cast<ulonglong2*>(&win[k][4 * lane + 2]) = make_ulonglong2(w4[2], w4[3]);
+        if (lane == 0) known_in[k] = word_a(w4[0]) == kKnown;                     // (the same in every channel)
+      }
+      __syncthreads();
+      int k = m - 1;
+      while (k >= 0 && !known_in[k]) --k;
+      if (k >= 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) win[k][4 * lane + j] = w4[j];
-        bool lost = false;
-        if (tid == 0 && (now_ns() - t0 > p.wait_ns || *reinterpret_cast<volatile uint32_t*>(p.status) & kStatusTimeout)) {
-          atomicOr(p.status, kStatusTimeout);
-          lost = true;
-        }
-        lost = __syncthreads_or(lost);
-        // fold forward from the nearest known value
-        bool found = true, gap = false;
+        for (int j = 0; j < 4; ++j) C[j] = word_h(win[k][4 * lane + j]);
+      } else if (tile >= kGroup) {
+        uint64_t w4[4];
+        wait_words(w4, mine - (m + 1) * row, p.wait_ns, p.status);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          int i = 0;
-          while (i < reach + kWarps && win[i][4 * lane + j] != kEmpty && word_a(win[i][4 * lane + j]) != kKnown) ++i;
-          if (i < reach + kWarps && win[i][4 * lane + j] != kEmpty) {
-            float c = word_h(win[i][4 * lane + j]);
-            while (--i >= 0) c = fmaf(word_a(win[i][4 * lane + j]), c, word_h(win[i][4 * lane + j]));
-            C[j] = c;
-          } else {
-            found = false;
-            gap |= i < reach + kWarps;
-          }
-        }
-        // (every warp sees the same words: these are uniform but for the lanes)
-        const int all = __syncthreads_and(found), hole = __syncthreads_or(gap);
-        if (all || lost) break;
-        reach = hole || reach + 2 * kWarps > kWindow ? 0 : reach + kWarps;
+        for (int j = 0; j < 4; ++j) C[j] = word_h(w4[j]);
+      }
+      while (++k < m) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) C[j] = fmaf(word_a(win[k][4 * lane + j]), C[j], word_h(win[k][4 * lane + j]));
       }
     }
-    if (warp == kWarps - 1 && !known) {
+    if (warp == kWarps - 1 && last && !known) {
       uint64_t w4[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) w4[j] = word(kKnown, fmaf(TA[j], C[j], TH[j]));
