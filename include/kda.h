@@ -453,8 +453,8 @@ typedef struct {
  * final_state (NULL: not written) [NS, D] fp32; final_state may be initial_state.  States are
  * fp32 throughout; y is each token's state rounded to io_dtype.
  * workspace: kda_glr_fwd_workspace_size(shape) bytes, uninitialised; its first word is the
- * status (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens, KDA_ERR_DEVICE_TIMEOUT; the results
- * of such a call are not meaningful).  A call without sequences leaves it as it was.
+ * status (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens; the results of such a call are not
+ * meaningful).  A call without sequences leaves it as it was.
  */
 KDA_API size_t kda_glr_fwd_workspace_size(const kda_glr_shape* shape);
 KDA_API kda_status kda_glr_fwd(const kda_glr_shape* shape, const void* x, const void* g, const float* initial_state,

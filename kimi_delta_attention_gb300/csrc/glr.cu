@@ -7,24 +7,25 @@
 // first token from its initial value.  Bound by HBM: each input is read and each output
 // written once, 8 bytes an element forward (bf16 with an fp32 gate), 14 backward.
 //
-// A block takes a tile of 128 channels and 64 tokens (32 in the fp32 backward), a warp 8 of the
-// tokens with 4 channels a thread, all of them in registers from one burst of loads.  A warp's
-// tokens act on what enters them as c -> A c + H; the warps' (A, H) join through shared memory, and the
-// tiles of a channel through words in the workspace.  16 tiles make a group: a tile publishes its
-// (A, H), reads those of its group's tiles before it and the value that enters the group, and
-// folds forward over them; the group's last tile publishes what enters the next one.  So the serial
-// part is one exchange through L2 for 1024 tokens, and every fold goes over the same terms in the
-// same order on every call.  Tiles are taken in order by a counter, so whoever a tile waits for is
-// already running; the waits are bounded all the same.
+// A CTA owns 32 channels and walks over the tokens in tiles of 128 (64 in the fp32 backward): 8
+// threads a row with 4 channels each, 4 neighbouring tokens a thread.  Any stretch of tokens acts on
+// what enters it as c -> A c + H; a thread's (A, H) join over the warp by shuffles, over the warps
+// through shared memory.  Where there are fewer channel tiles than places for CTAs, a cluster takes
+// its step's tiles side by side and each CTA writes its (A, H) into the others' shared memory: one
+// cluster barrier a step, and it is waited for a step later, under the next tile's sums.  So a
+// tile's inputs lie in a ring in shared memory from their load, one step ahead, until what enters
+// them is known, and the recurrence itself never leaves the chip.  Every fold goes over the same
+// terms in the same order on every call.
 #include "layer_ops.cuh"
 
 namespace kda {
 namespace glr {
 namespace {
 
-constexpr int kChannels = 128;  // of a tile: 4 a thread
-constexpr int kWarps = 8;
-constexpr int kGroup = 16;      // tiles joined without an exchange from one to the next
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kChannels = 32;             // of a tile: 4 a thread, 8 threads a row
+constexpr int kRows = kThreads / 8;       // threads along the tokens, each with R neighbours
+constexpr int kMaxCluster = 8;
 
 // 4 channels as they lie in memory
 template <typename T>
@@ -43,8 +44,8 @@ struct Raw4<float> {
   __device__ __forceinline__ float get(int j) const { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; }
 };
 
-// A thread's channels: c0 .. c0 + 3 (VEC: D % 4 = 0 and aligned rows), else c0, c0 + 32, ...
-template <bool VEC, typename T>
+// A thread's channels: c0 .. c0 + 3 (VEC: D % 4 = 0 and aligned rows), else c0, c0 + GAP, ...
+template <bool VEC, int GAP, typename T>
 __device__ __forceinline__ Raw4<T> load4(const T* row, int c0, int D) {
   Raw4<T> r;
   if constexpr (VEC) {
@@ -53,18 +54,18 @@ __device__ __forceinline__ Raw4<T> load4(const T* row, int c0, int D) {
   } else if constexpr (sizeof(T) == 2) {
     uint16_t v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = c0 + 32 * j < D ? __ldcs(reinterpret_cast<const unsigned short*>(row) + c0 + 32 * j) : uint16_t(0);
+    for (int j = 0; j < 4; ++j) v[j] = c0 + GAP * j < D ? __ldcs(reinterpret_cast<const unsigned short*>(row) + c0 + GAP * j) : uint16_t(0);
     r.u = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
   } else {
     float v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = c0 + 32 * j < D ? __ldcs(row + c0 + 32 * j) : 0.f;
+    for (int j = 0; j < 4; ++j) v[j] = c0 + GAP * j < D ? __ldcs(row + c0 + GAP * j) : 0.f;
     r.u = make_float4(v[0], v[1], v[2], v[3]);
   }
   return r;
 }
 
-template <bool VEC, typename T>
+template <bool VEC, int GAP, typename T>
 __device__ __forceinline__ void store4(T* row, int c0, int D, const float (&v)[4]) {
   if constexpr (VEC) {
     if (c0 >= D) return;
@@ -77,337 +78,354 @@ __device__ __forceinline__ void store4(T* row, int c0, int D, const float (&v)[4
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (c0 + 32 * j < D) row[c0 + 32 * j] = from_f32<T>(v[j]);
+      if (c0 + GAP * j < D) row[c0 + GAP * j] = from_f32<T>(v[j]);
   }
 }
 
 // A state row's 4 channels (fp32; zeros without one); through element loads, as states need 4-byte
 // alignment only and a sequence has one.
-template <bool VEC>
+template <bool VEC, int GAP>
 __device__ __forceinline__ void load_state(float (&v)[4], const float* states, int seq, int c0, int D) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = VEC ? c0 + j : c0 + 32 * j;
+    const int c = VEC ? c0 + j : c0 + GAP * j;
     v[j] = states && c < D ? states[static_cast<size_t>(seq) * D + c] : 0.f;
   }
 }
-template <bool VEC>
+template <bool VEC, int GAP>
 __device__ __forceinline__ void store_state(float* states, int seq, int c0, int D, const float (&v)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = VEC ? c0 + j : c0 + 32 * j;
+    const int c = VEC ? c0 + j : c0 + GAP * j;
     if (c < D) states[static_cast<size_t>(seq) * D + c] = v[j];
   }
 }
 
-// A published word: (A, H) of a tile, or (kKnown, its outgoing value) where nothing that enters it
-// gets through; kEmpty before.
-constexpr uint64_t kEmpty = ~0ull;
-constexpr float kKnown = -1.f;   // (an A is a product of exponentials, never below 0)
-
-__device__ __forceinline__ uint64_t word(float a, float h) {
-  if (a != a) a = __int_as_float(0x7FC00000);   // (no NaN looks like kEmpty)
-  return static_cast<uint64_t>(__float_as_uint(h)) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ float word_a(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
-__device__ __forceinline__ float word_h(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
-// Each word carries its own state, so no order between words is needed.
-__device__ __forceinline__ void store_words(uint64_t* p, const uint64_t (&w)[4]) {
-  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(w[0]), "l"(w[1]) : "memory");
-  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p + 2), "l"(w[2]), "l"(w[3]) : "memory");
-}
-__device__ __forceinline__ void load_words(uint64_t (&w)[4], const uint64_t* p) {
-  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(w[0]), "=l"(w[1]) : "l"(p) : "memory");
-  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(w[2]), "=l"(w[3]) : "l"(p + 2) : "memory");
+// 16 or 8 bytes to shared memory without passing through registers; the issuing thread alone reads
+// them, so waiting for its own groups is all it needs.  Zeros where there is nothing to copy.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)), bytes = there ? BYTES : 0;
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// 4 floats into the same place of another CTA of the cluster
+__device__ __forceinline__ void store_remote(float* mine, uint32_t rank, const float (&v)[4]) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  uint32_t to;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
 }
 
-// The last sequence that starts at or before token t (0 .. num_seqs - 1, whatever cu holds), by a whole
-// warp: 32 probes at a time.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t, int lane) {
-  int lo = 0, n = num_seqs;                // it is among lo .. lo + n - 1
-  while (n > 1) {
-    const int step = (n + 31) >> 5, at = lo + lane * step;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane * step < n && cu[at] <= t);
-    const int k = m ? 31 - __clz(m) : 0;
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
-}
-
-// Waits until a thread's 4 words are there; false where the wait gave up.
-__device__ __forceinline__ bool wait_words(uint64_t (&w)[4], const uint64_t* p, unsigned long long limit_ns, uint32_t* status) {
-  unsigned long long t0 = 0;
-  for (;;) {
-    load_words(w, p);
-    if (__all_sync(0xFFFFFFFFu, w[0] != kEmpty && w[1] != kEmpty && w[2] != kEmpty && w[3] != kEmpty)) return true;
-    const unsigned long long t = now_ns();
-    if (t0 == 0) t0 = t;
-    // (one clock for the warp: its lanes leave together)
-    const bool late = t - t0 > limit_ns || (*reinterpret_cast<volatile uint32_t*>(status) & kStatusTimeout);
-    if (__any_sync(0xFFFFFFFFu, late)) break;
-  }
-  if ((threadIdx.x & 31) == 0) atomicOr(status, kStatusTimeout);
-  return false;
-}
-
-struct Scan {
-  Params p;
-  int tiles, channel_tiles;      // tiles along the tokens; tiles of channels
-  uint64_t* words;               // [tiles][channel_tiles][128], or null for one tile along the tokens; what a
-                                 // group's last tile writes is what enters the next group
-  uint32_t* counter;
+// The sequence around a token: its number and tokens [begin, end); empty where the token is in none.
+struct Span {
+  int seq, begin, end;
 };
-
-// Sets up the words, the counter and the status of a scan of several tiles.
-__global__ void __launch_bounds__(256) glr_clear_kernel(ulonglong2* words, size_t pairs, uint32_t* counter, uint32_t* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (size_t i = blockIdx.x * 256ul + threadIdx.x; i < pairs; i += gridDim.x * 256ul) words[i] = make_ulonglong2(kEmpty, kEmpty);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = *status = 0u;
+__device__ __forceinline__ void locate(Span& s, const Params& p, int t) {
+  if (p.cu == nullptr) {
+    s.seq = t / p.T;
+    s.begin = s.seq * p.T;
+    s.end = s.begin + p.T;
+    return;
+  }
+  int lo = 0, hi = p.num_seqs;               // the last one that starts at or before t, whatever cu holds
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  s.seq = lo;
+  s.begin = p.cu[lo];
+  s.end = p.cu[lo + 1];
+  if (t < s.begin || t >= s.end) s.begin = s.end = -1;
 }
 
-template <typename IO, typename G, bool BWD, bool VEC, int R>
-__global__ void __launch_bounds__(32 * kWarps, 2) glr_scan_kernel(const Scan s) {
-  constexpr int TL = kWarps * R;
-  __shared__ __align__(16) float sa[kWarps][kChannels], sh[kWarps][kChannels];
-  __shared__ __align__(16) uint64_t win[kGroup][kChannels];
-  __shared__ uint8_t known_in[kGroup];
-  __shared__ uint32_t ticket;
-  __shared__ uint8_t closed_by[kWarps];
-  const Params& p = s.p;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t id = blockIdx.x;
-  if (s.words) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid == 0) ticket = atomicAdd(s.counter, 1u);
-    __syncthreads();
-    id = ticket;
-  }
-  const int tile = id / s.channel_tiles, ct = id % s.channel_tiles;
-  const int c0 = ct * kChannels + (VEC ? 4 * lane : lane);
-  const int total = static_cast<int>(p.tokens), D = p.D;
-  const long pos0 = static_cast<long>(tile) * TL + warp * R;          // of this warp's tokens, in scan order
-  const int n = pos0 >= total ? 0 : total - pos0 < R ? static_cast<int>(total - pos0) : R;
-  auto token = [&](int r) { return BWD ? total - 1 - static_cast<int>(pos0) - r : static_cast<int>(pos0) + r; };
-
-  // every load of the tile's inputs on its way
-  Raw4<IO> x[R], y[BWD ? R : 1];
-  Raw4<G> gr[R];
+// c -> A c + H; closed: the scan started anew on the way, nothing of c gets through
+struct Map {
+  float A[4], H[4];
+  bool closed;
+};
+// first `before`, then `m`
+__device__ __forceinline__ void after(Map& m, const Map& before) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (r < n) {
-      const size_t row = static_cast<size_t>(token(r)) * D;
-      gr[r] = load4<VEC>(static_cast<const G*>(p.g) + row, c0, D);
-      x[r] = load4<VEC>(static_cast<const IO*>(p.x) + row, c0, D);
-      if constexpr (BWD) {
-        if (token(r) > 0) y[r] = load4<VEC>(static_cast<const IO*>(p.y) + row - D, c0, D);
-        else y[r].u = {};
+  for (int j = 0; j < 4; ++j) {
+    if (!m.closed) m.H[j] = fmaf(m.A[j], before.H[j], m.H[j]);
+    m.A[j] *= before.A[j];
+  }
+  m.closed |= before.closed;
+}
+
+// Tokens of a thread, and stages of the ring: what leaves room for two blocks an SM.
+template <typename IO, bool BWD>
+constexpr int tokens_each() { return BWD && sizeof(IO) == 4 ? 2 : 4; }
+template <typename IO, bool BWD>
+constexpr int stage_bytes() { return tokens_each<IO, BWD>() * kThreads * (16 + (BWD ? 2 : 1) * 4 * static_cast<int>(sizeof(IO))); }
+template <typename IO, bool BWD>
+constexpr int stages() { return 98304 / stage_bytes<IO, BWD>(); }
+
+template <typename IO, typename G, bool BWD, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) glr_scan_kernel(const Params p, const int cluster) {
+  constexpr int R = tokens_each<IO, BWD>(), S = stages<IO, BWD>(), TL = kRows * R, GAP = 8;
+  using RawIO = decltype(Raw4<IO>::u);
+  using RawG = decltype(Raw4<G>::u);
+  static_assert(S >= 3, "a tile waits for what enters it, one is summed up, one is on its way");
+  // the ring, every thread's own 4 channels of its tokens: [S][R][thread]
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  float4* ring_g = reinterpret_cast<float4*>(dynamic);   // g as it lies in memory, then e^g (or what a sequence starts from)
+  RawIO* ring_x = reinterpret_cast<RawIO*>(ring_g + S * R * kThreads);
+  RawIO* ring_y = ring_x + S * R * kThreads;
+  __shared__ __align__(16) float warp_a[2][kWarps][kChannels], warp_h[2][kWarps][kChannels];
+  __shared__ bool warp_closed[2][kWarps];
+  // what the cluster's tiles of a step do: written by each into all; three steps, as one may be a step
+  // ahead of a CTA that still reads
+  __shared__ __align__(16) float tile_a[3][kMaxCluster][kChannels], tile_h[3][kMaxCluster][kChannels];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane >> 3, cq = lane & 7;
+  const int rank = blockIdx.x % cluster, ct = blockIdx.x / cluster;
+  const int c0 = ct * kChannels + (VEC ? 4 * cq : cq), D = p.D;
+  const int total = static_cast<int>(p.tokens);
+  const int steps = static_cast<int>((p.tokens + static_cast<long>(cluster) * TL - 1) / (static_cast<long>(cluster) * TL));
+  // in scan order, this thread's first token of a step
+  auto first = [&](int n) { return (static_cast<long>(n) * cluster + rank) * TL + (warp * 4 + sub) * R; };
+  auto token = [&](long pos) { return static_cast<int>(BWD ? total - 1 - pos : pos); };
+  auto slot = [&](int n, int r) { return (n % S * R + r) * kThreads + tid; };
+  const G* pg = static_cast<const G*>(p.g);
+  const IO* px = static_cast<const IO*>(p.x);
+  const IO* py = static_cast<const IO*>(p.y);
+
+  auto fetch = [&](int n) {                   // a step's inputs on their way
+    const long pos = first(n);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool there = n < steps && pos + r < total && c0 < D;
+      const int t = token(pos + r);
+      const size_t at = there ? static_cast<size_t>(t) * D + c0 : 0;
+      copy_async<4 * sizeof(G)>(&ring_g[slot(n, r)], pg + at, there);
+      copy_async<4 * sizeof(IO)>(&ring_x[slot(n, r)], px + at, there);
+      if constexpr (BWD) copy_async<4 * sizeof(IO)>(&ring_y[slot(n, r)], py + (there && t > 0 ? at - D : 0), there && t > 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // the same through registers, for rows that asynchronous copies cannot start at
+  Raw4<G> held_g[VEC ? 1 : R];
+  Raw4<IO> held_x[VEC ? 1 : R], held_y[VEC ? 1 : R];
+  auto load = [&](int n) {
+    const long pos = first(n);
+#pragma unroll
+    for (int r = 0; r < (VEC ? 0 : R); ++r) {
+      const bool there = n < steps && pos + r < total;
+      const int t = there ? token(pos + r) : 0;
+      const size_t row = static_cast<size_t>(t) * D;
+      held_g[r] = load4<false, GAP>(pg + row, c0, there ? D : 0);
+      held_x[r] = load4<false, GAP>(px + row, c0, there ? D : 0);
+      if constexpr (BWD) held_y[r] = load4<false, GAP>(py + (t > 0 ? row - D : 0), c0, there && t > 0 ? D : 0);
+    }
+  };
+  auto put = [&](int n) {
+#pragma unroll
+    for (int r = 0; r < (VEC ? 0 : R); ++r) {
+      *reinterpret_cast<RawG*>(&ring_g[slot(n, r)]) = held_g[r].u;
+      ring_x[slot(n, r)] = held_x[r].u;
+      if constexpr (BWD) ring_y[slot(n, r)] = held_y[r].u;
+    }
+  };
+
+  // What a thread's tokens of step n, and those before them in the tile, do to what enters the tile; its
+  // e^g go where g was.  The tile's own map goes to the cluster.
+  Span ahead{0, -1, -1};
+  auto sum_up = [&](int n, Map& m) {
+    m = {{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}, false};
+    const long pos = first(n);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (pos + r >= total) break;
+      const int t = token(pos + r);
+      if (t < ahead.begin || t >= ahead.end) locate(ahead, p, t);
+      if (ahead.end < 0) continue;            // (a token of no sequence leaves everything as it is)
+      const Raw4<G> g{*reinterpret_cast<const RawG*>(&ring_g[slot(n, r)])};
+      const Raw4<IO> x{ring_x[slot(n, r)]};
+      const bool start = t == (BWD ? ahead.end - 1 : ahead.begin);
+      float a[4], keep[4];
+      if (start) {
+        load_state<VEC, GAP>(m.H, p.init, ahead.seq, c0, D);
+        m.closed = true;
       }
-    } else {
-      gr[r].u = {};
-      x[r].u = {};
-      if constexpr (BWD) y[r].u = {};
-    }
-  }
-
-  // lane r < n: the sequence of the warp's token r, and whether the scan starts anew or ends there
-  int seq = 0;
-  bool starts = false, ends = false, live = false;
-  if (p.cu && n > 0) seq = find_seq(p.cu, p.num_seqs, token(BWD ? n - 1 : 0), lane);
-  if (lane < n) {
-    const int t = token(lane);
-    bool first, last;
-    if (p.cu) {
-      if (p.cu[seq + 1] <= t) {        // another one than that of the warp's earliest token
-        int hi = p.num_seqs;
-        while (hi - seq > 1) {
-          const int mid = (seq + hi) >> 1;
-          if (p.cu[mid] <= t) seq = mid;
-          else hi = mid;
-        }
-      }
-      const int a = p.cu[seq], b = p.cu[seq + 1];
-      live = a <= t && t < b;
-      first = t == a;
-      last = t + 1 == b;
-    } else {
-      seq = t / p.T;
-      live = true;
-      first = t == seq * p.T;
-      last = t + 1 == (seq + 1) * p.T;
-    }
-    starts = live && (BWD ? last : first);
-    ends = live && (BWD ? first : last);
-  }
-  const uint32_t m_start = __ballot_sync(0xFFFFFFFFu, starts), m_end = __ballot_sync(0xFFFFFFFFu, ends),
-                 m_live = __ballot_sync(0xFFFFFFFFu, live);
-
-  // c -> A c + H over the warp's tokens (closed: the scan started anew among them, and A is 0)
-  // (the last value that the scan started from is kept: where it goes on beyond this warp, its array may
-  // hold the final state by the time the tokens are gone through again)
-  float a[R][4], A[4] = {1.f, 1.f, 1.f, 1.f}, H[4] = {0.f, 0.f, 0.f, 0.f}, from[4] = {};
-  bool closed = false;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (m_start >> r & 1) {
-      load_state<VEC>(from, p.init, __shfl_sync(0xFFFFFFFFu, seq, r), c0, D);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) H[j] = from[j];
-      closed = true;
-    }
-    const bool on = m_live >> r & 1;        // (a token of no sequence leaves everything as it is)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[r][j] = on ? expf(gr[r].get(j)) : 1.f;
-      const float in = on ? x[r].get(j) : 0.f;
-      A[j] *= a[r][j];
-      H[j] = BWD ? a[r][j] * (H[j] + in) : fmaf(a[r][j], H[j], in);
-    }
-  }
-  *reinterpret_cast<float4*>(&sa[warp][4 * lane]) = make_float4(A[0], A[1], A[2], A[3]);
-  *reinterpret_cast<float4*>(&sh[warp][4 * lane]) = make_float4(H[0], H[1], H[2], H[3]);
-  if (lane == 0) closed_by[warp] = closed;
-  __syncthreads();
-
-  // what the warps before this one do to what enters the tile: PA c + PH
-  float PA[4] = {1.f, 1.f, 1.f, 1.f}, PH[4] = {0.f, 0.f, 0.f, 0.f};
-  bool pclosed = false;
-  for (int w = 0; w < warp; ++w) {
-    const float4 fa = *reinterpret_cast<const float4*>(&sa[w][4 * lane]), fh = *reinterpret_cast<const float4*>(&sh[w][4 * lane]);
-    const bool cl = closed_by[w];
-    const float ea[4] = {fa.x, fa.y, fa.z, fa.w}, eh[4] = {fh.x, fh.y, fh.z, fh.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      PH[j] = cl ? eh[j] : fmaf(ea[j], PH[j], eh[j]);
-      PA[j] *= ea[j];
-    }
-    pclosed |= cl;
-  }
-  float C[4] = {0.f, 0.f, 0.f, 0.f};       // what enters the tile
-  if (s.words) {
-    const size_t row = static_cast<size_t>(s.channel_tiles) * kChannels;          // words of a tile
-    uint64_t* mine = s.words + tile * row + ct * kChannels + 4 * lane;
-    const int m = tile % kGroup;                                                  // tiles of the group before this one
-    const bool last = m == kGroup - 1;
-    // the whole tile's A c + H, in the last warp
-    float TA[4], TH[4];
-    const bool known = pclosed || closed || tile == 0;
-    if (warp == kWarps - 1) {
-      uint64_t w4[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        TA[j] = PA[j] * A[j];
-        TH[j] = closed ? H[j] : fmaf(A[j], PH[j], H[j]);
-        w4[j] = word(known ? kKnown : TA[j], TH[j]);
+        a[j] = expf(g.get(j));
+        keep[j] = start ? m.H[j] : a[j];      // (a final state may take the initial one's place: read it once)
+        m.A[j] *= a[j];
+        m.H[j] = BWD ? a[j] * (m.H[j] + x.get(j)) : fmaf(a[j], m.H[j], x.get(j));
       }
-      if (known || !last) store_words(mine, w4);
+      ring_g[slot(n, r)] = make_float4(keep[0], keep[1], keep[2], keep[3]);
     }
-    // (uniform over the block: the tile's first token says whether anything enters)
-    if (tile > 0 && !__syncthreads_or(warp == 0 && (m_start & 1))) {
-      // the group's tiles before this one, a warp each
-      for (int k = warp; k < m; k += kWarps) {
-        uint64_t w4[4];
-        wait_words(w4, mine - (m - k) * row, p.wait_ns, p.status);
-        *reinterpret_cast<ulonglong2*>(&win[k][4 * lane]) = make_ulonglong2(w4[0], w4[1]);
-        *reinterpret_cast<ulonglong2*>(&win[k][4 * lane + 2]) = make_ulonglong2(w4[2], w4[3]);
-        if (lane == 0) known_in[k] = word_a(w4[0]) == kKnown;                     // (the same in every channel)
+    // over the warp's 4 threads of these channels
+#pragma unroll
+    for (int d = 8; d <= 16; d *= 2) {
+      Map b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b.A[j] = __shfl_up_sync(0xFFFFFFFFu, m.A[j], d);
+        b.H[j] = __shfl_up_sync(0xFFFFFFFFu, m.H[j], d);
       }
-      __syncthreads();
-      int k = m - 1;
-      while (k >= 0 && !known_in[k]) --k;
-      if (k >= 0) {
+      b.closed = __shfl_up_sync(0xFFFFFFFFu, m.closed, d);
+      if (lane >= d) after(m, b);
+    }
+    const int half = n & 1;
+    if (sub == 3) {
+      *reinterpret_cast<float4*>(&warp_a[half][warp][4 * cq]) = make_float4(m.A[0], m.A[1], m.A[2], m.A[3]);
+      *reinterpret_cast<float4*>(&warp_h[half][warp][4 * cq]) = make_float4(m.H[0], m.H[1], m.H[2], m.H[3]);
+      if (cq == 0) warp_closed[half][warp] = m.closed;
+    }
+    const Map whole = m;                       // (of the warp, where sub = 3)
+    // the threads before this one: the subs of the warp, and the warps
+    Map b{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}, false};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) C[j] = word_h(win[k][4 * lane + j]);
-      } else if (tile >= kGroup) {
-        uint64_t w4[4];
-        wait_words(w4, mine - (m + 1) * row, p.wait_ns, p.status);
+    for (int j = 0; j < 4; ++j) {
+      const float A = __shfl_up_sync(0xFFFFFFFFu, m.A[j], 8), H = __shfl_up_sync(0xFFFFFFFFu, m.H[j], 8);
+      if (sub > 0) b.A[j] = A, b.H[j] = H;
+    }
+    b.closed = __shfl_up_sync(0xFFFFFFFFu, m.closed, 8) && sub > 0;
+    __syncthreads();
+    Map w{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}, false};
+    for (int i = 0; i < warp; ++i) {
+      const float4 fa = *reinterpret_cast<const float4*>(&warp_a[half][i][4 * cq]),
+                   fh = *reinterpret_cast<const float4*>(&warp_h[half][i][4 * cq]);
+      Map next{{fa.x, fa.y, fa.z, fa.w}, {fh.x, fh.y, fh.z, fh.w}, warp_closed[half][i]};
+      after(next, w);
+      w = next;
+    }
+    m = b;
+    after(m, w);
+    return [whole, w]() { Map t = whole; after(t, w); return t; }();
+  };
+  auto publish = [&](int n, const Map& tile) {
+    if (warp == kWarps - 1 && sub == 3) {
+      // (where nothing gets through, an A of -1 says so: exponentials are never below 0)
+      float A[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) C[j] = word_h(w4[j]);
-      }
-      while (++k < m) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) C[j] = fmaf(word_a(win[k][4 * lane + j]), C[j], word_h(win[k][4 * lane + j]));
+      for (int j = 0; j < 4; ++j) A[j] = tile.closed ? -1.f : tile.A[j];
+      for (int q = 0; q < cluster; ++q) {
+        store_remote(&tile_a[n % 3][rank][4 * cq], q, A);
+        store_remote(&tile_h[n % 3][rank][4 * cq], q, tile.H);
       }
     }
-    if (warp == kWarps - 1 && last && !known) {
-      uint64_t w4[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w4[j] = word(kKnown, fmaf(TA[j], C[j], TH[j]));
-      store_words(mine, w4);
+    cluster_arrive();
+  };
+
+  float carry[4] = {0.f, 0.f, 0.f, 0.f};       // what enters the step, the same in every CTA of the cluster
+  Span here{0, -1, -1};
+  Map cur, next;
+  cluster_arrive();                            // (every CTA runs before another one writes into it)
+  if constexpr (VEC) {
+    for (int n = 0; n < S - 1; ++n) fetch(n);
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+  } else {
+    for (int n = 0; n < 2; ++n) {
+      load(n);
+      put(n);
     }
   }
-
-  // the warp's tokens again, from what enters them
-  float c[4];
+  cluster_wait();
+  if (steps > 0) publish(0, sum_up(0, cur));
+  for (int n = 0; n < steps; ++n) {
+    if constexpr (VEC) {
+      fetch(n + S - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    } else {
+      load(n + 2);
+    }
+    const bool more = n + 1 < steps;
+    Map tile;
+    if (more) tile = sum_up(n + 1, next);
+    cluster_wait();                            // the step's maps are there
+    if (more) publish(n + 1, tile);
+    float c[4];
+    for (int q = 0; q < cluster; ++q) {
+      const float4 fa = *reinterpret_cast<const float4*>(&tile_a[n % 3][q][4 * cq]),
+                   fh = *reinterpret_cast<const float4*>(&tile_h[n % 3][q][4 * cq]);
+      const float A[4] = {fa.x, fa.y, fa.z, fa.w}, H[4] = {fh.x, fh.y, fh.z, fh.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = pclosed ? PH[j] : fmaf(PA[j], C[j], PH[j]);
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (m_live >> r & 1) {
-      const int sq = __shfl_sync(0xFFFFFFFFu, seq, r);
-      if (m_start >> r & 1) {
-        if (m_start >> r == 1u) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[j] = from[j];
-        } else {
-          load_state<VEC>(c, p.init, sq, c0, D);
-        }
+      for (int j = 0; j < 4; ++j) {
+        if (q == rank) c[j] = carry[j];
+        carry[j] = A[j] == -1.f ? H[j] : fmaf(A[j], carry[j], H[j]);
       }
-      const bool end = m_end >> r & 1;
-      const size_t row = static_cast<size_t>(token(r)) * D;
-      float out[4];
-      if constexpr (BWD) {
-        float before[4], dg[4];
-        if (end) load_state<VEC>(before, p.h0, sq, c0, D);
+    }
+    // the step's tokens again, from what enters them
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = cur.closed ? cur.H[j] : fmaf(cur.A[j], c[j], cur.H[j]);
+    const long pos = first(n);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (pos + r >= total) break;
+      const int t = token(pos + r);
+      if (t < here.begin || t >= here.end) locate(here, p, t);
+      if (here.end < 0) continue;
+      const size_t row = static_cast<size_t>(t) * D;
+      const float4 kept = ring_g[slot(n, r)];
+      const Raw4<IO> x{ring_x[slot(n, r)]};
+      float a[4] = {kept.x, kept.y, kept.z, kept.w}, out[4];
+      if (t == (BWD ? here.end - 1 : here.begin)) {
+        const Raw4<G> g = load4<VEC, GAP>(pg + row, c0, D);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (!end) before[j] = y[r].get(j);
-          out[j] = c[j] + x[r].get(j);
-          c[j] = a[r][j] * out[j];
+          c[j] = a[j];
+          a[j] = expf(g.get(j));
+        }
+      }
+      const bool end = t == (BWD ? here.begin : here.end - 1);
+      if constexpr (BWD) {
+        const Raw4<IO> y{ring_y[slot(n, r)]};
+        float before[4], dg[4];
+        if (end) load_state<VEC, GAP>(before, p.h0, here.seq, c0, D);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!end) before[j] = y.get(j);
+          out[j] = c[j] + x.get(j);
+          c[j] = a[j] * out[j];
           dg[j] = c[j] * before[j];
         }
-        store4<VEC>(static_cast<G*>(p.dg) + row, c0, D, dg);
+        store4<VEC, GAP>(static_cast<G*>(p.dg) + row, c0, D, dg);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) out[j] = c[j] = fmaf(a[r][j], c[j], x[r].get(j));
+        for (int j = 0; j < 4; ++j) out[j] = c[j] = fmaf(a[j], c[j], x.get(j));
       }
-      store4<VEC>(static_cast<IO*>(p.out) + row, c0, D, out);
-      if (end && p.fin) store_state<VEC>(p.fin, sq, c0, D, c);
+      store4<VEC, GAP>(static_cast<IO*>(p.out) + row, c0, D, out);
+      if (end && p.fin) store_state<VEC, GAP>(p.fin, here.seq, c0, D, c);
     }
+    if constexpr (!VEC) put(n + 2);
+    cur = next;
   }
 
-  // sequences without tokens keep their initial value; one block checks cu_seqlens
-  if (tile == 0) {
+  // sequences without tokens keep their initial value; one block checks cu_seqlens and sets the status
+  if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");     // (zeros, past the last step)
+  if (p.cu) {
     bool bad = false;
-    if (p.cu)
-      for (int s0 = warp * 32; s0 < p.num_seqs; s0 += 32 * kWarps) {
-        const int q = s0 + lane;
-        bool none = false;
-        if (q < p.num_seqs) {
-          const int b = p.cu[q], e = p.cu[q + 1];
-          none = e <= b;
-          bad |= b < 0 || e < b || e > total || (q == 0 && b != 0) || (q == p.num_seqs - 1 && e != total);
-        }
-        for (uint32_t m = __ballot_sync(0xFFFFFFFFu, none && p.fin); m; m &= m - 1) {
-          float v[4];
-          load_state<VEC>(v, p.init, s0 + __ffs(m) - 1, c0, D);
-          store_state<VEC>(p.fin, s0 + __ffs(m) - 1, c0, D, v);
-        }
-      }
-    if (ct == 0) {
-      bad = __syncthreads_or(bad);
-      if (tid == 0) {
-        if (!s.words) *p.status = bad ? kStatusBounds : 0u;
-        else if (bad) atomicOr(p.status, kStatusBounds);
+    for (int s0 = (rank * kWarps + warp) * 32; s0 < p.num_seqs; s0 += 32 * kWarps * cluster) {
+      const int q = s0 + lane;
+      const bool none = q < p.num_seqs && p.cu[q + 1] <= p.cu[q] && p.fin;
+      const int c = ct * kChannels + lane;
+      for (uint32_t m = __ballot_sync(0xFFFFFFFFu, none); m; m &= m - 1) {
+        const size_t at = static_cast<size_t>(s0 + __ffs(m) - 1) * D + c;
+        if (c < D) p.fin[at] = p.init ? p.init[at] : 0.f;
       }
     }
+    if (blockIdx.x == 0) {
+      for (int q = tid; q < p.num_seqs; q += kThreads) {
+        const int b = p.cu[q], e = p.cu[q + 1];
+        bad |= b < 0 || e < b || e > total || (q == 0 && b != 0) || (q == p.num_seqs - 1 && e != total);
+      }
+      bad = __syncthreads_or(bad);
+      if (tid == 0) *p.status = bad ? kStatusBounds : 0u;
+    }
+  } else if (blockIdx.x == 0 && tid == 0) {
+    *p.status = 0u;
   }
+  cluster_arrive();                            // (nobody writes into a CTA that has ended)
+  cluster_wait();
 }
 
 // The serving step: 4 channels a thread, the state in registers between its load and its store.
@@ -419,15 +437,15 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const StepParams p) {
   const IO* x = static_cast<const IO*>(p.x) + row0;
   const G* g = static_cast<const G*>(p.g) + row0;
   IO* y = static_cast<IO*>(p.y) + row0;
-  Raw4<IO> xr = load4<VEC>(x, c0, D);
-  Raw4<G> gr = load4<VEC>(g, c0, D);
+  Raw4<IO> xr = load4<VEC, 32>(x, c0, D);
+  Raw4<G> gr = load4<VEC, 32>(g, c0, D);
   int slot = b;
   if (p.slots) {
     slot = p.slots[b];
     if (slot < 0 || slot >= p.num_slots) {
       if (slot >= p.num_slots && p.status && threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
       const float zero[4] = {};
-      for (int t = 0; t < p.T; ++t) store4<VEC>(y + static_cast<size_t>(t) * D, c0, D, zero);
+      for (int t = 0; t < p.T; ++t) store4<VEC, 32>(y + static_cast<size_t>(t) * D, c0, D, zero);
       return;
     }
   }
@@ -437,61 +455,56 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const StepParams p) {
     const float4 u = c0 < D ? *reinterpret_cast<const float4*>(state + c0) : make_float4(0.f, 0.f, 0.f, 0.f);
     h[0] = u.x; h[1] = u.y; h[2] = u.z; h[3] = u.w;
   } else {
-    load_state<false>(h, state, 0, c0, D);
+    load_state<false, 32>(h, state, 0, c0, D);
   }
   for (int t = 0; t < p.T; ++t) {
     const Raw4<IO> xt = xr;
     const Raw4<G> gt = gr;
     if (t + 1 < p.T) {
-      xr = load4<VEC>(x + static_cast<size_t>(t + 1) * D, c0, D);
-      gr = load4<VEC>(g + static_cast<size_t>(t + 1) * D, c0, D);
+      xr = load4<VEC, 32>(x + static_cast<size_t>(t + 1) * D, c0, D);
+      gr = load4<VEC, 32>(g + static_cast<size_t>(t + 1) * D, c0, D);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = fmaf(expf(gt.get(j)), h[j], xt.get(j));
-    store4<VEC>(y + static_cast<size_t>(t) * D, c0, D, h);
+    store4<VEC, 32>(y + static_cast<size_t>(t) * D, c0, D, h);
   }
   if constexpr (VEC) {
     if (c0 < D) *reinterpret_cast<float4*>(state + c0) = make_float4(h[0], h[1], h[2], h[3]);
   } else {
-    store_state<false>(state, 0, c0, D, h);
+    store_state<false, 32>(state, 0, c0, D, h);
   }
 }
-
-// Tokens a warp takes: 8, and 4 where dy, y and g of 8 would fill a thread's registers.
-constexpr int tokens_each(bool backward, bool bf16) { return backward && !bf16 ? 4 : 8; }
-
-long tiles_of(long tokens, bool backward, bool bf16) {
-  const long n = kWarps * tokens_each(backward, bf16);
-  return tokens > n ? (tokens + n - 1) / n : 1;
-}
-long channel_tiles_of(int D) { return (D + kChannels - 1) / kChannels; }
 
 template <typename IO, typename G, bool BWD, bool VEC>
 cudaError_t launch_scan(const Params& p, cudaStream_t st) {
-  constexpr int R = tokens_each(BWD, sizeof(IO) == 2);
-  const long tiles = tiles_of(p.tokens, BWD, sizeof(IO) == 2), cts = channel_tiles_of(p.D);
-  if (tiles * cts > INT32_MAX) return cudaErrorInvalidValue;
-  Scan s{p, static_cast<int>(tiles), static_cast<int>(cts), nullptr, nullptr};
+  constexpr int ring = stages<IO, BWD>() * stage_bytes<IO, BWD>(), TL = kRows * tokens_each<IO, BWD>();
+  const auto kernel = glr_scan_kernel<IO, G, BWD, VEC>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  static bool raised[64] = {};         // (a race raises it twice, to the same value)
+  if (dev < 0 || dev >= 64 || !raised[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) raised[dev] = true;
+  }
+  // CTAs of a cluster share a channel tile's tokens: as many as there are places for, and tiles
+  const long cts = (p.D + kChannels - 1) / kChannels, tiles = (p.tokens + TL - 1) / TL;
+  int cluster = 1;
+  while (cluster < kMaxCluster && cts * cluster * 2 <= 2 * sms && cluster * 2 <= tiles) cluster *= 2;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * cts));
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>(cts * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = ring;
   cfg.stream = st;
   cfg.attrs = &attr;
-  if (tiles > 1) {
-    s.counter = reinterpret_cast<uint32_t*>(p.work);
-    s.words = reinterpret_cast<uint64_t*>(p.work + 256);
-    const size_t pairs = static_cast<size_t>(tiles) * cts * kChannels / 2;
-    const size_t blocks = (pairs + 1023) / 1024;
-    glr_clear_kernel<<<static_cast<unsigned>(blocks < 608 ? blocks : 608), 256, 0, st>>>(reinterpret_cast<ulonglong2*>(s.words), pairs,
-                                                                                        s.counter, p.status);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cfg.numAttrs = 1;                 // starts under the kernel that clears, waits for its end
-  }
-  return cudaLaunchKernelEx(&cfg, glr_scan_kernel<IO, G, BWD, VEC, R>, s);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -525,11 +538,6 @@ cudaError_t launch_step_types(const StepParams& p, cudaStream_t st) {
 }
 
 }  // namespace
-
-size_t workspace_bytes(long tokens, int D, bool backward, bool bf16) {
-  const long tiles = tiles_of(tokens, backward, bf16);
-  return tiles > 1 ? 256 + static_cast<size_t>(tiles) * channel_tiles_of(D) * kChannels * sizeof(uint64_t) : 0;
-}
 
 cudaError_t launch(const Params& p, bool backward, bool bf16, bool gate_bf16, cudaStream_t st) {
   if (p.tokens == 0 && !p.cu) {       // no tokens: the initial values pass through

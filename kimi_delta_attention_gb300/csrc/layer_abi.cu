@@ -23,17 +23,6 @@ bool overlaps(const Span& a, const Span& b) {
   return a0 < b0 + b.n && b0 < a0 + a.n;
 }
 
-// Limit of the kernels' bounded waits: 2 s, or KDA_WAIT_LIMIT_NS (read at each call).
-unsigned long long wait_limit_ns() {
-  const char* e = std::getenv("KDA_WAIT_LIMIT_NS");
-  if (e) {
-    char* end = nullptr;
-    const unsigned long long v = std::strtoull(e, &end, 10);
-    if (end != e && v > 0) return v;
-  }
-  return 2000000000ull;
-}
-
 bool is_dtype(int64_t d) { return d == KDA_F32 || d == KDA_BF16; }
 size_t size_of(int64_t d) { return d == KDA_BF16 ? 2 : 4; }
 
@@ -55,19 +44,15 @@ kda_status check_glr(const kda_glr_shape* s, bool packed, GlrSizes& z) {
   return KDA_OK;
 }
 
-size_t glr_bytes(const kda_glr_shape* s, const GlrSizes& z, bool backward) {
-  return kda::kWorkspaceBytes + kda::glr::workspace_bytes(static_cast<long>(z.tokens), s->D, backward, s->io_dtype == KDA_BF16);
-}
-
-size_t glr_workspace_size(const kda_glr_shape* s, bool backward) {
+size_t glr_workspace_size(const kda_glr_shape* s) {
   GlrSizes z;
-  return check_glr(s, s && s->num_seqs > 0, z) == KDA_OK ? glr_bytes(s, z, backward) : 0;
+  return check_glr(s, s && s->num_seqs > 0, z) == KDA_OK ? kda::kWorkspaceBytes : 0;   // the status word
 }
 
 // Both directions: `ins` inputs, `outs` outputs (the last one may be the array `same`).
 kda_status run_glr(const kda_glr_shape* s, const GlrSizes& z, kda::glr::Params p, bool backward, const Span* ins, int n_ins,
                    const Span* outs, int n_outs, const void* same, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!workspace || workspace_bytes < glr_bytes(s, z, backward)) return KDA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < kda::kWorkspaceBytes) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return KDA_ERR_ALIGNMENT;
   const Span w{workspace, workspace_bytes};
   for (int i = 0; i < n_outs; ++i) {
@@ -82,8 +67,6 @@ kda_status run_glr(const kda_glr_shape* s, const GlrSizes& z, kda::glr::Params p
   if (z.ns == 0) return KDA_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   p.status = static_cast<uint32_t*>(workspace);
-  p.work = static_cast<uint8_t*>(workspace) + kda::kWorkspaceBytes;
-  p.wait_ns = wait_limit_ns();
   p.tokens = static_cast<long>(z.tokens);
   p.T = s->T;
   p.D = s->D;
@@ -123,8 +106,8 @@ bool clash(Range* r, int n) {
 
 extern "C" {
 
-size_t kda_glr_fwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s, false); }
-size_t kda_glr_bwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s, true); }
+size_t kda_glr_fwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s); }
+size_t kda_glr_bwd_workspace_size(const kda_glr_shape* s) { return glr_workspace_size(s); }
 
 kda_status kda_glr_fwd(const kda_glr_shape* s, const void* x, const void* g, const float* initial_state,
                        const int32_t* cu_seqlens, void* y, float* final_state, void* workspace, size_t workspace_bytes,

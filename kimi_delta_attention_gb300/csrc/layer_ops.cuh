@@ -22,13 +22,10 @@ struct Params {
   void* dg;             // backward: [tokens, D] gate type
   float* fin;           // forward: final states; backward: d_initial_state; [NS, D] or null
   uint32_t* status;     // device status word (null where nothing is reported)
-  uint8_t* work;        // the workspace behind it
-  unsigned long long wait_ns;
   long tokens;          // in all
   int T, D, num_seqs;   // T: tokens of a sequence (without cu)
 };
 
-size_t workspace_bytes(long tokens, int D, bool backward, bool bf16);
 cudaError_t launch(const Params& p, bool backward, bool bf16, bool gate_bf16, cudaStream_t stream);
 
 struct StepParams {
