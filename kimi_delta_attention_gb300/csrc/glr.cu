@@ -7,25 +7,31 @@
 // first token from its initial value.  Bound by HBM: each input is read and each output
 // written once, 8 bytes an element forward (bf16 with an fp32 gate), 14 backward.
 //
-// A CTA owns 32 channels and walks over the tokens in tiles of 128 (64 in the fp32 backward): 8
-// threads a row with 4 channels each, 4 neighbouring tokens a thread.  Any stretch of tokens acts on
-// what enters it as c -> A c + H; a thread's (A, H) join over the warp by shuffles, over the warps
-// through shared memory.  Where there are fewer channel tiles than places for CTAs, a cluster takes
-// its step's tiles side by side and each CTA writes its (A, H) into the others' shared memory: one
-// cluster barrier a step, and it is waited for a step later, under the next tile's sums.  So a
-// tile's inputs lie in a ring in shared memory from their load, one step ahead, until what enters
-// them is known, and the recurrence itself never leaves the chip.  Every fold goes over the same
-// terms in the same order on every call.
+// A CTA owns 32 channels and walks over the tokens in tiles of 128, the next tile on its way by TMA:
+// 8 threads a row with 4 channels each, 8 neighbouring tokens a thread.  Any stretch of tokens
+// acts on what enters it as c -> A c + H.  Each thread finds its stretch's (A, H), one warp folds
+// the 16 of a channel in their order, and each thread goes through its tokens again, still in
+// registers, from what enters them.  Where there are fewer channel tiles than places for CTAs, a
+// cluster takes its step's tiles side by side, and the folding warps send each other their
+// tile's (A, H) into shared memory.  Every fold goes over the same terms in the same order on
+// every call, and the recurrence never leaves the chip.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "layer_ops.cuh"
+#include "pairs.cuh"
+#include "sm103.cuh"
 
 namespace kda {
 namespace glr {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kChannels = 32;             // of a tile: 4 a thread, 8 threads a row
-constexpr int kRows = kThreads / 8;       // threads along the tokens, each with R neighbours
-constexpr int kMaxCluster = 8;
+constexpr int kThreads = 128;
+constexpr int kChannels = 32;              // of a tile: 4 a thread, 8 threads a row
+constexpr int kEach = 8;                   // neighbouring tokens of a thread
+constexpr int kSegs = kThreads / 8;        // threads along the tokens
+constexpr int kTile = kSegs * kEach;       // tokens of a tile
+constexpr int kMaxCluster = 16;
 
 // 4 channels as they lie in memory
 template <typename T>
@@ -37,12 +43,34 @@ struct Raw4<__nv_bfloat16> {
     const uint32_t w = j < 2 ? u.x : u.y;
     return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
   }
+  __device__ __forceinline__ uint64_t pair(int i) const { return pack2f(get(2 * i), get(2 * i + 1)); }
 };
 template <>
 struct Raw4<float> {
   float4 u;
   __device__ __forceinline__ float get(int j) const { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; }
+  __device__ __forceinline__ uint64_t pair(int i) const { return pack2f(get(2 * i), get(2 * i + 1)); }
 };
+
+// e^x of two values, x <= 88: 2^(x log2 e) with the product's rounding error put back to first order
+// (without it a strong decay loses |x| 2^-24 of itself).  Below -104 it is 0, as for -inf; NaN stays.
+// Half the instructions of two calls of expf, and with them a fifth of the kernel's.
+__device__ __forceinline__ uint64_t exp_pair(uint64_t x) {
+  constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.925963e-8f, kLn2 = 0.693147181f;
+  float a, b;
+  unpack2f(x, a, b);
+  asm("max.NaN.f32 %0, %1, 0fC2D00000;" : "=f"(a) : "f"(a));
+  asm("max.NaN.f32 %0, %1, 0fC2D00000;" : "=f"(b) : "f"(b));
+  x = pack2f(a, b);
+  const uint64_t L = pack2f(kLog2e, kLog2e);
+  const uint64_t hi = mul2(x, L);
+  const uint64_t lo = fma2(x, pack2f(kLog2eRest, kLog2eRest), fma2(x, L, hi ^ 0x8000000080000000ull));
+  unpack2f(hi, a, b);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(a));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(b));
+  const uint64_t r = pack2f(a, b);
+  return fma2(mul2(r, lo), pack2f(kLn2, kLn2), r);
+}
 
 // A thread's channels: c0 .. c0 + 3 (VEC: D % 4 = 0 and aligned rows), else c0, c0 + GAP, ...
 template <bool VEC, int GAP, typename T>
@@ -101,24 +129,17 @@ __device__ __forceinline__ void store_state(float* states, int seq, int c0, int 
   }
 }
 
-// 16 or 8 bytes to shared memory without passing through registers; the issuing thread alone reads
-// them, so waiting for its own groups is all it needs.  Zeros where there is nothing to copy.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
-  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)), bytes = there ? BYTES : 0;
-  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// 4 floats into the same place of another CTA of the cluster
-__device__ __forceinline__ void store_remote(float* mine, uint32_t rank, const float (&v)[4]) {
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
-  uint32_t to;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+// 2 floats into the same place of another CTA of the cluster, counted by the barrier at `bar` there (a
+// store and a releasing arrive would first wait for every store to HBM that the thread has under way)
+__device__ __forceinline__ void store_remote(float2* mine, uint64_t* bar, uint32_t rank, float2 v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   mapa_shared(smem_u32(mine), rank)),
+               "f"(v.x), "f"(v.y), "r"(mapa_shared(smem_u32(bar), rank))
+               : "memory");
 }
+constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // The sequence around a token: its number and tokens [begin, end); empty where the token is in none.
 struct Span {
@@ -143,268 +164,271 @@ __device__ __forceinline__ void locate(Span& s, const Params& p, int t) {
   if (t < s.begin || t >= s.end) s.begin = s.end = -1;
 }
 
-// c -> A c + H; closed: the scan started anew on the way, nothing of c gets through
-struct Map {
-  float A[4], H[4];
-  bool closed;
+constexpr uint64_t kOnes = 0x3F8000003F800000ull;
+// An A of -1 marks a stretch in which the scan started anew, so that nothing of what enters it gets
+// through (an A is a product of exponentials, never below 0; multiplying by 0 would let a NaN through).
+constexpr float kClosed = -1.f;
+__device__ __forceinline__ float apply(float A, float c, float H) { return A == kClosed ? H : fmaf(A, c, H); }
+
+struct Args {
+  Params p;
+  int cluster;
+  CUtensorMap g, x, y;   // boxes of 32 channels x 128 tokens
 };
-// first `before`, then `m`
-__device__ __forceinline__ void after(Map& m, const Map& before) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (!m.closed) m.H[j] = fmaf(m.A[j], before.H[j], m.H[j]);
-    m.A[j] *= before.A[j];
-  }
-  m.closed |= before.closed;
-}
 
-// Tokens of a thread, and stages of the ring: what leaves room for two blocks an SM.
+template <typename IO, typename G, bool BWD>
+constexpr int stage_bytes() { return kTile * kChannels * static_cast<int>(sizeof(G) + (BWD ? 2 : 1) * sizeof(IO)); }
+constexpr int maps_bytes(int cluster) { return 2 * cluster * kChannels * static_cast<int>(sizeof(float2)); }
+// CTAs an SM: what registers (a thread's tokens) and two stages each leave room for.
 template <typename IO, bool BWD>
-constexpr int tokens_each() { return BWD && sizeof(IO) == 4 ? 2 : 4; }
-template <typename IO, bool BWD>
-constexpr int stage_bytes() { return tokens_each<IO, BWD>() * kThreads * (16 + (BWD ? 2 : 1) * 4 * static_cast<int>(sizeof(IO))); }
-template <typename IO, bool BWD>
-constexpr int stages() { return 98304 / stage_bytes<IO, BWD>(); }
+constexpr int ctas_each() { return sizeof(IO) == 2 ? (BWD ? 3 : 4) : (BWD ? 2 : 3); }
 
-template <typename IO, typename G, bool BWD, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) glr_scan_kernel(const Params p, const int cluster) {
-  constexpr int R = tokens_each<IO, BWD>(), S = stages<IO, BWD>(), TL = kRows * R, GAP = 8;
+// TMA: rows are multiples of 16 bytes and aligned; else threads load their own elements, a tile at a time.
+template <typename IO, typename G, bool BWD, bool TMA>
+__global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kernel(const __grid_constant__ Args args) {
+  constexpr int R = kEach, GAP = 8;
   using RawIO = decltype(Raw4<IO>::u);
   using RawG = decltype(Raw4<G>::u);
-  static_assert(S >= 3, "a tile waits for what enters it, one is summed up, one is on its way");
-  // the ring, every thread's own 4 channels of its tokens: [S][R][thread]
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  float4* ring_g = reinterpret_cast<float4*>(dynamic);   // g as it lies in memory, then e^g (or what a sequence starts from)
-  RawIO* ring_x = reinterpret_cast<RawIO*>(ring_g + S * R * kThreads);
-  RawIO* ring_y = ring_x + S * R * kThreads;
-  __shared__ __align__(16) float warp_a[2][kWarps][kChannels], warp_h[2][kWarps][kChannels];
-  __shared__ bool warp_closed[2][kWarps];
-  // what the cluster's tiles of a step do: written by each into all; three steps, as one may be a step
-  // ahead of a CTA that still reads
-  __shared__ __align__(16) float tile_a[3][kMaxCluster][kChannels], tile_h[3][kMaxCluster][kChannels];
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane >> 3, cq = lane & 7;
+  extern __shared__ __align__(128) uint8_t stages[];        // [2] of g, x, y: [128 tokens][32 channels]
+  __shared__ __align__(16) float seg_a[kSegs][kChannels], seg_h[kSegs][kChannels];   // then what enters a stretch, over its H
+  __shared__ uint64_t full[2], arrived[2];
+  const Params& p = args.p;
+  const int cluster = args.cluster;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seg = tid >> 3, cq = lane & 7;
   const int rank = blockIdx.x % cluster, ct = blockIdx.x / cluster;
-  const int c0 = ct * kChannels + (VEC ? 4 * cq : cq), D = p.D;
+  const int c0 = ct * kChannels + (TMA ? 4 * cq : cq), D = p.D;
   const int total = static_cast<int>(p.tokens);
-  const int steps = static_cast<int>((p.tokens + static_cast<long>(cluster) * TL - 1) / (static_cast<long>(cluster) * TL));
-  // in scan order, this thread's first token of a step
-  auto first = [&](int n) { return (static_cast<long>(n) * cluster + rank) * TL + (warp * 4 + sub) * R; };
-  auto token = [&](long pos) { return static_cast<int>(BWD ? total - 1 - pos : pos); };
-  auto slot = [&](int n, int r) { return (n % S * R + r) * kThreads + tid; };
+  const int steps = static_cast<int>((p.tokens + static_cast<long>(cluster) * kTile - 1) / (static_cast<long>(cluster) * kTile));
   const G* pg = static_cast<const G*>(p.g);
   const IO* px = static_cast<const IO*>(p.x);
   const IO* py = static_cast<const IO*>(p.y);
-
-  auto fetch = [&](int n) {                   // a step's inputs on their way
-    const long pos = first(n);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool there = n < steps && pos + r < total && c0 < D;
-      const int t = token(pos + r);
-      const size_t at = there ? static_cast<size_t>(t) * D + c0 : 0;
-      copy_async<4 * sizeof(G)>(&ring_g[slot(n, r)], pg + at, there);
-      copy_async<4 * sizeof(IO)>(&ring_x[slot(n, r)], px + at, there);
-      if constexpr (BWD) copy_async<4 * sizeof(IO)>(&ring_y[slot(n, r)], py + (there && t > 0 ? at - D : 0), there && t > 0);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  auto tile_at = [&](int n) { return (static_cast<long>(n) * cluster + rank) * kTile; };   // in scan order
+  auto stage_g = [&](int n) { return reinterpret_cast<G*>(stages + (n & 1) * stage_bytes<IO, G, BWD>()); };
+  auto stage_x = [&](int n) { return reinterpret_cast<IO*>(stage_g(n) + kTile * kChannels); };
+  auto stage_y = [&](int n) { return stage_x(n) + kTile * kChannels; };
+  auto maps = [&](int n, int q) {                            // the cluster's tiles of a step: [2][cluster][32 channels]
+    return reinterpret_cast<float2*>(stages + (TMA ? 2 * stage_bytes<IO, G, BWD>() : 0)) + ((n & 1) * cluster + q) * kChannels;
   };
-  // the same through registers, for rows that asynchronous copies cannot start at
-  Raw4<G> held_g[VEC ? 1 : R];
-  Raw4<IO> held_x[VEC ? 1 : R], held_y[VEC ? 1 : R];
-  auto load = [&](int n) {
-    const long pos = first(n);
-#pragma unroll
-    for (int r = 0; r < (VEC ? 0 : R); ++r) {
-      const bool there = n < steps && pos + r < total;
-      const int t = there ? token(pos + r) : 0;
-      const size_t row = static_cast<size_t>(t) * D;
-      held_g[r] = load4<false, GAP>(pg + row, c0, there ? D : 0);
-      held_x[r] = load4<false, GAP>(px + row, c0, there ? D : 0);
-      if constexpr (BWD) held_y[r] = load4<false, GAP>(py + (t > 0 ? row - D : 0), c0, there && t > 0 ? D : 0);
-    }
-  };
-  auto put = [&](int n) {
-#pragma unroll
-    for (int r = 0; r < (VEC ? 0 : R); ++r) {
-      *reinterpret_cast<RawG*>(&ring_g[slot(n, r)]) = held_g[r].u;
-      ring_x[slot(n, r)] = held_x[r].u;
-      if constexpr (BWD) ring_y[slot(n, r)] = held_y[r].u;
-    }
+  auto issue = [&](int n) {                                  // one thread: a tile's inputs on their way
+    const long at = tile_at(n);
+    if (n >= steps || at >= total) return;
+    const int row = static_cast<int>(BWD ? total - at - kTile : at), col = ct * kChannels;
+    uint64_t* bar = &full[n & 1];
+    mbar_arrive_expect_tx(bar, stage_bytes<IO, G, BWD>());
+    tma_load_2d(stage_g(n), &args.g, bar, col, row);
+    tma_load_2d(stage_x(n), &args.x, bar, col, row);
+    if constexpr (BWD) tma_load_2d(stage_y(n), &args.y, bar, col, row - 1);   // (each token's state before it)
   };
 
-  // What a thread's tokens of step n, and those before them in the tile, do to what enters the tile; its
-  // e^g go where g was.  The tile's own map goes to the cluster.
-  Span ahead{0, -1, -1};
-  auto sum_up = [&](int n, Map& m) {
-    m = {{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}, false};
-    const long pos = first(n);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (pos + r >= total) break;
-      const int t = token(pos + r);
-      if (t < ahead.begin || t >= ahead.end) locate(ahead, p, t);
-      if (ahead.end < 0) continue;            // (a token of no sequence leaves everything as it is)
-      const Raw4<G> g{*reinterpret_cast<const RawG*>(&ring_g[slot(n, r)])};
-      const Raw4<IO> x{ring_x[slot(n, r)]};
-      const bool start = t == (BWD ? ahead.end - 1 : ahead.begin);
-      float a[4], keep[4];
-      if (start) {
-        load_state<VEC, GAP>(m.H, p.init, ahead.seq, c0, D);
-        m.closed = true;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j] = expf(g.get(j));
-        keep[j] = start ? m.H[j] : a[j];      // (a final state may take the initial one's place: read it once)
-        m.A[j] *= a[j];
-        m.H[j] = BWD ? a[j] * (m.H[j] + x.get(j)) : fmaf(a[j], m.H[j], x.get(j));
-      }
-      ring_g[slot(n, r)] = make_float4(keep[0], keep[1], keep[2], keep[3]);
+  bool lost = false;
+  if (tid == 0) {
+    if (blockIdx.x == 0) *p.status = 0u;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&arrived[i], 1);
     }
-    // over the warp's 4 threads of these channels
-#pragma unroll
-    for (int d = 8; d <= 16; d *= 2) {
-      Map b;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        b.A[j] = __shfl_up_sync(0xFFFFFFFFu, m.A[j], d);
-        b.H[j] = __shfl_up_sync(0xFFFFFFFFu, m.H[j], d);
-      }
-      b.closed = __shfl_up_sync(0xFFFFFFFFu, m.closed, d);
-      if (lane >= d) after(m, b);
-    }
-    const int half = n & 1;
-    if (sub == 3) {
-      *reinterpret_cast<float4*>(&warp_a[half][warp][4 * cq]) = make_float4(m.A[0], m.A[1], m.A[2], m.A[3]);
-      *reinterpret_cast<float4*>(&warp_h[half][warp][4 * cq]) = make_float4(m.H[0], m.H[1], m.H[2], m.H[3]);
-      if (cq == 0) warp_closed[half][warp] = m.closed;
-    }
-    const Map whole = m;                       // (of the warp, where sub = 3)
-    // the threads before this one: the subs of the warp, and the warps
-    Map b{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}, false};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float A = __shfl_up_sync(0xFFFFFFFFu, m.A[j], 8), H = __shfl_up_sync(0xFFFFFFFFu, m.H[j], 8);
-      if (sub > 0) b.A[j] = A, b.H[j] = H;
-    }
-    b.closed = __shfl_up_sync(0xFFFFFFFFu, m.closed, 8) && sub > 0;
-    __syncthreads();
-    Map w{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}, false};
-    for (int i = 0; i < warp; ++i) {
-      const float4 fa = *reinterpret_cast<const float4*>(&warp_a[half][i][4 * cq]),
-                   fh = *reinterpret_cast<const float4*>(&warp_h[half][i][4 * cq]);
-      Map next{{fa.x, fa.y, fa.z, fa.w}, {fh.x, fh.y, fh.z, fh.w}, warp_closed[half][i]};
-      after(next, w);
-      w = next;
-    }
-    m = b;
-    after(m, w);
-    return [whole, w]() { Map t = whole; after(t, w); return t; }();
-  };
-  auto publish = [&](int n, const Map& tile) {
-    if (warp == kWarps - 1 && sub == 3) {
-      // (where nothing gets through, an A of -1 says so: exponentials are never below 0)
-      float A[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) A[j] = tile.closed ? -1.f : tile.A[j];
-      for (int q = 0; q < cluster; ++q) {
-        store_remote(&tile_a[n % 3][rank][4 * cq], q, A);
-        store_remote(&tile_h[n % 3][rank][4 * cq], q, tile.H);
-      }
-    }
-    cluster_arrive();
-  };
-
-  float carry[4] = {0.f, 0.f, 0.f, 0.f};       // what enters the step, the same in every CTA of the cluster
-  Span here{0, -1, -1};
-  Map cur, next;
-  cluster_arrive();                            // (every CTA runs before another one writes into it)
-  if constexpr (VEC) {
-    for (int n = 0; n < S - 1; ++n) fetch(n);
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-  } else {
-    for (int n = 0; n < 2; ++n) {
-      load(n);
-      put(n);
-    }
+    fence_mbar_init();
   }
-  cluster_wait();
-  if (steps > 0) publish(0, sum_up(0, cur));
+  __syncthreads();
+  if (cluster > 1) cluster_arrive();           // (every CTA is ready before another one writes into it)
+  if (TMA && tid == 0) {
+    issue(0);
+    issue(1);
+  }
+  if (cluster > 1) cluster_wait();
+  float carry = 0.f;                           // the folding warp's: what enters the step, a channel a lane
+  Span span{0, -1, -1};
   for (int n = 0; n < steps; ++n) {
-    if constexpr (VEC) {
-      fetch(n + S - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-    } else {
-      load(n + 2);
-    }
-    const bool more = n + 1 < steps;
-    Map tile;
-    if (more) tile = sum_up(n + 1, next);
-    cluster_wait();                            // the step's maps are there
-    if (more) publish(n + 1, tile);
-    float c[4];
-    for (int q = 0; q < cluster; ++q) {
-      const float4 fa = *reinterpret_cast<const float4*>(&tile_a[n % 3][q][4 * cq]),
-                   fh = *reinterpret_cast<const float4*>(&tile_h[n % 3][q][4 * cq]);
-      const float A[4] = {fa.x, fa.y, fa.z, fa.w}, H[4] = {fh.x, fh.y, fh.z, fh.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (q == rank) c[j] = carry[j];
-        carry[j] = A[j] == -1.f ? H[j] : fmaf(A[j], carry[j], H[j]);
-      }
-    }
-    // the step's tokens again, from what enters them
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = cur.closed ? cur.H[j] : fmaf(cur.A[j], c[j], cur.H[j]);
-    const long pos = first(n);
+    const long pos = tile_at(n) + seg * R;
+    auto token = [&](int r) { return static_cast<int>(BWD ? total - 1 - pos - r : pos + r); };
+    if (TMA && !lost && tile_at(n) < total && !mbar_wait(&full[n & 1], n >> 1 & 1, kWaitNs)) lost = true;
+    Raw4<IO> x[R], y[BWD ? R : 1];
+    Raw4<G> g[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (pos + r >= total) break;
-      const int t = token(pos + r);
-      if (t < here.begin || t >= here.end) locate(here, p, t);
-      if (here.end < 0) continue;
-      const size_t row = static_cast<size_t>(t) * D;
-      const float4 kept = ring_g[slot(n, r)];
-      const Raw4<IO> x{ring_x[slot(n, r)]};
-      float a[4] = {kept.x, kept.y, kept.z, kept.w}, out[4];
-      if (t == (BWD ? here.end - 1 : here.begin)) {
-        const Raw4<G> g = load4<VEC, GAP>(pg + row, c0, D);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[j] = a[j];
-          a[j] = expf(g.get(j));
-        }
-      }
-      const bool end = t == (BWD ? here.begin : here.end - 1);
-      if constexpr (BWD) {
-        const Raw4<IO> y{ring_y[slot(n, r)]};
-        float before[4], dg[4];
-        if (end) load_state<VEC, GAP>(before, p.h0, here.seq, c0, D);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (!end) before[j] = y.get(j);
-          out[j] = c[j] + x.get(j);
-          c[j] = a[j] * out[j];
-          dg[j] = c[j] * before[j];
-        }
-        store4<VEC, GAP>(static_cast<G*>(p.dg) + row, c0, D, dg);
+      if constexpr (TMA) {
+        const int at = (BWD ? kTile - 1 - seg * R - r : seg * R + r) * kChannels + 4 * cq;
+        g[r].u = *reinterpret_cast<const RawG*>(stage_g(n) + at);
+        x[r].u = *reinterpret_cast<const RawIO*>(stage_x(n) + at);
+        if constexpr (BWD) y[r].u = *reinterpret_cast<const RawIO*>(stage_y(n) + at);
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) out[j] = c[j] = fmaf(a[j], c[j], x.get(j));
+        const bool there = pos + r < total;
+        const size_t row = static_cast<size_t>(there ? token(r) : 0) * D;
+        g[r] = load4<false, GAP>(pg + row, c0, there ? D : 0);
+        x[r] = load4<false, GAP>(px + row, c0, there ? D : 0);
+        if constexpr (BWD) y[r] = load4<false, GAP>(py + (row > 0 ? row - D : 0), c0, there && row > 0 ? D : 0);
       }
-      store4<VEC, GAP>(static_cast<IO*>(p.out) + row, c0, D, out);
-      if (end && p.fin) store_state<VEC, GAP>(p.fin, here.seq, c0, D, c);
     }
-    if constexpr (!VEC) put(n + 2);
-    cur = next;
-  }
+    // Tokens of a sequence's inside need no look at where sequences start and end.  Else, a bit each:
+    // the scan starts anew at a token, ends with it, and the token is one of a sequence.
+    uint32_t starts = 0, ends = 0, live = 0;
+    const int t_lo = BWD ? token(R - 1) : token(0), t_hi = BWD ? token(0) : token(R - 1);
+    const bool plain = __all_sync(0xFFFFFFFFu, pos + R <= total && t_lo > span.begin && t_hi < span.end - 1);
+    if (!plain) {
+      for (int r = 0; r < R && pos + r < total; ++r) {
+        const int t = token(r);
+        if (t < span.begin || t >= span.end) locate(span, p, t);
+        if (span.end < 0) continue;
+        live |= 1u << r;
+        starts |= (t == (BWD ? span.end - 1 : span.begin) ? 1u : 0u) << r;
+        ends |= (t == (BWD ? span.begin : span.end - 1) ? 1u : 0u) << r;
+      }
+    }
 
-  // sequences without tokens keep their initial value; one block checks cu_seqlens and sets the status
-  if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");     // (zeros, past the last step)
+    uint64_t a[R][2], A[2] = {kOnes, kOnes}, H[2] = {0ull, 0ull};
+    if (plain) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a[r][i] = exp_pair(g[r].pair(i));
+          A[i] = r == 0 ? a[r][i] : mul2(A[i], a[r][i]);
+          if constexpr (BWD) H[i] = mul2(a[r][i], r == 0 ? x[r].pair(i) : add2(H[i], x[r].pair(i)));
+          else H[i] = r == 0 ? x[r].pair(i) : fma2(a[r][i], H[i], x[r].pair(i));
+        }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!(live >> r & 1)) {                // (a token of no sequence leaves everything as it is)
+          a[r][0] = a[r][1] = kOnes;
+          continue;
+        }
+        const bool start = starts >> r & 1;
+        if (start) {
+          Span s;
+          locate(s, p, token(r));
+          float h[4];
+          load_state<TMA, GAP>(h, p.init, s.seq, c0, D);
+          H[0] = pack2f(h[0], h[1]);
+          H[1] = pack2f(h[2], h[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t e = exp_pair(g[r].pair(i));
+          a[r][i] = start ? H[i] : e;          // (a final state may take the initial one's place: read it once)
+          A[i] = mul2(A[i], e);
+          H[i] = BWD ? mul2(e, add2(H[i], x[r].pair(i))) : fma2(e, H[i], x[r].pair(i));
+        }
+      }
+      if (starts) A[0] = A[1] = pack2f(kClosed, kClosed);
+    }
+    *reinterpret_cast<ulonglong2*>(&seg_a[seg][4 * cq]) = make_ulonglong2(A[0], A[1]);
+    *reinterpret_cast<ulonglong2*>(&seg_h[seg][4 * cq]) = make_ulonglong2(H[0], H[1]);
+    __syncthreads();
+    if (TMA && tid == kThreads - 1) issue(n + 2);            // (the stage has been read)
+    if (warp == 0) {
+      float c = carry, sa[kSegs], sh[kSegs];
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i) {
+        sa[i] = seg_a[i][lane];
+        sh[i] = seg_h[i][lane];
+      }
+      if (cluster > 1) {
+        float TA = 1.f, TH = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+          TH = apply(sa[i], TH, sh[i]);
+          TA = sa[i] == kClosed || TA == kClosed ? kClosed : TA * sa[i];
+        }
+        for (int q = 0; q < cluster; ++q) store_remote(maps(n, rank) + lane, &arrived[n & 1], q, make_float2(TA, TH));
+        if (lane == 0) mbar_arrive_expect_tx_relaxed(&arrived[n & 1], cluster * kChannels * sizeof(float2));
+        if (!lost && !mbar_wait_cluster(&arrived[n & 1], n >> 1 & 1, kWaitNs)) lost = true;
+        for (int q = 0; q < cluster; ++q) {
+          const float2 m = maps(n, q)[lane];
+          if (q == rank) c = carry;
+          carry = apply(m.x, carry, m.y);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i) {
+        seg_h[i][lane] = c;
+        c = apply(sa[i], c, sh[i]);
+      }
+      if (cluster == 1) carry = c;
+    }
+    __syncthreads();
+
+    // the tokens again, from what enters them
+    const ulonglong2 in = *reinterpret_cast<const ulonglong2*>(&seg_h[seg][4 * cq]);
+    uint64_t c[2] = {in.x, in.y};
+    if (plain) {
+      long at = static_cast<long>(token(0)) * D;
+      const long stride = BWD ? -static_cast<long>(D) : D;
+#pragma unroll
+      for (int r = 0; r < R; ++r, at += stride) {
+        float out[4];
+        if constexpr (BWD) {
+          float dg[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t lam = add2(c[i], x[r].pair(i));
+            unpack2f(lam, out[2 * i], out[2 * i + 1]);
+            c[i] = mul2(a[r][i], lam);
+            unpack2f(mul2(c[i], y[r].pair(i)), dg[2 * i], dg[2 * i + 1]);
+          }
+          store4<TMA, GAP>(static_cast<G*>(p.dg) + at, c0, D, dg);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            c[i] = fma2(a[r][i], c[i], x[r].pair(i));
+            unpack2f(c[i], out[2 * i], out[2 * i + 1]);
+          }
+        }
+        store4<TMA, GAP>(static_cast<IO*>(p.out) + at, c0, D, out);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!(live >> r & 1)) continue;
+        const size_t row = static_cast<size_t>(token(r)) * D;
+        const bool end = ends >> r & 1;
+        Span s{0, -1, -1};
+        if (end) locate(s, p, token(r));
+        if (starts >> r & 1) {
+          const Raw4<G> g0 = load4<TMA, GAP>(pg + row, c0, D);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            c[i] = a[r][i];
+            a[r][i] = exp_pair(g0.pair(i));
+          }
+        }
+        float out[4], last[4];
+        if constexpr (BWD) {
+          float dg[4];
+          uint64_t before[2] = {y[r].pair(0), y[r].pair(1)};
+          if (end) {
+            float h[4];
+            load_state<TMA, GAP>(h, p.h0, s.seq, c0, D);
+            before[0] = pack2f(h[0], h[1]);
+            before[1] = pack2f(h[2], h[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t lam = add2(c[i], x[r].pair(i));
+            unpack2f(lam, out[2 * i], out[2 * i + 1]);
+            c[i] = mul2(a[r][i], lam);
+            unpack2f(mul2(c[i], before[i]), dg[2 * i], dg[2 * i + 1]);
+            unpack2f(c[i], last[2 * i], last[2 * i + 1]);
+          }
+          store4<TMA, GAP>(static_cast<G*>(p.dg) + row, c0, D, dg);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            c[i] = fma2(a[r][i], c[i], x[r].pair(i));
+            unpack2f(c[i], out[2 * i], out[2 * i + 1]);
+            unpack2f(c[i], last[2 * i], last[2 * i + 1]);
+          }
+        }
+        store4<TMA, GAP>(static_cast<IO*>(p.out) + row, c0, D, out);
+        if (end && p.fin) store_state<TMA, GAP>(p.fin, s.seq, c0, D, last);
+      }
+    }
+  }
+  if (lost) atomicOr(p.status, kStatusTimeout);
+
+  // sequences without tokens keep their initial value; one block checks cu_seqlens
   if (p.cu) {
-    bool bad = false;
-    for (int s0 = (rank * kWarps + warp) * 32; s0 < p.num_seqs; s0 += 32 * kWarps * cluster) {
+    for (int s0 = (rank * (kThreads / 32) + warp) * 32; s0 < p.num_seqs; s0 += kThreads * cluster) {
       const int q = s0 + lane;
       const bool none = q < p.num_seqs && p.cu[q + 1] <= p.cu[q] && p.fin;
       const int c = ct * kChannels + lane;
@@ -414,18 +438,21 @@ __global__ void __launch_bounds__(kThreads, 2) glr_scan_kernel(const Params p, c
       }
     }
     if (blockIdx.x == 0) {
+      bool bad = false;
       for (int q = tid; q < p.num_seqs; q += kThreads) {
         const int b = p.cu[q], e = p.cu[q + 1];
         bad |= b < 0 || e < b || e > total || (q == 0 && b != 0) || (q == p.num_seqs - 1 && e != total);
       }
-      bad = __syncthreads_or(bad);
-      if (tid == 0) *p.status = bad ? kStatusBounds : 0u;
+      if (bad) atomicOr(p.status, kStatusBounds);
     }
-  } else if (blockIdx.x == 0 && tid == 0) {
-    *p.status = 0u;
   }
-  cluster_arrive();                            // (nobody writes into a CTA that has ended)
-  cluster_wait();
+  if (TMA && lost && tid == 0)                 // (copies under way land before their memory goes)
+    for (int i = 0; i < 2; ++i)
+      for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {}
+  if (cluster > 1) {                           // (nobody writes into a CTA that has ended)
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // The serving step: 4 channels a thread, the state in registers between its load and its store.
@@ -475,46 +502,81 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const StepParams p) {
   }
 }
 
-template <typename IO, typename G, bool BWD, bool VEC>
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+template <typename T>
+bool make_map(CUtensorMap* m, const void* base, int D, long tokens) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * sizeof(T)};
+  const cuuint32_t box[2] = {kChannels, kTile}, step[2] = {1, 1};
+  return enc(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename IO, typename G, bool BWD, bool TMA>
 cudaError_t launch_scan(const Params& p, cudaStream_t st) {
-  constexpr int ring = stages<IO, BWD>() * stage_bytes<IO, BWD>(), TL = kRows * tokens_each<IO, BWD>();
-  const auto kernel = glr_scan_kernel<IO, G, BWD, VEC>;
+  constexpr int ring = TMA ? 2 * stage_bytes<IO, G, BWD>() : 0;
+  const auto kernel = glr_scan_kernel<IO, G, BWD, TMA>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  static bool raised[64] = {};         // (a race raises it twice, to the same value)
-  if (dev < 0 || dev >= 64 || !raised[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) raised[dev] = true;
+  {
+    static bool raised[64] = {};       // (a race raises it twice, to the same value)
+    if (dev < 0 || dev >= 64 || !raised[dev]) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + maps_bytes(kMaxCluster));
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) raised[dev] = true;
+    }
   }
-  // CTAs of a cluster share a channel tile's tokens: as many as there are places for, and tiles
-  const long cts = (p.D + kChannels - 1) / kChannels, tiles = (p.tokens + TL - 1) / TL;
-  int cluster = 1;
-  while (cluster < kMaxCluster && cts * cluster * 2 <= 2 * sms && cluster * 2 <= tiles) cluster *= 2;
+  Args args{};
+  args.p = p;
+  if (TMA && p.tokens > 0 &&
+      (!make_map<G>(&args.g, p.g, p.D, p.tokens) || !make_map<IO>(&args.x, p.x, p.D, p.tokens) ||
+       (BWD && !make_map<IO>(&args.y, p.y, p.D, p.tokens))))
+    return cudaErrorInvalidValue;
+  // CTAs of a cluster share a channel tile's tokens: as many as make up two CTAs an SM, and tiles.  46402
+  // tokens x 2048: 247 us for one an SM, 153 for two, 188 for four (more waits for one another);
+  // 4096 x 4096: 47, 39 and 35; 4 x 4096 x 4096 backward: 190, 161 and 212.
+  const long cts = (p.D + kChannels - 1) / kChannels, tiles = (p.tokens + kTile - 1) / kTile;
+  args.cluster = 1;
+  while (args.cluster < kMaxCluster && cts * args.cluster * 2 <= 2 * sms && args.cluster * 2 <= tiles) args.cluster *= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.x = args.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cts * cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(cts * args.cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ring;
+  cfg.dynamicSmemBytes = ring + maps_bytes(args.cluster);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
+  return cudaLaunchKernelEx(&cfg, kernel, args);
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <typename IO, typename G>
 cudaError_t launch_types(const Params& p, bool backward, cudaStream_t st) {
-  const bool vec = p.D % 4 == 0 && aligned(p.x, 4 * sizeof(IO)) && aligned(p.y, 4 * sizeof(IO)) && aligned(p.out, 4 * sizeof(IO)) &&
-                   aligned(p.g, 4 * sizeof(G)) && aligned(p.dg, 4 * sizeof(G));
-  if (backward) return vec ? launch_scan<IO, G, true, true>(p, st) : launch_scan<IO, G, true, false>(p, st);
-  return vec ? launch_scan<IO, G, false, true>(p, st) : launch_scan<IO, G, false, false>(p, st);
+  const bool tma = p.D * sizeof(IO) % 16 == 0 && p.D * sizeof(G) % 16 == 0 && aligned(p.x, 16) && aligned(p.y, 16) &&
+                   aligned(p.out, 16) && aligned(p.g, 16) && aligned(p.dg, 16);
+  if (backward) return tma ? launch_scan<IO, G, true, true>(p, st) : launch_scan<IO, G, true, false>(p, st);
+  return tma ? launch_scan<IO, G, false, true>(p, st) : launch_scan<IO, G, false, false>(p, st);
 }
 
 template <typename IO, typename G>
