@@ -145,8 +145,9 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 struct Span {
   int seq, begin, end;
 };
-__device__ __forceinline__ void locate(Span& s, const Params& p, int t) {
-  if (p.cu == nullptr) {
+constexpr int kMostCu = 2048;              // entries of cu_seqlens that a CTA keeps in shared memory
+__device__ __forceinline__ void locate(Span& s, const Params& p, const int32_t* cu, int t) {
+  if (cu == nullptr) {
     s.seq = t / p.T;
     s.begin = s.seq * p.T;
     s.end = s.begin + p.T;
@@ -155,12 +156,12 @@ __device__ __forceinline__ void locate(Span& s, const Params& p, int t) {
   int lo = 0, hi = p.num_seqs;               // the last one that starts at or before t, whatever cu holds
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (p.cu[mid] <= t) lo = mid;
+    if (cu[mid] <= t) lo = mid;
     else hi = mid;
   }
   s.seq = lo;
-  s.begin = p.cu[lo];
-  s.end = p.cu[lo + 1];
+  s.begin = cu[lo];
+  s.end = cu[lo + 1];
   if (t < s.begin || t >= s.end) s.begin = s.end = -1;
 }
 
@@ -220,6 +221,12 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
     if constexpr (BWD) tma_load_2d(stage_y(n), &args.y, bar, col, row - 1);   // (each token's state before it)
   };
 
+  const int32_t* cu = p.cu;
+  if (cu && p.num_seqs < kMostCu) {
+    int32_t* kept = reinterpret_cast<int32_t*>(maps(0, 0) + 2 * cluster * kChannels);
+    for (int i = tid; i <= p.num_seqs; i += kThreads) kept[i] = p.cu[i];
+    cu = kept;
+  }
   bool lost = false;
   if (tid == 0) {
     if (blockIdx.x == 0) *p.status = 0u;
@@ -263,11 +270,12 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
     // the scan starts anew at a token, ends with it, and the token is one of a sequence.
     uint32_t starts = 0, ends = 0, live = 0;
     const int t_lo = BWD ? token(R - 1) : token(0), t_hi = BWD ? token(0) : token(R - 1);
+    if (pos < total && (token(0) < span.begin || token(0) >= span.end)) locate(span, p, cu, token(0));
     const bool plain = __all_sync(0xFFFFFFFFu, pos + R <= total && t_lo > span.begin && t_hi < span.end - 1);
     if (!plain) {
       for (int r = 0; r < R && pos + r < total; ++r) {
         const int t = token(r);
-        if (t < span.begin || t >= span.end) locate(span, p, t);
+        if (t < span.begin || t >= span.end) locate(span, p, cu, t);
         if (span.end < 0) continue;
         live |= 1u << r;
         starts |= (t == (BWD ? span.end - 1 : span.begin) ? 1u : 0u) << r;
@@ -275,7 +283,9 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
       }
     }
 
-    uint64_t a[R][2], A[2] = {kOnes, kOnes}, H[2] = {0ull, 0ull};
+    // (the last value that the scan started from is kept: where that sequence goes on beyond this thread, its
+    // array may hold the final state by the time the tokens are gone through again)
+    uint64_t a[R][2], A[2] = {kOnes, kOnes}, H[2] = {0ull, 0ull}, from[2] = {0ull, 0ull};
     if (plain) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -293,21 +303,19 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
           a[r][0] = a[r][1] = kOnes;
           continue;
         }
-        const bool start = starts >> r & 1;
-        if (start) {
+        if (starts >> r & 1) {
           Span s;
-          locate(s, p, token(r));
+          locate(s, p, cu, token(r));
           float h[4];
           load_state<TMA, GAP>(h, p.init, s.seq, c0, D);
-          H[0] = pack2f(h[0], h[1]);
-          H[1] = pack2f(h[2], h[3]);
+          H[0] = from[0] = pack2f(h[0], h[1]);
+          H[1] = from[1] = pack2f(h[2], h[3]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint64_t e = exp_pair(g[r].pair(i));
-          a[r][i] = start ? H[i] : e;          // (a final state may take the initial one's place: read it once)
-          A[i] = mul2(A[i], e);
-          H[i] = BWD ? mul2(e, add2(H[i], x[r].pair(i))) : fma2(e, H[i], x[r].pair(i));
+          a[r][i] = exp_pair(g[r].pair(i));
+          A[i] = mul2(A[i], a[r][i]);
+          H[i] = BWD ? mul2(a[r][i], add2(H[i], x[r].pair(i))) : fma2(a[r][i], H[i], x[r].pair(i));
         }
       }
       if (starts) A[0] = A[1] = pack2f(kClosed, kClosed);
@@ -383,14 +391,15 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
         const size_t row = static_cast<size_t>(token(r)) * D;
         const bool end = ends >> r & 1;
         Span s{0, -1, -1};
-        if (end) locate(s, p, token(r));
-        if (starts >> r & 1) {
-          const Raw4<G> g0 = load4<TMA, GAP>(pg + row, c0, D);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            c[i] = a[r][i];
-            a[r][i] = exp_pair(g0.pair(i));
-          }
+        if (end || starts >> r & 1) locate(s, p, cu, token(r));
+        if (starts >> r == 1u) {
+          c[0] = from[0];
+          c[1] = from[1];
+        } else if (starts >> r & 1) {
+          float h[4];
+          load_state<TMA, GAP>(h, p.init, s.seq, c0, D);
+          c[0] = pack2f(h[0], h[1]);
+          c[1] = pack2f(h[2], h[3]);
         }
         float out[4], last[4];
         if constexpr (BWD) {
@@ -539,7 +548,7 @@ cudaError_t launch_scan(const Params& p, cudaStream_t st) {
   {
     static bool raised[64] = {};       // (a race raises it twice, to the same value)
     if (dev < 0 || dev >= 64 || !raised[dev]) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + maps_bytes(kMaxCluster));
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + maps_bytes(kMaxCluster) + kMostCu * sizeof(int32_t));
       if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) raised[dev] = true;
@@ -564,7 +573,7 @@ cudaError_t launch_scan(const Params& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cts * args.cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ring + maps_bytes(args.cluster);
+  cfg.dynamicSmemBytes = ring + maps_bytes(args.cluster) + (p.cu && p.num_seqs < kMostCu ? (p.num_seqs + 1) * sizeof(int32_t) : 0);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
