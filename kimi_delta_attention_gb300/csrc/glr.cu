@@ -560,12 +560,42 @@ cudaError_t launch_scan(const Params& p, cudaStream_t st) {
       (!make_map<G>(&args.g, p.g, p.D, p.tokens) || !make_map<IO>(&args.x, p.x, p.D, p.tokens) ||
        (BWD && !make_map<IO>(&args.y, p.y, p.D, p.tokens))))
     return cudaErrorInvalidValue;
-  // CTAs of a cluster share a channel tile's tokens: as many as make up two CTAs an SM, and tiles.  46402
-  // tokens x 2048: 247 us for one an SM, 153 for two, 188 for four (more waits for one another);
-  // 4096 x 4096: 47, 39 and 35; 4 x 4096 x 4096 backward: 190, 161 and 212.
+  const size_t cu_bytes = p.cu && p.num_seqs < kMostCu ? (p.num_seqs + 1) * sizeof(int32_t) : 0;
   const long cts = (p.D + kChannels - 1) / kChannels, tiles = (p.tokens + kTile - 1) / kTile;
   args.cluster = 1;
-  while (args.cluster < kMaxCluster && cts * args.cluster * 2 <= 2 * sms && args.cluster * 2 <= tiles) args.cluster *= 2;
+  if (tiles > 1) {
+    // CTAs of a cluster share a channel tile's tokens: as many as can all run at once, up to 8 CTAs for 3 SMs,
+    // and with more bytes an element (fp32, backward) 2 an SM.  us a call for 1, 2, 3, 4, 6 and 8 CTAs a cluster:
+    // 4096 x 4096 bf16 (128 channel tiles) 46, 39, 36.5, 34.4; 46402 x 2048 (64) 356, 249, 208, 152, 133, 139;
+    // 8192 x 8192 (256) 100, 108; 16384 x 4096 backward 190, 161, 184, 191; 65536 x 128 (4) 489, 342, 245, 178,
+    // 129, 98 and 61 for 16.
+    const long most = sizeof(IO) == 2 && !BWD ? 8 * sms / 3 : 2 * sms;
+    static int room[64][kMaxCluster + 1] = {};     // clusters of a size that run at once, with the most of cu_seqlens
+    for (int c = tiles < kMaxCluster ? static_cast<int>(tiles) : kMaxCluster; c > 1; --c) {
+      if (cts * c > most) continue;
+      int fit = dev >= 0 && dev < 64 ? room[dev][c] : 0;
+      if (fit == 0) {
+        cudaLaunchAttribute shape;
+        shape.id = cudaLaunchAttributeClusterDimension;
+        shape.val.clusterDim.x = c;
+        shape.val.clusterDim.y = shape.val.clusterDim.z = 1;
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(c);
+        q.blockDim = dim3(kThreads);
+        q.dynamicSmemBytes = ring + maps_bytes(c);
+        q.attrs = &shape;
+        q.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&fit, kernel, &q);
+        if (e != cudaSuccess) return e;
+        if (fit == 0) fit = -1;
+        if (dev >= 0 && dev < 64) room[dev][c] = fit;
+      }
+      if (fit >= cts) {
+        args.cluster = c;
+        break;
+      }
+    }
+  }
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = args.cluster;
@@ -573,7 +603,7 @@ cudaError_t launch_scan(const Params& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cts * args.cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ring + maps_bytes(args.cluster) + (p.cu && p.num_seqs < kMostCu ? (p.num_seqs + 1) * sizeof(int32_t) : 0);
+  cfg.dynamicSmemBytes = ring + maps_bytes(args.cluster) + cu_bytes;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
