@@ -2,8 +2,11 @@
 //
 //     m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
 //     p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
-// Every value is read once and written once.  The tensors' addresses travel in the launch's own
-// parameters, so a step needs no table in device memory, and a captured one keeps its own.
+// Every value is read once and written once.  With 32-bit states that is all there is to it (22 bytes a
+// value in bf16, 28 in fp32: bound by HBM); with 8-bit states (10 bytes) the instructions of the
+// rounding count as much, some 60 a value, so codes are made in integer arithmetic on the bits of
+// the scaled value.  The tensors' addresses travel in the launch's own parameters, so a step
+// needs no table in device memory, and a captured one keeps its own.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -15,7 +18,8 @@ namespace adamw {
 namespace {
 
 constexpr int kThreads = 256, kEach = 8;             // a thread's values: a warp holds a block of 256
-constexpr int kChunk = kThreads * kEach;             // values a thread block takes at once
+constexpr int kPass = kThreads * kEach;              // values a thread block takes at once
+constexpr int kChunk = 4 * kPass;                    // and in all
 constexpr int kBlock = KDA_ADAMW_BLOCK;
 static_assert(kBlock == 32 * kEach, "a warp holds a block of values that share a scale");
 
@@ -31,12 +35,22 @@ struct Entry {
 };
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kVector = 4 };
 
+// What learning rate and step number give, the same from either side.
+struct Rates {
+  float keep, rate, inv;               // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+};
+__host__ __device__ __forceinline__ Rates rates(float lr, double wd, double log_b1, double log_b2, int step) {
+  return {static_cast<float>(1 - lr * wd), static_cast<float>(lr / -expm1(step * log_b1)),
+          static_cast<float>(1 / sqrt(-expm1(step * log_b2)))};
+}
+
 struct Scalars {
-  float lr, wd, b1, c1, b2, c2, eps;   // c = 1 - b
-  double log_b1, log_b2;               // for the step's bias corrections
+  Rates r;
+  float lr, b1, c1, b2, c2, eps;       // c = 1 - b
+  double wd, log_b1, log_b2;
   int step;
-  uint32_t seed_lo, seed_hi;
-  const int32_t* step_device;
+  uint32_t key, seed_lo, seed_hi;      // key: of seed and step
+  const int32_t* step_device;          // with either of these two, r and key are found on the device
   const float* lr_device;
   const float* grad_scale;
   const float* skip;
@@ -53,12 +67,15 @@ struct Batch {
 };
 
 // A 32-bit mix of shifts and odd multiplications (each input bit turns over half of the output's).
-__device__ __forceinline__ uint32_t mix(uint32_t x) {
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x71C61315u;
   x = (x ^ (x >> 15)) * 0x189C32BFu;
   return x ^ (x >> 16);
 }
 constexpr uint32_t kSpread = 0x9E3779B1u;
+__host__ __device__ __forceinline__ uint32_t step_key(uint32_t lo, uint32_t hi, int step) {
+  return mix(lo ^ mix(hi ^ mix(static_cast<uint32_t>(step))));
+}
 
 template <typename T>
 __device__ __forceinline__ void load8(float (&x)[kEach], const T* src, int left, bool vector) {
@@ -72,11 +89,10 @@ __device__ __forceinline__ void load8(float (&x)[kEach], const T* src, int left,
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 u = reinterpret_cast<const float4*>(src)[i];
-        x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
-      }
+      // (32 bytes in one load: two of 16 would leave half of each sector to the other)
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                   : "l"(src));
     }
   } else {
 #pragma unroll
@@ -96,9 +112,9 @@ __device__ __forceinline__ void store8(T* dst, const float (&x)[kEach], int left
       }
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        reinterpret_cast<float4*>(dst)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                   "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "l"(dst)
+                   : "memory");
     }
   } else {
 #pragma unroll
@@ -107,62 +123,79 @@ __device__ __forceinline__ void store8(T* dst, const float (&x)[kEach], int left
   }
 }
 
-__device__ __forceinline__ float decode(uint8_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
-}
-
 __device__ __forceinline__ void load_codes(float (&x)[kEach], const uint8_t* src, float scale, int left, bool vector) {
-  uint8_t c[kEach];
+  uint32_t c[2] = {0u, 0u};
   if (vector && left >= kEach) {
-    *reinterpret_cast<uint2*>(c) = *reinterpret_cast<const uint2*>(src);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) c[i] = i < left ? src[i] : uint8_t(0);
-  }
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) x[i] = __fmul_rn(decode(c[i]), scale);
-}
-
-// The codes of a warp's 256 values, by random numbers in [0, 1) (16 bits of each hash from `shift`),
-// and their scale.  Each operation is rounded by itself, so the result is that of the formula in
-// fp32 operations whatever the compiler.  KEEP: a value above 0 keeps a code above 0.
-template <bool KEEP>
-__device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEach], const uint32_t (&hash)[kEach], int shift,
-                                             int left, bool vector) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) top = fmaxf(top, isfinite(x[i]) ? fabsf(x[i]) : 0.f);
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-  const bool some = top >= 0x1p-100f;
-  const float scale = some ? __fmul_rn(top, static_cast<float>(1.0 / 448)) : 0.f;
-  const float up0 = some ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
-  uint8_t c[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const float a = fabsf(x[i]), y = __fmul_rn(a, up0);
-    const int e = min(max((__float_as_int(y) >> 23) - 127, -6), 8);        // (subnormal codes share their step)
-    const float u = static_cast<float>((hash[i] >> shift) & 0xFFFFu) * 0x1p-16f;
-    float q = __fmul_rn(floorf(__fadd_rn(__fmul_rn(y, __int_as_float((130 - e) << 23)), u)), __int_as_float((124 + e) << 23));
-    q = fminf(q, 448.f);
-    if (KEEP && a > 0.f && q == 0.f) q = 0x1p-9f;
-    if (!isfinite(a)) q = __int_as_float(0x7FFFFFFF);
-    c[i] = __nv_cvt_float_to_fp8(copysignf(q, x[i]), __NV_SATFINITE, __NV_E4M3);
-  }
-  if (vector && left >= kEach) {
-    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(c);
+    const uint2 u = *reinterpret_cast<const uint2*>(src);
+    c[0] = u.x;
+    c[1] = u.y;
   } else {
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-      if (i < left) dst[i] = c[i];
+      if (i < left) c[i / 4] |= static_cast<uint32_t>(src[i]) << 8 * (i % 4);
+  }
+#pragma unroll
+  for (int i = 0; i < kEach / 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c[i / 2] >> 16 * (i % 2)), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * i] = __fmul_rn(f.x, scale);
+    x[2 * i + 1] = __fmul_rn(f.y, scale);
+  }
+}
+
+// The codes of a warp's 256 values, by 16 bits of each value's hash from `SHIFT` on, and their scale.  With y =
+// |x| 448 / top, a code's step in y is 2^(e - 3) for 2^e <= y < 2^(e + 1), and 2^-9 below 2^-6; the random
+// number, in steps, is added and the rest cut off.  On the bits of y that is one integer addition
+// (the exponent follows the mantissa, in fp32 as in the code).
+// KEEP: a value above 0 keeps a code above 0.
+template <int SHIFT, bool KEEP>
+__device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEach], const uint32_t (&hash)[kEach], int left,
+                                             bool vector) {
+  uint32_t top = 0u;                   // magnitudes compare as their bits do
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  const bool bad = top >= 0x7F800000u; // (the whole warp) values that are not finite: NaN codes, and they count for no scale
+  if (bad) {
+    top = 0u;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      top = max(top, b < 0x7F800000u ? b : 0u);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+  }
+  const float largest = __uint_as_float(top);
+  const bool some = largest >= 0x1p-100f;
+  const float scale = some ? __fmul_rn(largest, static_cast<float>(1.0 / 448)) : 0.f;
+  const float up = some ? __fmul_rn(__frcp_rn(largest), 448.f) : 0.f;
+  uint32_t c[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const float y = fabsf(__fmul_rn(x[i], up));
+    const uint32_t u = SHIFT == 0 ? hash[i] << 4 & 0xFFFF0u : hash[i] >> 12 & 0xFFFF0u;
+    uint32_t code = min((__float_as_uint(y) + u - 0x3C000000u) >> 20, 126u);          // (960 << 20: the exponents' offset)
+    // floor(512 y + random number): the sum rounded down at 2^23 has it in its last bits
+    const float z = fmaf(y, 512.f, __uint_as_float(0x3F800000u | u << 3) - 1.f);
+    if (y < 0x1p-6f) code = __float_as_uint(__fadd_rd(z, 0x1p23f)) & 15u;
+    if (KEEP && x[i] > 0.f) code = max(code, 1u);
+    if (bad && (__float_as_uint(x[i]) & 0x7FFFFFFFu) >= 0x7F800000u) code = 0x7Fu;
+    if (!KEEP) code |= __float_as_uint(x[i]) >> 24 & 0x80u;
+    c[i / 4] |= code << 8 * (i % 4);
+  }
+  if (vector && left >= kEach) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (i < left) dst[i] = static_cast<uint8_t>(c[i / 4] >> 8 * (i % 4));
   }
   return scale;
 }
 
 template <int CAP, bool BITS8>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Batch<CAP> b) {
-  __shared__ float sh[5];
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Batch<CAP> b) {
+  __shared__ Rates sh;
   __shared__ uint32_t sh_key;
   const Scalars& s = b.s;
   if (s.skip && *s.skip != 0.f) return;
@@ -172,66 +205,77 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if (b.first[mid] <= blockIdx.x) lo = mid;
     else hi = mid;
   }
-  if (threadIdx.x == 0) {
-    const int step = s.step_device ? *s.step_device : s.step;
-    const float lr = s.lr_device ? *s.lr_device : s.lr;
-    const float bc1 = static_cast<float>(-expm1(step * s.log_b1)), bc2 = static_cast<float>(-expm1(step * s.log_b2));
-    sh[0] = 1.f - lr * s.wd;
-    sh[1] = lr / bc1;
-    sh[2] = 1.f / sqrtf(bc2);
-    sh[3] = s.grad_scale ? *s.grad_scale : 1.f;
-    const uint32_t key = mix(s.seed_lo ^ mix(s.seed_hi ^ mix(static_cast<uint32_t>(step))));
-    sh_key = mix(key + static_cast<uint32_t>(b.number + lo) * kSpread);
+  Rates r = s.r;
+  uint32_t key = s.key;
+  if (s.step_device || s.lr_device) {
+    if (threadIdx.x == 0) {
+      const int step = s.step_device ? *s.step_device : s.step;
+      sh = rates(s.lr_device ? *s.lr_device : s.lr, s.wd, s.log_b1, s.log_b2, step);
+      sh_key = step_key(s.seed_lo, s.seed_hi, step);
+    }
+    __syncthreads();
+    r = sh;
+    key = sh_key;
   }
-  __syncthreads();
-  const float keep = sh[0], rate = sh[1], inv = sh[2], gs = sh[3];
+  key = mix(key + static_cast<uint32_t>(b.number + lo) * kSpread);
+  const float gs = s.grad_scale ? *s.grad_scale : 1.f;
   const Entry& t = b.t[lo];
   const uint32_t flags = b.flags[lo];
   const bool vector = flags & kVector;
-  const long at = static_cast<long>(blockIdx.x - b.first[lo]) * kChunk + threadIdx.x * kEach;
-  if ((at & ~static_cast<long>(kBlock - 1)) >= t.n) return;            // (whole warps)
-  const long rest = t.n - at;
-  const int left = rest < 0 ? 0 : rest > kEach ? kEach : static_cast<int>(rest);
-  const long blk = at / kBlock;
-  float p[kEach], g[kEach], m[kEach], v[kEach];
-  if (t.master) load8(p, t.master + at, left, vector);
-  else if (flags & kParamBf16) load8(p, static_cast<const __nv_bfloat16*>(t.p) + at, left, vector);
-  else load8(p, static_cast<const float*>(t.p) + at, left, vector);
-  if (flags & kGradBf16) load8(g, static_cast<const __nv_bfloat16*>(t.g) + at, left, vector);
-  else load8(g, static_cast<const float*>(t.g) + at, left, vector);
-  if constexpr (BITS8) {
-    load_codes(m, static_cast<const uint8_t*>(t.m) + at, t.m_scale[blk], left, vector);
-    load_codes(v, static_cast<const uint8_t*>(t.v) + at, t.v_scale[blk], left, vector);
-  } else {
-    load8(m, static_cast<const float*>(t.m) + at, left, vector);
-    load8(v, static_cast<const float*>(t.v) + at, left, vector);
-  }
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const float d = s.grad_scale ? __fmul_rn(g[i], gs) : g[i];
-    m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(d, s.c1));
-    v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(d, d), s.c2));
-    p[i] = p[i] * keep - rate * (m[i] / fmaf(sqrtf(v[i]), inv, s.eps));
-  }
-  if (t.master) store8(t.master + at, p, left, vector);
-  if (flags & kParamBf16) store8(static_cast<__nv_bfloat16*>(t.p) + at, p, left, vector);
-  else store8(static_cast<float*>(t.p) + at, p, left, vector);
-  if constexpr (BITS8) {
-    uint32_t hash[kEach];
+  const long from = static_cast<long>(blockIdx.x - b.first[lo]) * kChunk + threadIdx.x * kEach;
+#pragma unroll 1
+  for (long at = from; at < from + kChunk; at += kPass) {
+    if ((at & ~static_cast<long>(kBlock - 1)) >= t.n) return;          // (whole warps)
+    const long rest = t.n - at;
+    const int left = rest < 0 ? 0 : rest > kEach ? kEach : static_cast<int>(rest);
+    const long blk = at / kBlock;
+    float p[kEach], g[kEach], m[kEach], v[kEach];
+    if (t.master) load8(p, t.master + at, left, vector);
+    else if (flags & kParamBf16) load8(p, static_cast<const __nv_bfloat16*>(t.p) + at, left, vector);
+    else load8(p, static_cast<const float*>(t.p) + at, left, vector);
+    if (flags & kGradBf16) load8(g, static_cast<const __nv_bfloat16*>(t.g) + at, left, vector);
+    else load8(g, static_cast<const float*>(t.g) + at, left, vector);
+    if constexpr (BITS8) {
+      load_codes(m, static_cast<const uint8_t*>(t.m) + at, t.m_scale[blk], left, vector);
+      load_codes(v, static_cast<const uint8_t*>(t.v) + at, t.v_scale[blk], left, vector);
+    } else {
+      load8(m, static_cast<const float*>(t.m) + at, left, vector);
+      load8(v, static_cast<const float*>(t.v) + at, left, vector);
+    }
+    // m and v: each operation rounded by itself, as the formula's (the codes go by their bits)
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      hash[i] = mix((static_cast<uint32_t>(at + i) * kSpread) ^ sh_key);
-      if (i >= left) m[i] = v[i] = 0.f;
+      const float d = s.grad_scale ? __fmul_rn(g[i], gs) : g[i];
+      m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(d, s.c1));
+      v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(d, d), s.c2));
     }
-    const float ms = store_codes<false>(static_cast<uint8_t*>(t.m) + at, m, hash, 0, left, vector);
-    const float vs = store_codes<true>(static_cast<uint8_t*>(t.v) + at, v, hash, 16, left, vector);
-    if ((threadIdx.x & 31) == 0) {
-      t.m_scale[blk] = ms;
-      t.v_scale[blk] = vs;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      float root;
+      asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i]));
+      p[i] = fmaf(p[i], r.keep, -r.rate * __fdividef(m[i], fmaf(root, r.inv, s.eps)));
     }
-  } else {
-    store8(static_cast<float*>(t.m) + at, m, left, vector);
-    store8(static_cast<float*>(t.v) + at, v, left, vector);
+    if (t.master) store8(t.master + at, p, left, vector);
+    if (flags & kParamBf16) store8(static_cast<__nv_bfloat16*>(t.p) + at, p, left, vector);
+    else store8(static_cast<float*>(t.p) + at, p, left, vector);
+    if constexpr (BITS8) {
+      uint32_t hash[kEach];
+      const uint32_t h0 = static_cast<uint32_t>(at) * kSpread;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        hash[i] = mix((h0 + i * kSpread) ^ key);
+        if (i >= left) m[i] = v[i] = 0.f;
+      }
+      const float ms = store_codes<0, false>(static_cast<uint8_t*>(t.m) + at, m, hash, left, vector);
+      const float vs = store_codes<16, true>(static_cast<uint8_t*>(t.v) + at, v, hash, left, vector);
+      if ((threadIdx.x & 31) == 0) {
+        t.m_scale[blk] = ms;
+        t.v_scale[blk] = vs;
+      }
+    } else {
+      store8(static_cast<float*>(t.m) + at, m, left, vector);
+      store8(static_cast<float*>(t.v) + at, v, left, vector);
+    }
   }
 }
 
@@ -245,9 +289,9 @@ cudaError_t launch_batch(const kda_adamw_tensor* tensors, int from, int to, cons
   uint64_t blocks = 0;
   for (int i = from; i < to; ++i) {
     const kda_adamw_tensor& t = tensors[i];
-    const uintptr_t state = bits8 ? 7 : 15;
+    const uintptr_t state = bits8 ? 7 : 31, param = t.param_dtype == KDA_BF16 ? 15 : 31, grad = t.grad_dtype == KDA_BF16 ? 15 : 31;
     auto off = [](const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q) & mask) != 0; };
-    const bool vector = !off(t.param, 15) && !off(t.grad, 15) && !off(t.m, state) && !off(t.v, state) && !off(t.master, 15);
+    const bool vector = !off(t.param, param) && !off(t.grad, grad) && !off(t.m, state) && !off(t.v, state) && !off(t.master, 31);
     b.first[b.count] = static_cast<uint32_t>(blocks);
     b.flags[b.count] = (t.param_dtype == KDA_BF16 ? kParamBf16 : 0u) | (t.grad_dtype == KDA_BF16 ? kGradBf16 : 0u) |
                        (vector ? kVector : 0u);
@@ -267,11 +311,25 @@ constexpr int kMany = 440, kFew = 24;
 }  // namespace
 
 cudaError_t launch(const kda_adamw_tensor* tensors, int count, const kda_adamw_config& c, cudaStream_t st) {
-  const Scalars s{static_cast<float>(c.lr), static_cast<float>(c.weight_decay), static_cast<float>(c.beta1),
-                  static_cast<float>(1 - c.beta1), static_cast<float>(c.beta2), static_cast<float>(1 - c.beta2),
-                  static_cast<float>(c.eps), std::log(c.beta1), std::log(c.beta2), static_cast<int>(c.step),
-                  static_cast<uint32_t>(c.seed), static_cast<uint32_t>(c.seed >> 32), c.step_device, c.lr_device,
-                  c.grad_scale, c.skip};
+  Scalars s{};
+  s.lr = static_cast<float>(c.lr);
+  s.wd = c.weight_decay;
+  s.b1 = static_cast<float>(c.beta1);
+  s.c1 = static_cast<float>(1 - c.beta1);
+  s.b2 = static_cast<float>(c.beta2);
+  s.c2 = static_cast<float>(1 - c.beta2);
+  s.eps = static_cast<float>(c.eps);
+  s.log_b1 = std::log(c.beta1);
+  s.log_b2 = std::log(c.beta2);
+  s.step = static_cast<int>(c.step);
+  s.r = rates(s.lr, s.wd, s.log_b1, s.log_b2, s.step);
+  s.seed_lo = static_cast<uint32_t>(c.seed);
+  s.seed_hi = static_cast<uint32_t>(c.seed >> 32);
+  s.key = step_key(s.seed_lo, s.seed_hi, s.step);
+  s.step_device = c.step_device;
+  s.lr_device = c.lr_device;
+  s.grad_scale = c.grad_scale;
+  s.skip = c.skip;
   for (int from = 0; from < count; from += kMany) {
     const int to = count - from < kMany ? count : from + kMany;
     const cudaError_t e = to - from <= kFew ? launch_batch<kFew>(tensors, from, to, s, c.state_bits == 8, st)
