@@ -148,40 +148,60 @@ __device__ __forceinline__ void load_codes(float (&x)[kEach], const uint8_t* src
 // number, in steps, is added and the rest cut off.  On the bits of y that is one integer addition
 // (the exponent follows the mantissa, in fp32 as in the code).
 // KEEP: a value above 0 keeps a code above 0.
+// Logic, shifts, compares and selections run at half the rate of multiplications and additions and bound this
+// kernel, so what can be a multiplication is one.
 template <int SHIFT, bool KEEP>
 __device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEach], const uint32_t (&hash)[kEach], int left,
                                              bool vector) {
-  uint32_t top = 0u;                   // magnitudes compare as their bits do
+  float largest = 0.f, odd = 0.f;      // (odd becomes NaN by a value that is not finite)
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  const bool bad = top >= 0x7F800000u; // (the whole warp) values that are not finite: NaN codes, and they count for no scale
-  if (bad) {
-    top = 0u;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-      top = max(top, b < 0x7F800000u ? b : 0u);
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
+  for (int i = 0; i < kEach; ++i) {
+    largest = fmaxf(largest, fabsf(x[i]));
+    odd = fmaf(x[i], 0.f, odd);
   }
-  const float largest = __uint_as_float(top);
+  const bool bad = __any_sync(0xFFFFFFFFu, odd != 0.f);
+  if (bad) {                           // (the whole warp) such values count for no scale
+    largest = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) largest = fmaxf(largest, isfinite(x[i]) ? fabsf(x[i]) : 0.f);
+  }
+  largest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest)));   // magnitudes compare as their bits do
   const bool some = largest >= 0x1p-100f;
   const float scale = some ? __fmul_rn(largest, static_cast<float>(1.0 / 448)) : 0.f;
   const float up = some ? __fmul_rn(__frcp_rn(largest), 448.f) : 0.f;
-  uint32_t c[2] = {0u, 0u};
+  uint32_t code[kEach];
+  float least = 448.f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const float y = fabsf(__fmul_rn(x[i], up));
-    const uint32_t u = SHIFT == 0 ? hash[i] << 4 & 0xFFFF0u : hash[i] >> 12 & 0xFFFF0u;
-    uint32_t code = min((__float_as_uint(y) + u - 0x3C000000u) >> 20, 126u);          // (960 << 20: the exponents' offset)
-    // floor(512 y + random number): the sum rounded down at 2^23 has it in its last bits
-    const float z = fmaf(y, 512.f, __uint_as_float(0x3F800000u | u << 3) - 1.f);
-    if (y < 0x1p-6f) code = __float_as_uint(__fadd_rd(z, 0x1p23f)) & 15u;
-    if (KEEP && x[i] > 0.f) code = max(code, 1u);
-    if (bad && (__float_as_uint(x[i]) & 0x7FFFFFFFu) >= 0x7F800000u) code = 0x7Fu;
-    if (!KEEP) code |= __float_as_uint(x[i]) >> 24 & 0x80u;
-    c[i / 4] |= code << 8 * (i % 4);
+    least = fminf(least, y);
+    const uint32_t u = SHIFT == 0 ? hash[i] & 0xFFFFu : hash[i] >> 16;
+    code[i] = static_cast<uint32_t>(min(static_cast<int>((__float_as_uint(y) + u * 16u) >> 20) - 960, 126));   // 960: the exponents' offset
+  }
+  if (__any_sync(0xFFFFFFFFu, least < 0x1p-6f)) {      // below: the codes' own subnormals
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const float y = fabsf(__fmul_rn(x[i], up));
+      const uint32_t u = SHIFT == 0 ? hash[i] & 0xFFFFu : hash[i] >> 16;
+      // floor(512 y + random number): the sum rounded down at 2^23 has it in its last bits
+      const float z = fmaf(y, 512.f, __uint_as_float(u * 128u + 0x3F800000u) - 1.f);
+      if (y < 0x1p-6f) code[i] = __float_as_uint(__fadd_rd(z, 0x1p23f)) - 0x4B000000u;
+      if (KEEP && x[i] > 0.f) code[i] = max(code[i], 1u);
+    }
+  }
+  if (bad)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (!isfinite(x[i])) code[i] = 0x7Fu;
+  uint32_t c[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    c[k] = code[4 * k] + code[4 * k + 1] * 0x100u + code[4 * k + 2] * 0x10000u + code[4 * k + 3] * 0x1000000u;
+    if (!KEEP) {                       // the signs: the values' top bytes side by side
+      const uint32_t a = __byte_perm(__float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]), 0x0073);
+      const uint32_t b = __byte_perm(__float_as_uint(x[4 * k + 2]), __float_as_uint(x[4 * k + 3]), 0x0073);
+      c[k] |= __byte_perm(a, b, 0x5410) & 0x80808080u;
+    }
   }
   if (vector && left >= kEach) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
@@ -253,7 +273,9 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     for (int i = 0; i < kEach; ++i) {
       float root;
       asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i]));
-      p[i] = fmaf(p[i], r.keep, -r.rate * __fdividef(m[i], fmaf(root, r.inv, s.eps)));
+      float part;                      // 1 / (sqrt(v) / sqrt(1 - b2^t) + eps): never so small or large that ftz counts
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(part) : "f"(fmaf(root, r.inv, s.eps)));
+      p[i] = fmaf(p[i], r.keep, -r.rate * (m[i] * part));
     }
     if (t.master) store8(t.master + at, p, left, vector);
     if (flags & kParamBf16) store8(static_cast<__nv_bfloat16*>(t.p) + at, p, left, vector);
