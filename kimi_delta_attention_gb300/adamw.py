@@ -1,0 +1,90 @@
+"""AdamW over the library's step for many tensors: a torch optimizer with states in 32 or 8 bits.
+
+    opt = AdamW(layer.parameters(), lr=3e-3, state_bits=8)
+    loss.backward(); opt.step(); opt.zero_grad()
+
+All of a group's parameters go into one call (a launch for some 440 tensors).  States are fp32, or
+e4m3 codes with a scale for 256 values, whatever the parameters' type; ``masters=True`` keeps an
+fp32 copy of each bf16 parameter, of which the parameter is the rounded value.  With
+``capturable=True`` the step number and the learning rate lie on the device, so that a captured
+step goes on counting, and a schedule writes ``group["lr"].fill_(...)``.
+"""
+from __future__ import annotations
+
+import torch
+
+from ._adamw import BLOCK, E4M3, kda_adamw_step
+from ._lib import KdaError
+
+
+class AdamW(torch.optim.Optimizer):
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, masters=False, seed=0,
+                 capturable=False):
+        if state_bits not in (8, 32):
+            raise KdaError(1, "state_bits must be 8 or 32")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                                      masters=masters, seed=seed, capturable=capturable))
+
+    def _init_state(self, p, group):
+        st = self.state[p]
+        st["step"] = 0
+        for name in ("exp_avg", "exp_avg_sq"):
+            if group["state_bits"] == 32:
+                st[name] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+            else:
+                st[name] = torch.zeros(p.numel(), dtype=torch.uint8, device=p.device).view(E4M3)
+                st[name + "_scale"] = torch.zeros(-(-p.numel() // BLOCK), dtype=torch.float32, device=p.device)
+        if group["masters"] and p.dtype != torch.float32:
+            st["master"] = p.detach().float()
+
+    def _device_words(self, group, device):
+        """The step number and the learning rate of a capturable group, on the device."""
+        if "step_device" not in group:
+            group["step_device"] = torch.zeros(1, dtype=torch.int32, device=device)
+        if not torch.is_tensor(group["lr"]):
+            group["lr"] = torch.full((1,), group["lr"], dtype=torch.float32, device=device)
+        return group["step_device"], group["lr"]
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None, skip=None):
+        """One step of every parameter that has a gradient; grad_scale and skip as kda_adamw_step's (a skipped
+        step counts all the same)."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            batches = {}                    # parameters that have taken the same number of steps, device by device
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.is_sparse:
+                    raise KdaError(1, "sparse gradients are not supported")
+                if not self.state[p]:
+                    self._init_state(p, group)
+                self.state[p]["step"] += 1
+                batches.setdefault((p.device, 0 if group["capturable"] else self.state[p]["step"]), []).append(p)
+            for (device, step), params in batches.items():
+                lr = group["lr"]
+                if group["capturable"]:
+                    step, lr = self._device_words(group, device)
+                    step.add_(1)
+                states = [self.state[p] for p in params]
+                column = lambda name: [s[name] for s in states]
+                small = group["state_bits"] == 8
+                kda_adamw_step(params, [p.grad.contiguous() for p in params], column("exp_avg"), column("exp_avg_sq"), step, lr=lr,
+                               betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
+                               masters=[s.get("master") for s in states] if group["masters"] else None,
+                               exp_avg_scales=column("exp_avg_scale") if small else None,
+                               exp_avg_sq_scales=column("exp_avg_sq_scale") if small else None, seed=group["seed"],
+                               grad_scale=grad_scale, skip=skip)
+        return loss
+
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        # (torch casts floating states to their parameter's type: put them back as they were)
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        for i, p in zip(ids, (p for g in self.param_groups for p in g["params"])):
+            for name, value in state_dict["state"].get(i, {}).items():
+                if torch.is_tensor(value):
+                    self.state[p][name] = value.detach().clone().to(p.device)

@@ -6,8 +6,8 @@ Layer norm, projections (torch matrix products), the delta rule and the output p
 with a residual.  ``layer_norm`` and ``gated_delta_rule`` are autograd functions over the
 library's forward and backward (first derivatives; a second one raises); ``GatedDeltaLayer``
 trains with them, and serves with the chunked forward for a prompt and the recurrent step for
-each token after it, the requests' states in one pool.  The command trains a layer for some
-steps on synthetic data, then serves the same tokens and compares.
+each token after it, the requests' states in one pool.  The command trains a layer with the library's
+AdamW for some steps on synthetic data, then serves the same tokens and compares.
 """
 from __future__ import annotations
 
@@ -19,6 +19,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _gdr
 from ._lib import KdaError, _check, kda_read_device_status
+from .adamw import AdamW
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -122,7 +123,7 @@ def demo(width=512, heads=4, value_heads=8, B=4, T=200, steps=20, seed=0):
     layer = GatedDeltaLayer(width, heads, value_heads)
     x = torch.randn(B, T, width, device="cuda").bfloat16()
     target = torch.roll(x, 3, dims=1)                    # recall the token three back
-    opt = torch.optim.Adam(layer.parameters(), lr=3e-3)
+    opt = AdamW(layer.parameters(), lr=3e-3, weight_decay=0.0)
     losses = []
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     for _ in range(steps):
