@@ -13,6 +13,7 @@
 // Statistics and sums are fp32; deviations are taken around a value of the group's own (no
 // cancellation of large squares), and every sum is taken in a fixed order.
 #include "layer_ops.cuh"
+#include "pairs.cuh"
 
 namespace kda {
 namespace gn {
@@ -25,6 +26,27 @@ __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __ex
 __device__ __forceinline__ float silu_slope(float z) {
   const float s = __fdividef(1.f, 1.f + __expf(-z));
   return s * fmaf(z, 1.f - s, 1.f);
+}
+
+// Two values at once: 1 / (1 + e^-z), with e^-z as 2^(-z log2 e) and the hardware's reciprocal (0 for an infinite one)
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+  float a, b;
+  unpack2f(mul2(z, pack2f(-1.44269504f, -1.44269504f)), a, b);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(a));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(b));
+  unpack2f(add2(pack2f(a, b), pack2f(1.f, 1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(b));
+  return pack2f(a, b);
+}
+__device__ __forceinline__ uint64_t slope2(uint64_t z) {
+  const uint64_t s = sigmoid2(z), one = pack2f(1.f, 1.f);
+  return mul2(s, fma2(z, fma2(s, pack2f(-1.f, -1.f), one), one));
+}
+__device__ __forceinline__ float both(uint64_t v) {
+  float a, b;
+  unpack2f(v, a, b);
+  return a + b;
 }
 
 // VEC values: a load of 16 bytes, or one element
@@ -114,6 +136,24 @@ __host__ __device__ inline RowLayout row_layout(int groups, int tpu) {
   return groups >= all ? RowLayout{all, 1} : RowLayout{groups, all / groups};
 }
 
+template <int NV, int VEC, int TPU>
+__device__ __forceinline__ void load_pairs(uint64_t (&v)[NV][VEC / 2], const float* p, int c0, float def) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float f[VEC];
+    load_param<VEC>(f, p, c0 + TPU * VEC * j, def);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v[j][i] = pack2f(f[2 * i], f[2 * i + 1]);
+  }
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ void to_pairs(const Raw<IO, VEC>& raw, uint64_t (&v)[VEC / 2]) {
+  float f[VEC];
+  raw.to(f);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) v[i] = pack2f(f[2 * i], f[2 * i + 1]);
+}
+
 template <typename IO, int VEC, int NV, int TPU, bool ACT>
 __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
   constexpr int W = TPU * NV * VEC;              // values of a group
@@ -122,12 +162,10 @@ __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
   const int grp = blockIdx.x * lay.groups_each + unit % lay.groups_each;
   const bool on = unit < lay.groups_each * lay.rows_each && grp < p.groups;
   const int c0 = grp * W + t * VEC;
-  float w[NV][VEC], b[NV][VEC];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    load_param<VEC>(w[j], on ? p.w : nullptr, c0 + TPU * VEC * j, 1.f);
-    load_param<VEC>(b[j], on ? p.b : nullptr, c0 + TPU * VEC * j, 0.f);
-  }
+  constexpr int NP = VEC / 2;                    // arithmetic on pairs of values
+  uint64_t w[NV][NP], b[NV][NP];
+  load_pairs<NV, VEC, TPU>(w, on ? p.w : nullptr, c0, 1.f);
+  load_pairs<NV, VEC, TPU>(b, on ? p.b : nullptr, c0, 0.f);
   const long step = static_cast<long>(gridDim.y) * lay.rows_each;
   long row = static_cast<long>(blockIdx.y) * lay.rows_each + unit / lay.groups_each;
   Raw<IO, VEC> next[NV];
@@ -142,28 +180,30 @@ __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
   fetch(row);
   // (a warp's lanes go on together: its groups may be of two rows)
   for (; __any_sync(0xFFFFFFFFu, on && row < p.N); row += step) {
-    float v[NV][VEC], s = 0.f;
+    uint64_t v[NV][NP], s2 = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      next[j].to(v[j]);
+      to_pairs<IO, VEC>(next[j], v[j]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s += v[j][e];
+      for (int i = 0; i < NP; ++i) s2 = add2(s2, v[j][i]);
     }
     fetch(row + step);
+    float s = both(s2);
 #pragma unroll
     for (int m = TPU / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
     const float mu = s * (1.f / W);
-    s = 0.f;
+    s2 = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        v[j][e] -= mu;
-        s = fmaf(v[j][e], v[j][e], s);
+      for (int i = 0; i < NP; ++i) {
+        v[j][i] = add2(v[j][i], pack2f(-mu, -mu));
+        s2 = fma2(v[j][i], v[j][i], s2);
       }
+    s = both(s2);
 #pragma unroll
     for (int m = TPU / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-    const float r = 1.f / sqrtf(fmaf(s, 1.f / W, p.eps));
+    const float r = rsqrtf(fmaf(s, 1.f / W, p.eps));
     if (!on || row >= p.N) continue;
     if (t == 0) {
       if (p.mean) p.mean[row * p.groups + grp] = mu;
@@ -172,12 +212,14 @@ __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
     IO* y = static_cast<IO*>(p.out) + row * p.C + c0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      float out[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float z = fmaf(v[j][e] * r, w[j][e], b[j][e]);
-        v[j][e] = ACT ? silu(z) : z;
+      for (int i = 0; i < NP; ++i) {
+        uint64_t z = fma2(mul2(v[j][i], pack2f(r, r)), w[j][i], b[j][i]);
+        if (ACT) z = mul2(z, sigmoid2(z));
+        unpack2f(z, out[2 * i], out[2 * i + 1]);
       }
-      Raw<IO, VEC>::store(y + TPU * VEC * j, v[j]);
+      Raw<IO, VEC>::store(y + TPU * VEC * j, out);
     }
   }
 }
@@ -193,14 +235,14 @@ __global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_rows_bwd_kerne
   const int grp = blockIdx.x * lay.groups_each + unit % lay.groups_each;
   const bool on = unit < lay.groups_each * lay.rows_each && grp < p.groups;
   const int c0 = grp * W + t * VEC;
-  float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+  constexpr int NP = VEC / 2;                    // arithmetic on pairs of values
+  uint64_t w[NV][NP], b[NV][NP], dw[NV][NP], db[NV][NP];
+  load_pairs<NV, VEC, TPU>(w, on ? p.w : nullptr, c0, 1.f);
+  load_pairs<NV, VEC, TPU>(b, on ? p.b : nullptr, c0, 0.f);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    load_param<VEC>(w[j], on ? p.w : nullptr, c0 + TPU * VEC * j, 1.f);
-    load_param<VEC>(b[j], on ? p.b : nullptr, c0 + TPU * VEC * j, 0.f);
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
-  }
+    for (int i = 0; i < NP; ++i) dw[j][i] = db[j][i] = 0ull;
   const long step = static_cast<long>(gridDim.y) * lay.rows_each;
   long row = static_cast<long>(blockIdx.y) * lay.rows_each + line;
   Raw<IO, VEC> nx[NV], ny[NV];
@@ -222,44 +264,53 @@ __global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_rows_bwd_kerne
   fetch(row);
   for (; __any_sync(0xFFFFFFFFu, on && row < p.N); row += step) {
     const bool live = on && row < p.N;
-    float xh[NV][VEC], a[NV][VEC], s0 = 0.f, s1 = 0.f;
-    const float mu = nmu, r = nr;
+    uint64_t xh[NV][NP], a[NV][NP], s0 = 0ull, s1 = 0ull;
+    const float mu = nmu, r = live ? nr : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      nx[j].to(xh[j]);
-      ny[j].to(a[j]);
+      to_pairs<IO, VEC>(nx[j], xh[j]);
+      to_pairs<IO, VEC>(ny[j], a[j]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        xh[j][e] = (xh[j][e] - mu) * r;
-        const float dz = dz_of(a[j][e], fmaf(xh[j][e], w[j][e], b[j][e]), ACT);
+      for (int i = 0; i < NP; ++i) {
+        xh[j][i] = mul2(add2(xh[j][i], pack2f(-mu, -mu)), pack2f(r, r));
+        if (ACT) a[j][i] = mul2(a[j][i], slope2(fma2(xh[j][i], w[j][i], b[j][i])));
         if (live) {
-          dw[j][e] = fmaf(dz, xh[j][e], dw[j][e]);
-          db[j][e] += dz;
+          dw[j][i] = fma2(a[j][i], xh[j][i], dw[j][i]);
+          db[j][i] = add2(db[j][i], a[j][i]);
         }
-        a[j][e] = dz * w[j][e];
-        s0 += a[j][e];
-        s1 = fmaf(a[j][e], xh[j][e], s1);
+        a[j][i] = mul2(a[j][i], w[j][i]);
+        s0 = add2(s0, a[j][i]);
+        s1 = fma2(a[j][i], xh[j][i], s1);
       }
     }
     fetch(row + step);
+    float m0 = both(s0), m1 = both(s1);
 #pragma unroll
     for (int m = TPU / 2; m >= 1; m >>= 1) {
-      s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, m);
-      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, m);
+      m0 += __shfl_xor_sync(0xFFFFFFFFu, m0, m);
+      m1 += __shfl_xor_sync(0xFFFFFFFFu, m1, m);
     }
     if (!live || !p.out) continue;
-    const float m0 = s0 * (1.f / W), m1 = s1 * (1.f / W);
+    m0 *= -1.f / W;
+    m1 *= -1.f / W;
     IO* dx = static_cast<IO*>(p.out) + row * p.C + c0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      float out[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) a[j][e] = r * (a[j][e] - m0 - xh[j][e] * m1);
-      Raw<IO, VEC>::store(dx + TPU * VEC * j, a[j]);
+      for (int i = 0; i < NP; ++i)
+        unpack2f(mul2(pack2f(r, r), fma2(xh[j][i], pack2f(m1, m1), add2(a[j][i], pack2f(m0, m0)))), out[2 * i], out[2 * i + 1]);
+      Raw<IO, VEC>::store(dx + TPU * VEC * j, out);
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto write = [&](const float (&v)[NV][VEC], float* part) {
+  auto write = [&](const uint64_t (&sums)[NV][NP], float* part) {
     if (!part) return;
+    float v[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) unpack2f(sums[j][i], v[j][2 * i], v[j][2 * i + 1]);
     float* to = part + static_cast<size_t>(blockIdx.y) * p.C;
     if (lay.rows_each == 1) {
       if (on)
@@ -439,6 +490,7 @@ struct Shares {
   __device__ __forceinline__ int thread(const ChunkLayout& l, int k, int i) const { return i / each * l.across + k * each + i % each; }
 };
 
+constexpr int kBatch = 4;
 template <typename IO, int VEC>
 __global__ void __launch_bounds__(kThreads) group_moments_kernel(const ChunkArgs a) {
   __shared__ Moments sh[kThreads];
@@ -451,25 +503,39 @@ __global__ void __launch_bounds__(kThreads) group_moments_kernel(const ChunkArgs
   for (int v = k.tc; v < l.vectors && k.tr < l.down; v += l.across) {
     if (k.g0 + v / width >= p.groups) break;
     const IO* x = base + (static_cast<size_t>(k.g0) * width + v) * VEC;
-    float shift[VEC], s1[VEC], s2[VEC];          // deviations from the column's first value
-    Raw<IO, VEC> raw;
-    raw.load(x + k.r0 * p.C);
-    raw.to(shift);
+    // deviations from the thread's first value of the column; kBatch rows on their way while as many are summed up
+    float shift[VEC], s1[VEC], s2[VEC];
+    Raw<IO, VEC> raw[2][kBatch];
+    auto fetch = [&](Raw<IO, VEC> (&to)[kBatch], long row) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (row + i * l.down < k.r1) to[i].load(x + (row + i * l.down) * p.C);
+    };
+    long row = k.r0 + k.tr;
+    fetch(raw[0], row);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) s1[e] = s2[e] = 0.f;
+    raw[0][0].to(shift);
     int n = 0;
-#pragma unroll 4
-    for (long row = k.r0 + k.tr; row < k.r1; row += l.down) {
-      float f[VEC];
-      raw.load(x + row * p.C);
-      raw.to(f);
+    for (; row < k.r1;) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        f[e] -= shift[e];
-        s1[e] += f[e];
-        s2[e] = fmaf(f[e], f[e], s2[e]);
+      for (int h = 0; h < 2; ++h) {
+        fetch(raw[h ^ 1], row + kBatch * l.down);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (row + i * l.down < k.r1) {
+            float f[VEC];
+            raw[h][i].to(f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              f[e] -= shift[e];
+              s1[e] += f[e];
+              s2[e] = fmaf(f[e], f[e], s2[e]);
+            }
+            ++n;
+          }
+        row += kBatch * l.down;
       }
-      ++n;
     }
     if (n > 0)
 #pragma unroll
@@ -566,15 +632,29 @@ __global__ void __launch_bounds__(kThreads) group_sums_kernel(const ChunkArgs a)
   }
 }
 
-// The second pass of both directions.
+// The second pass of both directions.  Its first rows are on their way before it waits for the sums.
 template <typename IO, int VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) group_finish_kernel(const ChunkArgs a) {
-  __shared__ float4 stats[kThreads];             // a group's mean, rstd and, backward, the means of a and a xh
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // the sums: this kernel starts under the one that writes them
+  constexpr int U = BWD ? 2 : kBatch;
+  __shared__ float4 stats[kThreads];             // a group's mean, rstd and, backward, minus the means of a and a xh
   const Params& p = a.p;
   const ChunkLayout& l = a.l;
   const Work k(a, gridDim.x - 1 - blockIdx.x);   // what was read last first
   const int width = p.C / p.groups / VEC, lane = threadIdx.x & 31;
+  const size_t base = static_cast<size_t>(k.sample) * p.L * p.C;
+  Raw<IO, VEC> rx[2][U], ry[2][BWD ? U : 1];
+  auto fetch = [&](int h, int c, long row) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (row + i * l.down < k.r1) {
+        const size_t at = base + (row + i * l.down) * p.C + c;
+        rx[h][i].load(static_cast<const IO*>(p.x) + at);
+        if constexpr (BWD) ry[h][i].load(static_cast<const IO*>(p.dy) + at);
+      }
+  };
+  const bool on = k.tr < l.down && k.g0 + k.tc / width < p.groups;
+  if (on) fetch(0, (k.g0 * width + k.tc) * VEC, k.r0 + k.tr);
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the sums: this kernel starts under the one that writes them
   const float n = static_cast<float>(p.L) * (width * VEC);
   for (int g = threadIdx.x >> 5; g < l.groups_each && k.g0 + g < p.groups; g += kThreads / 32) {
     const long st = k.sample * p.groups + k.g0 + g;
@@ -586,7 +666,7 @@ __global__ void __launch_bounds__(kThreads) group_finish_kernel(const ChunkArgs 
         m.y += sums[i].y;
       }
       m = warp_sum(m);
-      if (lane == 0) stats[g] = make_float4(p.mean[st], p.rstd[st], m.x / n, m.y / n);
+      if (lane == 0) stats[g] = make_float4(p.mean[st], p.rstd[st], -m.x / n, -m.y / n);
     } else {
       Moments m{0.f, 0.f, 0.f};
       for (int i = lane; i < l.chunks; i += 32) {
@@ -594,7 +674,7 @@ __global__ void __launch_bounds__(kThreads) group_finish_kernel(const ChunkArgs 
         m = join(m, {static_cast<float>(rows) * (width * VEC), sums[i].x, sums[i].y});
       }
       m = warp_join(m);
-      const float r = 1.f / sqrtf(m.m2 / n + p.eps);
+      const float r = rsqrtf(m.m2 / n + p.eps);
       if (lane == 0) {
         stats[g] = make_float4(m.mean, r, 0.f, 0.f);
         if (k.chunk == 0) {
@@ -605,39 +685,42 @@ __global__ void __launch_bounds__(kThreads) group_finish_kernel(const ChunkArgs 
     }
   }
   __syncthreads();
-  const size_t base = static_cast<size_t>(k.sample) * p.L * p.C;
-  for (int v = k.tc; v < l.vectors && k.tr < l.down; v += l.across) {
+  for (int v = k.tc; on && v < l.vectors; v += l.across) {
     const int g = v / width, c = (k.g0 * width + v) * VEC;
-    if (k.g0 + g >= p.groups) break;
     const float4 st = stats[g];
     float w[VEC], b[VEC];
     load_param<VEC>(w, p.w, c, 1.f);
     load_param<VEC>(b, p.b, c, 0.f);
-#pragma unroll 4
-    for (long row = k.r0 + k.tr; row < k.r1; row += l.down) {
-      const size_t at = base + row * p.C + c;
-      Raw<IO, VEC> raw;
-      float f[VEC];
-      raw.load(static_cast<const IO*>(p.x) + at);
-      raw.to(f);
-      if constexpr (BWD) {
-        float d[VEC];
-        Raw<IO, VEC> ry;
-        ry.load(static_cast<const IO*>(p.dy) + at);
-        ry.to(d);
+    long row = k.r0 + k.tr;
+    if (v != k.tc) fetch(0, c, row);
+    for (; row < k.r1;) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float xh = (f[e] - st.x) * st.y, av = dz_of(d[e], fmaf(xh, w[e], b[e]), p.silu) * w[e];
-          f[e] = st.y * (av - st.z - xh * st.w);
-        }
-      } else {
+      for (int h = 0; h < 2; ++h) {
+        fetch(h ^ 1, c, row + U * l.down);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float z = fmaf((f[e] - st.x) * st.y, w[e], b[e]);
-          f[e] = p.silu ? silu(z) : z;
-        }
+        for (int i = 0; i < U; ++i)
+          if (row + i * l.down < k.r1) {
+            float f[VEC];
+            rx[h][i].to(f);
+            if constexpr (BWD) {
+              float d[VEC];
+              ry[h][i].to(d);
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const float xh = (f[e] - st.x) * st.y, av = dz_of(d[e], fmaf(xh, w[e], b[e]), p.silu) * w[e];
+                f[e] = st.y * fmaf(xh, st.w, av + st.z);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const float z = fmaf((f[e] - st.x) * st.y, w[e], b[e]);
+                f[e] = p.silu ? silu(z) : z;
+              }
+            }
+            Raw<IO, VEC>::store(static_cast<IO*>(p.out) + base + (row + i * l.down) * p.C + c, f);
+          }
+        row += U * l.down;
       }
-      Raw<IO, VEC>::store(static_cast<IO*>(p.out) + at, f);
     }
   }
 }
@@ -698,7 +781,7 @@ long weight_blocks(long rows, int C) {                     // shares of the rows
   return want < most ? want : most < 1 ? 1 : most;
 }
 // whether the chunks' first pass leaves the parts of dw and db too (few against the values themselves)
-bool chunk_parts(const ChunkLayout& l) { return l.rows_each >= 16; }
+bool chunk_parts(const ChunkLayout& l) { return l.rows_each >= 4; }
 
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 size_t chunk_sums_bytes(long N, int groups, const ChunkLayout& l) { return up16(static_cast<size_t>(N) * groups * l.chunks * sizeof(float2)); }
