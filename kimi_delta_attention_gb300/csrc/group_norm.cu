@@ -93,6 +93,28 @@ __device__ __forceinline__ void load_param(float (&v)[VEC], const float* p, int 
   for (int e = 0; e < VEC; ++e) v[e] = p ? p[c + e] : def;
 }
 
+// In pairs (a single value's partner is 0).
+template <int VEC>
+__device__ __forceinline__ void pack(const float (&f)[VEC], uint64_t (&v)[(VEC + 1) / 2]) {
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i) v[i] = pack2f(f[2 * i], VEC > 1 ? f[(2 * i + 1) % VEC] : 0.f);
+}
+template <int VEC>
+__device__ __forceinline__ void unpack(const uint64_t (&v)[(VEC + 1) / 2], float (&f)[VEC]) {
+  float none;
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i) {
+    if constexpr (VEC > 1) unpack2f(v[i], f[2 * i], f[2 * i + 1]);
+    else unpack2f(v[i], f[0], none);
+  }
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ void to_pairs(const Raw<IO, VEC>& raw, uint64_t (&v)[(VEC + 1) / 2]) {
+  float f[VEC];
+  raw.to(f);
+  pack<VEC>(f, v);
+}
+
 __device__ __forceinline__ float dz_of(float dy, float z, bool act) { return act ? dy * silu_slope(z) : dy; }
 
 // The sums of n values with deviations from `shift`: their mean and the sum of squares around it.
@@ -142,16 +164,8 @@ __device__ __forceinline__ void load_pairs(uint64_t (&v)[NV][VEC / 2], const flo
   for (int j = 0; j < NV; ++j) {
     float f[VEC];
     load_param<VEC>(f, p, c0 + TPU * VEC * j, def);
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) v[j][i] = pack2f(f[2 * i], f[2 * i + 1]);
+    pack<VEC>(f, v[j]);
   }
-}
-template <typename IO, int VEC>
-__device__ __forceinline__ void to_pairs(const Raw<IO, VEC>& raw, uint64_t (&v)[VEC / 2]) {
-  float f[VEC];
-  raw.to(f);
-#pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) v[i] = pack2f(f[2 * i], f[2 * i + 1]);
 }
 
 template <typename IO, int VEC, int NV, int TPU, bool ACT>
@@ -183,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
     uint64_t v[NV][NP], s2 = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      to_pairs<IO, VEC>(next[j], v[j]);
+      to_pairs(next[j], v[j]);
 #pragma unroll
       for (int i = 0; i < NP; ++i) s2 = add2(s2, v[j][i]);
     }
@@ -268,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_rows_bwd_kerne
     const float mu = nmu, r = live ? nr : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      to_pairs<IO, VEC>(nx[j], xh[j]);
-      to_pairs<IO, VEC>(ny[j], a[j]);
+      to_pairs(nx[j], xh[j]);
+      to_pairs(ny[j], a[j]);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         xh[j][i] = mul2(add2(xh[j][i], pack2f(-mu, -mu)), pack2f(r, r));
@@ -481,7 +495,48 @@ struct Work {
   __device__ __forceinline__ Work(const ChunkArgs& a, unsigned block)
       : tc(threadIdx.x % a.l.across), tr(threadIdx.x / a.l.across), g0(blockIdx.y * a.l.groups_each), chunk(block % a.l.chunks),
         sample(block / a.l.chunks), r0(chunk * a.l.rows_each), r1(r0 + a.l.rows_each < a.p.L ? r0 + a.l.rows_each : a.p.L) {}
+  // how many of the positions r0 + tr, + down, ... are below r1
+  __device__ __forceinline__ int rows(int down) const { return r0 + tr < r1 ? static_cast<int>((r1 - r0 - tr - 1) / down) + 1 : 0; }
 };
+
+// f(row) for n rows from the loads of `at`, `stride` values from one to the next; U loads at once.
+template <int U, typename IO, int VEC, typename F>
+__device__ __forceinline__ void walk(const IO* at, long stride, int n, F f) {
+  for (; n >= U; n -= U) {
+    Raw<IO, VEC> raw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) raw[i].load(at + i * stride);
+#pragma unroll
+    for (int i = 0; i < U; ++i) f(raw[i]);
+    at += U * stride;
+  }
+  for (; n > 0; --n, at += stride) {
+    Raw<IO, VEC> raw;
+    raw.load(at);
+    f(raw);
+  }
+}
+// The same over x and dy side by side, with the values' offset.
+template <int U, typename IO, int VEC, typename F>
+__device__ __forceinline__ void walk2(const IO* x, const IO* dy, size_t at, long stride, int n, F f) {
+  for (; n >= U; n -= U) {
+    Raw<IO, VEC> rx[U], ry[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      rx[i].load(x + at + i * stride);
+      ry[i].load(dy + at + i * stride);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) f(rx[i], ry[i], at + i * stride);
+    at += U * stride;
+  }
+  for (; n > 0; --n, at += stride) {
+    Raw<IO, VEC> rx, ry;
+    rx.load(x + at);
+    ry.load(dy + at);
+    f(rx, ry, at);
+  }
+}
 
 // The group k of a block over its threads' shares, a warp a group: `of` entries of thread numbers.
 struct Shares {
@@ -490,59 +545,50 @@ struct Shares {
   __device__ __forceinline__ int thread(const ChunkLayout& l, int k, int i) const { return i / each * l.across + k * each + i % each; }
 };
 
-constexpr int kBatch = 4;
 template <typename IO, int VEC>
-__global__ void __launch_bounds__(kThreads) group_moments_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) group_moments_kernel(const ChunkArgs a) {
+  constexpr int NP = (VEC + 1) / 2;
   __shared__ Moments sh[kThreads];
   const Params& p = a.p;
   const ChunkLayout& l = a.l;
   const Work k(a, blockIdx.x);
-  const int width = p.C / p.groups / VEC;
-  const IO* base = static_cast<const IO*>(p.x) + static_cast<size_t>(k.sample) * p.L * p.C;
+  const int width = p.C / p.groups / VEC, n = k.rows(l.down);
+  const IO* base = static_cast<const IO*>(p.x) + (static_cast<size_t>(k.sample) * p.L + k.r0 + k.tr) * p.C;
   Moments mine{0.f, 0.f, 0.f};
-  for (int v = k.tc; v < l.vectors && k.tr < l.down; v += l.across) {
+  for (int v = k.tc; v < l.vectors && k.tr < l.down && n > 0; v += l.across) {
     if (k.g0 + v / width >= p.groups) break;
     const IO* x = base + (static_cast<size_t>(k.g0) * width + v) * VEC;
-    // deviations from the thread's first value of the column; kBatch rows on their way while as many are summed up
-    float shift[VEC], s1[VEC], s2[VEC];
-    Raw<IO, VEC> raw[2][kBatch];
-    auto fetch = [&](Raw<IO, VEC> (&to)[kBatch], long row) {
+    uint64_t shift[NP], s1[NP], s2[NP];          // deviations from the thread's first value of the column
+    {
+      Raw<IO, VEC> first;
+      first.load(x);
+      to_pairs(first, shift);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (row + i * l.down < k.r1) to[i].load(x + (row + i * l.down) * p.C);
-    };
-    long row = k.r0 + k.tr;
-    fetch(raw[0], row);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s1[e] = s2[e] = 0.f;
-    raw[0][0].to(shift);
-    int n = 0;
-    for (; row < k.r1;) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        fetch(raw[h ^ 1], row + kBatch * l.down);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (row + i * l.down < k.r1) {
-            float f[VEC];
-            raw[h][i].to(f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              f[e] -= shift[e];
-              s1[e] += f[e];
-              s2[e] = fmaf(f[e], f[e], s2[e]);
-            }
-            ++n;
-          }
-        row += kBatch * l.down;
+      for (int i = 0; i < NP; ++i) {
+        shift[i] ^= 0x8000000080000000ull;
+        s1[i] = s2[i] = 0ull;
       }
     }
-    if (n > 0)
+    walk<4, IO, VEC>(x, static_cast<long>(l.down) * p.C, n, [&](const Raw<IO, VEC>& raw) {
+      uint64_t f[NP];
+      to_pairs(raw, f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float m = s1[e] / n, m2 = fmaf(-m, s1[e], s2[e]);
-        mine = join(mine, {static_cast<float>(n), shift[e] + m, m2 < 0.f ? 0.f : m2});
+      for (int i = 0; i < NP; ++i) {
+        f[i] = add2(f[i], shift[i]);
+        s1[i] = add2(s1[i], f[i]);
+        s2[i] = fma2(f[i], f[i], s2[i]);
       }
+    });
+    float f0[VEC], f1[VEC], f2[VEC];
+    unpack<VEC>(shift, f0);
+    unpack<VEC>(s1, f1);
+    unpack<VEC>(s2, f2);
+    const float inv = 1.f / n;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float m = f1[e] * inv, m2 = fmaf(-m, f1[e], f2[e]);
+      mine = join(mine, {static_cast<float>(n), m - f0[e], m2 < 0.f ? 0.f : m2});
+    }
   }
   sh[threadIdx.x] = mine;
   __syncthreads();
@@ -557,7 +603,8 @@ __global__ void __launch_bounds__(kThreads) group_moments_kernel(const ChunkArgs
 }
 
 template <typename IO, int VEC>
-__global__ void __launch_bounds__(kThreads) group_sums_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) group_sums_kernel(const ChunkArgs a) {
+  constexpr int NP = (VEC + 1) / 2;
   __shared__ float2 sh[kThreads];
   __shared__ float cols[2][kThreads * VEC];
   const Params& p = a.p;
@@ -574,23 +621,26 @@ __global__ void __launch_bounds__(kThreads) group_sums_kernel(const ChunkArgs a)
     float w[VEC], b[VEC], dw[VEC], db[VEC];
     load_param<VEC>(w, p.w, c, 1.f);
     load_param<VEC>(b, p.b, c, 0.f);
+    uint64_t w2[NP], b2[NP], sw[NP], sb[NP];
+    pack<VEC>(w, w2);
+    pack<VEC>(b, b2);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[e] = db[e] = 0.f;
-#pragma unroll 2
-    for (long row = k.r0 + k.tr; row < k.r1; row += l.down) {
-      Raw<IO, VEC> rx, ry;
-      float f[VEC], d[VEC];
-      rx.load(static_cast<const IO*>(p.x) + base + row * p.C + c);
-      ry.load(static_cast<const IO*>(p.dy) + base + row * p.C + c);
-      rx.to(f);
-      ry.to(d);
+    for (int i = 0; i < NP; ++i) sw[i] = sb[i] = 0ull;
+    walk2<2, IO, VEC>(static_cast<const IO*>(p.x), static_cast<const IO*>(p.dy), base + (k.r0 + k.tr) * p.C + c,
+                      static_cast<long>(l.down) * p.C, k.rows(l.down), [&](const Raw<IO, VEC>& rx, const Raw<IO, VEC>& ry, size_t) {
+      uint64_t xh[NP], dz[NP];
+      to_pairs(rx, xh);
+      to_pairs(ry, dz);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (f[e] - mu) * r, dz = dz_of(d[e], fmaf(xh, w[e], b[e]), p.silu);
-        dw[e] = fmaf(dz, xh, dw[e]);
-        db[e] += dz;
+      for (int i = 0; i < NP; ++i) {
+        xh[i] = mul2(add2(xh[i], pack2f(-mu, -mu)), pack2f(r, r));
+        if (p.silu) dz[i] = mul2(dz[i], slope2(fma2(xh[i], w2[i], b2[i])));
+        sw[i] = fma2(dz[i], xh[i], sw[i]);
+        sb[i] = add2(sb[i], dz[i]);
       }
-    }
+    });
+    unpack<VEC>(sw, dw);
+    unpack<VEC>(sb, db);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {              // the group's sums of a = dz w and a xh are its columns'
       s.x = fmaf(db[e], w[e], s.x);
@@ -632,29 +682,16 @@ __global__ void __launch_bounds__(kThreads) group_sums_kernel(const ChunkArgs a)
   }
 }
 
-// The second pass of both directions.  Its first rows are on their way before it waits for the sums.
+// The second pass of both directions.
 template <typename IO, int VEC, bool BWD>
-__global__ void __launch_bounds__(kThreads) group_finish_kernel(const ChunkArgs a) {
-  constexpr int U = BWD ? 2 : kBatch;
+__global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) group_finish_kernel(const ChunkArgs a) {
+  constexpr int NP = (VEC + 1) / 2;
   __shared__ float4 stats[kThreads];             // a group's mean, rstd and, backward, minus the means of a and a xh
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the sums: this kernel starts under the one that writes them
   const Params& p = a.p;
   const ChunkLayout& l = a.l;
   const Work k(a, gridDim.x - 1 - blockIdx.x);   // what was read last first
   const int width = p.C / p.groups / VEC, lane = threadIdx.x & 31;
-  const size_t base = static_cast<size_t>(k.sample) * p.L * p.C;
-  Raw<IO, VEC> rx[2][U], ry[2][BWD ? U : 1];
-  auto fetch = [&](int h, int c, long row) {
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (row + i * l.down < k.r1) {
-        const size_t at = base + (row + i * l.down) * p.C + c;
-        rx[h][i].load(static_cast<const IO*>(p.x) + at);
-        if constexpr (BWD) ry[h][i].load(static_cast<const IO*>(p.dy) + at);
-      }
-  };
-  const bool on = k.tr < l.down && k.g0 + k.tc / width < p.groups;
-  if (on) fetch(0, (k.g0 * width + k.tc) * VEC, k.r0 + k.tr);
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // the sums: this kernel starts under the one that writes them
   const float n = static_cast<float>(p.L) * (width * VEC);
   for (int g = threadIdx.x >> 5; g < l.groups_each && k.g0 + g < p.groups; g += kThreads / 32) {
     const long st = k.sample * p.groups + k.g0 + g;
@@ -685,42 +722,53 @@ __global__ void __launch_bounds__(kThreads) group_finish_kernel(const ChunkArgs 
     }
   }
   __syncthreads();
-  for (int v = k.tc; on && v < l.vectors; v += l.across) {
+  const long stride = static_cast<long>(l.down) * p.C;
+  const size_t base = (static_cast<size_t>(k.sample) * p.L + k.r0 + k.tr) * p.C;
+  for (int v = k.tc; v < l.vectors && k.tr < l.down; v += l.across) {
     const int g = v / width, c = (k.g0 * width + v) * VEC;
+    if (k.g0 + g >= p.groups) break;
     const float4 st = stats[g];
-    float w[VEC], b[VEC];
-    load_param<VEC>(w, p.w, c, 1.f);
-    load_param<VEC>(b, p.b, c, 0.f);
-    long row = k.r0 + k.tr;
-    if (v != k.tc) fetch(0, c, row);
-    for (; row < k.r1;) {
+    const uint64_t mu = pack2f(-st.x, -st.x), r = pack2f(st.y, st.y);
+    uint64_t w[NP], b[NP];
+    {
+      float f[VEC];
+      load_param<VEC>(f, p.w, c, 1.f);
+      pack<VEC>(f, w);
+      load_param<VEC>(f, p.b, c, 0.f);
+      pack<VEC>(f, b);
+    }
+    IO* out = static_cast<IO*>(p.out);
+    if constexpr (BWD) {
+      walk2<2, IO, VEC>(static_cast<const IO*>(p.x), static_cast<const IO*>(p.dy), base + c, stride, k.rows(l.down),
+                        [&](const Raw<IO, VEC>& rx, const Raw<IO, VEC>& ry, size_t at) {
+        uint64_t xh[NP], d[NP];
+        float f[VEC];
+        to_pairs(rx, xh);
+        to_pairs(ry, d);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        fetch(h ^ 1, c, row + U * l.down);
+        for (int i = 0; i < NP; ++i) {
+          xh[i] = mul2(add2(xh[i], mu), r);
+          if (p.silu) d[i] = mul2(d[i], slope2(fma2(xh[i], w[i], b[i])));
+          d[i] = mul2(r, fma2(xh[i], pack2f(st.w, st.w), fma2(d[i], w[i], pack2f(st.z, st.z))));
+        }
+        unpack<VEC>(d, f);
+        Raw<IO, VEC>::store(out + at, f);
+      });
+    } else {
+      out += base + c;
+      walk<4, IO, VEC>(static_cast<const IO*>(p.x) + base + c, stride, k.rows(l.down), [&](const Raw<IO, VEC>& raw) {
+        uint64_t z[NP];
+        float f[VEC];
+        to_pairs(raw, z);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (row + i * l.down < k.r1) {
-            float f[VEC];
-            rx[h][i].to(f);
-            if constexpr (BWD) {
-              float d[VEC];
-              ry[h][i].to(d);
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                const float xh = (f[e] - st.x) * st.y, av = dz_of(d[e], fmaf(xh, w[e], b[e]), p.silu) * w[e];
-                f[e] = st.y * fmaf(xh, st.w, av + st.z);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                const float z = fmaf((f[e] - st.x) * st.y, w[e], b[e]);
-                f[e] = p.silu ? silu(z) : z;
-              }
-            }
-            Raw<IO, VEC>::store(static_cast<IO*>(p.out) + base + (row + i * l.down) * p.C + c, f);
-          }
-        row += U * l.down;
-      }
+        for (int i = 0; i < NP; ++i) {
+          z[i] = fma2(mul2(add2(z[i], mu), r), w[i], b[i]);
+          if (p.silu) z[i] = mul2(z[i], sigmoid2(z[i]));
+        }
+        unpack<VEC>(z, f);
+        Raw<IO, VEC>::store(out, f);
+        out += stride;
+      });
     }
   }
 }
