@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256, kEach = 8;             // a thread's values: a warp holds a block of 256
 constexpr int kPass = kThreads * kEach;              // values a thread block takes at once
-constexpr int kChunk = 4 * kPass;                    // and in all
+constexpr int kChunk = 8 * kPass;                    // and in all
 constexpr int kBlock = KDA_ADAMW_BLOCK;
 static_assert(kBlock == 32 * kEach, "a warp holds a block of values that share a scale");
 
@@ -77,9 +77,10 @@ __host__ __device__ __forceinline__ uint32_t step_key(uint32_t lo, uint32_t hi, 
   return mix(lo ^ mix(hi ^ mix(static_cast<uint32_t>(step))));
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(float (&x)[kEach], const T* src, int left, bool vector) {
-  if (vector && left >= kEach) {
+// FULL: a whole pass of values at aligned addresses; else `left` of a thread's own, one by one.
+template <bool FULL, typename T>
+__device__ __forceinline__ void load8(float (&x)[kEach], const T* src, int left) {
+  if constexpr (FULL) {
     if constexpr (sizeof(T) == 2) {
       const uint4 u = *reinterpret_cast<const uint4*>(src);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -100,9 +101,9 @@ __device__ __forceinline__ void load8(float (&x)[kEach], const T* src, int left,
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&x)[kEach], int left, bool vector) {
-  if (vector && left >= kEach) {
+template <bool FULL, typename T>
+__device__ __forceinline__ void store8(T* dst, const float (&x)[kEach], int left) {
+  if constexpr (FULL) {
     if constexpr (sizeof(T) == 2) {
       uint32_t w[4];
 #pragma unroll
@@ -123,9 +124,10 @@ __device__ __forceinline__ void store8(T* dst, const float (&x)[kEach], int left
   }
 }
 
-__device__ __forceinline__ void load_codes(float (&x)[kEach], const uint8_t* src, float scale, int left, bool vector) {
+template <bool FULL>
+__device__ __forceinline__ void load_codes(float (&x)[kEach], const uint8_t* src, float scale, int left) {
   uint32_t c[2] = {0u, 0u};
-  if (vector && left >= kEach) {
+  if constexpr (FULL) {
     const uint2 u = *reinterpret_cast<const uint2*>(src);
     c[0] = u.x;
     c[1] = u.y;
@@ -150,9 +152,8 @@ __device__ __forceinline__ void load_codes(float (&x)[kEach], const uint8_t* src
 // KEEP: a value above 0 keeps a code above 0.
 // Logic, shifts, compares and selections run at half the rate of multiplications and additions and bound this
 // kernel, so what can be a multiplication is one.
-template <int SHIFT, bool KEEP>
-__device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEach], const uint32_t (&hash)[kEach], int left,
-                                             bool vector) {
+template <bool FULL, int SHIFT, bool KEEP>
+__device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEach], const uint32_t (&hash)[kEach], int left) {
   float largest = 0.f, odd = 0.f;      // (odd becomes NaN by a value that is not finite)
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -203,7 +204,7 @@ __device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEac
       c[k] |= __byte_perm(a, b, 0x5410) & 0x80808080u;
     }
   }
-  if (vector && left >= kEach) {
+  if constexpr (FULL) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
   } else {
 #pragma unroll
@@ -213,8 +214,85 @@ __device__ __forceinline__ float store_codes(uint8_t* dst, const float (&x)[kEac
   return scale;
 }
 
+// Where a block's values begin: what is alike for all its threads is worked out once, and a thread adds a
+// 32-bit offset.
+struct Chunk {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+};
+
+// A thread's values from the chunk's `at` on; place: the first one's in its tensor.
+template <bool BITS8, bool FULL>
+__device__ __forceinline__ void update(const Scalars& s, const Rates& r, float gs, uint32_t key, const Chunk& t, uint32_t flags,
+                                       uint32_t at, uint32_t place, int left) {
+  const uint32_t blk = at / kBlock;
+  float p[kEach], g[kEach], m[kEach], v[kEach];
+  if (t.master) load8<FULL>(p, t.master + at, left);
+  else if (flags & kParamBf16) load8<FULL>(p, static_cast<const __nv_bfloat16*>(t.p) + at, left);
+  else load8<FULL>(p, static_cast<const float*>(t.p) + at, left);
+  if (flags & kGradBf16) load8<FULL>(g, static_cast<const __nv_bfloat16*>(t.g) + at, left);
+  else load8<FULL>(g, static_cast<const float*>(t.g) + at, left);
+  if constexpr (BITS8) {
+    load_codes<FULL>(m, static_cast<const uint8_t*>(t.m) + at, t.m_scale[blk], left);
+    load_codes<FULL>(v, static_cast<const uint8_t*>(t.v) + at, t.v_scale[blk], left);
+  } else {
+    load8<FULL>(m, static_cast<const float*>(t.m) + at, left);
+    load8<FULL>(v, static_cast<const float*>(t.v) + at, left);
+  }
+  // m and v: each operation rounded by itself, as the formula's (the codes go by their bits)
+  if (s.grad_scale)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) g[i] = __fmul_rn(g[i], gs);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(g[i], s.c1));
+    v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(g[i], g[i]), s.c2));
+  }
+  // part: 1 / (sqrt(v) / sqrt(1 - b2^t) + eps), never so small or large that ftz counts.  A root below 1e-19 is nothing
+  // beside an eps of 1e-15, so it may be flushed to 0 there, which is three instructions less.
+  float part[kEach];
+  if (s.eps >= 1e-15f) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(part[i]) : "f"(v[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) asm("sqrt.approx.f32 %0, %1;" : "=f"(part[i]) : "f"(v[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(part[i]) : "f"(fmaf(part[i], r.inv, s.eps)));
+    p[i] = fmaf(p[i], r.keep, -r.rate * (m[i] * part[i]));
+  }
+  if (t.master) store8<FULL>(t.master + at, p, left);
+  if (flags & kParamBf16) store8<FULL>(static_cast<__nv_bfloat16*>(t.p) + at, p, left);
+  else store8<FULL>(static_cast<float*>(t.p) + at, p, left);
+  if constexpr (BITS8) {
+    uint32_t hash[kEach];
+    const uint32_t h0 = place * kSpread;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      hash[i] = mix((h0 + i * kSpread) ^ key);
+      if (!FULL && i >= left) m[i] = v[i] = 0.f;
+    }
+    const float ms = store_codes<FULL, 0, false>(static_cast<uint8_t*>(t.m) + at, m, hash, left);
+    const float vs = store_codes<FULL, 16, true>(static_cast<uint8_t*>(t.v) + at, v, hash, left);
+    if ((threadIdx.x & 31) == 0) {
+      t.m_scale[blk] = ms;
+      t.v_scale[blk] = vs;
+    }
+  } else {
+    store8<FULL>(static_cast<float*>(t.m) + at, m, left);
+    store8<FULL>(static_cast<float*>(t.v) + at, v, left);
+  }
+}
+
 template <int CAP, bool BITS8>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Batch<CAP> b) {
+__global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const __grid_constant__ Batch<CAP> b) {
   __shared__ Rates sh;
   __shared__ uint32_t sh_key;
   const Scalars& s = b.s;
@@ -239,64 +317,23 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   }
   key = mix(key + static_cast<uint32_t>(b.number + lo) * kSpread);
   const float gs = s.grad_scale ? *s.grad_scale : 1.f;
-  const Entry& t = b.t[lo];
+  const Entry& e = b.t[lo];
   const uint32_t flags = b.flags[lo];
-  const bool vector = flags & kVector;
-  const long from = static_cast<long>(blockIdx.x - b.first[lo]) * kChunk + threadIdx.x * kEach;
+  const long from = static_cast<long>(blockIdx.x - b.first[lo]) * kChunk;
+  const long rest = e.n - from;
+  const uint32_t n = rest < kChunk ? static_cast<uint32_t>(rest) : kChunk;      // values of this block (at least one)
+  auto moved = [&](auto* at, long bytes) { return at ? static_cast<decltype(at)>(static_cast<void*>(const_cast<char*>(static_cast<const char*>(static_cast<const void*>(at))) + bytes)) : at; };
+  const long ps = flags & kParamBf16 ? 2 : 4, gsz = flags & kGradBf16 ? 2 : 4, ss = BITS8 ? 1 : 4;
+  const Chunk t{moved(e.p, from * ps), moved(e.g, from * gsz), moved(e.m, from * ss), moved(e.v, from * ss),
+                moved(e.m_scale, from / kBlock * 4), moved(e.v_scale, from / kBlock * 4), moved(e.master, from * 4)};
+  const uint32_t place = static_cast<uint32_t>(from);
 #pragma unroll 1
-  for (long at = from; at < from + kChunk; at += kPass) {
-    if ((at & ~static_cast<long>(kBlock - 1)) >= t.n) return;          // (whole warps)
-    const long rest = t.n - at;
-    const int left = rest < 0 ? 0 : rest > kEach ? kEach : static_cast<int>(rest);
-    const long blk = at / kBlock;
-    float p[kEach], g[kEach], m[kEach], v[kEach];
-    if (t.master) load8(p, t.master + at, left, vector);
-    else if (flags & kParamBf16) load8(p, static_cast<const __nv_bfloat16*>(t.p) + at, left, vector);
-    else load8(p, static_cast<const float*>(t.p) + at, left, vector);
-    if (flags & kGradBf16) load8(g, static_cast<const __nv_bfloat16*>(t.g) + at, left, vector);
-    else load8(g, static_cast<const float*>(t.g) + at, left, vector);
-    if constexpr (BITS8) {
-      load_codes(m, static_cast<const uint8_t*>(t.m) + at, t.m_scale[blk], left, vector);
-      load_codes(v, static_cast<const uint8_t*>(t.v) + at, t.v_scale[blk], left, vector);
-    } else {
-      load8(m, static_cast<const float*>(t.m) + at, left, vector);
-      load8(v, static_cast<const float*>(t.v) + at, left, vector);
-    }
-    // m and v: each operation rounded by itself, as the formula's (the codes go by their bits)
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const float d = s.grad_scale ? __fmul_rn(g[i], gs) : g[i];
-      m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(d, s.c1));
-      v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(d, d), s.c2));
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      float root;
-      asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i]));
-      float part;                      // 1 / (sqrt(v) / sqrt(1 - b2^t) + eps): never so small or large that ftz counts
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(part) : "f"(fmaf(root, r.inv, s.eps)));
-      p[i] = fmaf(p[i], r.keep, -r.rate * (m[i] * part));
-    }
-    if (t.master) store8(t.master + at, p, left, vector);
-    if (flags & kParamBf16) store8(static_cast<__nv_bfloat16*>(t.p) + at, p, left, vector);
-    else store8(static_cast<float*>(t.p) + at, p, left, vector);
-    if constexpr (BITS8) {
-      uint32_t hash[kEach];
-      const uint32_t h0 = static_cast<uint32_t>(at) * kSpread;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        hash[i] = mix((h0 + i * kSpread) ^ key);
-        if (i >= left) m[i] = v[i] = 0.f;
-      }
-      const float ms = store_codes<0, false>(static_cast<uint8_t*>(t.m) + at, m, hash, left, vector);
-      const float vs = store_codes<16, true>(static_cast<uint8_t*>(t.v) + at, v, hash, left, vector);
-      if ((threadIdx.x & 31) == 0) {
-        t.m_scale[blk] = ms;
-        t.v_scale[blk] = vs;
-      }
-    } else {
-      store8(static_cast<float*>(t.m) + at, m, left, vector);
-      store8(static_cast<float*>(t.v) + at, v, left, vector);
+  for (uint32_t pass = 0; pass < n; pass += kPass) {
+    const uint32_t at = pass + threadIdx.x * kEach;
+    if ((flags & kVector) && pass + kPass <= n) {
+      update<BITS8, true>(s, r, gs, key, t, flags, at, place + at, kEach);
+    } else if ((at & ~static_cast<uint32_t>(kBlock - 1)) < n) {                  // (whole warps)
+      update<BITS8, false>(s, r, gs, key, t, flags, at, place + at, at >= n ? 0 : min(static_cast<int>(n - at), kEach));
     }
   }
 }

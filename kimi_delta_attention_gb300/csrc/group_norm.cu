@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
 // Backward: a thread meets the same columns in every row, so its shares of dw and db stay in registers; the
 // block's rows' shares are added in their order and written as the block's part of [blocks, C].
 template <typename IO, int VEC, int NV, int TPU, bool ACT>
-__global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_rows_bwd_kernel(const Params p, float* pw, float* pb) {
+__global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : NV == 2 ? 2 : 3) group_rows_bwd_kernel(const Params p, float* pw, float* pb) {
   constexpr int W = TPU * NV * VEC;
   extern __shared__ float share[];               // [rows_each][groups_each W] where there are several rows
   const RowLayout lay = row_layout(p.groups, TPU);
@@ -471,8 +471,9 @@ ChunkLayout chunk_layout(long N, long L, int C, int groups, int vec, int sms) {
   l.vectors = l.groups_each * width;
   l.across = l.vectors < kThreads ? l.vectors : kThreads;
   l.down = kThreads / l.across;
-  // about 8 blocks an SM, each with several positions a thread
-  long want = (8l * sms + N * l.blocks - 1) / (N * l.blocks);
+  // 3 blocks an SM, all of which run at once (4 samples of 4096 x 4096 in 2, 3, 4, 6, 8 and 16: 83, 76, 76, 89, 90, 118
+  // us forward, 155, 134, 167, 149, 163, 186 backward), each with several positions a thread
+  long want = (3l * sms + N * l.blocks - 1) / (N * l.blocks);
   const long most = (L + 4l * l.down - 1) / (4l * l.down);
   want = want < 1 ? 1 : want > most ? most : want;
   l.rows_each = (L + want - 1) / want;
@@ -822,7 +823,7 @@ unsigned row_blocks(long N, int C, int groups, int tpu, int per_sm, unsigned& ac
   return static_cast<unsigned>(want < most ? want : most < 65535 ? most : 65535);
 }
 int lanes_of(int vectors) { return vectors < 32 ? vectors : 32; }
-constexpr int kRowsPerSm = 8, kBwdRowsPerSm = 2;
+constexpr int kRowsPerSm = 8, kBwdRowsPerSm = 3;   // blocks (backward 16384 x 4096: 105 us for 2, 94 for 3, 98 for 6)
 
 long weight_blocks(long rows, int C) {                     // shares of the rows for group_weights_kernel
   const long want = 8l * sm_count() / ((C + 31) / 32) + 1, most = (rows + 31) / 32;
