@@ -46,7 +46,8 @@ def kda_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0
     captured steps: step (int32) and lr (fp32) may be device tensors, grad_scale (fp32: multiplies
     the gradients) and skip (fp32: not 0 leaves everything as it is) are device tensors or None."""
     lib = _lib._lib or load_library()
-    params, grads = list(params), list(grads)
+    params, grads, exp_avgs, exp_avg_sqs = list(params), list(grads), list(exp_avgs), list(exp_avg_sqs)
+    masters, exp_avg_scales, exp_avg_sq_scales = (None if x is None else list(x) for x in (masters, exp_avg_scales, exp_avg_sq_scales))
     count = len(params)
     if count == 0:
         return

@@ -125,6 +125,24 @@ def test_final_states_over_initial_ones(lengths):
         assert s2 is state and torch.equal(y, y2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("lengths", [[2000, 3, 0, 900], [64] * 40, [5, 1000] * 9])
+def test_initial_gradients_over_final_ones(lengths):
+    """At the C entry d_initial_state may be the array of d_final_state."""
+    D = 384
+    d = make_glr(lengths, D, BF, F32, seed=21)
+    lib = kda.load_library()
+    y, _ = kda.kda_glr_fwd(d["x"], d["g"], initial_state=d["s0"], cu_seqlens=d["cu"])
+    ref = kda.kda_glr_bwd(d["g"], y, d["dy"], initial_state=d["s0"], cu_seqlens=d["cu"], d_final_state=d["ds"])
+    shape = kda.KdaGlrShape(1, sum(lengths), D, len(lengths), 1, 0)
+    ws = torch.empty(kda.kda_glr_bwd_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        state, dx, dg = d["ds"].clone(), torch.empty_like(y), torch.empty_like(d["g"])
+        code = lib.kda_glr_bwd(shape, *(t.data_ptr() for t in (d["g"], y, d["dy"], d["s0"], d["cu"], state, dx, dg, state, ws)), ws.numel(),
+                               torch.cuda.current_stream().cuda_stream)
+        assert code == 0 and kda.kda_read_device_status(ws) == 0
+        assert all(torch.equal(a, b) for a, b in zip((dx, dg, state), ref))
+
+
 def test_gradients_against_differences():
     d = make_glr([9, 6], 3, F32, F32, seed=13)
     y, _ = kda.kda_glr_fwd(d["x"], d["g"], initial_state=d["s0"], cu_seqlens=d["cu"])
