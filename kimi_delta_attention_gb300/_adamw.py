@@ -6,6 +6,7 @@ at a time; addresses are read at every call and nothing is kept between calls.
 from __future__ import annotations
 
 import itertools
+import operator
 import struct
 
 import torch
@@ -16,16 +17,28 @@ from ._lib import KdaAdamwConfig, KdaError, _increment_version, _lend, load_libr
 
 BLOCK = 256                   # values of a tensor that share a scale (KDA_ADAMW_BLOCK)
 E4M3 = torch.float8_e4m3fn
+_TYPES = set(_IO)
+
+
+# (over whole lists these are a third faster than attribute by attribute)
+_dtype, _device, _contiguous = operator.attrgetter("dtype"), torch.Tensor.get_device, torch.Tensor.is_contiguous
+_numel, _address = torch.Tensor.numel, torch.Tensor.data_ptr
 
 
 def _list(name, tensors, count, dtypes, index, sizes):
-    """A list's addresses after its checks; `sizes`: how many values each has to hold."""
+    """(addresses, types in use) of a list after its checks; `sizes`: how many values each has to hold."""
     if len(tensors) != count:
         raise KdaError(1, f"{name} must have one tensor for each of the {count} params")
-    if any(t.get_device() != index or t.dtype not in dtypes or not t.is_contiguous() for t in tensors) or \
-            [t.numel() for t in tensors] != sizes:
+    found = set(map(_dtype, tensors))
+    if set(map(_device, tensors)) - {index} or not found <= dtypes or not all(map(_contiguous, tensors)) or \
+            list(map(_numel, tensors)) != sizes:
         raise KdaError(1, f"{name} must be contiguous {' or '.join(map(str, dtypes))} tensors of the params' sizes on cuda:{index}")
-    return [t.data_ptr() for t in tensors]
+    return list(map(_address, tensors)), found
+
+
+def _kinds(tensors, found):
+    """The kda_dtype of each tensor."""
+    return itertools.repeat(_IO[next(iter(found))]) if len(found) == 1 else [_IO[t.dtype] for t in tensors]
 
 
 def _word(name, t, dtype, index):
@@ -54,18 +67,20 @@ def kda_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0
     index = params[0].get_device()
     if index < 0:
         raise KdaError(1, "params must be CUDA tensors")
-    sizes = [t.numel() for t in params]
-    columns = [_list("params", params, count, tuple(_IO), index, sizes), _list("grads", grads, count, tuple(_IO), index, sizes)]
+    sizes = list(map(_numel, params))
+    at_params, param_types = _list("params", params, count, _TYPES, index, sizes)
+    at_grads, grad_types = _list("grads", grads, count, _TYPES, index, sizes)
     bits8 = exp_avg_scales is not None or exp_avg_sq_scales is not None
-    of = (E4M3,) if bits8 else (_f32,)
+    of = {E4M3} if bits8 else {_f32}
     written = [*params, *exp_avgs, *exp_avg_sqs]
-    columns += [_list("exp_avgs", exp_avgs, count, of, index, sizes), _list("exp_avg_sqs", exp_avg_sqs, count, of, index, sizes)]
+    columns = [at_params, at_grads, _list("exp_avgs", exp_avgs, count, of, index, sizes)[0],
+               _list("exp_avg_sqs", exp_avg_sqs, count, of, index, sizes)[0]]
     if bits8:
         if exp_avg_scales is None or exp_avg_sq_scales is None:
             raise KdaError(1, "8-bit states need exp_avg_scales and exp_avg_sq_scales")
         blocks = [-(-n // BLOCK) for n in sizes]
-        columns += [_list("exp_avg_scales", exp_avg_scales, count, (_f32,), index, blocks),
-                    _list("exp_avg_sq_scales", exp_avg_sq_scales, count, (_f32,), index, blocks)]
+        columns += [_list("exp_avg_scales", exp_avg_scales, count, {_f32}, index, blocks)[0],
+                    _list("exp_avg_sq_scales", exp_avg_sq_scales, count, {_f32}, index, blocks)[0]]
         written += [*exp_avg_scales, *exp_avg_sq_scales]
     else:
         columns += [itertools.repeat(0)] * 2
@@ -75,10 +90,10 @@ def kda_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0
         have = [t for t in masters if t is not None]
         if len(masters) != count:
             raise KdaError(1, f"masters must have one entry for each of the {count} params")
-        at = iter(_list("masters", have, len(have), (_f32,), index, [n for n, t in zip(sizes, masters) if t is not None]))
+        at = iter(_list("masters", have, len(have), {_f32}, index, [n for n, t in zip(sizes, masters) if t is not None])[0])
         columns.append([0 if t is None else next(at) for t in masters])
         written += have
-    columns += [sizes, [_IO[t.dtype] for t in params], [_IO[t.dtype] for t in grads]]
+    columns += [sizes, _kinds(params, param_types), _kinds(grads, grad_types)]
     table = struct.pack(f"={10 * count}q", *itertools.chain.from_iterable(zip(*columns)))
     step, step_at = _word("step", step, torch.int32, index)
     lr, lr_at = _word("lr", lr, _f32, index)

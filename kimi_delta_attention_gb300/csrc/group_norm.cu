@@ -6,7 +6,8 @@
 // Bound by HBM: 2 passes over the values forward, 3 backward.  Three ways, by the group's shape:
 //   rows   L = 1 and a group of 1 to 128 vectors of 16 bytes, a power of two (heads): the group lies in
 //          the registers of a few neighbouring lanes, is read once, and its sums are shuffles.
-//   warps  other groups of at most 2048 values: a warp each, which reads its group again from L1.
+//   warps  other groups of at most 2048 values: up to 512 in the registers of 1 to 32 lanes, more by a warp each that
+//          reads its group again from L1.
 //   chunks larger groups: blocks sum up chunks of a sample's positions, then blocks finish the sums and
 //          write; the second reading comes from L2 where that holds the samples (it begins with
 //          the chunks that were read last).
@@ -353,6 +354,106 @@ __global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : NV == 2 ? 2 : 3) group_
   };
   write(dw, pw);
   write(db, pb);
+}
+
+// ------------------------------------------------------------------- small --
+// Groups of at most OWN values a lane, LANES neighbouring lanes each: a group is read once and stays in
+// registers.  (A warp for every group, as larger ones have: 5990 rows of 71 groups of 9 in bf16 164 us.)
+// FLAT: L = 1, a group's values lie side by side.
+constexpr int kMostSmall = 512;
+
+template <typename IO, int LANES, int OWN, bool FLAT, bool BWD>
+__global__ void __launch_bounds__(kThreads) group_small_kernel(const Params p) {
+  const long unit = (static_cast<long>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+  const bool on = unit < p.N * p.groups;         // (idle lanes go along: their neighbours' shuffles need them)
+  const int t = threadIdx.x % LANES, width = p.C / p.groups, n = static_cast<int>(p.L) * width;
+  const int grp = on ? static_cast<int>(unit % p.groups) : 0;
+  const size_t base = on ? unit / p.groups * p.L * p.C + static_cast<size_t>(grp) * width : 0;
+  const float* w = p.w ? p.w + grp * width : nullptr;
+  const float* b = p.b ? p.b + grp * width : nullptr;
+  // f(i, offset, channel) for the lane's values i: value t + LANES i of the group lies at position / width
+  auto each = [&](auto f) {
+    if constexpr (FLAT) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i)
+        if (on && t + LANES * i < n) f(i, base + t + LANES * i, t + LANES * i);
+    } else {
+      int c = t % width;
+      size_t at = base + static_cast<size_t>(t / width) * p.C + c;
+      const int dl = LANES / width, dc = LANES % width;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        if (on && t + LANES * i < n) f(i, at, c);
+        at += static_cast<size_t>(dl) * p.C + dc;
+        c += dc;
+        if (c >= width) {
+          c -= width;
+          at += p.C - width;
+        }
+      }
+    }
+  };
+  auto sum = [](float x) {
+#pragma unroll
+    for (int m = LANES / 2; m >= 1; m >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
+    return x;
+  };
+  const IO* x = static_cast<const IO*>(p.x);
+  IO* out = static_cast<IO*>(p.out);
+  float v[OWN];
+#pragma unroll
+  for (int i = 0; i < OWN; ++i) v[i] = 0.f;
+  each([&](int i, size_t at, int) { v[i] = to_f32(x[at]); });
+  const float inv = 1.f / n;
+  if constexpr (!BWD) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) s += v[i];
+    const float mu = sum(s) * inv;
+    s = 0.f;
+    each([&](int i, size_t, int) {
+      v[i] -= mu;
+      s = fmaf(v[i], v[i], s);
+    });
+    const float r = rsqrtf(fmaf(sum(s), inv, p.eps));
+    if (on && t == 0) {
+      if (p.mean) p.mean[unit] = mu;
+      if (p.rstd) p.rstd[unit] = r;
+    }
+    each([&](int i, size_t at, int c) {
+      const float z = fmaf(v[i] * r, w ? w[c] : 1.f, b ? b[c] : 0.f);
+      out[at] = from_f32<IO>(p.silu ? silu(z) : z);
+    });
+  } else {
+    const IO* dy = static_cast<const IO*>(p.dy);
+    const float mu = on ? p.mean[unit] : 0.f, r = on ? p.rstd[unit] : 0.f;
+    float a[OWN], s0 = 0.f, s1 = 0.f;
+    each([&](int i, size_t at, int c) {
+      const float wc = w ? w[c] : 1.f;
+      v[i] = (v[i] - mu) * r;
+      a[i] = dz_of(to_f32(dy[at]), fmaf(v[i], wc, b ? b[c] : 0.f), p.silu) * wc;
+      s0 += a[i];
+      s1 = fmaf(a[i], v[i], s1);
+    });
+    const float m0 = sum(s0) * inv, m1 = sum(s1) * inv;
+    each([&](int i, size_t at, int) { out[at] = from_f32<IO>(r * (a[i] - m0 - v[i] * m1)); });
+  }
+}
+
+template <typename IO, bool FLAT, bool BWD>
+cudaError_t launch_small(const Params& p, cudaStream_t st) {
+  const long n = p.L * (p.C / p.groups), units = p.N * p.groups;
+  auto blocks = [&](int lanes) { return static_cast<unsigned>((units * lanes + kThreads - 1) / kThreads); };
+  if (n <= 8) group_small_kernel<IO, 1, 8, FLAT, BWD><<<blocks(1), kThreads, 0, st>>>(p);
+  else if (n <= 32) group_small_kernel<IO, 4, 8, FLAT, BWD><<<blocks(4), kThreads, 0, st>>>(p);
+  else if (n <= 128) group_small_kernel<IO, 16, 8, FLAT, BWD><<<blocks(16), kThreads, 0, st>>>(p);
+  else if (n <= 256) group_small_kernel<IO, 32, 8, FLAT, BWD><<<blocks(32), kThreads, 0, st>>>(p);
+  else group_small_kernel<IO, 32, 16, FLAT, BWD><<<blocks(32), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+template <typename IO, bool BWD>
+cudaError_t small_way(const Params& p, cudaStream_t st) {
+  return p.L == 1 ? launch_small<IO, true, BWD>(p, st) : launch_small<IO, false, BWD>(p, st);
 }
 
 // ------------------------------------------------------------------- warps --
@@ -913,6 +1014,7 @@ cudaError_t fwd(const Params& p, cudaStream_t st) {
   switch (way(p.L, p.C, p.groups, vec)) {
     case Way::rows: return rows_way<IO, E>(p, false, nullptr, nullptr, parts, st);
     case Way::warps:
+      if (p.L * (p.C / p.groups) <= kMostSmall) return small_way<IO, false>(p, st);
       group_warp_kernel<IO, false><<<static_cast<unsigned>((p.N * p.groups + 7) / 8), kThreads, 0, st>>>(p);
       return cudaGetLastError();
     default: break;
@@ -942,7 +1044,10 @@ cudaError_t bwd(const Params& p, cudaStream_t st) {
     e = rows_way<IO, E>(p, true, pw, pb, parts, st);
     weights = false;
   } else if (p.N > 0 && by == Way::warps) {
-    if (p.out) group_warp_kernel<IO, true><<<static_cast<unsigned>((p.N * p.groups + 7) / 8), kThreads, 0, st>>>(p);
+    if (p.out) {
+      if (p.L * (p.C / p.groups) <= kMostSmall) small_way<IO, true>(p, st);
+      else group_warp_kernel<IO, true><<<static_cast<unsigned>((p.N * p.groups + 7) / 8), kThreads, 0, st>>>(p);
+    }
     e = cudaGetLastError();
   } else if (p.N > 0) {
     ChunkArgs a{p, chunk_layout(p.N, p.L, p.C, p.groups, vec, sm_count()), reinterpret_cast<float2*>(ws), nullptr, nullptr};

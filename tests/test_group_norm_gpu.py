@@ -83,6 +83,15 @@ def test_many_rows(io):
         check(x, dy, groups, w, b, "silu")
 
 
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("L,width", [(1, 2), (1, 7), (1, 9), (4, 2), (2, 4), (1, 33), (3, 11), (5, 13), (1, 127), (1, 129), (43, 3), (8, 32),
+                                     (1, 257), (511, 1), (2, 256), (19, 27), (1, 515), (1, 1030), (683, 3), (1, 2047), (1, 2051)])
+def test_groups_of_few_values(L, width, io):
+    """Around the sizes at which a group takes more lanes, a whole warp, or chunks."""
+    x, dy, w, b = make(37, L, 3 * width, io, "wb", width)
+    check(x, dy, 3, w, b, "silu")
+
+
 def test_one_group_a_row_is_layer_norm():
     x, dy, w, b = make(50, 1, 640, F32, "wb", 1)
     y, mean, rstd = kda.kda_group_norm_fwd(x, 1, w, b, EPS)
