@@ -437,8 +437,8 @@ KDA_API kda_status kda_layer_norm_bwd(int64_t rows, int D, kda_dtype io_dtype, c
  * g is a natural-log decay, at most 0 (-inf included: the state is dropped); a positive g is
  * taken as it is as long as no product of e^g over a sequence overflows.
  * Sequences as above: [B, T] tokens, or packed with cu_seqlens (B = 1, num_seqs >= 1).
- * Pointers need their element's alignment only (16-byte aligned rows of D % 4 = 0 channels run
- * the vector kernels).
+ * Pointers need their element's alignment only (16-byte aligned arrays whose rows are multiples of
+ * 16 bytes come by TMA, others value by value).
  */
 typedef struct {
   int B, T;              /* sequences and tokens of each; packed: 1 and all tokens */
@@ -453,8 +453,8 @@ typedef struct {
  * final_state (NULL: not written) [NS, D] fp32; final_state may be initial_state.  States are
  * fp32 throughout; y is each token's state rounded to io_dtype.
  * workspace: kda_glr_fwd_workspace_size(shape) bytes, uninitialised; its first word is the
- * status (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens; the results of such a call are not
- * meaningful).  A call without sequences leaves it as it was.
+ * status (KDA_ERR_DEVICE_BOUNDS for a malformed cu_seqlens, KDA_ERR_DEVICE_TIMEOUT; the results of
+ * such a call are not meaningful).  A call without sequences leaves it as it was.
  */
 KDA_API size_t kda_glr_fwd_workspace_size(const kda_glr_shape* shape);
 KDA_API kda_status kda_glr_fwd(const kda_glr_shape* shape, const void* x, const void* g, const float* initial_state,

@@ -920,7 +920,7 @@ Way way(long L, int C, int groups, int vec) {
   return L * width <= kWarpValues ? Way::warps : Way::chunks;
 }
 
-unsigned row_blocks(long N, int C, int groups, int tpu, int per_sm, unsigned& across) {
+unsigned row_blocks(long N, int groups, int tpu, int per_sm, unsigned& across) {
   const RowLayout lay = row_layout(groups, tpu);
   across = (groups + lay.groups_each - 1) / lay.groups_each;
   const long want = (N + lay.rows_each - 1) / lay.rows_each, most = (static_cast<long>(per_sm) * sm_count() + across - 1) / across;
@@ -957,7 +957,7 @@ cudaError_t with_launch(F kernel, dim3 grid, int threads, size_t smem, cudaStrea
 template <typename IO, int VEC, int NV, int TPU>
 cudaError_t launch_rows(const Params& p, bool bwd, float* pw, float* pb, unsigned& parts, cudaStream_t st) {
   unsigned across;
-  const unsigned down = row_blocks(p.N, p.C, p.groups, TPU, bwd ? kBwdRowsPerSm : kRowsPerSm, across);
+  const unsigned down = row_blocks(p.N, p.groups, TPU, bwd ? kBwdRowsPerSm : kRowsPerSm, across);
   const dim3 grid(across, down);
   parts = down;
   if (!bwd) {
@@ -1040,7 +1040,7 @@ cudaError_t bwd(const Params& p, cudaStream_t st) {
   bool weights = p.dw || p.db;                   // still to be found by a kernel of their own
   if (p.N > 0 && by == Way::rows) {
     unsigned across;
-    place(ws, row_blocks(p.N, p.C, p.groups, lanes_of(p.C / p.groups / E), kBwdRowsPerSm, across));
+    place(ws, row_blocks(p.N, p.groups, lanes_of(p.C / p.groups / E), kBwdRowsPerSm, across));
     e = rows_way<IO, E>(p, true, pw, pb, parts, st);
     weights = false;
   } else if (p.N > 0 && by == Way::warps) {
@@ -1096,7 +1096,7 @@ size_t bwd_workspace_bytes(long N, long L, int C, int groups) {
     const Way by = way(L, C, groups, vec);
     if (by == Way::rows) {
       unsigned across;
-      n = row_blocks(N, C, groups, lanes_of(C / groups / vec), kBwdRowsPerSm, across) * row;
+      n = row_blocks(N, groups, lanes_of(C / groups / vec), kBwdRowsPerSm, across) * row;
     } else if (by == Way::chunks) {
       const ChunkLayout l = chunk_layout(N, L, C, groups, vec, sm_count());
       n = chunk_sums_bytes(N, groups, l) + (chunk_parts(l) ? static_cast<size_t>(N) * l.chunks * row : weights);
