@@ -11,7 +11,7 @@
 //   chunks larger groups: blocks sum up chunks of a sample's positions, then blocks finish the sums and
 //          write; the second reading comes from L2 where that holds the samples (it begins with
 //          the chunks that were read last).
-// Measured (bf16): 16384 rows of 32 heads of 128 with SiLU 56 us (268 MB, 70 % of the copy rate; instruction
+// Measured (bf16): 16384 rows of 32 heads of 128 with SiLU 55 us (268 MB, 72 % of the copy rate; instruction
 // issue, 19 a value), backward 93 (403 MB, 64 %; latency of the rows' sums at 24 warps an SM, and 7 for the
 // parts' sum); 4 samples of 4096 x 4096 74 (268 MB and a second reading of 134).
 // Statistics and sums are fp32; deviations are taken around a value of the group's own (no
@@ -927,7 +927,9 @@ unsigned row_blocks(long N, int groups, int tpu, int per_sm, unsigned& across) {
   return static_cast<unsigned>(want < most ? want : most < 65535 ? most : 65535);
 }
 int lanes_of(int vectors) { return vectors < 32 ? vectors : 32; }
-constexpr int kRowsPerSm = 8, kBwdRowsPerSm = 3;   // blocks (backward 16384 x 4096: 105 us for 2, 94 for 3, 98 for 6)
+// Blocks an SM, walking over the rows: 16384 x 4096 forward 57.2 us for 4, 58.5 for 8, 61.2 for 16; backward 105 for 2, 94
+// for 3, 98 for 6.
+constexpr int kRowsPerSm = 4, kBwdRowsPerSm = 3;
 
 long weight_blocks(long rows, int C) {                     // shares of the rows for group_weights_kernel
   const long want = 8l * sm_count() / ((C + 31) / 32) + 1, most = (rows + 31) / 32;
