@@ -18,7 +18,7 @@
 // says so); nothing but a fault of the device makes them run out.
 //
 // Measured: 4 x 4096 x 4096 backward 155 us (939 MB, 90 % of the copy rate); 4096 x 4096 forward 34 (134 MB, 58 %;
-// a kernel that only streams the same arrays 26); 46402 packed x 2048 forward with a bf16 gate 172 (570 MB, 49 %).
+// a kernel that only streams the same arrays 26); 46402 packed x 2048 forward with a bf16 gate 168 (570 MB, 50 %).
 // What is short of the copy rate is a step's latency: 20 instructions a value by 8 to 12 warps an SM, two
 // barriers, the fold and the exchange, some 1.7 us a step of two to three CTAs.
 #include <cuda.h>
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
     // Tokens of a sequence's inside need no look at where sequences start and end.  Else, a bit each:
     // the scan starts anew at a token, ends with it, and the token is one of a sequence.
     uint32_t starts = 0, ends = 0, live = 0;
+    int start_seq = 0, end_seq = 0;                          // of the thread's last start and end
     const int t_lo = BWD ? token(R - 1) : token(0), t_hi = BWD ? token(0) : token(R - 1);
     if (pos < total && (token(0) < span.begin || token(0) >= span.end)) locate(span, p, cu, token(0));
     const bool plain = __all_sync(0xFFFFFFFFu, pos + R <= total && t_lo > span.begin && t_hi < span.end - 1);
@@ -284,8 +285,14 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
         if (t < span.begin || t >= span.end) locate(span, p, cu, t);
         if (span.end < 0) continue;
         live |= 1u << r;
-        starts |= (t == (BWD ? span.end - 1 : span.begin) ? 1u : 0u) << r;
-        ends |= (t == (BWD ? span.begin : span.end - 1) ? 1u : 0u) << r;
+        if (t == (BWD ? span.end - 1 : span.begin)) {
+          starts |= 1u << r;
+          start_seq = span.seq;
+        }
+        if (t == (BWD ? span.begin : span.end - 1)) {
+          ends |= 1u << r;
+          end_seq = span.seq;
+        }
       }
     }
 
@@ -310,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
           continue;
         }
         if (starts >> r & 1) {
-          Span s;
-          locate(s, p, cu, token(r));
+          Span s{start_seq, 0, 0};
+          if (starts >> r != 1u) locate(s, p, cu, token(r));
           float h[4];
           load_state<TMA, GAP>(h, p.init, s.seq, c0, D);
           H[0] = from[0] = pack2f(h[0], h[1]);
@@ -398,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
         if (!(live >> r & 1)) continue;
         const size_t row = static_cast<size_t>(token(r)) * D;
         const bool end = ends >> r & 1;
-        Span s{0, -1, -1};
-        if (end || starts >> r & 1) locate(s, p, cu, token(r));
+        Span s{end_seq, 0, 0};
+        if ((end && ends >> r != 1u) || (starts >> r & 1 && starts >> r != 1u)) locate(s, p, cu, token(r));
         if (starts >> r == 1u) {
           c[0] = from[0];
           c[1] = from[1];
