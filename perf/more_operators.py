@@ -351,10 +351,10 @@ def _quantise(x, u, keep):
     scale = torch.where(some, top * (1.0 / 448), 0.0)
     y = a * torch.where(some, 448.0 / top, 0.0)[:, None]
     e = ((y.view(torch.int32) >> 23) - 127).clamp(-6, 8)
-    up = ((130 - e) << 23).view(torch.float32)                                      # 1 / step = 2^(3 - e)
+    up = torch.ldexp(torch.ones_like(y), 3 - e)                                     # 1 / step
     q = ((y * up + u).floor() / up).clamp(max=448.0)
     if keep:
-        q = torch.where((a > 0) & (q == 0), 2.0 ** -9, q)
+        q = torch.where((y > 0) & (q == 0), 2.0 ** -9, q)
     q = torch.where(torch.isfinite(a), q, float("nan"))
     return torch.copysign(q, x).to(torch.float8_e4m3fn), scale
 
