@@ -1081,6 +1081,7 @@ cudaError_t bwd(const Params& p, cudaStream_t st) {
 
 size_t fwd_workspace_bytes(long N, long L, int C, int groups) {
   size_t most = 0;
+  if (N == 0) return 0;                // (no samples: no layout, and nothing to keep)
   for (int vec : {1, 4, 8})            // (the call's types and alignment are not known here)
     if (C / groups % vec == 0 && way(L, C, groups, vec) == Way::chunks) {
       const size_t n = chunk_sums_bytes(N, groups, chunk_layout(N, L, C, groups, vec, sm_count()));
@@ -1090,6 +1091,7 @@ size_t fwd_workspace_bytes(long N, long L, int C, int groups) {
 }
 
 size_t bwd_workspace_bytes(long N, long L, int C, int groups) {
+  if (N == 0) return 0;
   const size_t row = 2 * static_cast<size_t>(C) * sizeof(float), weights = weight_blocks(N * L, C) * row;
   size_t most = 0;
   for (int vec : {1, 4, 8}) {

@@ -205,3 +205,10 @@ def test_no_samples():
     y, mean, rstd = kda.kda_group_norm_fwd(x, 4)
     dx, dw, db = kda.kda_group_norm_bwd(x, x, 4, None, None, mean, rstd)
     assert y.shape == x.shape and mean.shape == (0, 4) and (dw == 0).all() and (db == 0).all()
+
+
+def test_no_samples_of_large_groups():
+    x = torch.empty(0, 4096, 512, device="cuda")
+    y, mean, rstd = kda.kda_group_norm_fwd(x, 4)
+    dx, dw, db = kda.kda_group_norm_bwd(x, x, 4, None, None, mean, rstd)
+    assert y.shape == dx.shape == x.shape and (dw == 0).all() and (db == 0).all()

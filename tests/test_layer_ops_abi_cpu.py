@@ -136,6 +136,15 @@ def test_group_norm_backward_arguments(lib):
     assert norm_bwd(lib, dx=at(0)) == 1 and norm_bwd(lib, dw=at(8)) == 1 and norm_bwd(lib, ws=at(1)) == 1 and norm_bwd(lib, db=at(3)) == 1
 
 
+def test_group_norm_of_no_samples(lib):
+    """Groups of every way of the kernels: nothing to do, and no layout to work out."""
+    for kw in (dict(L=3, C=64), dict(L=4096, C=512), dict(L=1, C=1024), dict(L=1, C=1 << 16), dict(L=77, C=1004)):
+        size = dict(N=0, groups=4, **kw)
+        assert lib.kda_group_norm_fwd_workspace_size(*(size[n] for n in ("N", "L", "C", "groups"))) == 256
+        assert lib.kda_group_norm_bwd_workspace_size(*(size[n] for n in ("N", "L", "C", "groups"))) == 256
+        assert norm(lib, **size) == 0 and norm(lib, x=None, y=None, **size) == 0
+
+
 # ------------------------------------------------------------------- AdamW --
 def tensor(i=0, n=1000, bits=8, param_type=BF, grad_type=BF, **kw):
     base = 10 * i
