@@ -6,8 +6,9 @@
 All of a group's parameters go into one call (a launch for some 440 tensors).  States are fp32, or
 e4m3 codes with a scale for 256 values, whatever the parameters' type; ``masters=True`` keeps an
 fp32 copy of each bf16 parameter, of which the parameter is the rounded value.  With
-``capturable=True`` the step number and the learning rate lie on the device, so that a captured
-step goes on counting, and a schedule writes ``group["lr"].fill_(...)``.
+``capturable=True`` the step numbers and the learning rate lie on the device, so that a captured
+step goes on counting, and a schedule writes ``group["lr"].fill_(...)``.  Either way each parameter
+counts the steps that it took; parameters whose counts differ go in calls of their own.
 """
 from __future__ import annotations
 
@@ -37,13 +38,37 @@ class AdamW(torch.optim.Optimizer):
         if group["masters"] and p.dtype != torch.float32:
             st["master"] = p.detach().float()
 
-    def _device_words(self, group, device):
-        """The step number and the learning rate of a capturable group, on the device."""
-        if "step_device" not in group:
-            group["step_device"] = torch.zeros(1, dtype=torch.int32, device=device)
+    def _device_words(self, group, params):
+        """A capturable group's step numbers on the device: [(word, those of `params` that it counts for)].  Parameters
+        that have taken the same number of steps share a word (the first one is the group's); a parameter
+        without a gradient takes a word of its own along when the others go on."""
+        joining, members, batches = {}, {}, {}
+        for p in params:
+            st = self.state[p]
+            if "step_device" not in st:
+                key = (p.device, st["step"])
+                if key not in joining:
+                    joining[key] = torch.full((1,), st["step"], dtype=torch.int32, device=p.device)
+                    group.setdefault("step_device", joining[key])
+                st["step_device"] = joining[key]
+            batches.setdefault(id(st["step_device"]), (st["step_device"], []))[1].append(p)
+        for p in group["params"]:
+            word = self.state[p].get("step_device") if p in self.state else None
+            if word is not None:
+                members.setdefault(id(word), []).append(p)
+        for word, live in batches.values():
+            if len(members[id(word)]) > len(live):
+                own, live = word.clone(), set(live)
+                for p in members[id(word)]:
+                    if p not in live:
+                        self.state[p]["step_device"] = own
+        return list(batches.values())
+
+    def _device_lr(self, group, device):
+        """The learning rate of a capturable group, on the device."""
         if not torch.is_tensor(group["lr"]):
             group["lr"] = torch.full((1,), group["lr"], dtype=torch.float32, device=device)
-        return group["step_device"], group["lr"]
+        return group["lr"]
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None, skip=None):
@@ -54,21 +79,26 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         for group in self.param_groups:
-            batches = {}                    # parameters that have taken the same number of steps, device by device
-            for p in group["params"]:
-                if p.grad is None:
-                    continue
+            live = [p for p in group["params"] if p.grad is not None]
+            for p in live:
                 if p.grad.is_sparse:
                     raise KdaError(1, "sparse gradients are not supported")
                 if not self.state[p]:
                     self._init_state(p, group)
-                self.state[p]["step"] += 1
-                batches.setdefault((p.device, 0 if group["capturable"] else self.state[p]["step"]), []).append(p)
-            for (device, step), params in batches.items():
+            if group["capturable"]:
+                batches = self._device_words(group, live)
+            else:
+                alike = {}                  # parameters that have taken the same number of steps, device by device
+                for p in live:
+                    alike.setdefault((p.device, self.state[p]["step"] + 1), []).append(p)
+                batches = [(step, params) for (_, step), params in alike.items()]
+            for step, params in batches:
                 lr = group["lr"]
                 if group["capturable"]:
-                    step, lr = self._device_words(group, device)
+                    lr = self._device_lr(group, params[0].device)
                     step.add_(1)
+                for p in params:
+                    self.state[p]["step"] += 1
                 states = [self.state[p] for p in params]
                 column = lambda name: [s[name] for s in states]
                 small = group["state_bits"] == 8

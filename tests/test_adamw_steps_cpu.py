@@ -1,0 +1,78 @@
+"""Which step number the optimizer hands to the library for which parameter (no GPU: the library's step is
+replaced by a recorder)."""
+import random
+
+import pytest
+import torch
+
+from kimi_delta_attention_gb300 import adamw
+from kimi_delta_attention_gb300.adamw import AdamW
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Every call's (params, step number, learning rate)."""
+    got = []
+
+    def record(params, grads, exp_avgs, exp_avg_sqs, step, lr, **kw):
+        got.append((list(params), int(step), float(lr)))
+
+    monkeypatch.setattr(adamw, "kda_adamw_step", record)
+    return got
+
+
+def parameters(n):
+    return [torch.nn.Parameter(torch.zeros(3)) for _ in range(n)]
+
+
+def take(opt, params, which):
+    for i, p in enumerate(params):
+        p.grad = torch.ones_like(p) if i in which else None
+    opt.step()
+
+
+def counts(calls, params):
+    """{parameter's number: the step numbers it was given}; the list is emptied."""
+    out = {i: [] for i in range(len(params))}
+    for some, step, _ in calls:
+        for p in some:
+            out[next(i for i, q in enumerate(params) if q is p)].append(step)
+    calls.clear()
+    return out
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_late_parameter_counts_from_one(calls, capturable):
+    params = parameters(3)
+    opt = AdamW(params, capturable=capturable)
+    for k in range(6):
+        take(opt, params, {0, 2} if k < 4 else {0, 1, 2})
+    assert counts(calls, params) == {0: [1, 2, 3, 4, 5, 6], 1: [1, 2], 2: [1, 2, 3, 4, 5, 6]}
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+@pytest.mark.parametrize("seed", range(5))
+def test_each_parameter_counts_its_own_steps(calls, capturable, seed):
+    rng = random.Random(seed)
+    params = parameters(7)
+    opt = AdamW([dict(params=params[:4]), dict(params=params[4:])], capturable=capturable)
+    want = {i: [] for i in range(7)}
+    for _ in range(12):
+        which = {i for i in range(7) if rng.random() < 0.7}
+        for i in which:
+            want[i].append(len(want[i]) + 1)
+        take(opt, params, which)
+    assert counts(calls, params) == want
+
+
+def test_parameters_that_step_together_share_a_call(calls):
+    """Also after one has missed a step: those that go on keep the group's word, which a captured step reads."""
+    params = parameters(5)
+    opt = AdamW(params, capturable=True)
+    take(opt, params, range(5))
+    word = opt.param_groups[0]["step_device"]
+    take(opt, params, {0, 1, 2})
+    take(opt, params, range(5))
+    assert [len(some) for some, _, _ in calls] == [5, 3, 3, 2]
+    assert word is opt.param_groups[0]["step_device"] and word.item() == 3
+    assert [opt.state[p]["step_device"] is word for p in params] == [True] * 3 + [False] * 2

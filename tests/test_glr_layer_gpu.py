@@ -200,3 +200,52 @@ def test_refusals():
         with pytest.raises(kda.KdaError):
             kda.kda_adamw_step(**a)
     assert (p == 0).all()
+
+
+# -------------------------------------------- optimizer, counts on the device --
+def follow(params, twin, opt, ref, rn, which):
+    """One step of both with the same gradients for the parameters in `which`."""
+    for i, (p, q) in enumerate(zip(params, twin)):
+        g = rn(*p.shape) if i in which else None
+        p.grad, q.grad = g, None if g is None else g.double()
+    opt.step()
+    ref.step()
+
+
+def near(params, twin, steps, lr):
+    for p, q in zip(params, twin):
+        # each step off by some 20 roundings of an update of at most 3 lr and two of p
+        assert (p.double() - q).abs().max() <= steps * (20 * 3 * lr + 2 * q.abs().max().item()) * 2.0 ** -24
+
+
+def test_capturable_parameters_without_gradients_and_late_ones():
+    """As without capturable: each parameter counts its own steps."""
+    params, rn = problem(4)
+    params = [params[0], params[2], torch.nn.Parameter(rn(40))]
+    twin = [p.detach().double().requires_grad_() for p in params]
+    opt, ref = AdamW(params, lr=1e-2, capturable=True), torch.optim.AdamW(twin, lr=1e-2)
+    for k in range(8):
+        follow(params, twin, opt, ref, rn, {0} | ({1} if k >= 3 else set()) | ({2} if k != 4 else set()))
+    near(params, twin, 8, 1e-2)
+
+
+def test_captured_step_of_parameters_with_counts_apart():
+    """Replays count on for a parameter that began later, too."""
+    params, rn = problem(5)
+    params = [params[0], params[2]]
+    twin = [p.detach().double().requires_grad_() for p in params]
+    opt, ref = AdamW(params, lr=1e-2, capturable=True), torch.optim.AdamW(twin, lr=1e-2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for k in range(4):
+            follow(params, twin, opt, ref, rn, {0} if k < 3 else {0, 1})
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    for _ in range(3):
+        graph.replay()
+        ref.step()                              # (the gradients stay as they are)
+    assert [opt.state[p]["step_device"].item() for p in params] == [7, 4]
+    near(params, twin, 7, 1e-2)
