@@ -65,7 +65,7 @@ class AdamW(torch.optim.Optimizer):
         return list(batches.values())
 
     def _device_lr(self, group, device):
-        """The learning rate of a capturable group, on the device."""
+        """The learning rate of a capturable group, on the device of its first parameter that steps."""
         if not torch.is_tensor(group["lr"]):
             group["lr"] = torch.full((1,), group["lr"], dtype=torch.float32, device=device)
         return group["lr"]
@@ -73,7 +73,8 @@ class AdamW(torch.optim.Optimizer):
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None, skip=None):
         """One step of every parameter that has a gradient; grad_scale and skip as kda_adamw_step's (a skipped
-        step counts all the same)."""
+        step counts all the same).  A group's parameters may lie on several devices: words that lie on
+        one of them are copied to the others."""
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -93,21 +94,22 @@ class AdamW(torch.optim.Optimizer):
                     alike.setdefault((p.device, self.state[p]["step"] + 1), []).append(p)
                 batches = [(step, params) for (_, step), params in alike.items()]
             for step, params in batches:
-                lr = group["lr"]
+                device, lr = params[0].device, group["lr"]
                 if group["capturable"]:
-                    lr = self._device_lr(group, params[0].device)
+                    lr = self._device_lr(group, device)
                     step.add_(1)
                 for p in params:
                     self.state[p]["step"] += 1
                 states = [self.state[p] for p in params]
                 column = lambda name: [s[name] for s in states]
+                here = lambda t: t.to(device) if torch.is_tensor(t) and t.device != device else t
                 small = group["state_bits"] == 8
-                kda_adamw_step(params, [p.grad.contiguous() for p in params], column("exp_avg"), column("exp_avg_sq"), step, lr=lr,
+                kda_adamw_step(params, [p.grad.contiguous() for p in params], column("exp_avg"), column("exp_avg_sq"), step, lr=here(lr),
                                betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
                                masters=[s.get("master") for s in states] if group["masters"] else None,
                                exp_avg_scales=column("exp_avg_scale") if small else None,
                                exp_avg_sq_scales=column("exp_avg_sq_scale") if small else None, seed=group["seed"],
-                               grad_scale=grad_scale, skip=skip)
+                               grad_scale=here(grad_scale), skip=here(skip))
         return loss
 
     def load_state_dict(self, state_dict):

@@ -76,3 +76,24 @@ def test_parameters_that_step_together_share_a_call(calls):
     assert [len(some) for some, _, _ in calls] == [5, 3, 3, 2]
     assert word is opt.param_groups[0]["step_device"] and word.item() == 3
     assert [opt.state[p]["step_device"] is word for p in params] == [True] * 3 + [False] * 2
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_group_on_two_devices(monkeypatch, capturable):
+    """Each device's parameters with words of that device, each counted once a step."""
+    got = []
+    monkeypatch.setattr(adamw, "kda_adamw_step", lambda params, g, m, v, step, **kw: got.append((params[0].device, step, kw)))
+    params = [torch.nn.Parameter(torch.zeros(3, device=d)) for d in ("cpu", "meta", "cpu")]
+    opt = AdamW(params, lr=0.5, capturable=capturable)
+    for _ in range(3):
+        for p in params:
+            p.grad = torch.ones_like(p)
+        opt.step(grad_scale=torch.ones(1), skip=torch.zeros(1))
+    assert [d.type for d, _, _ in got] == ["cpu", "meta"] * 3
+    for device, step, kw in got:
+        words = [kw["grad_scale"], kw["skip"]] + ([step, kw["lr"]] if capturable else [])
+        assert all(t.device == device and t.numel() == 1 for t in words)
+    if capturable:
+        assert opt.state[params[0]]["step_device"].item() == 3 and opt.state[params[0]]["step_device"] is opt.state[params[2]]["step_device"]
+        assert got[1][1] is got[3][1] is got[5][1]
+    assert [opt.state[p]["step"] for p in params] == [3, 3, 3]
