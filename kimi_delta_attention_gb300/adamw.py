@@ -114,9 +114,26 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         super().load_state_dict(state_dict)
-        # (torch casts floating states to their parameter's type: put them back as they were)
-        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
-        for i, p in zip(ids, (p for g in self.param_groups for p in g["params"])):
-            for name, value in state_dict["state"].get(i, {}).items():
-                if torch.is_tensor(value):
-                    self.state[p][name] = value.detach().clone().to(p.device)
+        for group, saved in zip(self.param_groups, state_dict["param_groups"]):
+            # (torch casts floating states to their parameter's type: put them back as they were)
+            params = [(p, state_dict["state"][i]) for i, p in zip(saved["params"], group["params"]) if i in state_dict["state"]]
+            for p, state in params:
+                for name, value in state.items():
+                    if torch.is_tensor(value) and name != "step_device":
+                        self.state[p][name] = value.detach().clone().to(p.device)
+            if not params:
+                continue
+            device = params[0][0].device
+            if torch.is_tensor(group["lr"]):
+                group["lr"] = group["lr"].to(device)
+            if not group["capturable"]:
+                continue
+            # counts alike share a word again (a state without one, of an older file, has the group's)
+            counts = {id(t): int(t) for t in [saved.get("step_device")] + [s.get("step_device") for _, s in params] if t is not None}
+            words = {}
+            word = lambda d, n: words.setdefault((d, n), torch.full((1,), n, dtype=torch.int32, device=d))
+            for p, state in params:
+                t = state.get("step_device", saved.get("step_device"))
+                self.state[p]["step_device"] = word(p.device, state["step"] if t is None else counts[id(t)])
+            if saved.get("step_device") is not None:
+                group["step_device"] = word(device, counts[id(saved["step_device"])])

@@ -1,5 +1,6 @@
 """Which step number the optimizer hands to the library for which parameter (no GPU: the library's step is
 replaced by a recorder)."""
+import io
 import random
 
 import pytest
@@ -97,3 +98,41 @@ def test_a_group_on_two_devices(monkeypatch, capturable):
         assert opt.state[params[0]]["step_device"].item() == 3 and opt.state[params[0]]["step_device"] is opt.state[params[2]]["step_device"]
         assert got[1][1] is got[3][1] is got[5][1]
     assert [opt.state[p]["step"] for p in params] == [3, 3, 3]
+
+
+def through_a_file(opt):
+    file = io.BytesIO()
+    torch.save(opt.state_dict(), file)
+    file.seek(0)
+    return torch.load(file, map_location="cpu", weights_only=False)
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_counts_go_on_after_a_file(calls, capturable):
+    params, twin = parameters(5), parameters(5)
+    opt = AdamW([dict(params=params[:4]), dict(params=params[4:], lr=0.25)], lr=0.125, capturable=capturable)
+    for which in (range(3), {0, 1, 4}, range(3)):
+        take(opt, params, which)
+    other = AdamW([dict(params=twin[:4]), dict(params=twin[4:])], capturable=capturable)
+    other.load_state_dict(through_a_file(opt))
+    calls.clear()
+    take(other, twin, range(5))
+    assert [(len(some), step, lr) for some, step, lr in calls] == [(2, 4, 0.125), (1, 3, 0.125), (1, 1, 0.125), (1, 2, 0.25)]
+    if capturable:                              # the group's word is again the one of those that stepped at every step
+        assert other.param_groups[0]["step_device"] is other.state[twin[0]]["step_device"]
+
+
+def test_counts_of_a_file_without_words_by_parameter(calls):
+    """A capturable group saved with its one word (which replays advance, and host counts do not follow)."""
+    params, twin = parameters(3), parameters(3)
+    opt = AdamW(params, capturable=True)
+    take(opt, params, {0, 1})
+    old = through_a_file(opt)
+    old["param_groups"][0]["step_device"].fill_(9)
+    for state in old["state"].values():
+        del state["step_device"]
+    other = AdamW(twin, capturable=True)
+    other.load_state_dict(old)
+    calls.clear()
+    take(other, twin, range(3))
+    assert counts(calls, twin) == {0: [10], 1: [10], 2: [1]}

@@ -249,3 +249,45 @@ def test_captured_step_of_parameters_with_counts_apart():
         ref.step()                              # (the gradients stay as they are)
     assert [opt.state[p]["step_device"].item() for p in params] == [7, 4]
     near(params, twin, 7, 1e-2)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_capturable_state_goes_through_a_file_on_the_host(bits):
+    """Saved, read onto the host and loaded: the next steps are the same, bit for bit, and so is a captured one's."""
+    import io
+
+    params, rn = problem(6)
+    twin = [torch.nn.Parameter(p.detach().clone()) for p in params]
+    kw = dict(lr=1e-2, state_bits=bits, masters=True, seed=5, capturable=True)
+    opt, other = AdamW(params, **kw), AdamW(twin, **kw)
+
+    def take(opt, params, grads):
+        for p, t in zip(params, grads):
+            p.grad = None if t is None else t.clone()
+        opt.step()
+
+    grads = [[rn(*p.shape).to(p.dtype) if k or i else None for i, p in enumerate(params)] for k in range(4)]
+    for g in grads[:3]:
+        take(opt, params, g)
+    opt.param_groups[0]["lr"].fill_(3e-3)
+    file = io.BytesIO()
+    torch.save(opt.state_dict(), file)
+    file.seek(0)
+    other.load_state_dict(torch.load(file, map_location="cpu", weights_only=False))
+    with torch.no_grad():
+        for p, q in zip(params, twin):
+            q.copy_(p)
+    side = torch.cuda.Stream()
+    for o, ps in ((opt, params), (other, twin)):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            take(o, ps, grads[3])
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o.step()
+        graph.replay()
+        torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(params, twin))
+    assert [other.state[p]["step_device"].item() for p in twin] == [4, 5, 5]
+    assert other.param_groups[0]["lr"].item() == opt.param_groups[0]["lr"].item()
