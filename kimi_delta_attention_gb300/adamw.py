@@ -98,18 +98,23 @@ class AdamW(torch.optim.Optimizer):
                 if group["capturable"]:
                     lr = self._device_lr(group, device)
                     step.add_(1)
-                for p in params:
-                    self.state[p]["step"] += 1
                 states = [self.state[p] for p in params]
                 column = lambda name: [s[name] for s in states]
                 here = lambda t: t.to(device) if torch.is_tensor(t) and t.device != device else t
                 small = group["state_bits"] == 8
-                kda_adamw_step(params, [p.grad.contiguous() for p in params], column("exp_avg"), column("exp_avg_sq"), step, lr=here(lr),
-                               betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
-                               masters=[s.get("master") for s in states] if group["masters"] else None,
-                               exp_avg_scales=column("exp_avg_scale") if small else None,
-                               exp_avg_sq_scales=column("exp_avg_sq_scale") if small else None, seed=group["seed"],
-                               grad_scale=here(grad_scale), skip=here(skip))
+                try:
+                    kda_adamw_step(params, [p.grad.contiguous() for p in params], column("exp_avg"), column("exp_avg_sq"), step,
+                                   lr=here(lr), betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
+                                   masters=[s.get("master") for s in states] if group["masters"] else None,
+                                   exp_avg_scales=column("exp_avg_scale") if small else None,
+                                   exp_avg_sq_scales=column("exp_avg_sq_scale") if small else None, seed=group["seed"],
+                                   grad_scale=here(grad_scale), skip=here(skip))
+                except Exception:           # (a call that was refused has not counted)
+                    if group["capturable"]:
+                        step.sub_(1)
+                    raise
+                for st in states:
+                    st["step"] += 1
         return loss
 
     def load_state_dict(self, state_dict):

@@ -136,3 +136,21 @@ def test_counts_of_a_file_without_words_by_parameter(calls):
     calls.clear()
     take(other, twin, range(3))
     assert counts(calls, twin) == {0: [10], 1: [10], 2: [1]}
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_refused_call_counts_nothing(calls, monkeypatch, capturable):
+    params = parameters(2)
+    opt = AdamW(params, capturable=capturable)
+    take(opt, params, {0, 1})
+    with monkeypatch.context() as m:
+        m.setattr(adamw, "kda_adamw_step", refuse)
+        with pytest.raises(adamw.KdaError):
+            take(opt, params, {0, 1})
+    calls.clear()
+    take(opt, params, {0, 1})
+    assert counts(calls, params) == {0: [2], 1: [2]} and opt.state[params[0]]["step"] == 2
+
+
+def refuse(*a, **kw):
+    raise adamw.KdaError(1, "not contiguous")
