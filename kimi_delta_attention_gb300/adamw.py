@@ -8,7 +8,8 @@ e4m3 codes with a scale for 256 values, whatever the parameters' type; ``masters
 fp32 copy of each bf16 parameter, of which the parameter is the rounded value.  With
 ``capturable=True`` the step numbers and the learning rate lie on the device, so that a captured
 step goes on counting, and a schedule writes ``group["lr"].fill_(...)``.  Either way each parameter
-counts the steps that it took; parameters whose counts differ go in calls of their own.
+counts the steps that it took; parameters whose counts differ go in calls of their own.  A step is
+captured after at least one with the same gradients has been taken; others are refused.
 """
 from __future__ import annotations
 
@@ -16,6 +17,16 @@ import torch
 
 from ._adamw import BLOCK, E4M3, kda_adamw_step
 from ._lib import KdaError
+
+
+def _capturing():
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+def _before_capture(what):
+    """Refuses to make what steps share during a capture: every replay would make it anew."""
+    if _capturing():
+        raise KdaError(1, f"a step under capture has no {what} yet: take one step with the same gradients before the capture")
 
 
 class AdamW(torch.optim.Optimizer):
@@ -47,6 +58,7 @@ class AdamW(torch.optim.Optimizer):
             st = self.state[p]
             if "step_device" not in st:
                 key = (p.device, st["step"])
+                _before_capture("step number of a parameter on the device")
                 if key not in joining:
                     joining[key] = torch.full((1,), st["step"], dtype=torch.int32, device=p.device)
                     group.setdefault("step_device", joining[key])
@@ -58,6 +70,7 @@ class AdamW(torch.optim.Optimizer):
                 members.setdefault(id(word), []).append(p)
         for word, live in batches.values():
             if len(members[id(word)]) > len(live):
+                _before_capture("step number apart for the parameters without a gradient")
                 own, live = word.clone(), set(live)
                 for p in members[id(word)]:
                     if p not in live:
@@ -67,6 +80,7 @@ class AdamW(torch.optim.Optimizer):
     def _device_lr(self, group, device):
         """The learning rate of a capturable group, on the device of its first parameter that steps."""
         if not torch.is_tensor(group["lr"]):
+            _before_capture("learning rate on the device")
             group["lr"] = torch.full((1,), group["lr"], dtype=torch.float32, device=device)
         return group["lr"]
 
@@ -80,11 +94,14 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         for group in self.param_groups:
+            if not group["capturable"] and _capturing():
+                raise KdaError(1, "a step under capture needs capturable=True: every replay would take the same step number")
             live = [p for p in group["params"] if p.grad is not None]
             for p in live:
                 if p.grad.is_sparse:
                     raise KdaError(1, "sparse gradients are not supported")
                 if not self.state[p]:
+                    _before_capture("state of a parameter")
                     self._init_state(p, group)
             if group["capturable"]:
                 batches = self._device_words(group, live)

@@ -154,3 +154,30 @@ def test_a_refused_call_counts_nothing(calls, monkeypatch, capturable):
 
 def refuse(*a, **kw):
     raise adamw.KdaError(1, "not contiguous")
+
+
+def test_what_a_capture_would_make_anew_is_refused(calls, monkeypatch):
+    params = parameters(3)
+    opt = AdamW(params, capturable=True)
+    with monkeypatch.context() as m:
+        m.setattr(adamw, "_capturing", lambda: True)
+        with pytest.raises(adamw.KdaError, match="state"):
+            take(opt, params, {0, 1})
+    take(opt, params, {0, 1})
+    calls.clear()
+    with monkeypatch.context() as m:
+        m.setattr(adamw, "_capturing", lambda: True)
+        with pytest.raises(adamw.KdaError, match="state"):              # one joins
+            take(opt, params, {0, 1, 2})
+        with pytest.raises(adamw.KdaError, match="apart"):              # one stays behind
+            take(opt, params, {0})
+        take(opt, params, {0, 1})
+        opt.param_groups[0]["lr"] = 0.5
+        with pytest.raises(adamw.KdaError, match="learning rate"):
+            take(opt, params, {0, 1})
+        plain = AdamW(params)
+        with pytest.raises(adamw.KdaError, match="capturable=True"):
+            take(plain, params, {0})
+    opt.param_groups[0]["lr"] = 0.5
+    take(opt, params, {0, 1, 2})
+    assert [step for _, step, _ in calls] == [2, 3, 1]

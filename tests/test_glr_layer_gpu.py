@@ -291,3 +291,16 @@ def test_capturable_state_goes_through_a_file_on_the_host(bits):
     assert all(torch.equal(p, q) for p, q in zip(params, twin))
     assert [other.state[p]["step_device"].item() for p in twin] == [4, 5, 5]
     assert other.param_groups[0]["lr"].item() == opt.param_groups[0]["lr"].item()
+
+
+def test_captures_that_replays_would_undo_are_refused():
+    p = torch.nn.Parameter(torch.ones(5, device="cuda"))
+    p.grad = torch.ones_like(p)
+    for opt in (AdamW([p], capturable=True), AdamW([p])):
+        with pytest.raises(kda.KdaError):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                opt.step()
+        assert (p == 1).all()
+    opt = AdamW([p], lr=0.5, capturable=True, weight_decay=0.0)
+    opt.step()
+    assert torch.allclose(p, torch.full_like(p, 0.5)) and opt.state[p]["step_device"].item() == 1
