@@ -4,7 +4,9 @@
     loss.backward(); opt.step(); opt.zero_grad()
 
 All of a group's parameters go into one call (a launch for some 440 tensors).  States are fp32, or
-e4m3 codes with a scale for 256 values, whatever the parameters' type; ``masters=True`` keeps an
+e4m3 codes with a scale for 256 values, whatever the parameters' type.  In codes a second moment wanders about
+its fp32 value by some 12 % at beta2 = 0.95, 20 % at 0.99 and 23 % at 0.999, and one below 1 / 229376 of the
+largest of its 256 is held as that: such a value moves less than with fp32 states.  ``masters=True`` keeps an
 fp32 copy of each bf16 parameter, of which the parameter is the rounded value.  With
 ``capturable=True`` the step numbers and the learning rate lie on the device, so that a captured
 step goes on counting, and a schedule writes ``group["lr"].fill_(...)``.  Either way each parameter

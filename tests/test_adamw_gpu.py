@@ -300,3 +300,27 @@ def test_versions_rise():
     before, grads = [d[n][0]._version for n in names], d["grads"][0]._version
     step(d, 1)
     assert all(d[n][0]._version > b for n, b in zip(names, before)) and d["grads"][0]._version == grads
+
+
+def test_how_far_codes_of_v_wander():
+    """Under normal gradients, at the default beta2: without a bias (rounding is fair), and by some 23 % of the fp32 value.
+    In units of v, a step takes it r (1 - beta2) off its code with E|r| = 0.97; rounding adds a variance of that times a code's
+    step (0.068 to 0.125, 0.09 in the mean) and as much again because the block's largest, and with it the grid, moves alike; the
+    average forgets at 2 (1 - beta2): sqrt(2 * 0.97 * 0.09 / 2) = 0.30 at most, 0.21 from the value's own steps alone.  Both are
+    estimates to a quarter.  The mean of 51200 such values: 6 * 0.30 / sqrt(51200) = 0.008."""
+    n, beta2 = 200 * 256, 0.999
+    size = 10.0 ** (-2 * torch.rand(n, device="cuda"))
+    kw = dict(lr=0.0, betas=(0.9, beta2), weight_decay=0.0)
+    p = torch.zeros(n, device="cuda")
+    v = size.square()
+    scale = v.view(-1, 256).amax(1) / 448
+    code = (v / scale.repeat_interleave(256)).to(E4M3)
+    zero = lambda *s: torch.zeros(*s, device="cuda")
+    m, m8, ms = zero(n), zero(n).to(E4M3), zero(200)
+    for t in range(1, 4001):
+        g = [size * torch.randn(n, device="cuda")]
+        kda.kda_adamw_step([p], g, [m], [v], t, **kw)
+        kda.kda_adamw_step([p], g, [m8], [code], t, exp_avg_scales=[ms], exp_avg_sq_scales=[scale], seed=3, **kw)
+    ratio = code.double() * scale.double().repeat_interleave(256) / v.double()
+    assert abs(ratio.mean().item() - 1) <= 0.008
+    assert 0.75 * 0.21 <= ratio.std().item() <= 1.25 * 0.30
