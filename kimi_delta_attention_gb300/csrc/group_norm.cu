@@ -591,6 +591,7 @@ struct ChunkArgs {
   float2* sums;                  // [N][groups][chunks]: mean and squares around it, or the sums of a and a xh
   float* pw;                     // backward: [N chunks][C] parts of dw and db, or null
   float* pb;
+  int first = 0;                 // blocks over the channels in the launches before this one
 };
 
 // What a block of either pass works on.
@@ -598,8 +599,8 @@ struct Work {
   int tc, tr, g0, chunk;         // its thread's place, its first group
   long sample, r0, r1;           // positions [r0, r1)
   __device__ __forceinline__ Work(const ChunkArgs& a, unsigned block)
-      : tc(threadIdx.x % a.l.across), tr(threadIdx.x / a.l.across), g0(blockIdx.y * a.l.groups_each), chunk(block % a.l.chunks),
-        sample(block / a.l.chunks), r0(chunk * a.l.rows_each), r1(r0 + a.l.rows_each < a.p.L ? r0 + a.l.rows_each : a.p.L) {}
+      : tc(threadIdx.x % a.l.across), tr(threadIdx.x / a.l.across), g0((a.first + static_cast<int>(blockIdx.y)) * a.l.groups_each),
+        chunk(block % a.l.chunks), sample(block / a.l.chunks), r0(chunk * a.l.rows_each), r1(r0 + a.l.rows_each < a.p.L ? r0 + a.l.rows_each : a.p.L) {}
   // how many of the positions r0 + tr, + down, ... are below r1
   __device__ __forceinline__ int rows(int down) const { return r0 + tr < r1 ? static_cast<int>((r1 - r0 - tr - 1) / down) + 1 : 0; }
 };
@@ -907,6 +908,8 @@ int sm_count() {
   return n;
 }
 
+constexpr int kMostY = 65535;          // of a grid's second dimension
+
 enum class Way { rows, warps, chunks };
 constexpr long kWarpValues = 2048;     // of a group that one warp takes
 
@@ -924,7 +927,7 @@ unsigned row_blocks(long N, int groups, int tpu, int per_sm, unsigned& across) {
   const RowLayout lay = row_layout(groups, tpu);
   across = (groups + lay.groups_each - 1) / lay.groups_each;
   const long want = (N + lay.rows_each - 1) / lay.rows_each, most = (static_cast<long>(per_sm) * sm_count() + across - 1) / across;
-  return static_cast<unsigned>(want < most ? want : most < 65535 ? most : 65535);
+  return static_cast<unsigned>(want < most ? want : most < kMostY ? most : kMostY);
 }
 int lanes_of(int vectors) { return vectors < 32 ? vectors : 32; }
 // Blocks an SM, walking over the rows: 16384 x 4096 forward 57.2 us for 4, 58.5 for 8, 61.2 for 16; backward 105 for 2, 94
@@ -989,15 +992,18 @@ cudaError_t rows_way(const Params& p, bool bwd, float* pw, float* pb, unsigned& 
 }
 
 template <typename IO, int VEC, bool BWD>
-cudaError_t chunks_way(const ChunkArgs& a, cudaStream_t st) {
+cudaError_t chunks_way(ChunkArgs a, cudaStream_t st) {
   const Params& p = a.p;
-  if (static_cast<uint64_t>(p.N) * a.l.chunks > INT32_MAX || a.l.blocks > 65535) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(p.N * a.l.chunks), a.l.blocks);
-  if constexpr (BWD) group_sums_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(a);
-  else group_moments_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !p.out) return e;
-  return with_launch(group_finish_kernel<IO, VEC, BWD>, grid, kThreads, 0, st, true, a);
+  for (; a.first < a.l.blocks; a.first += kMostY) {
+    // (samples x chunks are no more than samples x positions)
+    const dim3 grid(static_cast<unsigned>(p.N * a.l.chunks), a.l.blocks - a.first < kMostY ? a.l.blocks - a.first : kMostY);
+    if constexpr (BWD) group_sums_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(a);
+    else group_moments_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && p.out) e = with_launch(group_finish_kernel<IO, VEC, BWD>, grid, kThreads, 0, st, true, a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

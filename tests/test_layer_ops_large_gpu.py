@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import kimi_delta_attention_gb300 as kda
-from layer_ops_testutil import glr_bwd_reference, glr_reference, gn_reference, make_glr, within
+from layer_ops_testutil import glr_bwd_reference, glr_reference, gn_bwd_reference, gn_reference, make_glr, within
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -113,3 +113,23 @@ def test_many_groups():
     y, mean, rstd = kda.kda_group_norm_fwd(x, 30000)
     ry, rm, rr = gn_reference(x, 30000, None, None, 1e-5, "none")
     assert ((y.double() - ry).abs() <= 2e-5 * (1 + ry.abs())).all()
+
+
+@pytest.mark.parametrize("io,L,width", [(F32, 16, 129), (BF, 2, 1032)])
+def test_more_large_groups_than_a_grids_second_dimension(io, L, width):
+    """Groups that take a block each, one value at a time and in vectors, forward and backward.  Groups of some
+    2000 values: 1e-5 of the terms as in the group norm tests, and half a step of the type."""
+    groups = 70001
+    C = groups * width
+    x, dy = (torch.randn(1, L, C, device="cuda").to(io) for _ in range(2))
+    w = 1 + 0.2 * torch.randn(C, device="cuda")
+    y, mean, rstd = kda.kda_group_norm_fwd(x, groups, w, None)
+    step = torch.finfo(io).eps / 2
+    ry, rm, rr = gn_reference(x, groups, w, None, 1e-5, "none")
+    assert ((y.double() - ry).abs() <= 2e-5 * (1 + ry.abs()) + step * ry.abs()).all()
+    assert (mean - rm).abs().max() <= 1e-5 and (rstd / rr - 1).abs().max() <= 1e-5
+    del y, ry
+    got = kda.kda_group_norm_bwd(x, dy, groups, w, None, mean, rstd)
+    refs, terms = gn_bwd_reference(x, dy, groups, w, None, mean, rstd, "none")
+    for g, r, t in zip(got, refs, terms):
+        assert ((g.double() - r).abs() <= 1e-5 * t + (step * r.abs() if g.dtype == BF else 0) + 1e-30).all()
