@@ -2,10 +2,10 @@
 // (include/kda.h): host-side validation, workspace sizing and dispatch.
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "../../include/kda.h"
 #include "gdr_common.cuh"
+#include "wait_limit.h"
 
 namespace kda {
 namespace gdr {
@@ -70,17 +70,6 @@ kda_status check_shape(const kda_shape* s, bool packed, Sizes& z) {
   return KDA_OK;
 }
 
-// Limit of the kernels' bounded waits: 2 s, or KDA_WAIT_LIMIT_NS (read at each call).
-unsigned long long wait_limit_ns() {
-  const char* e = std::getenv("KDA_WAIT_LIMIT_NS");
-  if (e) {
-    char* end = nullptr;
-    const unsigned long long v = std::strtoull(e, &end, 10);
-    if (end != e && v > 0) return v;
-  }
-  return 2000000000ull;
-}
-
 // The chunk kernels' part of a workspace: 128-byte aligned, after the status word.
 constexpr size_t kChunkAlign = 128;
 uint8_t* chunk_part(void* workspace) {
@@ -133,7 +122,7 @@ kda_status kda_gdr_fwd(const kda_shape* s, const void* q, const void* k, const v
                            s->H, s->HV, static_cast<int>(z.ns)};
   if (!chunked(s, z) && cudaMemsetAsync(status, 0, sizeof(uint32_t), cs) != cudaSuccess) return KDA_ERR_CUDA;
   const cudaError_t e =
-      chunked(s, z) ? kda::gdr::launch_chunk_fwd(p, chunk_part(workspace), wait_limit_ns(), s->K, s->V, cs)
+      chunked(s, z) ? kda::gdr::launch_chunk_fwd(p, chunk_part(workspace), kda::wait_limit_ns(), s->K, s->V, cs)
                     : kda::gdr::launch_recurrent(p, s->K, s->V, s->io_dtype == KDA_BF16, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -198,7 +187,7 @@ kda_status kda_gdr_bwd(const kda_shape* s, const void* q, const void* k, const v
                            s->H, s->HV, static_cast<int>(z.ns)};
   uint8_t* ws = chunk_part(workspace);
   return kda::gdr::launch_chunk_bwd(p, d_out, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state, ws, reinterpret_cast<float*>(ws + bwd_shares_at(s, z)),
-                                    wait_limit_ns(), s->K, s->V, cs) == cudaSuccess
+                                    kda::wait_limit_ns(), s->K, s->V, cs) == cudaSuccess
              ? KDA_OK
              : KDA_ERR_CUDA;
 }

@@ -14,8 +14,8 @@
 // registers, from what enters them.  Where there are fewer channel tiles than places for CTAs, a
 // cluster takes its step's tiles side by side, and the folding warps send each other their
 // tile's (A, H) into shared memory.  Every fold goes over the same terms in the same order on
-// every call, and the recurrence never leaves the chip.  All waits are bounded (2 s, then the status
-// says so); nothing but a fault of the device makes them run out.
+// every call, and the recurrence never leaves the chip.  All waits are bounded (2 s, or KDA_WAIT_LIMIT_NS, then the
+// status says so; 2 s more for what is under way).
 //
 // Measured: 4 x 4096 x 4096 backward 155 us (939 MB, 90 % of the copy rate); 4096 x 4096 forward 34 (134 MB, 58 %;
 // a kernel that only streams the same arrays 26); 46402 packed x 2048 forward with a bf16 gate 168 (570 MB, 50 %).
@@ -145,7 +145,34 @@ __device__ __forceinline__ void store_remote(float2* mine, uint64_t* bar, uint32
                "f"(v.x), "f"(v.y), "r"(mapa_shared(smem_u32(bar), rank))
                : "memory");
 }
-constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// A wait for what is under way and comes by itself (copies that were issued, a step's maps, which every CTA of a
+// cluster sends).  Longer than the call's limit it is reported, and waited for all the same, so that nothing is
+// left under way when a block ends; false if it has not come kDrainNs later either, which takes a
+// fault of the device.  try_wait may suspend a thread until the phase completes, so a limit below kPollNs is
+// kept by looks that do not; the timer advances in steps of up to kTickNs, so one below that is over at once.
+constexpr unsigned long long kDrainNs = 2000000000ull, kPollNs = 20000ull, kTickNs = 1000ull;
+template <bool CLUSTER>
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, uint32_t* status) {
+  const unsigned long long t0 = globaltimer_ns();
+  bool late = false;
+#pragma unroll 1
+  do {
+    const unsigned long long t = globaltimer_ns() - t0;
+    if (t + kTickNs > limit_ns && !late) {
+      late = true;
+      atomicOr(status, kStatusTimeout);
+    }
+    if (t > kDrainNs && t - kDrainNs > limit_ns) return false;
+  } while (!(limit_ns < kPollNs ? (CLUSTER ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity))
+                                : (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))));
+  return true;
+}
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, uint32_t* status) {
+  if (limit_ns >= kPollNs && (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+  return wait_longer<CLUSTER>(bar, parity, limit_ns, status);
+}
 
 // The sequence around a token: its number and tokens [begin, end); empty where the token is in none.
 struct Span {
@@ -169,6 +196,19 @@ __device__ __forceinline__ void locate(Span& s, const Params& p, const int32_t* 
   s.begin = cu[lo];
   s.end = cu[lo + 1];
   if (t < s.begin || t >= s.end) s.begin = s.end = -1;
+}
+
+// The number of the sequence that holds token t, for threads with several starts or ends.  (A function, as it
+// stands at each of a thread's tokens in both passes: written out, 4096 x 4096 took 35.1 us for 34.3, 46402 packed x 2048 171 for 167.5.)
+__device__ __noinline__ int sequence_of(const int32_t* cu, int num_seqs, int T, int t) {
+  if (cu == nullptr) return t / T;
+  int lo = 0, hi = num_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 constexpr uint64_t kOnes = 0x3F8000003F800000ull;
@@ -233,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
     for (int i = tid; i <= p.num_seqs; i += kThreads) kept[i] = p.cu[i];
     cu = kept;
   }
-  bool lost = false;
+  bool lost = false;                           // a wait has been given up: no more copies, and no exchange
   if (tid == 0) {
     if (blockIdx.x == 0) *p.status = 0u;
     for (int i = 0; i < 2; ++i) {
@@ -254,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
   for (int n = 0; n < steps; ++n) {
     const long pos = tile_at(n) + seg * R;
     auto token = [&](int r) { return static_cast<int>(BWD ? total - 1 - pos - r : pos + r); };
-    if (TMA && !lost && tile_at(n) < total && !mbar_wait(&full[n & 1], n >> 1 & 1, kWaitNs)) lost = true;
+    if (TMA && !lost && tile_at(n) < total && !wait_phase<false>(&full[n & 1], n >> 1 & 1, p.wait_ns, p.status)) lost = true;
     Raw4<IO> x[R], y[BWD ? R : 1];
     Raw4<G> g[R];
 #pragma unroll
@@ -318,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
         }
         if (starts >> r & 1) {
           Span s{start_seq, 0, 0};
-          if (starts >> r != 1u) locate(s, p, cu, token(r));
+          if (starts >> r != 1u) s.seq = sequence_of(cu, p.num_seqs, p.T, token(r));
           float h[4];
           load_state<TMA, GAP>(h, p.init, s.seq, c0, D);
           H[0] = from[0] = pack2f(h[0], h[1]);
@@ -355,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
           for (int q = 0; q < cluster; ++q) store_remote(maps(n, rank) + lane, &arrived[n & 1], q, make_float2(TA, TH));
           if (lane == 0) mbar_arrive_expect_tx_relaxed(&arrived[n & 1], cluster * kChannels * sizeof(float2));
         }
-        if (!lost && !mbar_wait_cluster(&arrived[n & 1], n >> 1 & 1, kWaitNs)) lost = true;
+        if (!lost && !wait_phase<true>(&arrived[n & 1], n >> 1 & 1, p.wait_ns, p.status)) lost = true;
         for (int q = 0; q < cluster; ++q) {
           const float2 m = maps(n, q)[lane];
           if (q == rank) c = carry;
@@ -406,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
         const size_t row = static_cast<size_t>(token(r)) * D;
         const bool end = ends >> r & 1;
         Span s{end_seq, 0, 0};
-        if ((end && ends >> r != 1u) || (starts >> r & 1 && starts >> r != 1u)) locate(s, p, cu, token(r));
+        if ((end && ends >> r != 1u) || (starts >> r & 1 && starts >> r != 1u)) s.seq = sequence_of(cu, p.num_seqs, p.T, token(r));
         if (starts >> r == 1u) {
           c[0] = from[0];
           c[1] = from[1];
@@ -448,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
       }
     }
   }
-  if (lost) atomicOr(p.status, kStatusTimeout);
 
   // sequences without tokens keep their initial value; one block checks cu_seqlens
   if (p.cu) {
@@ -470,9 +509,6 @@ __global__ void __launch_bounds__(kThreads, ctas_each<IO, BWD>()) glr_scan_kerne
       if (bad) atomicOr(p.status, kStatusBounds);
     }
   }
-  if (TMA && lost && tid == 0)                 // (copies under way land before their memory goes)
-    for (int i = 0; i < 2; ++i)
-      for (const unsigned long long t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {}
   if (cluster > 1) {                           // (nobody writes into a CTA that has ended)
     cluster_arrive();
     cluster_wait();

@@ -8,6 +8,7 @@
 
 #include "../../include/kda.h"
 #include "kda_common.cuh"
+#include "wait_limit.h"
 
 namespace kda {
 cudaError_t launch_recurrent_fwd(const FwdParams& p, bool bf16, cudaStream_t stream);
@@ -54,18 +55,6 @@ size_t workspace_needed(const kda_shape* s, bool use_tc) {
   const int ns = s->num_seqs > 0 ? s->num_seqs : s->B;
   if (ns <= 0) return kda::kWorkspaceBytes;
   return kda::kRingOffset + kda::chunk_tc_ring_bytes(ns, s->HV);
-}
-
-// Limit of the kernels' bounded waits for work: 2 s, or KDA_WAIT_LIMIT_NS (a positive
-// integer, read at each call) for tests that make those waits run out.
-unsigned long long wait_limit_ns() {
-  const char* e = std::getenv("KDA_WAIT_LIMIT_NS");
-  if (e) {
-    char* end = nullptr;
-    const unsigned long long v = std::strtoull(e, &end, 10);
-    if (end != e && v > 0) return v;
-  }
-  return 2000000000ull;
 }
 
 // KDA_BACKWARD=recurrent (read at each call) selects the token-recurrence backward.
@@ -126,7 +115,7 @@ kda_status validate(bool use_tc, const kda_shape* s, const void* q, const void* 
   p.q = q; p.k = k; p.v = v; p.g = static_cast<const float*>(g); p.beta = beta; p.s0 = s0; p.cu = cu;
   p.out = out; p.sfin = sfin; p.status = static_cast<uint32_t*>(ws);
   p.ring = ws_bytes > kda::kRingOffset ? static_cast<uint8_t*>(ws) + kda::kRingOffset : nullptr;
-  p.wait_ns = wait_limit_ns();
+  p.wait_ns = kda::wait_limit_ns();
   p.scale = scale; p.T = s->T; p.H = s->H; p.HV = s->HV; p.K = s->K; p.V = s->V;
   p.num_seqs = static_cast<int>(ns);
   c.bf16 = s->io_dtype == KDA_BF16;
@@ -408,7 +397,7 @@ kda_status kda_backward(const kda_shape* s, const void* q, const void* k, const 
   if (!backward_recurrent()) {
     const cudaError_t e = kda::launch_backward_chunk(
         q, k, v, g, beta, initial_state, cu_seqlens, d_out, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state,
-        scratch, status, wait_limit_ns(), scale, s->T, s->H, s->HV, s->K, s->V, static_cast<int>(ns),
+        scratch, status, kda::wait_limit_ns(), scale, s->T, s->H, s->HV, s->K, s->V, static_cast<int>(ns),
         s->io_dtype == KDA_BF16, cs);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
   }

@@ -7,6 +7,7 @@
 
 #include "../../include/kda.h"
 #include "layer_ops.cuh"
+#include "wait_limit.h"
 
 namespace {
 
@@ -67,6 +68,7 @@ kda_status run_glr(const kda_glr_shape* s, const GlrSizes& z, kda::glr::Params p
   if (z.ns == 0) return KDA_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   p.status = static_cast<uint32_t*>(workspace);
+  p.wait_ns = kda::wait_limit_ns();
   p.tokens = static_cast<long>(z.tokens);
   p.T = s->T;
   p.D = s->D;

@@ -22,6 +22,7 @@ struct Params {
   void* dg;             // backward: [tokens, D] gate type
   float* fin;           // forward: final states; backward: d_initial_state; [NS, D] or null
   uint32_t* status;     // device status word (null where nothing is reported)
+  unsigned long long wait_ns;  // limit of a bounded wait for work (drains have their own)
   long tokens;          // in all
   int T, D, num_seqs;   // T: tokens of a sequence (without cu)
 };
