@@ -622,10 +622,13 @@ cudaError_t launch_scan(const Params& p, cudaStream_t st) {
     // 8192 x 8192 (256) 100, 108; 16384 x 4096 backward 190, 161, 184, 191; 65536 x 128 (4) 489, 342, 245, 178,
     // 129, 98 and 61 for 16.
     const long most = sizeof(IO) == 2 && !BWD ? 8 * sms / 3 : 2 * sms;
-    static int room[64][kMaxCluster + 1] = {};     // clusters of a size that run at once, with the most of cu_seqlens
+    // clusters of a size that run at once, by device and by the KB that cu_seqlens takes beside the tiles (fp32
+    // backward: two CTAs an SM in clusters of 16 with 4 KB of it, of 9 with 8 KB)
+    static int room[64][kMostCu / 256 + 1][kMaxCluster + 1] = {};
+    const int kb = static_cast<int>((cu_bytes + 1023) / 1024);
     for (int c = tiles < kMaxCluster ? static_cast<int>(tiles) : kMaxCluster; c > 1; --c) {
       if (cts * c > most) continue;
-      int fit = dev >= 0 && dev < 64 ? room[dev][c] : 0;
+      int fit = dev >= 0 && dev < 64 ? room[dev][kb][c] : 0;
       if (fit == 0) {
         cudaLaunchAttribute shape;
         shape.id = cudaLaunchAttributeClusterDimension;
@@ -634,13 +637,13 @@ cudaError_t launch_scan(const Params& p, cudaStream_t st) {
         cudaLaunchConfig_t q = {};
         q.gridDim = dim3(c);
         q.blockDim = dim3(kThreads);
-        q.dynamicSmemBytes = ring + maps_bytes(c);
+        q.dynamicSmemBytes = ring + maps_bytes(c) + kb * 1024;
         q.attrs = &shape;
         q.numAttrs = 1;
         e = cudaOccupancyMaxActiveClusters(&fit, kernel, &q);
         if (e != cudaSuccess) return e;
         if (fit == 0) fit = -1;
-        if (dev >= 0 && dev < 64) room[dev][c] = fit;
+        if (dev >= 0 && dev < 64) room[dev][kb][c] = fit;
       }
       if (fit >= cts) {
         args.cluster = c;
