@@ -677,7 +677,7 @@ template <typename IO, typename G>
 cudaError_t launch_step_types(const StepParams& p, cudaStream_t st) {
   const bool vec = p.D % 4 == 0 && aligned(p.x, 4 * sizeof(IO)) && aligned(p.y, 4 * sizeof(IO)) && aligned(p.g, 4 * sizeof(G)) &&
                    aligned(p.state, 16);
-  for (int b = 0; b < p.B; b += 65535) {        // (a grid's second dimension)
+  for (long b = 0; b < p.B; b += 65535) {       // (a grid's second dimension)
     StepParams q = p;
     const size_t row = static_cast<size_t>(b) * p.T * p.D;
     q.x = static_cast<const IO*>(p.x) + row;
@@ -685,7 +685,7 @@ cudaError_t launch_step_types(const StepParams& p, cudaStream_t st) {
     q.y = static_cast<IO*>(p.y) + row;
     if (p.slots) q.slots = p.slots + b;
     else q.state = p.state + static_cast<size_t>(b) * p.D;
-    q.B = p.B - b < 65535 ? p.B - b : 65535;
+    q.B = static_cast<int>(p.B - b < 65535 ? p.B - b : 65535);
     const dim3 grid((p.D + 511) / 512, q.B);
     if (vec) glr_step_kernel<IO, G, true><<<grid, 128, 0, st>>>(q);
     else glr_step_kernel<IO, G, false><<<grid, 128, 0, st>>>(q);

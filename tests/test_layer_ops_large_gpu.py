@@ -133,3 +133,17 @@ def test_more_large_groups_than_a_grids_second_dimension(io, L, width):
     refs, terms = gn_bwd_reference(x, dy, groups, w, None, mean, rstd, "none")
     for g, r, t in zip(got, refs, terms):
         assert ((g.double() - r).abs() <= 1e-5 * t + (step * r.abs() if g.dtype == BF else 0) + 1e-30).all()
+
+
+def test_step_of_as_many_sequences_as_an_int_counts():
+    """2^31 - 1 sequences of one channel: the last rows, where the count of the launches passes 31 bits."""
+    B = 2 ** 31 - 1
+    x = torch.full((B, 1, 1), 0.5, dtype=BF, device="cuda")
+    g = torch.full((B, 1, 1), -1.0, dtype=BF, device="cuda")
+    state = torch.full((B, 1), 2.0, device="cuda")
+    x[-70000:, 0, 0] = torch.randn(70000, device="cuda").to(BF)
+    y = kda.kda_glr_step(x, g, state)
+    for rows in (slice(0, 70000), slice(B // 2, B // 2 + 70000), slice(-70000, None)):
+        want = 2.0 * torch.exp(torch.tensor(-1.0, dtype=torch.float64)).item() + x[rows, 0].double()
+        assert ((state[rows].double() - want).abs() <= 1e-6 * (1 + want.abs())).all()
+        assert ((y[rows, 0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-6).all()
