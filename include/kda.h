@@ -442,7 +442,7 @@ KDA_API kda_status kda_layer_norm_bwd(int64_t rows, int D, kda_dtype io_dtype, c
  */
 typedef struct {
   int B, T;              /* sequences and tokens of each; packed: 1 and all tokens */
-  int D;                 /* channels */
+  int D;                 /* channels, at most 2^30 */
   int num_seqs;          /* packed sequences, else 0 */
   kda_dtype io_dtype;    /* x, y and their gradients */
   kda_dtype gate_dtype;  /* g and its gradient */
@@ -490,7 +490,8 @@ KDA_API kda_status kda_glr_step(const kda_glr_shape* shape, const void* x, const
  * token).
  *     xh = (x - mean) rstd,  z = xh weight + bias,  y = act(z);  rstd = 1 / sqrt(var + eps)
  * x, y contiguous, io_dtype; weight and bias [C] fp32 or NULL (ones, zeros); mean and rstd
- * [N, groups] fp32 or NULL (not written); var biased.  Any sizes >= 1 with C % groups = 0;
+ * [N, groups] fp32 or NULL (not written); var biased.  Any sizes >= 1 with C % groups = 0 (N 0 too), N L
+ * and N groups below 2^31 and C at most 2^30;
  * pointers need their element's alignment only.  Outputs must not overlap inputs or each other.
  * workspace: kda_group_norm_fwd_workspace_size bytes (of the current device, as the call's own),
  * uninitialised.

@@ -27,6 +27,8 @@ bool overlaps(const Span& a, const Span& b) {
 bool is_dtype(int64_t d) { return d == KDA_F32 || d == KDA_BF16; }
 size_t size_of(int64_t d) { return d == KDA_BF16 ? 2 : 4; }
 
+constexpr int kMostChannels = 1 << 30;  // channels, and steps past the last one, are counted in 32 bits on the device
+
 // ------------------------------------------------------------ linear recurrence --
 struct GlrSizes {
   size_t ns, tokens, io, gate, state;  // sequences, tokens, bytes
@@ -38,7 +40,7 @@ kda_status check_glr(const kda_glr_shape* s, bool packed, GlrSizes& z) {
   if (packed ? (s->B != 1 || s->num_seqs < 1) : s->num_seqs != 0) return KDA_ERR_INVALID_ARG;
   z.ns = packed ? static_cast<size_t>(s->num_seqs) : static_cast<size_t>(s->B);
   z.tokens = static_cast<size_t>(s->B) * s->T;
-  if (z.tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;  // tokens are counted in 32 bits on the device
+  if (z.tokens > INT32_MAX || s->D > kMostChannels) return KDA_ERR_UNSUPPORTED;  // tokens are counted in 32 bits on the device
   z.io = z.tokens * s->D * size_of(s->io_dtype);
   z.gate = z.tokens * s->D * size_of(s->gate_dtype);
   z.state = z.ns * s->D * 4;
@@ -80,7 +82,7 @@ kda_status run_glr(const kda_glr_shape* s, const GlrSizes& z, kda::glr::Params p
 kda_status check_gn(int64_t N, int64_t L, int C, int groups) {
   if (N < 0 || L < 1 || C < 1 || groups < 1 || C % groups != 0) return KDA_ERR_INVALID_ARG;
   // rows (samples x positions) are counted in 32 bits on the device
-  if (N > INT32_MAX || L > INT32_MAX || N * L > INT32_MAX || N * groups > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (N > INT32_MAX || L > INT32_MAX || N * L > INT32_MAX || N * groups > INT32_MAX || C > kMostChannels) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 

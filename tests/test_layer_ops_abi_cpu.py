@@ -136,6 +136,15 @@ def test_group_norm_backward_arguments(lib):
     assert norm_bwd(lib, dx=at(0)) == 1 and norm_bwd(lib, dw=at(8)) == 1 and norm_bwd(lib, ws=at(1)) == 1 and norm_bwd(lib, db=at(3)) == 1
 
 
+def test_more_channels_than_32_bits_count_on_the_device(lib):
+    for D in ((1 << 30) + 1, (1 << 31) - 8):
+        for entry in (fwd, bwd, step):
+            assert entry(lib, S(B=1, T=1, D=D)) == 2
+        for entry in (norm, norm_bwd):
+            assert entry(lib, ws_bytes=1 << 20, N=1, L=1, C=D, groups=1) == 2
+            assert entry(lib, ws_bytes=1 << 20, N=1, L=3000, C=D, groups=D) == 2
+
+
 def test_group_norm_of_no_samples(lib):
     """Groups of every way of the kernels: nothing to do, and no layout to work out."""
     for kw in (dict(L=3, C=64), dict(L=4096, C=512), dict(L=1, C=1024), dict(L=1, C=1 << 16), dict(L=77, C=1004)):
