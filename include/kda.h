@@ -550,7 +550,7 @@ typedef struct {           /* addresses of device arrays, each with its element'
 } kda_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps, weight_decay;
+  double lr, beta1, beta2, eps, weight_decay;   /* at least 0 and finite in fp32; eps 0, or at least 2^-126; betas below 1 */
   int64_t step;                /* 1, 2, ... (up to 2^31 - 1) */
   uint64_t seed;               /* of the rounding of 8-bit states */
   int state_bits;              /* 8 or 32 */

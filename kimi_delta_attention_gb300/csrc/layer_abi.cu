@@ -1,6 +1,7 @@
 // layer_abi.cu -- C ABI of the gated linear recurrence, of group norm and of the AdamW step
 // (include/kda.h): host-side validation, workspace sizing and dispatch.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -239,8 +240,9 @@ kda_status kda_adamw_step(const kda_adamw_tensor* tensors, int count, const kda_
   if (count < 0 || count > (1 << 20) || (count > 0 && !tensors) || !c) return KDA_ERR_INVALID_ARG;
   if (c->state_bits != 8 && c->state_bits != 32) return KDA_ERR_INVALID_ARG;
   const bool packed = c->state_bits == 8;
-  auto good = [](double v) { return v >= 0 && std::isfinite(v); };
-  if (!good(c->lr) || !good(c->eps) || !good(c->weight_decay) || !(c->beta1 >= 0 && c->beta1 < 1) ||
+  auto good = [](double v) { return v >= 0 && std::isfinite(static_cast<float>(v)); };   // (the step is one in fp32)
+  // an eps that fp32 holds as a subnormal, or not at all, would be nothing beside a v of 0, and m = 0 over it NaN
+  if (!good(c->lr) || !good(c->eps) || !good(c->weight_decay) || (c->eps > 0 && c->eps < FLT_MIN) || !(c->beta1 >= 0 && c->beta1 < 1) ||
       !(c->beta2 >= 0 && c->beta2 < 1))
     return KDA_ERR_INVALID_ARG;
   if (!c->step_device && (c->step < 1 || c->step > INT32_MAX)) return KDA_ERR_INVALID_ARG;

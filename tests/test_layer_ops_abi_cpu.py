@@ -184,6 +184,13 @@ def test_adamw_settings(lib):
     assert adamw(lib, [tensor(n=0, m=0, v=0)]) == 0                   # nothing in it: no address needed
 
 
+def test_adamw_settings_that_fp32_does_not_hold(lib):
+    for kw in (dict(lr=1e39), dict(weight_decay=1e39), dict(eps=1e39), dict(eps=1e-38), dict(eps=1e-50), dict(eps=5e-324)):
+        assert adamw(lib, [tensor()], **kw) == 1, kw
+    t = tensor(n=0, m=0, v=0)
+    assert adamw(lib, [t], eps=0.0) == 0 and adamw(lib, [t], eps=2.0 ** -126) == 0
+
+
 def test_adamw_tensors(lib):
     for n in ("param", "grad", "m", "v", "ms", "vs"):
         assert adamw(lib, [tensor(**{n: 0})]) == 1, n
