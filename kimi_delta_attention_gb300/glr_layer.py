@@ -96,7 +96,8 @@ class GatedRecurrentLayer(nn.Module):
     def _project(self, x):
         u, r = (layer_norm(x, self.norm_weight, self.norm_bias) @ self.w_in).split(self.channels, dim=-1)
         g = -torch.nn.functional.softplus(r.float() + self.gate_bias) / 8
-        return (torch.sqrt(-torch.expm1(2 * g)) * u.float()).to(x.dtype), g
+        # (a gate below -103 rounds to g = 0, where the root's slope is infinite: its argument stays a normal number)
+        return (torch.sqrt((-torch.expm1(2 * g)).clamp_min(2.0 ** -126)) * u.float()).to(x.dtype), g
 
     def _finish(self, x, y):
         o = group_norm(y.reshape(-1, self.channels), self.heads, self.head_weight, self.head_bias, activation="silu")

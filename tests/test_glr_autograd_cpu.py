@@ -72,3 +72,20 @@ def test_group_norm(kernels):
     grad, = torch.autograd.grad((glr_layer.group_norm(x, 2, w, b) * x).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         grad.square().sum().backward()
+
+
+@pytest.mark.parametrize("bias", [-20.0, -103.0, -104.0, -200.0, 50.0])
+def test_closed_gates_have_finite_gradients(monkeypatch, bias):
+    """A gate so far closed that its g rounds to 0 (or so far open that e^2g does) passes gradients on, not NaN."""
+    monkeypatch.setattr(glr_layer, "layer_norm", lambda x, w, b: x)
+    layer = glr_layer.GatedRecurrentLayer(8, 1, head_dim=16, device="cpu")
+    with torch.no_grad():
+        layer.w_in.normal_()
+        layer.w_in[:, 16:] *= 0.01
+        layer.gate_bias[:8] = bias
+    x = torch.randn(2, 3, 8).bfloat16().requires_grad_()
+    u, g = layer._project(x)
+    (u.float().sum() + g.sum()).backward()
+    assert torch.isfinite(u).all() and torch.isfinite(g).all()
+    for t in (x, layer.w_in, layer.gate_bias):
+        assert torch.isfinite(t.grad).all()
