@@ -490,9 +490,9 @@ KDA_API kda_status kda_glr_step(const kda_glr_shape* shape, const void* x, const
  * token).
  *     xh = (x - mean) rstd,  z = xh weight + bias,  y = act(z);  rstd = 1 / sqrt(var + eps)
  * x, y contiguous, io_dtype; weight and bias [C] fp32 or NULL (ones, zeros); mean and rstd
- * [N, groups] fp32 or NULL (not written); var biased.  Any sizes >= 1 with C % groups = 0 (N 0 too), N L
- * and N groups below 2^31 and C at most 2^30;
- * pointers need their element's alignment only.  Outputs must not overlap inputs or each other.
+ * [N, groups] fp32 or NULL (not written); var biased.  Any sizes >= 1 with C % groups = 0 (N may be 0),
+ * N L and N groups below 2^31 and C at most 2^30; pointers need their element's alignment only.
+ * Outputs must not overlap inputs or each other.
  * workspace: kda_group_norm_fwd_workspace_size bytes (of the current device, as the call's own),
  * uninitialised.
  */
@@ -505,7 +505,8 @@ KDA_API kda_status kda_group_norm_fwd(int64_t N, int64_t L, int C, int groups, k
 /*
  * Its gradients, from the forward's x, mean and rstd: dx [N, L, C] io_dtype, dweight and dbias
  * [C] fp32 (each may be NULL, not all three).  Every sum is taken in a fixed order (the same
- * bits on every call); workspace: kda_group_norm_bwd_workspace_size, as the forward's.
+ * bits on every call); workspace: kda_group_norm_bwd_workspace_size, as the forward's (many short
+ * samples of groups above 2048 values take the most: up to 8 C bytes for every 4 positions).
  */
 KDA_API size_t kda_group_norm_bwd_workspace_size(int64_t N, int64_t L, int C, int groups);
 KDA_API kda_status kda_group_norm_bwd(int64_t N, int64_t L, int C, int groups, kda_dtype io_dtype, kda_activation act,
@@ -562,7 +563,7 @@ typedef struct {
 } kda_adamw_config;
 
 /*
- * `tensors` is an array of the host, read before the call returns.  What a call writes must not
+ * `tensors` is an array of the host, read before the call returns (count at most 2^20, n 2^40).  What a call writes must not
  * overlap anything else that it reads or writes.  No workspace.
  */
 KDA_API kda_status kda_adamw_step(const kda_adamw_tensor* tensors, int count, const kda_adamw_config* config,

@@ -59,7 +59,8 @@ struct Raw4<float> {
 };
 
 // e^x of two values, x <= 88: 2^(x log2 e) with the product's rounding error put back to first order
-// (without it a strong decay loses |x| 2^-24 of itself).  Below -104 it is 0, as for -inf; NaN stays.
+// (without it a strong decay loses |x| 2^-24 of itself).  Below some -87.3, where e^x is no normal number any
+// more, it is 0, as for -inf (expf, in the step, keeps the subnormals: 1e-38 of a state at most); NaN stays.
 // Half the instructions of two calls of expf, and with them a fifth of the kernel's.
 __device__ __forceinline__ uint64_t exp_pair(uint64_t x) {
   constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.925963e-8f, kLn2 = 0.693147181f;

@@ -11,9 +11,10 @@
 //   chunks larger groups: blocks sum up chunks of a sample's positions, then blocks finish the sums and
 //          write; the second reading comes from L2 where that holds the samples (it begins with
 //          the chunks that were read last).
-// Measured (bf16): 16384 rows of 32 heads of 128 with SiLU 55 us (268 MB, 72 % of the copy rate; instruction
-// issue, 19 a value), backward 93 (403 MB, 64 %; latency of the rows' sums at 24 warps an SM, and 7 for the
-// parts' sum); 4 samples of 4096 x 4096 74 (268 MB and a second reading of 134).
+// Measured (bf16): 16384 rows of 32 heads of 128 with SiLU 55 us (268 MB, 73 % of the copy rate; loads are what its
+// warps wait for most, and 19 instructions a value use 62 % of the issue slots), backward 93 (403 MB, 64 %;
+// latency of the rows' sums at 24 warps an SM, and 7 for the parts' sum); 4 samples of 4096 x 4096 74 (268 MB and a
+// second reading of 134), backward 134.
 // Statistics and sums are fp32; deviations are taken around a value of the group's own (no
 // cancellation of large squares), and every sum is taken in a fixed order.
 #include "layer_ops.cuh"
@@ -172,6 +173,7 @@ __device__ __forceinline__ void load_pairs(uint64_t (&v)[NV][VEC / 2], const flo
   }
 }
 
+// Values go two at a time (16384 x 4096 62.7 -> 56 us).
 template <typename IO, int VEC, int NV, int TPU, bool ACT>
 __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
   constexpr int W = TPU * NV * VEC;              // values of a group
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) group_rows_kernel(const Params p) {
   }
 }
 
-// Values go two at a time (62.7 -> 56 us).  Backward: a thread meets the same columns in every row, so its shares of dw and db stay in registers; the
+// Backward: a thread meets the same columns in every row, so its shares of dw and db stay in registers; the
 // block's rows' shares are added in their order and written as the block's part of [blocks, C].
 template <typename IO, int VEC, int NV, int TPU, bool ACT>
 __global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : NV == 2 ? 2 : 3) group_rows_bwd_kernel(const Params p, float* pw, float* pb) {
@@ -938,7 +940,10 @@ long weight_blocks(long rows, int C) {                     // shares of the rows
   const long want = 8l * sm_count() / ((C + 31) / 32) + 1, most = (rows + 31) / 32;
   return want < most ? want : most < 1 ? 1 : most;
 }
-// whether the chunks' first pass leaves the parts of dw and db too (few against the values themselves)
+// Whether the chunks' first pass leaves the parts of dw and db too: 8 bytes a channel and chunk, so with chunks of 4
+// positions as much workspace as a bf16 x, and with fewer positions more than that, which is where
+// group_weights_kernel takes over although it is slower (128 M values, parts against that kernel: 32768 samples of 4 x
+// 1024 741 us, 1153; of 8 465, 905; of 1024 317, 835; 16384 of 2 x 4096 823, 1012).
 bool chunk_parts(const ChunkLayout& l) { return l.rows_each >= 4; }
 
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
