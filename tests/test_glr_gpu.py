@@ -273,3 +273,19 @@ def test_step_slot_out_of_range():
     y = kda.kda_glr_step(d["x"], d["g"], state, slots=torch.tensor([4, 1, -7], dtype=torch.int32, device="cuda"), status=status)
     assert status.item() == 2 and (y[0] == 0).all() and (y[2] == 0).all()
     assert torch.equal(state[[0, 2, 3]], before[[0, 2, 3]]) and not torch.equal(state[1], before[1])
+
+
+@pytest.mark.parametrize("g_range,T", [((-0.01, -0.001), 400), ((-0.3, -0.01), 60)])
+def test_decays_multiply_without_a_bias(g_range, T):
+    """A state that only decays is e^(g T): each e^g has an error of its own channel's, 0.55 of 2^-24 as a deviation,
+    which T tokens add up; over 4096 channels such errors average to 0.55 / 64 = 0.009 of T 2^-24 (6 deviations:
+    0.05), so a mean above 0.1 is a bias of the exponential.  The same for the gradients' way back."""
+    D = 4096
+    lo, hi = g_range
+    g = (lo + (hi - lo) * torch.rand(D, device="cuda")).expand(1, T, D).contiguous()
+    zero, one = torch.zeros(1, T, D, device="cuda"), torch.ones(1, D, device="cuda")
+    want = torch.exp(g[0, 0].double() * T)
+    y, state = kda.kda_glr_fwd(zero, g, initial_state=one)
+    ds0 = kda.kda_glr_bwd(g, y, zero, initial_state=one, d_final_state=one)[2]
+    for got in (state, ds0):
+        assert abs((got[0].double() / want - 1).mean().item()) <= 0.1 * T * 2.0 ** -24
