@@ -4,7 +4,7 @@
 //     p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // Every value is read once and written once.  With 32-bit states that is all there is to it (22 bytes a
 // value in bf16, 28 in fp32 and in bf16 with masters): 134 M values 440 us, 551 and 559, 6.7 to 6.8 TB/s, the copy rate.
-// With 8-bit states (10 bytes) the instructions count as much: 403 M values 1029 us, 58 % of the copy rate, 71 % of the
+// With 8-bit states (10 bytes) the instructions count as much: 403 M values 1035 us, 58 % of the copy rate, 71 % of the
 // issue slots used, 87 instructions a value: 37 for
 // the rounding, 12 for its random numbers, 9 for the step, the rest loads, decoding, averages and stores.
 // So codes are made in integer arithmetic on the bits of the scaled value, and what is rare (subnormal codes,

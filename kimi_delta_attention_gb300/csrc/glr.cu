@@ -17,8 +17,8 @@
 // every call, and the recurrence never leaves the chip.  All waits are bounded (2 s, or KDA_WAIT_LIMIT_NS, then the
 // status says so; 2 s more for what is under way).
 //
-// Measured: 4 x 4096 x 4096 backward 155 us (939 MB, 90 % of the copy rate); 4096 x 4096 forward 34 (134 MB, 58 %;
-// a kernel that only streams the same arrays 26); 46402 packed x 2048 forward with a bf16 gate 168 (570 MB, 50 %).
+// Measured: 4 x 4096 x 4096 backward 152 us (939 MB, 91 % of the copy rate); 4096 x 4096 forward 34.5 (134 MB, 57 %;
+// a kernel that only streams the same arrays 26); 46402 packed x 2048 forward with a bf16 gate 169 (570 MB, 50 %).
 // What is short of the copy rate is a step's latency: 20 instructions a value by 8 to 12 warps an SM, two
 // barriers, the fold and the exchange, some 1.7 us a step of two to three CTAs.
 #include <cuda.h>
