@@ -31,6 +31,14 @@ def _before_capture(what):
         raise KdaError(1, f"a step under capture has no {what} yet: take one step with the same gradients before the capture")
 
 
+def _on(device, t):
+    """A word, or a number, on a device."""
+    if torch.is_tensor(t) and t.device != device:
+        _before_capture(f"word on {device} (one of its words lies on {t.device})")
+        t = t.to(device)
+    return t
+
+
 class AdamW(torch.optim.Optimizer):
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, masters=False, seed=0,
                  capturable=False):
@@ -119,7 +127,7 @@ class AdamW(torch.optim.Optimizer):
                     step.add_(1)
                 states = [self.state[p] for p in params]
                 column = lambda name: [s[name] for s in states]
-                here = lambda t: t.to(device) if torch.is_tensor(t) and t.device != device else t
+                here = lambda t: _on(device, t)
                 small = group["state_bits"] == 8
                 try:
                     kda_adamw_step(params, [p.grad.contiguous() for p in params], column("exp_avg"), column("exp_avg_sq"), step,

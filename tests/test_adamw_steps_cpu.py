@@ -181,3 +181,16 @@ def test_what_a_capture_would_make_anew_is_refused(calls, monkeypatch):
     opt.param_groups[0]["lr"] = 0.5
     take(opt, params, {0, 1, 2})
     assert [step for _, step, _ in calls] == [2, 3, 1]
+
+
+def test_words_of_another_device_are_not_copied_under_capture(calls, monkeypatch):
+    params = parameters(1)
+    opt = AdamW(params, capturable=True)
+    take(opt, params, {0})
+    calls.clear()
+    word = opt.state[params[0]]["step_device"]
+    opt.param_groups[0]["lr"] = opt.param_groups[0]["lr"].to("meta")
+    monkeypatch.setattr(adamw, "_capturing", lambda: True)
+    with pytest.raises(adamw.KdaError, match="word on cpu"):
+        take(opt, params, {0})
+    assert not calls and word.item() == 1
