@@ -116,9 +116,13 @@ class AdamW(torch.optim.Optimizer):
             if group["capturable"]:
                 batches = self._device_words(group, live)
             else:
+                group.pop("step_device", None)
                 alike = {}                  # parameters that have taken the same number of steps, device by device
                 for p in live:
-                    alike.setdefault((p.device, self.state[p]["step"] + 1), []).append(p)
+                    st = self.state[p]
+                    if "step_device" in st:  # (it was capturable: replays have counted there alone)
+                        st["step"] = int(st.pop("step_device"))
+                    alike.setdefault((p.device, st["step"] + 1), []).append(p)
                 batches = [(step, params) for (_, step), params in alike.items()]
             for step, params in batches:
                 device, lr = params[0].device, group["lr"]

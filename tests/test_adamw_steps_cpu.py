@@ -194,3 +194,19 @@ def test_words_of_another_device_are_not_copied_under_capture(calls, monkeypatch
     with pytest.raises(adamw.KdaError, match="word on cpu"):
         take(opt, params, {0})
     assert not calls and word.item() == 1
+
+
+def test_counts_when_a_group_changes_its_mode(calls):
+    """Replays advance the words and not the host's counts; a group that is no longer capturable goes on from the
+    words, and one that becomes capturable from the counts."""
+    params = parameters(3)
+    opt = AdamW(params, capturable=True)
+    take(opt, params, {0, 1})
+    opt.state[params[0]]["step_device"].add_(5)                     # (as replays do)
+    group = opt.param_groups[0]
+    group["capturable"] = False
+    take(opt, params, {0, 2})
+    group["capturable"] = True
+    calls.clear()
+    take(opt, params, {0, 1, 2})
+    assert counts(calls, params) == {0: [8], 1: [7], 2: [2]}
